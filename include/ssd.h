@@ -423,6 +423,173 @@ SSD_API ssd_status_t ssd_decode_step(const ssd_desc_t* desc, const void* x, cons
                              const float* A, const void* B, const void* C, const float* D,
                              float* state, void* y, void* stream);
 
+/* ---- the layer operators around the scan ------------------------------------
+ *
+ * The selective scan (a decay of its own for every channel and state, where
+ * the SSD form has one scalar per head), the short convolution for any
+ * channels and packed sequences, both also for single tokens, and the group
+ * norm behind the scan.
+ *
+ * They share the conventions above, with these differences:
+ *  - Inputs marked "strided" may be views: rows (tokens) of contiguous
+ *    channels, with the distance from one token to the next and from one batch
+ *    row to the next in elements. Halves of a projection's output, padded
+ *    buffers and time-major arrays are read in place. A stride of 0 means
+ *    dense. Rows may not overlap (strides >= the row's width; a token stride
+ *    is at most 2^24). Outputs and states are dense.
+ *  - Base pointers need the alignment of their elements only; 16-byte aligned
+ *    bases, widths and strides are read in 16-byte accesses.
+ *  - The stream's device must be the current device.
+ */
+typedef struct {
+  int64_t token; /* elements from one token (row) to the next; 0: dense      */
+  int64_t batch; /* elements from one batch row to the next; 0: dense        */
+} ssd_stride_t;
+
+/* The selective scan: E = channels, N = dstate (1..256), G = ngroups (E % G
+ * == 0, channel e reads group e / (E / G)); per channel e and state n
+ *     d_t       = pre(dt_t[e])
+ *     h_t[e,n]  = exp(d_t A[e,n]) h_{t-1}[e,n] + d_t x_t[e] B_t[g,n]
+ *     y_t[e]    = (sum_n h_t[e,n] C_t[g,n] + D[e] x_t[e]) * silu(z_t[e])
+ * with pre() the bias, softplus and clamp of ssd_desc_t, h_{-1} the initial
+ * state (zeros when NULL), and the D and gate factors left out when D or z is
+ * NULL. States, sums and decays are fp32; y is rounded once.
+ *     x, z       [batch, L, E]     io dtype, strided (z nullable)
+ *     dt         [batch, L, E]     dt dtype, strided
+ *     B, C       [batch, L, G, N]  io dtype, strided ([G, N] contiguous)
+ *     A          [E, N]            fp32, finite (A <= 0 expected)
+ *     D          [E]               fp32, nullable
+ *     y          [batch, L, E]     io dtype
+ *     states     [batch, E, N]     fp32 */
+typedef struct {
+  int64_t batch;
+  int64_t seqlen;   /* L; packed sequences: the total token count T            */
+  int64_t channels; /* E, up to 2^20                                           */
+  int64_t dstate;   /* N                                                       */
+  int64_t ngroups;  /* G                                                       */
+  int32_t io_dtype; /* ssd_dtype_t of x, z, B, C, y                            */
+  int32_t dt_dtype; /* ssd_dtype_t of dt: fp32, or the io dtype                */
+  const float* dt_bias; /* [E] fp32 device pointer, nullable                   */
+  int32_t dt_softplus;
+  int32_t dt_clamp;     /* requires dt_min <= dt_max                           */
+  float dt_min;
+  float dt_max;
+  ssd_stride_t x_stride, dt_stride, z_stride, B_stride, C_stride;
+} ssd_selective_desc_t;
+
+/* Bytes of workspace for ssd_selective_scan (num_seqs = 0) or
+ * ssd_selective_scan_varlen: 0 where the batch rows and channels alone fill
+ * the card; otherwise the tokens are cut into segments, walked side by side,
+ * whose end states it holds. Pure host computation. */
+SSD_API ssd_status_t ssd_selective_scan_workspace_bytes(const ssd_selective_desc_t* desc, int64_t num_seqs,
+                                                        size_t* bytes);
+
+/* The scan over a batch of prompts. final_state is nullable and may be the
+ * same pointer as init_state; any other overlap of an output with an argument
+ * is refused. workspace: nullable (then allocated and freed in stream order),
+ * 256-byte aligned, of at least the bytes above; calls that may run at the
+ * same time need one each. Results do not depend on what it held, and are the
+ * same bits from one call to the next. */
+SSD_API ssd_status_t ssd_selective_scan(const ssd_selective_desc_t* desc, const void* x, const void* dt,
+                                        const float* A, const void* B, const void* C, const float* D,
+                                        const void* z, const float* init_state, void* y, float* final_state,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* The scan over num_seqs packed sequences (desc->batch = 1, seqlen = T): as
+ * ssd_forward_varlen, sequence s holds tokens [cu_seqlens[s],
+ * cu_seqlens[s+1]), from init_states[s] to final_states[s] ([num_seqs, E, N]).
+ * A sequence may be empty: its state is handed on. Tokens behind the last
+ * sequence are not read, and their y is left as it was. cu_seqlens is clamped
+ * into [0, T] on the device. */
+SSD_API ssd_status_t ssd_selective_scan_varlen(const ssd_selective_desc_t* desc, const int32_t* cu_seqlens,
+                                               int64_t num_seqs, const void* x, const void* dt, const float* A,
+                                               const void* B, const void* C, const float* D, const void* z,
+                                               const float* init_states, void* y, float* final_states,
+                                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token of every row (desc->seqlen = 1; the token strides are not used),
+ * the states kept in a pool between calls:
+ *   state        [num_slots, E, N] fp32, updated in place
+ *   state_slots  [batch] int32 DEVICE pointer, nullable (row b uses slot b;
+ *                num_slots >= batch then). A row whose slot is negative or
+ *                >= num_slots is padding: nothing of it is written, its y is
+ *                left as it was. Of several rows that name one slot the first
+ *                has it; the others are treated as padding.
+ * state and y must not overlap each other or any input. No workspace. */
+SSD_API ssd_status_t ssd_selective_step(const ssd_selective_desc_t* desc, const void* x, const void* dt,
+                                        const float* A, const void* B, const void* C, const float* D,
+                                        const void* z, float* state, const int32_t* state_slots,
+                                        int64_t num_slots, void* y, void* stream);
+
+/* The short causal depthwise convolution of ssd_conv1d_split for any number
+ * of channels CH:
+ *   z[t] = bias[ch] + sum_{k<K} weight[ch][k] * in[t - (K-1) + k],
+ *   out[t] = silu ? z * sigmoid(z) : z,
+ * K = conv_width in 1..4. The channels may go to up to three dense outputs, in
+ * order (x | B | C for the SSD scan): out_channels[i] of them to output i, 0
+ * for an output that is not there; together CH. */
+typedef struct {
+  int64_t batch;
+  int64_t seqlen;   /* packed sequences: the total token count T               */
+  int64_t channels; /* CH, up to 2^20                                          */
+  int64_t out_channels[3];
+  int32_t conv_width;
+  int32_t silu;
+  int32_t io_dtype; /* ssd_dtype_t of x and the outputs                        */
+  ssd_stride_t x_stride;
+} ssd_conv1d_desc_t;
+
+/* The convolution over prompts: a batch (cu_seqlens NULL, num_seqs 0), or
+ * packed sequences (batch 1; cu_seqlens as for ssd_selective_scan_varlen, the
+ * same rules for empty sequences and for tokens behind the last).
+ *   x               [batch, L, CH]           strided
+ *   weight, bias    [CH, K], [CH]            fp32 (bias nullable)
+ *   conv_state_in   [batch or num_seqs, CH, K-1] fp32, nullable: the K-1
+ *                   inputs before each sequence (zeros when NULL)
+ *   conv_state_out  likewise, nullable: the last K-1 inputs of each
+ *   out, out_b, out_c  [batch, L, out_channels[i]]
+ * No output may overlap an input or another output (conv_state_out is not
+ * written in place). */
+SSD_API ssd_status_t ssd_conv1d(const ssd_conv1d_desc_t* desc, const int32_t* cu_seqlens, int64_t num_seqs,
+                                const void* x, const float* weight, const float* bias,
+                                const float* conv_state_in, float* conv_state_out, void* out, void* out_b,
+                                void* out_c, void* stream);
+
+/* The convolution at one token (desc->seqlen = 1): the K-1 inputs kept per
+ * slot are used and moved on by one, in place.
+ *   conv_state   [num_slots, CH, K-1] fp32
+ *   state_slots  as for ssd_selective_step (padding, repeated slots). */
+SSD_API ssd_status_t ssd_conv1d_step(const ssd_conv1d_desc_t* desc, const void* x, const float* weight,
+                                     const float* bias, float* conv_state, const int32_t* state_slots,
+                                     int64_t num_slots, void* out, void* out_b, void* out_c, void* stream);
+
+/* Group norm over the channels of each token, with the layer's gate: per row
+ * and group of S = channels / ngroups channels (S <= 16384)
+ *     v   = x * silu(z) when z != NULL and gate_first, else x
+ *     mu  = center ? mean(v) : 0;   var = mean((v - mu)^2)
+ *     o   = (v - mu) / sqrt(var + eps) * weight + bias
+ *     out = o * silu(z) when z != NULL and not gate_first;
+ *           o * sigmoid(o) when silu (z must be NULL);  else o
+ * center = 0 is the root-mean-square form. Statistics are fp32.
+ *   x, z          [batch, rows, channels]   io dtype, strided (z nullable)
+ *   weight, bias  [channels]                fp32, nullable (1 and 0)
+ *   out           [batch, rows, channels]   io dtype; overlaps no input */
+typedef struct {
+  int64_t batch;
+  int64_t rows;
+  int64_t channels;
+  int64_t ngroups;
+  int32_t io_dtype;
+  int32_t center;
+  int32_t gate_first;
+  int32_t silu;
+  float eps; /* >= 0 */
+  ssd_stride_t x_stride, z_stride;
+} ssd_group_norm_desc_t;
+
+SSD_API ssd_status_t ssd_group_norm(const ssd_group_norm_desc_t* desc, const void* x, const float* weight,
+                                    const float* bias, const void* z, void* out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

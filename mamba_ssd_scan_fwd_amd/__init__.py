@@ -17,16 +17,26 @@ from .binding import (  # noqa: F401
     chunk_cumsum,
     chunk_scan,
     chunk_state,
+    conv1d,
     conv1d_split,
+    conv1d_split_step,
+    conv1d_split_varlen,
+    conv1d_step,
+    conv1d_varlen,
     cumsum_chunk_state,
     decode_step,
     effective_chunk_size,
     forward,
     forward_noalloc,
     forward_varlen,
+    group_norm,
     lib_path,
     load_library,
     make_desc,
+    selective_scan,
+    selective_scan_varlen,
+    selective_scan_workspace_bytes,
+    selective_step,
     state_passing,
     status_string,
     workspace_bytes,

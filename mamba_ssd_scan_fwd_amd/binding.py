@@ -35,6 +35,16 @@ __all__ = [
     "decode_step",
     "forward_varlen",
     "conv1d_split",
+    "selective_scan",
+    "selective_scan_varlen",
+    "selective_scan_workspace_bytes",
+    "selective_step",
+    "conv1d",
+    "conv1d_varlen",
+    "conv1d_split_varlen",
+    "conv1d_step",
+    "conv1d_split_step",
+    "group_norm",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -60,6 +70,13 @@ EXPORTED_SYMBOLS = (
     "ssd_forward_varlen",
     "ssd_workspace_status_varlen",
     "ssd_conv1d_split",
+    "ssd_selective_scan_workspace_bytes",
+    "ssd_selective_scan",
+    "ssd_selective_scan_varlen",
+    "ssd_selective_step",
+    "ssd_conv1d",
+    "ssd_conv1d_step",
+    "ssd_group_norm",
 )
 
 SSD_DTYPE_F32 = 0
@@ -87,6 +104,61 @@ class SSDDesc(ctypes.Structure):
         ("dt_clamp", ctypes.c_int32),
         ("dt_min", ctypes.c_float),
         ("dt_max", ctypes.c_float),
+    ]
+
+
+class Stride(ctypes.Structure):
+    _fields_ = [("token", ctypes.c_int64), ("batch", ctypes.c_int64)]
+
+
+class SelectiveDesc(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("seqlen", ctypes.c_int64),
+        ("channels", ctypes.c_int64),
+        ("dstate", ctypes.c_int64),
+        ("ngroups", ctypes.c_int64),
+        ("io_dtype", ctypes.c_int32),
+        ("dt_dtype", ctypes.c_int32),
+        ("dt_bias", ctypes.c_void_p),
+        ("dt_softplus", ctypes.c_int32),
+        ("dt_clamp", ctypes.c_int32),
+        ("dt_min", ctypes.c_float),
+        ("dt_max", ctypes.c_float),
+        ("x_stride", Stride),
+        ("dt_stride", Stride),
+        ("z_stride", Stride),
+        ("B_stride", Stride),
+        ("C_stride", Stride),
+    ]
+
+
+class Conv1dDesc(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("seqlen", ctypes.c_int64),
+        ("channels", ctypes.c_int64),
+        ("out_channels", ctypes.c_int64 * 3),
+        ("conv_width", ctypes.c_int32),
+        ("silu", ctypes.c_int32),
+        ("io_dtype", ctypes.c_int32),
+        ("x_stride", Stride),
+    ]
+
+
+class GroupNormDesc(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("rows", ctypes.c_int64),
+        ("channels", ctypes.c_int64),
+        ("ngroups", ctypes.c_int64),
+        ("io_dtype", ctypes.c_int32),
+        ("center", ctypes.c_int32),
+        ("gate_first", ctypes.c_int32),
+        ("silu", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("x_stride", Stride),
+        ("z_stride", Stride),
     ]
 
 
@@ -153,6 +225,22 @@ def load_library():
         lib.ssd_forward_varlen.restype = ctypes.c_int
         lib.ssd_conv1d_split.argtypes = [dp, i32, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp]
         lib.ssd_conv1d_split.restype = ctypes.c_int
+        i64 = ctypes.c_int64
+        sp, cp, gp = ctypes.POINTER(SelectiveDesc), ctypes.POINTER(Conv1dDesc), ctypes.POINTER(GroupNormDesc)
+        lib.ssd_selective_scan_workspace_bytes.argtypes = [sp, i64, ctypes.POINTER(sz)]
+        lib.ssd_selective_scan_workspace_bytes.restype = ctypes.c_int
+        lib.ssd_selective_scan.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        lib.ssd_selective_scan.restype = ctypes.c_int
+        lib.ssd_selective_scan_varlen.argtypes = [sp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        lib.ssd_selective_scan_varlen.restype = ctypes.c_int
+        lib.ssd_selective_step.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp, vp]
+        lib.ssd_selective_step.restype = ctypes.c_int
+        lib.ssd_conv1d.argtypes = [cp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        lib.ssd_conv1d.restype = ctypes.c_int
+        lib.ssd_conv1d_step.argtypes = [cp, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp]
+        lib.ssd_conv1d_step.restype = ctypes.c_int
+        lib.ssd_group_norm.argtypes = [gp, vp, vp, vp, vp, vp, vp]
+        lib.ssd_group_norm.restype = ctypes.c_int
         _lib = lib
     return _lib
 
@@ -568,3 +656,401 @@ def conv1d_split(xbc, weight, bias=None, *, nheads, headdim, ngroups, dstate, si
                                            _ptr(conv_state_out), _ptr(x), _ptr(B), _ptr(C), _stream(stream, dev)),
            "ssd_conv1d_split")
     return x, B, C
+
+
+# ---- the layer operators around the scan -------------------------------------
+#
+# Inputs may be views of wider buffers (rows of contiguous channels, any
+# distance between tokens and batch rows); a call for one token is short, so
+# the checks below are kept few.
+
+_IO = {torch.float32: SSD_DTYPE_F32, torch.bfloat16: SSD_DTYPE_BF16}
+
+
+def _io(t, name):
+    code = _IO.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: unsupported io dtype {t.dtype}")
+    return code
+
+
+def _rows(t, name, dtype, device, shape):
+    """Stride of a strided input of ``shape`` = (batch, tokens, channels..),
+    or (batch, channels..) with ``tokens`` None: channels contiguous."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    return t.stride()
+
+
+def _inner(st, shape, lead, name):
+    """The width of a row whose trailing dimensions are contiguous."""
+    width = 1
+    for i in range(len(shape) - 1, lead - 1, -1):
+        if shape[i] != 1 and st[i] != width:
+            raise ValueError(f"{name}: the channels of a token must be contiguous")
+        width *= shape[i]
+    return width
+
+
+def _stride_of(t, name, dtype, device, shape, lead=2):
+    st = _rows(t, name, dtype, device, shape)
+    width = _inner(st, shape, lead, name)
+    batch = st[0] if shape[0] > 1 else 0
+    token = (st[1] if shape[1] > 1 else 0) if lead == 2 else 0
+    # (0 stands for dense, so a dimension repeated by expand() is refused here)
+    if (shape[0] > 1 and batch < width) or (lead == 2 and shape[1] > 1 and token < width):
+        raise ValueError(f"{name}: tokens must not overlap (an expanded dimension needs a copy)")
+    if token == 0 and batch != 0:
+        token = width
+    elif batch == 0 and token != 0:
+        batch = (shape[1] - 1) * token + width if lead == 2 else width
+    return Stride(token, batch)
+
+
+def _vec(t, name, device, shape):
+    """A dense fp32 argument, or None."""
+    if t is None:
+        return None
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
+    if t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape {shape} on {device}")
+    return t.data_ptr()
+
+
+def _out(t, name, dtype, device, shape):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} on {device}")
+    return t
+
+
+def _ints(t, name, device, numel=None):
+    if t is None:
+        return None
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
+    if t.device != device or t.dim() != 1 or not t.is_contiguous() or (numel is not None and t.numel() != numel):
+        raise ValueError(f"{name} must be a contiguous vector{'' if numel is None else f' of {numel}'} on {device}")
+    return t.data_ptr()
+
+
+def _dim(t, name, n):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, got {t.dim()}")
+
+
+class _On:
+    """Device and stream of one call: outputs and workspaces allocated inside
+    belong to ``stream``, so their memory is not handed out again before the
+    kernels that use it have run."""
+
+    __slots__ = ("guards", "handle")
+
+    def __init__(self, device, stream):
+        self.guards = []
+        if device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(device))
+        if stream is None:
+            self.handle = torch.cuda.current_stream(device).cuda_stream
+        else:
+            self.handle = stream.cuda_stream
+            if stream != torch.cuda.current_stream(device):
+                self.guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+        return False
+
+
+def _selective_desc(x, dt, A, B, C, z, dt_pre, lead):
+    dev, io = x.device, x.dtype
+    shape = tuple(x.shape)
+    E = shape[-1]
+    _dim(A, "A", 2)
+    N = A.shape[1]
+    _dim(B, "B", lead + 2)
+    _dim(C, "C", lead + 2)
+    _dim(dt, "dt", lead + 1)
+    G = B.shape[lead]
+    bc = shape[:lead] + (G, N)
+    d = SelectiveDesc()
+    d.batch, d.seqlen, d.channels, d.dstate, d.ngroups = shape[0], shape[1] if lead == 2 else 1, E, N, G
+    d.io_dtype = _io(x, "x")
+    if dt.dtype not in (torch.float32, io):
+        raise TypeError(f"dt must be torch.float32 or {io}, got {dt.dtype}")
+    d.dt_dtype = _IO[dt.dtype]
+    d.x_stride = _stride_of(x, "x", io, dev, shape, lead)
+    d.dt_stride = _stride_of(dt, "dt", dt.dtype, dev, shape, lead)
+    d.B_stride = _stride_of(B, "B", io, dev, bc, lead)
+    d.C_stride = _stride_of(C, "C", io, dev, bc, lead)
+    if z is not None:
+        _dim(z, "z", lead + 1)
+        d.z_stride = _stride_of(z, "z", io, dev, shape, lead)
+    if dt_pre:
+        d.dt_bias = _vec(dt_pre.get("bias"), "dt bias", dev, (E,))
+        d.dt_softplus = 1 if dt_pre.get("softplus") else 0
+        limit = dt_pre.get("limit")
+        if limit is not None:
+            d.dt_clamp, d.dt_min, d.dt_max = 1, float(limit[0]), float(limit[1])
+    return d
+
+
+def _data(t):
+    return None if t is None else t.data_ptr()
+
+
+def selective_scan_workspace_bytes(desc: SelectiveDesc, num_seqs: int = 0) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().ssd_selective_scan_workspace_bytes(ctypes.byref(desc), num_seqs, ctypes.byref(n)),
+           "ssd_selective_scan_workspace_bytes")
+    return int(n.value)
+
+
+def _selective_prompts(x, dt, A, B, C, D, z, cu, S, init, y, final, want_final, workspace, dt_pre, stream):
+    dev = x.device
+    d = _selective_desc(x, dt, A, B, C, z, dt_pre, 2)
+    E, N = d.channels, d.dstate
+    states = (S if S else d.batch, E, N)
+    Ap, Dp = _vec(A, "A", dev, (E, N)), _vec(D, "D", dev, (E,))
+    ip = _vec(init, "init_states" if S else "init_state", dev, states)
+    lib = load_library()
+    with _On(dev, stream) as sp:
+        y = _out(y, "y", x.dtype, dev, x.shape)
+        if final is not None or want_final:
+            final = _out(final, "final_states" if S else "final_state", torch.float32, dev, states)
+        need = selective_scan_workspace_bytes(d, S)
+        if workspace is None:
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        elif not workspace.is_contiguous() or workspace.device != dev or workspace.nbytes < need:
+            raise ValueError(f"workspace needs {need} contiguous bytes on {dev}")
+        size = 0 if workspace is None else workspace.nbytes
+        if S:
+            st = lib.ssd_selective_scan_varlen(ctypes.byref(d), cu, S, x.data_ptr(), dt.data_ptr(), Ap, B.data_ptr(),
+                                               C.data_ptr(), Dp, _data(z), ip, y.data_ptr(), _data(final),
+                                               _data(workspace), size, sp)
+            _check(st, "ssd_selective_scan_varlen")
+        else:
+            st = lib.ssd_selective_scan(ctypes.byref(d), x.data_ptr(), dt.data_ptr(), Ap, B.data_ptr(), C.data_ptr(),
+                                        Dp, _data(z), ip, y.data_ptr(), _data(final), _data(workspace), size, sp)
+            _check(st, "ssd_selective_scan")
+    return y, final
+
+
+def selective_scan(x, dt, A, B, C, D=None, z=None, init_state=None, *, return_final_state: bool = True, y=None,
+                   final_state=None, workspace=None, dt_pre=None, stream=None):
+    """Selective scan over a batch of prompts (a decay for every channel and
+    state). Returns (y [b, L, E], final_state [b, E, N] fp32 or None).
+
+    x, z [b, L, E] and B, C [b, L, G, N] in fp32 or bf16 (all the same; z
+    optional: y is multiplied by silu(z)); dt [b, L, E] in fp32 or the same;
+    A [E, N], D [E] (optional) and init_state [b, E, N] (optional) in fp32.
+    x, dt, z, B and C may be views of wider buffers. ``dt_pre`` as for
+    ``forward``, its bias [E]. ``final_state`` may be ``init_state``.
+    """
+    _dim(x, "x", 3)
+    return _selective_prompts(x, dt, A, B, C, D, z, None, 0, init_state, y, final_state, return_final_state,
+                              workspace, dt_pre, stream)
+
+
+def selective_scan_varlen(x, dt, A, B, C, D=None, z=None, *, cu_seqlens, init_states=None,
+                          return_final_states: bool = True, y=None, final_states=None, workspace=None, dt_pre=None,
+                          stream=None):
+    """``selective_scan`` over packed sequences: x, dt, z [1, T, E], B, C
+    [1, T, G, N], sequence s being tokens [cu_seqlens[s], cu_seqlens[s+1])
+    (int32 device tensor [S+1]). Returns (y, final_states [S, E, N] or None).
+    Where cu_seqlens ends before T, y of the tokens behind it is not written."""
+    _dim(x, "x", 3)
+    if x.shape[0] != 1:
+        raise ValueError("packed sequences: x must be [1, T, E]")
+    cu = _ints(cu_seqlens, "cu_seqlens", x.device)
+    if cu is None or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must hold num_seqs + 1 offsets, num_seqs >= 1")
+    return _selective_prompts(x, dt, A, B, C, D, z, cu, cu_seqlens.numel() - 1, init_states, y, final_states,
+                              return_final_states, workspace, dt_pre, stream)
+
+
+def selective_step(x, dt, A, B, C, D, z, state, *, state_slots=None, y=None, dt_pre=None, stream=None):
+    """One token through the selective scan: x, dt, z [b, E], B, C [b, G, N],
+    ``state`` [slots, E, N] fp32 updated in place. Row b's state is slot
+    ``state_slots[b]`` (int32 [b]; slot b without it); a row with a slot
+    outside the pool, or one that an earlier row has, is left alone. Returns
+    y [b, E] (pass ``y`` to keep what such rows held)."""
+    _dim(x, "x", 2)
+    dev = x.device
+    d = _selective_desc(x, dt, A, B, C, z, dt_pre, 1)
+    E, N = d.channels, d.dstate
+    _dim(state, "state", 3)
+    n = state.shape[0]
+    sp, Ap, Dp = _vec(state, "state", dev, (n, E, N)), _vec(A, "A", dev, (E, N)), _vec(D, "D", dev, (E,))
+    slots = _ints(state_slots, "state_slots", dev, d.batch)
+    with _On(dev, stream) as handle:
+        y = _out(y, "y", x.dtype, dev, x.shape)
+        st = load_library().ssd_selective_step(ctypes.byref(d), x.data_ptr(), dt.data_ptr(), Ap, B.data_ptr(),
+                                               C.data_ptr(), Dp, _data(z), sp, slots, n, y.data_ptr(), handle)
+    _check(st, "ssd_selective_step")
+    return y
+
+
+def _conv_desc(x, weight, widths, silu, lead):
+    dev = x.device
+    shape = tuple(x.shape)
+    _dim(weight, "weight", 2)
+    CH, K = weight.shape
+    if CH != shape[-1]:
+        raise ValueError(f"weight must have shape ({shape[-1]}, K), got {tuple(weight.shape)}")
+    d = Conv1dDesc()
+    d.batch, d.seqlen, d.channels = shape[0], shape[1] if lead == 2 else 1, CH
+    d.out_channels[0], d.out_channels[1], d.out_channels[2] = widths
+    d.conv_width, d.silu, d.io_dtype = K, 1 if silu else 0, _io(x, "x")
+    d.x_stride = _stride_of(x, "x", x.dtype, dev, shape, lead)
+    return d
+
+
+def _split_widths(CH, nheads, headdim, ngroups, dstate):
+    if CH != nheads * headdim + 2 * ngroups * dstate:
+        raise ValueError("xbc channels must be H*P + 2*G*N")
+    return nheads * headdim, ngroups * dstate, ngroups * dstate
+
+
+def _conv_prompts(x, weight, bias, widths, shapes, outs, cu, S, state_in, state_out, silu, stream):
+    dev = x.device
+    d = _conv_desc(x, weight, widths, silu, 2)
+    CH, K = d.channels, d.conv_width
+    states = (S if S else d.batch, CH, K - 1)
+    wp, bp = _vec(weight, "weight", dev, (CH, K)), _vec(bias, "bias", dev, (CH,))
+    name = "conv_states" if S else "conv_state"
+    ip, op = _vec(state_in, name + "_in", dev, states), _vec(state_out, name + "_out", dev, states)
+    with _On(dev, stream) as handle:
+        outs = [_out(o, "y", x.dtype, dev, s) for o, s in zip(outs, shapes)]
+        ptrs = [o.data_ptr() for o in outs] + [None] * (3 - len(outs))
+        st = load_library().ssd_conv1d(ctypes.byref(d), cu, S, x.data_ptr(), wp, bp, ip, op, *ptrs, handle)
+    _check(st, "ssd_conv1d")
+    return outs
+
+
+def conv1d(x, weight, bias=None, *, silu=True, conv_state_in=None, conv_state_out=None, y=None, stream=None):
+    """Short causal depthwise convolution of x [b, L, CH] (fp32 or bf16, a
+    view of a wider buffer or dense), weight [CH, K] fp32, K in 1..4, with an
+    optional SiLU. ``conv_state_in`` and ``conv_state_out`` [b, CH, K-1] fp32
+    hold the inputs before the first token and the last ones. Returns y."""
+    _dim(x, "x", 3)
+    return _conv_prompts(x, weight, bias, (x.shape[2], 0, 0), [x.shape], [y], None, 0, conv_state_in,
+                         conv_state_out, silu, stream)[0]
+
+
+def _packed(x, cu_seqlens):
+    _dim(x, "x", 3)
+    if x.shape[0] != 1:
+        raise ValueError("packed sequences: x must be [1, T, CH]")
+    cu = _ints(cu_seqlens, "cu_seqlens", x.device)
+    if cu is None or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must hold num_seqs + 1 offsets, num_seqs >= 1")
+    return cu, cu_seqlens.numel() - 1
+
+
+def conv1d_varlen(x, weight, bias=None, *, cu_seqlens, silu=True, conv_states_in=None, conv_states_out=None, y=None,
+                  stream=None):
+    """``conv1d`` over packed sequences x [1, T, CH]: sequence s is tokens
+    [cu_seqlens[s], cu_seqlens[s+1]) (int32 device tensor [S+1]), its states
+    row s of ``conv_states_in`` and ``conv_states_out`` [S, CH, K-1]."""
+    cu, S = _packed(x, cu_seqlens)
+    return _conv_prompts(x, weight, bias, (x.shape[2], 0, 0), [x.shape], [y], cu, S, conv_states_in,
+                         conv_states_out, silu, stream)[0]
+
+
+def conv1d_split_varlen(xbc, weight, bias=None, *, cu_seqlens, nheads, headdim, ngroups, dstate, silu=True,
+                        conv_states_in=None, conv_states_out=None, stream=None):
+    """``conv1d_split`` over packed sequences: xbc [1, T, H*P + 2*G*N] into
+    the x [1, T, H, P], B and C [1, T, G, N] that ``forward_varlen`` reads."""
+    cu, S = _packed(xbc, cu_seqlens)
+    T = xbc.shape[1]
+    widths = _split_widths(xbc.shape[2], nheads, headdim, ngroups, dstate)
+    shapes = [(1, T, nheads, headdim), (1, T, ngroups, dstate), (1, T, ngroups, dstate)]
+    return tuple(_conv_prompts(xbc, weight, bias, widths, shapes, [None] * 3, cu, S, conv_states_in,
+                               conv_states_out, silu, stream))
+
+
+def _conv_token(x, weight, bias, widths, shapes, outs, conv_state, state_slots, silu, stream):
+    dev = x.device
+    d = _conv_desc(x, weight, widths, silu, 1)
+    CH, K = d.channels, d.conv_width
+    _dim(conv_state, "conv_state", 3)
+    n = conv_state.shape[0]
+    wp, bp = _vec(weight, "weight", dev, (CH, K)), _vec(bias, "bias", dev, (CH,))
+    cp, slots = _vec(conv_state, "conv_state", dev, (n, CH, K - 1)), _ints(state_slots, "state_slots", dev, d.batch)
+    with _On(dev, stream) as handle:
+        outs = [_out(o, "y", x.dtype, dev, s) for o, s in zip(outs, shapes)]
+        ptrs = [o.data_ptr() for o in outs] + [None] * (3 - len(outs))
+        st = load_library().ssd_conv1d_step(ctypes.byref(d), x.data_ptr(), wp, bp, cp, slots, n, *ptrs, handle)
+    _check(st, "ssd_conv1d_step")
+    return outs
+
+
+def conv1d_step(x, weight, bias, conv_state, *, silu=True, state_slots=None, y=None, stream=None):
+    """``conv1d`` at one token: x [b, CH], ``conv_state`` [slots, CH, K-1]
+    fp32 moved on in place. ``state_slots`` as for ``selective_step``.
+    Returns y [b, CH]."""
+    _dim(x, "x", 2)
+    return _conv_token(x, weight, bias, (x.shape[1], 0, 0), [x.shape], [y], conv_state, state_slots, silu, stream)[0]
+
+
+def conv1d_split_step(xbc, weight, bias, conv_state, *, nheads, headdim, ngroups, dstate, silu=True,
+                      state_slots=None, stream=None):
+    """``conv1d_split`` at one token: xbc [b, H*P + 2*G*N] into the x
+    [b, H, P], B and C [b, G, N] that ``decode_step`` reads; ``conv_state`` and
+    ``state_slots`` as for ``conv1d_step``."""
+    _dim(xbc, "xbc", 2)
+    b = xbc.shape[0]
+    widths = _split_widths(xbc.shape[1], nheads, headdim, ngroups, dstate)
+    shapes = [(b, nheads, headdim), (b, ngroups, dstate), (b, ngroups, dstate)]
+    return tuple(_conv_token(xbc, weight, bias, widths, shapes, [None] * 3, conv_state, state_slots, silu, stream))
+
+
+def group_norm(x, weight=None, bias=None, z=None, *, ngroups=1, eps=1e-5, center=True, gate_first=False, silu=False,
+               out=None, stream=None):
+    """Group norm over the channels of each token of x [.., C] (up to two
+    leading dimensions, views allowed), weight and bias [C] fp32. ``center``
+    False gives the root-mean-square form. ``z`` (like x) gates with silu(z),
+    before the norm with ``gate_first``, else behind it; ``silu`` applies the
+    SiLU to the result instead."""
+    if not 1 <= x.dim() <= 3:
+        raise ValueError("x must have 1 to 3 dimensions")
+    _dim(x, "x", x.dim())
+    dev, io = x.device, x.dtype
+    shape = tuple(x.shape)
+    if z is not None and tuple(z.shape) != shape:
+        raise ValueError(f"z must have shape {shape}, got {tuple(z.shape)}")
+    lead = (1,) * (3 - len(shape))
+    d = GroupNormDesc()
+    s3 = lead + shape
+    d.batch, d.rows, d.channels, d.ngroups = s3[0], s3[1], s3[2], int(ngroups)
+    d.io_dtype, d.center, d.gate_first, d.silu = _io(x, "x"), int(bool(center)), int(bool(gate_first)), int(bool(silu))
+    d.eps = float(eps)
+    d.x_stride = _stride_of(x.view(s3) if lead else x, "x", io, dev, s3)
+    if z is not None:
+        d.z_stride = _stride_of(z.view(s3) if lead else z, "z", io, dev, s3)
+    wp, bp = _vec(weight, "weight", dev, (s3[2],)), _vec(bias, "bias", dev, (s3[2],))
+    with _On(dev, stream) as handle:
+        out = _out(out, "out", io, dev, shape)
+        st = load_library().ssd_group_norm(ctypes.byref(d), x.data_ptr(), wp, bp, _data(z), out.data_ptr(), handle)
+    _check(st, "ssd_group_norm")
+    return out

@@ -9,6 +9,7 @@
 #include <cstdlib>
 #include <cstdio>
 
+#include "host_checks.h"
 #include "ssd_internal.h"
 
 namespace ssd {
@@ -49,10 +50,6 @@ hipError_t launch_chunk_scan_mfma(const Plan& p, const void* x, const void* B, c
 
 namespace {
 
-constexpr size_t kWsAlign = 256;
-
-size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-
 bool is_pow2_in(int64_t v, int64_t lo, int64_t hi) {
   return v >= lo && v <= hi && (v & (v - 1)) == 0;
 }
@@ -69,8 +66,6 @@ int default_chunk(const ssd_desc_t& d) {
   if (d.headdim == 16 && d.dstate == 256) return 128;
   return d.headdim <= 64 ? 256 : 128;
 }
-
-bool aligned(const void* ptr, size_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; }
 
 ssd_status_t make_plan(const ssd_desc_t* d, Plan* p) {
   if (d == nullptr || p == nullptr) return SSD_ERR_NULL_POINTER;
@@ -228,20 +223,6 @@ VarlenLayout varlen_layout(const Plan& p, int64_t num_seqs) {
   v.total = v.stat_off + kStatBytes;
   return v;
 }
-
-struct Range {
-  uintptr_t lo, hi;  // [lo, hi)
-};
-Range range_of(const void* ptr, size_t bytes) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(ptr);
-  return Range{lo, lo + bytes};
-}
-bool overlap(const Range& a, const Range& b) {
-  if (a.lo == a.hi || b.lo == b.hi || a.lo == 0 || b.lo == 0) return false;
-  return a.lo < b.hi && b.lo < a.hi;
-}
-
-ssd_status_t from_hip(hipError_t e) { return e == hipSuccess ? SSD_OK : SSD_ERR_HIP; }
 
 bool debug_enabled() {
   static const bool on = [] {

@@ -1,0 +1,300 @@
+// The short causal convolution for any channel count, strided rows and packed
+// sequences, and its single-token step.
+//     y[t][ch] = act(bias[ch] + sum_{k<K} w[ch][k] in[t - (K-1) + k][ch])
+// where in[] before a sequence's first token is its carried state.
+//
+// Prompts: each thread owns V consecutive channels (16 bytes of a row where
+// alignment allows) and walks a tile of tokens with the K - 1 inputs before
+// it in registers, kU tokens' loads in flight ahead of the ones in use. Each
+// input is read once, plus K - 1 rows at the start of a tile, and the work
+// per element is far below what the memory traffic costs.
+//
+// Packed sequences cut the packed stream into the same tiles: a tile is a
+// list of runs, one for each sequence with tokens in it, and a run starts
+// from its own sequence's inputs or carried state.
+#include "selective.h"
+
+namespace ssd {
+namespace {
+
+constexpr int kThreads = 64;
+constexpr int kU = 8;  // tokens whose loads are issued together
+
+// The output that holds channel ch: its base for row 0 and its row length.
+// (V channels never straddle outputs: the widths are multiples of V.)
+template <typename TIO>
+__device__ __forceinline__ TIO* output_of(void* const (&out)[3], const int (&width)[3], int ch, int& stride) {
+  int o = 0;
+  if (ch >= width[0]) {
+    ch -= width[0];
+    o = 1;
+    if (ch >= width[1]) {
+      ch -= width[1];
+      o = 2;
+    }
+  }
+  stride = width[o];
+  return static_cast<TIO*>(out[o]) + ch;
+}
+
+template <typename TIO, int K, int V>
+__global__ __launch_bounds__(kThreads) void conv1d_kernel(const Conv1dArgs a) {
+  constexpr int H = K > 1 ? K - 1 : 1;
+  constexpr bool VEC = V > 1;
+  const int ch = V * (blockIdx.x * kThreads + threadIdx.x);
+  const bool mine = ch < a.CH;
+  const int cc = mine ? ch : 0;
+  const int64_t b = blockIdx.z;
+  const int64_t t0 = (int64_t)blockIdx.y * a.tile;
+  const int64_t t1 = t0 + a.tile < a.L ? t0 + a.tile : a.L;
+  const TIO* in = static_cast<const TIO*>(a.x) + b * a.xs.batch + cc;
+  int os;
+  TIO* out = output_of<TIO>(a.out, a.width, cc, os);
+  out += b * a.L * os;
+
+  float w[K][V], bias[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    bias[v] = a.bias != nullptr ? a.bias[cc + v] : 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) w[k][v] = a.w[(cc + v) * K + k];
+  }
+  // input j of the K - 1 that row's carried state holds (zeros without one)
+  auto carried = [&](int64_t row, int j, float (&f)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      f[v] = a.state_in != nullptr ? a.state_in[(row * a.CH + cc + v) * H + j] : 0.f;
+  };
+  auto keep = [&](int64_t row, const float (&hist)[H][V]) {
+    if (!mine) return;
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+      for (int v = 0; v < V; ++v) a.state_out[(row * a.CH + cc + v) * H + j] = hist[j][v];
+  };
+
+  // Tokens [r0, r1) of the sequence `row` that began at `first`.
+  auto walk = [&](int64_t row, int64_t first, int64_t r0, int64_t r1, bool ends) {
+    float hist[H][V];
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+      const int64_t t = r0 - (K - 1) + j;
+      if (t >= first) {
+        const Pack<TIO, V> p = load_pack<TIO, V, VEC>(in + t * a.xs.token, V);
+#pragma unroll
+        for (int v = 0; v < V; ++v) hist[j][v] = Elem<TIO>::f32(p.v[v]);
+      } else {
+        carried(row, (int)(t - first) + K - 1, hist[j]);
+      }
+    }
+    Pack<TIO, V> nxt[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+      nxt[u] = load_pack<TIO, V, VEC>(in + (r0 + u < r1 ? r0 + u : r1 - 1) * a.xs.token, V);
+    for (int64_t tb = r0; tb < r1; tb += kU) {
+      Pack<TIO, V> cur[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) cur[u] = nxt[u];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int64_t t = tb + kU + u;
+        nxt[u] = load_pack<TIO, V, VEC>(in + (t < r1 ? t : r1 - 1) * a.xs.token, V);
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        if (tb + u < r1) {
+          float z[V];
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const float now = Elem<TIO>::f32(cur[u].v[v]);
+            z[v] = bias[v];
+#pragma unroll
+            for (int k = 0; k < K - 1; ++k) z[v] = fmaf(w[k][v], hist[k][v], z[v]);
+            z[v] = fmaf(w[K - 1][v], now, z[v]);
+            if (a.silu) z[v] = silu_f32(z[v]);
+#pragma unroll
+            for (int k = 0; k + 1 < K - 1; ++k) hist[k][v] = hist[k + 1][v];
+            hist[H - 1][v] = now;
+          }
+          if (mine) store_pack<TIO, V, VEC>(out + (tb + u) * os, z, V);
+        }
+      }
+    }
+    if (ends && a.state_out != nullptr) keep(row, hist);
+  };
+
+  if (a.cu == nullptr) {
+    walk(b, 0, t0, t1, t1 == a.L);
+    return;
+  }
+  int64_t row = seq_of(a.cu, a.nseq, a.L, t0), pos = t0;
+  while (pos < t1 && row < a.nseq) {
+    const int64_t first = seq_offset(a.cu, row, a.L), last = seq_offset(a.cu, row + 1, a.L);
+    if (last > pos && first <= pos) {
+      const int64_t r1 = last < t1 ? last : t1;
+      walk(row, first, pos, r1, last <= t1);
+      pos = r1;
+    }
+    ++row;
+  }
+  // sequences without tokens keep their state: this tile's share of them
+  if (a.state_out != nullptr) {
+    const int lane = threadIdx.x & 63;
+    for (int64_t r = (int64_t)blockIdx.y * 64; r < a.nseq; r += (int64_t)gridDim.y * 64) {
+      const int64_t i = r + lane < a.nseq ? r + lane : a.nseq - 1;
+      uint64_t empty = __ballot(r + lane < a.nseq && seq_offset(a.cu, i + 1, a.L) <= seq_offset(a.cu, i, a.L));
+      while (empty != 0) {
+        const int k = __builtin_ctzll(empty);
+        empty &= empty - 1;
+        float hist[H][V];
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) carried(r + k, j, hist[j]);
+        keep(r + k, hist);
+      }
+    }
+  }
+}
+
+// One token per row: V channels to a thread, their K - 1 old inputs read and
+// written as one block of V (K - 1) floats. Rows without a slot of their own
+// (negative, behind the pool, or named by an earlier row) are padding.
+constexpr int kStepThreads = 256;
+
+template <typename TIO, int K, int V, int R>
+__global__ __launch_bounds__(kStepThreads) void conv1d_step_kernel(const Conv1dStepArgs a) {
+  constexpr int H = K > 1 ? K - 1 : 1;
+  constexpr bool VEC = V > 1;
+  const int ch = V * (blockIdx.x * kStepThreads + threadIdx.x);
+  const bool mine = ch < a.CH;
+  const int cc = mine ? ch : 0;
+  const int64_t row0 = (int64_t)blockIdx.y * R;
+  int os;
+  TIO* out = output_of<TIO>(a.out, a.width, cc, os);
+
+  Pack<float, V> w[K], bias;
+#pragma unroll
+  for (int k = 0; k < K; ++k) w[k] = load_pack<float, V, VEC>(a.w + cc * K + k * V, V);
+  bias = load_pack<float, V, false>(a.bias != nullptr ? a.bias + cc : a.w, V);
+  Pack<float, V> old[R][H];
+  Pack<TIO, V> xv[R];
+  int64_t slot[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t row = row0 + r < a.batch ? row0 + r : a.batch - 1;
+    slot[r] = a.slots != nullptr ? a.slots[row] : row;
+    if (row0 + r >= a.batch || slot[r] < 0 || slot[r] >= a.nslots) slot[r] = -1;
+    const int64_t from = slot[r] < 0 ? 0 : slot[r];
+    if constexpr (K > 1) {
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j)
+        old[r][j] = load_pack<float, V, VEC>(a.state + (from * a.CH + cc) * H + j * V, V);
+    }
+    xv[r] = load_pack<TIO, V, VEC>(static_cast<const TIO*>(a.x) + row * a.xs + cc, V);
+  }
+  if (a.slots != nullptr) {
+    const uint32_t again = repeated_slots<R, kStepThreads>(a.slots, row0, a.batch);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (again >> r & 1) slot[r] = -1;
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (slot[r] < 0 || !mine) continue;
+    float z[V], kept[H][V];  // element i of a block is channel i / H, input i % H
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float now = Elem<TIO>::f32(xv[r].v[v]);
+      z[v] = a.bias != nullptr ? bias.v[v] : 0.f;
+#pragma unroll
+      for (int k = 0; k < K - 1; ++k) {
+        const int i = v * H + k, j = v * K + k;
+        z[v] = fmaf(w[j / V].v[j % V], old[r][i / V].v[i % V], z[v]);
+        const int n = v * H + k + 1;
+        kept[i / V][i % V] = k + 1 < K - 1 ? old[r][(k + 1 < K - 1 ? n : i) / V].v[(k + 1 < K - 1 ? n : i) % V] : now;
+      }
+      const int j = v * K + K - 1;
+      z[v] = fmaf(w[j / V].v[j % V], now, z[v]);
+      if (a.silu) z[v] = silu_f32(z[v]);
+    }
+    if constexpr (K > 1) {
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j)
+        store_pack<float, V, VEC>(a.state + (slot[r] * a.CH + cc) * H + j * V, kept[j], V);
+    }
+    store_pack<TIO, V, VEC>(out + (row0 + r) * os, z, V);
+  }
+}
+
+bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// Whether rows of CH channels can be taken V at a time in accesses of
+// V elements: outputs' widths, row strides and bases all multiples of that.
+template <int V, typename TIO, typename Args>
+bool whole_packs(const Args& a, int64_t token, int64_t batch) {
+  const size_t bytes = V * sizeof(TIO);
+  if (token % V || batch % V || reinterpret_cast<uintptr_t>(a.x) % bytes) return false;
+  for (int i = 0; i < 3; ++i)
+    if (a.width[i] % V || reinterpret_cast<uintptr_t>(a.out[i]) % bytes) return false;
+  return true;
+}
+
+template <typename TIO, int K>
+hipError_t launch_conv_k(const Conv1dArgs& args, int64_t batch, hipStream_t s) {
+  constexpr int W = 16 / sizeof(TIO);
+  Conv1dArgs a = args;
+  const bool vec = whole_packs<W, TIO>(a, a.xs.token, a.xs.batch);
+  const int64_t gx = (a.CH + kThreads * (vec ? W : 1) - 1) / (kThreads * (vec ? W : 1));
+  // short tiles while they are needed to fill the card, then long ones, whose
+  // K - 1 repeated rows weigh less
+  int64_t tile = 64;
+  while (tile > 8 && gx * batch * ((a.L + tile - 1) / tile) < 2048) tile /= 2;
+  if ((a.L + tile - 1) / tile > 65535) tile = (a.L + 65534) / 65535;
+  a.tile = (int)tile;
+  const dim3 grid((unsigned)gx, (unsigned)((a.L + tile - 1) / tile), (unsigned)batch);
+  if (vec) conv1d_kernel<TIO, K, W><<<grid, kThreads, 0, s>>>(a);
+  else conv1d_kernel<TIO, K, 1><<<grid, kThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <typename TIO, int K>
+hipError_t launch_step_k(const Conv1dStepArgs& a, hipStream_t s) {
+  const bool vec = whole_packs<4, TIO>(a, a.xs, 0) && on16(a.state) && on16(a.w);
+  const int64_t gx = (a.CH + kStepThreads * (vec ? 4 : 1) - 1) / (kStepThreads * (vec ? 4 : 1));
+  auto go = [&](auto kern, int rows) {
+    kern<<<dim3((unsigned)gx, (unsigned)((a.batch + rows - 1) / rows)), kStepThreads, 0, s>>>(a);
+    return hipGetLastError();
+  };
+  if (!vec) return go(conv1d_step_kernel<TIO, K, 1, 1>, 1);
+  // several rows a workgroup share the weights once that leaves the card full
+  return gx * a.batch >= 4 * 512 ? go(conv1d_step_kernel<TIO, K, 4, 4>, 4) : go(conv1d_step_kernel<TIO, K, 4, 1>, 1);
+}
+
+}  // namespace
+
+hipError_t launch_conv1d(const Conv1dArgs& a, int io, int K, int64_t batch, hipStream_t s) {
+  auto with = [&](auto t) {
+    using T = decltype(t);
+    switch (K) {
+      case 1: return launch_conv_k<T, 1>(a, batch, s);
+      case 2: return launch_conv_k<T, 2>(a, batch, s);
+      case 3: return launch_conv_k<T, 3>(a, batch, s);
+      default: return launch_conv_k<T, 4>(a, batch, s);
+    }
+  };
+  return io == kBF16 ? with(__hip_bfloat16{}) : with(float{});
+}
+
+hipError_t launch_conv1d_step(const Conv1dStepArgs& a, int io, int K, hipStream_t s) {
+  auto with = [&](auto t) {
+    using T = decltype(t);
+    switch (K) {
+      case 1: return launch_step_k<T, 1>(a, s);
+      case 2: return launch_step_k<T, 2>(a, s);
+      case 3: return launch_step_k<T, 3>(a, s);
+      default: return launch_step_k<T, 4>(a, s);
+    }
+  };
+  return io == kBF16 ? with(__hip_bfloat16{}) : with(float{});
+}
+
+}  // namespace ssd

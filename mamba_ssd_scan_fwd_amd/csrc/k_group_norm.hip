@@ -1,0 +1,192 @@
+// Group norm over the channels of each token (channels last), with the gate
+// of the layer around the scan. For every row and group of S = C / G channels:
+//     v = x silu(z) where the gate comes first, else x
+//     mu = mean(v) if centred, else 0;   var = mean((v - mu)^2)
+//     o = (v - mu) / sqrt(var + eps) * w + bias
+//     o = o silu(z) where the gate comes last;  or silu(o)
+//
+// One pass over memory: a team of lanes holds a group's channels in registers
+// (M packs of V consecutive ones to a lane), so the mean and the squares
+// around it are both taken from registers, in fp32. A team keeps its group
+// and walks over rows, with its weights in registers and the next row's loads
+// issued before the current row is reduced (not in the 1024-lane teams of the
+// largest groups: 128 registers a lane hold the row and nothing beside it).
+// Teams up to a wave reduce by lane exchanges; larger groups take a
+// workgroup, which exchanges its waves' sums through LDS.
+#include "selective.h"
+
+namespace ssd {
+namespace {
+
+template <typename TIO, int V, int M, bool VEC, int T, bool Z>
+__global__ __launch_bounds__(T > 64 ? T : 256) void group_norm_kernel(const GroupNormArgs a) {
+  constexpr int THREADS = T > 64 ? T : 256;
+  constexpr int TEAMS = THREADS / T;  // teams per workgroup
+  constexpr int WAVES = THREADS / 64;
+  __shared__ float part[2][T > 64 ? WAVES : 1];
+  const int S = a.C / a.G;
+  const int lane = threadIdx.x % T;
+  const int64_t team = (int64_t)blockIdx.x * TEAMS + threadIdx.x / T;
+  const int64_t nteams = (int64_t)gridDim.x * TEAMS;  // a multiple of G (launch)
+  const int g = (int)(team % a.G);
+  const int64_t step = nteams / a.G;
+  const int64_t rows = a.batch * a.rows;
+  const float inv = 1.f / (float)S;
+  int par = 0;
+
+  int at[M], nn[M];  // this lane's packs: first channel, channels present
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    const int c = (m * T + lane) * V;
+    nn[m] = S - c < 0 ? 0 : S - c > V ? V : S - c;
+    at[m] = g * S + (nn[m] > 0 ? c : 0);
+  }
+  constexpr bool HOLD = T < 1024;
+  auto weight = [&](int m, int v) { return a.w != nullptr ? a.w[at[m] + (v < nn[m] ? v : 0)] : 1.f; };
+  auto offset = [&](int m, int v) { return a.bias != nullptr ? a.bias[at[m] + (v < nn[m] ? v : 0)] : 0.f; };
+  float w[HOLD ? M : 1][V], bias[HOLD ? M : 1][V];
+  if constexpr (HOLD) {
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int v = 0; v < V; ++v) w[m][v] = weight(m, v), bias[m][v] = offset(m, v);
+  }
+
+  Pack<TIO, V> xn[M], zn[Z ? M : 1];
+  auto fetch = [&](int64_t r) {
+    const int64_t b = r / a.rows, t = r - b * a.rows;
+    const TIO* xp = static_cast<const TIO*>(a.x) + b * a.xs.batch + t * a.xs.token;
+    const TIO* zp = static_cast<const TIO*>(a.z) + b * a.zs.batch + t * a.zs.token;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      xn[m] = load_pack<TIO, V, VEC>(xp + at[m], nn[m]);
+      if constexpr (Z) zn[m] = load_pack<TIO, V, VEC>(zp + at[m], nn[m]);
+    }
+  };
+  auto team_sum = [&](float v) {
+#pragma unroll
+    for (int off = (T > 64 ? 64 : T) / 2; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+    if constexpr (T > 64) {
+      // two buffers: the next sum's writes meet no reader of this one
+      par ^= 1;
+      if ((threadIdx.x & 63) == 0) part[par][threadIdx.x / 64] = v;
+      __syncthreads();
+      v = 0.f;
+#pragma unroll
+      for (int i = 0; i < WAVES; ++i) v += part[par][i];
+    }
+    return v;
+  };
+
+  int64_t r = team / a.G;
+  // (all lanes of a workgroup-wide team share r, so its barriers are met by all)
+  if (r >= rows) return;
+  fetch(r);
+  for (; r < rows; r += step) {
+    float x[M][V];
+    Pack<TIO, V> zc[Z ? M : 1];
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      if constexpr (Z) zc[m] = zn[m];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        x[m][v] = Elem<TIO>::f32(xn[m].v[v]);
+        if constexpr (Z) {
+          if (a.gate_first) x[m][v] *= silu_f32(Elem<TIO>::f32(zc[m].v[v]));
+        }
+      }
+    }
+    if (HOLD && r + step < rows) fetch(r + step);
+    float mu = 0.f;
+    if (a.center) {
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (v < nn[m]) mu += x[m][v];
+      mu = team_sum(mu) * inv;
+    }
+    float sq = 0.f;
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        x[m][v] -= mu;
+        if (v < nn[m]) sq = fmaf(x[m][v], x[m][v], sq);
+      }
+    const float var = team_sum(sq) * inv + a.eps;
+    // one Newton step on the hardware's reciprocal root (1 ulp)
+    float rs = __builtin_amdgcn_rsqf(var);
+    rs = var > 0.f && var < 1e38f ? rs * fmaf(-0.5f * var * rs, rs, 1.5f) : rs;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      float o[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if constexpr (HOLD) o[v] = fmaf(x[m][v] * rs, w[m][v], bias[m][v]);
+        else o[v] = fmaf(x[m][v] * rs, weight(m, v), offset(m, v));
+        if constexpr (Z) {
+          if (!a.gate_first) o[v] *= silu_f32(Elem<TIO>::f32(zc[m].v[v]));
+        } else {
+          if (a.silu) o[v] = silu_f32(o[v]);
+        }
+      }
+      if (nn[m] > 0) store_pack<TIO, V, VEC>(static_cast<TIO*>(a.out) + r * a.C + at[m], o, nn[m]);
+    }
+    if (!HOLD && r + step < rows) fetch(r + step);
+  }
+}
+
+template <typename TIO, bool VEC, bool Z>
+hipError_t launch_z(const GroupNormArgs& a, hipStream_t s) {
+  constexpr int V = 16 / sizeof(TIO);
+  const int64_t S = a.C / a.G, packs = (S + V - 1) / V, rows = a.batch * a.rows;
+  auto go = [&](auto kern, int team) {
+    const int threads = team > 64 ? team : 256, per = threads / team;
+    // teams for all rows and groups, but no more than fill the card, and a
+    // whole number of rows' worth: a team keeps its group
+    int64_t want = rows * a.G;
+    const int64_t full = (int64_t)device_cu_count() * (2048 / team);
+    int64_t teams = want < full ? want : full;
+    // smallest number of workgroups that is a multiple of G / gcd(G, per)
+    int64_t x = a.G, y = per;
+    while (y != 0) {
+      const int64_t t = x % y;
+      x = y;
+      y = t;
+    }
+    const int64_t unit = a.G / x;
+    int64_t blocks = ((teams + per - 1) / per + unit - 1) / unit * unit;
+    kern<<<dim3((unsigned)blocks), threads, 0, s>>>(a);
+    return hipGetLastError();
+  };
+  if (packs <= 8) return go(group_norm_kernel<TIO, V, 1, VEC, 8, Z>, 8);
+  if (packs <= 16) return go(group_norm_kernel<TIO, V, 1, VEC, 16, Z>, 16);
+  if (packs <= 32) return go(group_norm_kernel<TIO, V, 1, VEC, 32, Z>, 32);
+  if (packs <= 64) return go(group_norm_kernel<TIO, V, 1, VEC, 64, Z>, 64);
+  if (packs <= 128) return go(group_norm_kernel<TIO, V, 2, VEC, 64, Z>, 64);
+  if (packs <= 256) return go(group_norm_kernel<TIO, V, 1, VEC, 256, Z>, 256);
+  if (packs <= 512) return go(group_norm_kernel<TIO, V, 2, VEC, 256, Z>, 256);
+  if (packs <= 1024) return go(group_norm_kernel<TIO, V, 4, VEC, 256, Z>, 256);
+  constexpr int M = (int)(kGroupNormMaxGroup / 1024 / V);
+  return go(group_norm_kernel<TIO, V, M, VEC, 1024, Z>, 1024);
+}
+
+template <typename TIO>
+hipError_t launch_io(const GroupNormArgs& a, hipStream_t s) {
+  constexpr int V = 16 / sizeof(TIO);
+  auto on = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+  // 16-byte accesses: groups, row strides and bases in whole packs
+  const bool vec = (a.C / a.G) % V == 0 && a.xs.token % V == 0 && a.xs.batch % V == 0 && on(a.x) && on(a.out) &&
+                   (a.z == nullptr || (a.zs.token % V == 0 && a.zs.batch % V == 0 && on(a.z)));
+  if (a.z != nullptr) return vec ? launch_z<TIO, true, true>(a, s) : launch_z<TIO, false, true>(a, s);
+  return vec ? launch_z<TIO, true, false>(a, s) : launch_z<TIO, false, false>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_group_norm(const GroupNormArgs& a, int io, hipStream_t s) {
+  return io == kBF16 ? launch_io<__hip_bfloat16>(a, s) : launch_io<float>(a, s);
+}
+
+}  // namespace ssd
