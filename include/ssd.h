@@ -436,7 +436,7 @@ SSD_API ssd_status_t ssd_decode_step(const ssd_desc_t* desc, const void* x, cons
  *    row to the next in elements. Halves of a projection's output, padded
  *    buffers and time-major arrays are read in place. A stride of 0 means
  *    dense. Rows may not overlap (strides >= the row's width; a token stride
- *    is at most 2^24). Outputs and states are dense.
+ *    is below 2^22). Outputs and states are dense.
  *  - Base pointers need the alignment of their elements only; 16-byte aligned
  *    bases, widths and strides are read in 16-byte accesses.
  *  - The stream's device must be the current device.

@@ -12,8 +12,9 @@ namespace {
 constexpr int64_t kMaxElems = int64_t(1) << 40;
 constexpr int64_t kMaxRows = int64_t(1) << 31;  // tokens, sequences, batch rows, slots
 constexpr int64_t kMaxChannels = int64_t(1) << 20;
-// a token stride in elements: 31 rows of it stay within 32-bit byte offsets
-constexpr int64_t kMaxTokenStride = int64_t(1) << 24;
+// a token stride in elements: fewer than 2^24 bytes of either type (a factor of
+// the kernels' 24-bit products for offsets inside a tile)
+constexpr int64_t kMaxTokenStride = (int64_t(1) << 22) - 1;
 constexpr int64_t kMaxGridZ = 65535;
 
 bool io_of(int32_t dtype, int* io) {

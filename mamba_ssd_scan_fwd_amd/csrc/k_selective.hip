@@ -40,10 +40,17 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kChannels = 64;  // channels per workgroup
+// Elements from one token to the next in LDS: a quarter row more than its
+// channels, so the four tokens that a wave reads at once lie in other banks.
+constexpr int kPitch = kChannels + 16;
 
 // One lane of the quad's value in all four (DPP quad_perm [j, j, j, j]).
 template <int J> __device__ __forceinline__ float quad_bcast(float v) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), J * 0x55, 0xf, 0xf, true));
+}
+// j is a constant wherever this is called, once the loops are unrolled.
+__device__ __forceinline__ float quad_bcast_of(int j, float v) {
+  return j == 0 ? quad_bcast<0>(v) : j == 1 ? quad_bcast<1>(v) : j == 2 ? quad_bcast<2>(v) : quad_bcast<3>(v);
 }
 // Lane q ^ X of the quad (X = 1: [1, 0, 3, 2], X = 2: [2, 3, 0, 1]).
 template <int X> __device__ __forceinline__ float quad_xor(float v) {
@@ -51,8 +58,53 @@ template <int X> __device__ __forceinline__ float quad_xor(float v) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, 0xf, 0xf, true));
 }
 
-template <typename T> __device__ __forceinline__ typename Elem<T>::raw load_raw(const T* p, uint32_t off) {
-  return *reinterpret_cast<const typename Elem<T>::raw*>(reinterpret_cast<const char*>(p) + off);
+// V consecutive elements in 32-bit words, as they lie in memory. (Words, not
+// elements: 16-bit values that come from two branches would be unpacked, and
+// so waited for, right behind the loads.)
+template <typename T, int V> struct Words {
+  static constexpr int BYTES = V * (int)sizeof(T);
+  static constexpr int N = BYTES < 4 ? 1 : BYTES / 4;
+  uint32_t w[N];
+  __device__ __forceinline__ float f32(int k) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[k]);
+    else return __uint_as_float(k % 2 == 0 ? w[k / 2] << 16 : w[k / 2] & 0xffff0000u);
+  }
+  // to V elements in LDS, aligned to them (up to 16 bytes)
+  __device__ __forceinline__ void put(typename Elem<T>::raw* at) const {
+    if constexpr (BYTES == 2) *at = (typename Elem<T>::raw)w[0];
+    else *reinterpret_cast<Pack<float, N>*>(at) = __builtin_bit_cast(Pack<float, N>, *this);
+  }
+};
+
+// Elements at `row` (of the wave) + `off` bytes from p, of which n are there
+// (at least one; the first stands in for the others), in accesses of up to
+// 16 bytes where WHOLE.
+template <bool WHOLE, typename T, int V>
+__device__ __forceinline__ void load_row(Words<T, V>& r, const T* p, uint64_t row, uint32_t off, int n) {
+  using W = Words<T, V>;
+  const char* at = reinterpret_cast<const char*>(p) + row + off;
+  if constexpr (W::BYTES == 2) {
+    r.w[0] = *reinterpret_cast<const uint16_t*>(at);
+  } else if constexpr (WHOLE) {
+    r = __builtin_bit_cast(W, *reinterpret_cast<const Pack<float, W::N>*>(at));
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) r.w[k] = reinterpret_cast<const uint32_t*>(at)[k < n ? k : 0];
+  } else {
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) {
+      const uint16_t* e = reinterpret_cast<const uint16_t*>(at);
+      r.w[k] = e[2 * k < n ? 2 * k : 0] | (uint32_t)e[2 * k + 1 < n ? 2 * k + 1 : 0] << 16;
+    }
+  }
+}
+
+// Moves a byte offset of the whole wave on. The empty asm keeps it in its
+// registers: as a function of the loop count it would be recomputed with
+// 64-bit products on every tile.
+__device__ __forceinline__ void advance(uint64_t& off, uint32_t bytes) {
+  off += bytes;
+  asm volatile("" : "+s"(off));
 }
 
 // Tokens per tile (a multiple of 4): the unrolled tile has tokens * states / 4
@@ -66,14 +118,22 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
   constexpr int SPL = NP / 4;  // states per lane: n = 16 i + 4 q + k
   constexpr int TT = tile_tokens(NP);
   constexpr int GR = TT / 4;   // groups of four tokens per tile
+  constexpr int VU = SPL / 4;  // units of four states per lane and token
   constexpr int ROW = OUT ? 2 * NP : NP;  // LDS row of a token: B, then C
-  constexpr int PER = TT * NP / kThreads;  // elements of B (and of C) a thread stages
+  constexpr int PER = TT * NP / kThreads;         // states of B (and of C) a thread stages
+  constexpr int PK = TT * kChannels / kThreads;   // channels of one token it stages of x, dt and z
+  using RX = typename Elem<TIO>::raw;
+  using RD = typename Elem<TDT>::raw;
   __shared__ float4 bc4[2][TT * ROW / 4];
+  __shared__ __attribute__((aligned(16))) RX xl[2][TT * kPitch];
+  __shared__ __attribute__((aligned(16))) RX zl[OUT ? 2 : 1][OUT ? TT * kPitch : 1];
+  __shared__ __attribute__((aligned(16))) RD dl[2][TT * kPitch];
 
   const int tid = threadIdx.x;
   const int q = tid & 3;
   const int g = blockIdx.x / a.tiles;
-  const int cg = (blockIdx.x % a.tiles) * kChannels + tid / 4;
+  const int ch0 = (blockIdx.x % a.tiles) * kChannels;
+  const int cg = ch0 + tid / 4;
   const bool mine = cg < a.epg;
   const int e = g * a.epg + (mine ? cg : a.epg - 1);
   const int64_t b = blockIdx.z;
@@ -81,18 +141,19 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
   const int64_t s0 = (int64_t)seg * a.seg_len;
   const int64_t s1 = s0 + a.seg_len < a.L ? s0 + a.seg_len : a.L;
 
-  const TIO* xb = static_cast<const TIO*>(a.x) + b * a.xs.batch;
-  const TDT* db = static_cast<const TDT*>(a.dt) + b * a.ds.batch;
-  const TIO* zb = OUT && a.z != nullptr ? static_cast<const TIO*>(a.z) + b * a.zs.batch : xb;
+  const TIO* xb = static_cast<const TIO*>(a.x) + b * a.xs.batch + (int64_t)g * a.epg;
+  const TDT* db = static_cast<const TDT*>(a.dt) + b * a.ds.batch + (int64_t)g * a.epg;
+  const TIO* zb = OUT && a.z != nullptr ? static_cast<const TIO*>(a.z) + b * a.zs.batch + (int64_t)g * a.epg : xb;
   const int64_t zt = OUT && a.z != nullptr ? a.zs.token : a.xs.token;
   const TIO* Bb = static_cast<const TIO*>(a.B) + b * a.bs.batch + (int64_t)g * a.N;
   const TIO* Cb = static_cast<const TIO*>(a.C) + b * a.cs.batch + (int64_t)g * a.N;
-  TIO* yb = static_cast<TIO*>(a.y) + b * a.L * a.E;
-  // this lane's place in the rows of a group of four tokens, in bytes
-  const uint32_t xo = (uint32_t)((q * a.xs.token + e) * sizeof(TIO));
-  const uint32_t dof = (uint32_t)((q * a.ds.token + e) * sizeof(TDT));
-  const uint32_t zo = (uint32_t)((q * zt + e) * sizeof(TIO));
-  const uint32_t yo = (uint32_t)(((int64_t)q * a.E + e) * sizeof(TIO));
+  TIO* yb = static_cast<TIO*>(a.y) + b * a.L * a.E + (int64_t)g * a.epg;
+  // row strides in bytes
+  const uint32_t xs = (uint32_t)(a.xs.token * sizeof(TIO)), ds = (uint32_t)(a.ds.token * sizeof(TDT));
+  const uint32_t zs = (uint32_t)(zt * sizeof(TIO));
+  const uint32_t bs = (uint32_t)(a.bs.token * sizeof(TIO)), cs = (uint32_t)(a.cs.token * sizeof(TIO));
+  const uint32_t ys = (uint32_t)(a.E * sizeof(TIO));
+  const bool o1 = q & 1, o2 = q & 2;
 
   float A2[SPL], h[SPL];
 #pragma unroll
@@ -130,117 +191,187 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
   };
 
   int buf = 0;
-  using RX = typename Elem<TIO>::raw;
-  using RD = typename Elem<TDT>::raw;
+  const int wave_slot = __builtin_amdgcn_s_getreg(4 | 0 << 6 | 3 << 11);  // HW_ID: wave of its SIMD
 
   // One run: tokens [r0, r1) of one sequence, h updated over them.
   auto walk = [&](int64_t r0, int64_t r1) {
-    RX bn[PER], cn[OUT ? PER : 1];
-    RX xn[GR], zn[OUT ? GR : 1];
-    RD dn[GR];
-    // loads of the tile at t0, all from addresses inside the run
-    auto fetch = [&](int64_t t0) {
-#pragma unroll
-      for (int k = 0; k < PER; ++k) {
-        const int el = tid + k * kThreads, n = el % NP;
-        int64_t t = t0 + el / NP;
-        t = t < r1 ? t : r1 - 1;
-        const int nn = n < a.N ? n : a.N - 1;
-        bn[k] = *reinterpret_cast<const RX*>(Bb + t * a.bs.token + nn);
-        if constexpr (OUT) cn[k] = *reinterpret_cast<const RX*>(Cb + t * a.cs.token + nn);
-      }
-      if (t0 + TT <= r1) {
-#pragma unroll
-        for (int i = 0; i < GR; ++i) {
-          dn[i] = load_raw(db + (t0 + 4 * i) * a.ds.token, dof);
-          xn[i] = load_raw(xb + (t0 + 4 * i) * a.xs.token, xo);
-          if constexpr (OUT) zn[i] = load_raw(zb + (t0 + 4 * i) * zt, zo);
+    // what this thread stages: states bn0.. of token btk, channels xc0.. of
+    // token xtk (the group's first where it has none there)
+    const int btk = tid * PER / NP, bn0 = tid * PER % NP;
+    const int xtk = tid * PK / kChannels, xc0 = tid * PK % kChannels;
+    const int there = a.epg - ch0 - xc0;
+    const int xn0 = there > 0 ? ch0 + xc0 : 0, xnn = there > 0 ? there : 1;
+    Words<TIO, PER> bn, cn;
+    Words<TIO, PK> xn, zn;
+    Words<TDT, PK> dn;
+    // the next tile's rows, and the tokens left from there on
+    uint64_t xr = r0 * xs, dr = r0 * ds, zr = r0 * zs, br = r0 * bs, cr = r0 * cs, yr = r0 * ys;
+    int left = (int)(r1 - r0);
+    // loads of the next tile, all from addresses inside the run
+    auto fetch = [&](int left) {
+      const int bt = btk < left ? btk : left - 1, xt = xtk < left ? xtk : left - 1;
+      const int nb = bn0 < a.N ? bn0 : 0, nbn = a.N - nb;
+      auto load = [&](auto whole) {
+        constexpr bool W = decltype(whole)::value;
+        load_row<W>(dn, db, dr, __umul24(xt, ds) + (uint32_t)(xn0 * sizeof(TDT)), xnn);
+        load_row<W>(xn, xb, xr, __umul24(xt, xs) + (uint32_t)(xn0 * sizeof(TIO)), xnn);
+        load_row<W>(bn, Bb, br, __umul24(bt, bs) + (uint32_t)(nb * sizeof(TIO)), nbn);
+        if constexpr (OUT) {
+          load_row<W>(cn, Cb, cr, __umul24(bt, cs) + (uint32_t)(nb * sizeof(TIO)), nbn);
+          load_row<W>(zn, zb, zr, __umul24(xt, zs) + (uint32_t)(xn0 * sizeof(TIO)), xnn);
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < GR; ++i) {
-          int64_t t = t0 + 4 * i + q;
-          t = t < r1 ? t : r1 - 1;
-          dn[i] = load_raw(db + t * a.ds.token + e, 0);
-          xn[i] = load_raw(xb + t * a.xs.token + e, 0);
-          if constexpr (OUT) zn[i] = load_raw(zb + t * zt + e, 0);
-        }
+      };
+      if (a.whole_in) load(std::true_type{});
+      else load(std::false_type{});
+      advance(xr, TT * xs);
+      advance(dr, TT * ds);
+      advance(br, TT * bs);
+      if constexpr (OUT) {
+        advance(zr, TT * zs);
+        advance(cr, TT * cs);
       }
     };
-    // B and C into the other buffer (zeros behind the run and behind N)
-    auto stage = [&](int64_t t0) {
-      float* dst = reinterpret_cast<float*>(bc4[buf]);
+    // into a buffer: B and C in fp32 (zeros behind the run and behind
+    // N), the rest as it is
+    auto stage = [&](int left, int buf) {
+      float* dst = reinterpret_cast<float*>(bc4[buf]) + btk * ROW + bn0;
 #pragma unroll
       for (int k = 0; k < PER; ++k) {
-        const int el = tid + k * kThreads, n = el % NP, tk = el / NP;
-        const bool in = n < a.N && t0 + tk < r1;
-        dst[tk * ROW + n] = in ? Elem<TIO>::f32(bn[k]) : 0.f;
-        if constexpr (OUT) dst[tk * ROW + NP + n] = in ? Elem<TIO>::f32(cn[k]) : 0.f;
+        const bool in = bn0 + k < a.N && btk < left;
+        dst[k] = in ? bn.f32(k) : 0.f;
+        if constexpr (OUT) dst[NP + k] = in ? cn.f32(k) : 0.f;
       }
+      const int at = xtk * kPitch + xc0;
+      xn.put(xl[buf] + at);
+      dn.put(dl[buf] + at);
+      if constexpr (OUT) zn.put(zl[buf] + at);
     };
 
-    fetch(r0);
-    for (int64_t t0 = r0; t0 < r1; t0 += TT) {
-      buf ^= 1;
-      stage(t0);
-      RX xc[GR], zc[OUT ? GR : 1];
-      RD dc[GR];
+    fetch(left);
+    buf ^= 1;
+    stage(left, buf);
+    __syncthreads();
+    for (; left > 0; left -= TT) {
+      // the older of two waves on a SIMD would otherwise run at its own pace
+      // and leave the other to finish alone, at half of the SIMD's rate
+      if ((left / TT ^ wave_slot) & 1) __builtin_amdgcn_s_setprio(2);
+      else __builtin_amdgcn_s_setprio(0);
+      if (left > TT) fetch(left - TT);
+      // step sizes and inputs of this lane's tokens; behind the run a step of
+      // zero leaves the state as it is
+      RX* xq = xl[buf] + q * kPitch + tid / 4;
+      const RD* dq = dl[buf] + q * kPitch + tid / 4;
+      float dv[GR], xv[GR];
 #pragma unroll
       for (int i = 0; i < GR; ++i) {
-        xc[i] = xn[i];
-        dc[i] = dn[i];
-        if constexpr (OUT) zc[i] = zn[i];
+        dv[i] = Elem<TDT>::f32(dq[4 * i * kPitch]) + bias;
+        xv[i] = Elem<TIO>::f32(xq[4 * i * kPitch]);
       }
-      __syncthreads();
-      if (t0 + TT < r1) fetch(t0 + TT);
+      if (a.dto.softplus) {
+#pragma unroll
+        for (int i = 0; i < GR; ++i) dv[i] = softplus_f32(dv[i]);
+      }
+      if (a.dto.clamp) {
+#pragma unroll
+        for (int i = 0; i < GR; ++i) dv[i] = fminf(fmaxf(dv[i], a.dto.lo), a.dto.hi);
+      }
+      if (left < TT) {
+#pragma unroll
+        for (int i = 0; i < GR; ++i) {
+          const bool in = 4 * i + q < left;
+          dv[i] = in ? dv[i] : 0.f;
+          xv[i] = in ? xv[i] : 0.f;
+        }
+      }
       const float4* row = bc4[buf] + q;
-      const int left = (int)(r1 - t0 < TT ? r1 - t0 : TT);
+      float yv[OUT ? GR : 1], uv[GR];
 #pragma unroll
       for (int i = 0; i < GR; ++i) {
-        const bool in = 4 * i + q < left;
-        // tokens behind the run: a step of zero leaves the state as it is
-        const float dv = in ? step_size(Elem<TDT>::f32(dc[i]), bias, a.dto) : 0.f;
-        const float xv = in ? Elem<TIO>::f32(xc[i]) : 0.f;
-        const float uv = dv * xv;
-        float acc[4];
-        auto token = [&](auto jc) {
-          constexpr int j = decltype(jc)::value;
-          const float d = quad_bcast<j>(dv), u = quad_bcast<j>(uv);
-          const float4* rj = row + (4 * i + j) * (ROW / 4);
-          float p = 0.f;
+        uv[i] = dv[i] * xv[i];
+        if constexpr (OUT) yv[i] = Dv * xv[i];
+        else dsum += dv[i];
+      }
+      // Four states of one token make a unit. A unit's B and C are read two
+      // units ahead and its decays computed one ahead, so neither LDS nor the
+      // exp2 is waited for; the scheduling barrier keeps the compiler from
+      // moving them back to their use.
+      float4 bq[3], cq[OUT ? 3 : 1];
+      float dec[2][4], acc[4];
+      auto read = [&](int w) {
+        const int at = (w / VU) * (ROW / 4) + 4 * (w % VU);
+        bq[w % 3] = row[at];
+        if constexpr (OUT) cq[w % 3] = row[at + NP / 4];
+      };
+      auto decay = [&](int w) {
+        const int tk = w / VU, v = w % VU;
+        const float d = quad_bcast_of(tk % 4, dv[tk / 4]);
 #pragma unroll
-          for (int v = 0; v < SPL / 4; ++v) {
-            const float4 bv = rj[4 * v];
-            float4 cv = make_float4(0.f, 0.f, 0.f, 0.f);
-            if constexpr (OUT) cv = rj[NP / 4 + 4 * v];
-            const float bb[4] = {bv.x, bv.y, bv.z, bv.w}, cc[4] = {cv.x, cv.y, cv.z, cv.w};
+        for (int k = 0; k < 4; ++k) dec[w % 2][k] = __builtin_amdgcn_exp2f(d * A2[4 * v + k]);
+      };
+      read(0);
+      read(1);
+      decay(0);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int s = 4 * v + k;
-              h[s] = fmaf(__builtin_amdgcn_exp2f(d * A2[s]), h[s], u * bb[k]);
-              if constexpr (OUT) p = fmaf(h[s], cc[k], p);
-            }
-          }
-          acc[j] = p;
-        };
-        token(std::integral_constant<int, 0>{});
-        token(std::integral_constant<int, 1>{});
-        token(std::integral_constant<int, 2>{});
-        token(std::integral_constant<int, 3>{});
-        if constexpr (OUT) {
+      for (int w = 0; w < TT * VU; ++w) {
+        const int tk = w / VU, v = w % VU, i = tk / 4, j = tk % 4;
+        if (w + 2 < TT * VU) read(w + 2);
+        if (w + 1 < TT * VU) decay(w + 1);
+        const float u = quad_bcast_of(j, uv[i]);
+        const float4 bv = bq[w % 3], cv = cq[OUT ? w % 3 : 0];
+        const float bb[4] = {bv.x, bv.y, bv.z, bv.w}, cc[4] = {cv.x, cv.y, cv.z, cv.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int s = 4 * v + k;
+          h[s] = fmaf(dec[w % 2][k], h[s], u * bb[k]);
+          if constexpr (OUT) acc[j] = s == 0 ? h[s] * cc[k] : fmaf(h[s], cc[k], acc[j]);
+        }
+        if (OUT && j == 3 && v == VU - 1) {
           // sum over the quad, transposed: lane q ends with token q's
-          const bool o1 = q & 1, o2 = q & 2;
           const float k0 = o1 ? acc[1] : acc[0], m0 = o1 ? acc[0] : acc[1];
           const float k1 = o1 ? acc[3] : acc[2], m1 = o1 ? acc[2] : acc[3];
           const float v0 = k0 + quad_xor<1>(m0), v1 = k1 + quad_xor<1>(m1);
-          float yv = (o2 ? v1 : v0) + quad_xor<2>(o2 ? v0 : v1);
-          yv = fmaf(Dv, xv, yv);
-          if (a.z != nullptr) yv *= silu_f32(Elem<TIO>::f32(zc[i]));
-          if (in && mine)
-            *reinterpret_cast<RX*>(reinterpret_cast<char*>(yb + (t0 + 4 * i) * a.E) + yo) = Elem<TIO>::bits(yv);
-        } else {
-          dsum += dv;
+          yv[i] += (o2 ? v1 : v0) + quad_xor<2>(o2 ? v0 : v1);
         }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // (the states are final here: without a use of them the compiler would
+      // move the whole computation behind the next branch, out of its order)
+#pragma unroll
+      for (int s = 0; s < SPL; ++s) asm volatile("" : "+v"(h[s]));
+      // the next tile's loads are all that is in flight here; y's stores, below,
+      // then have the whole of the next tile to land
+      if (left > TT) stage(left - TT, buf ^ 1);
+      if constexpr (OUT) {
+        if (a.z != nullptr) {
+          const RX* zq = zl[buf] + q * kPitch + tid / 4;
+#pragma unroll
+          for (int i = 0; i < GR; ++i) yv[i] *= silu_f32(Elem<TIO>::f32(zq[4 * i * kPitch]));
+        }
+        // y takes the places of x, which no other lane reads; then each lane
+        // writes PK channels of a token of its wave's 16
+#pragma unroll
+        for (int i = 0; i < GR; ++i) xq[4 * i * kPitch] = Elem<TIO>::bits(yv[i]);
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        const int ytk = (tid & 63) * PK / 16, yc0 = (tid / 64) * 16 + (tid & 63) * PK % 16;
+        const Pack<TIO, PK> out = *reinterpret_cast<const Pack<TIO, PK>*>(xl[buf] + ytk * kPitch + yc0);
+        const int yn = a.epg - ch0 - yc0;
+        if (ytk < left && yn > 0) {
+          RX* to = reinterpret_cast<RX*>(reinterpret_cast<char*>(yb) + yr + (ytk * ys + (uint32_t)((ch0 + yc0) * sizeof(TIO))));
+          if (a.whole_y) {
+            *reinterpret_cast<Pack<TIO, PK>*>(to) = out;
+          } else {
+#pragma unroll
+            for (int k = 0; k < PK; ++k)
+              if (k < yn) to[k] = out.v[k];
+          }
+        }
+        advance(yr, TT * ys);
+      }
+      if (left > TT) {
+        __syncthreads();
+        buf ^= 1;
       }
     }
   };
@@ -301,36 +432,31 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
         load_state(a.init, row);
       }
     };
-    if (a.cu == nullptr) {
-      if (seg == 0) begin(b, a.L > s1); else enter(0);
-      walk(s0, s1);
-      if (s1 == a.L && a.final_state != nullptr) store_state(a.final_state, b);
-    } else {
-      int64_t row = seq_of(a.cu, a.nseq, a.L, s0);
-      int64_t pos = s0;
-      while (pos < s1 && row < a.nseq) {
-        const int64_t first = seq_offset(a.cu, row, a.L), last = seq_offset(a.cu, row + 1, a.L);
-        if (last > pos && first <= pos) {
-          const int64_t r1 = last < s1 ? last : s1;
-          if (first < s0) enter(first / a.seg_len); else begin(row, last > s1);
-          walk(pos, r1);
-          if (last <= s1 && a.final_state != nullptr) store_state(a.final_state, row);
-          pos = r1;
-        }
-        ++row;
-      }
+    // batched: one sequence, the batch row's
+    const bool packed = a.cu != nullptr;
+    int64_t row = packed ? seq_of(a.cu, a.nseq, a.L, s0) : b;
+    const int64_t rows = packed ? a.nseq : b + 1;
+    for (int64_t pos = s0; pos < s1 && row < rows; ++row) {
+      const int64_t first = packed ? seq_offset(a.cu, row, a.L) : 0;
+      const int64_t last = packed ? seq_offset(a.cu, row + 1, a.L) : a.L;
+      if (last <= pos || first > pos) continue;
+      const int64_t r1 = last < s1 ? last : s1;
+      if (first < s0) enter(first / a.seg_len); else begin(row, last > s1);
+      walk(pos, r1);
+      if (last <= s1 && a.final_state != nullptr) store_state(a.final_state, row);
+      pos = r1;
+    }
+    if (packed && a.final_state != nullptr) {
       // sequences without tokens keep their state: this segment's share of them
-      if (a.final_state != nullptr) {
-        const int lane = tid & 63;
-        for (int64_t r = (int64_t)seg * 64; r < a.nseq; r += (int64_t)a.nseg * 64) {
-          const int64_t i = r + lane < a.nseq ? r + lane : a.nseq - 1;
-          uint64_t empty = __ballot(r + lane < a.nseq && seq_offset(a.cu, i + 1, a.L) <= seq_offset(a.cu, i, a.L));
-          while (empty != 0) {
-            const int k = __builtin_ctzll(empty);
-            empty &= empty - 1;
-            load_state(a.init, r + k);
-            store_state(a.final_state, r + k);
-          }
+      const int lane = tid & 63;
+      for (int64_t r = (int64_t)seg * 64; r < a.nseq; r += (int64_t)a.nseg * 64) {
+        const int64_t i = r + lane < a.nseq ? r + lane : a.nseq - 1;
+        uint64_t empty = __ballot(r + lane < a.nseq && seq_offset(a.cu, i + 1, a.L) <= seq_offset(a.cu, i, a.L));
+        while (empty != 0) {
+          const int k = __builtin_ctzll(empty);
+          empty &= empty - 1;
+          load_state(a.init, r + k);
+          store_state(a.final_state, r + k);
         }
       }
     }
@@ -338,7 +464,19 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
 }
 
 template <typename TIO, typename TDT, int NP>
-hipError_t launch_np(const SelectiveArgs& a, int64_t batch, hipStream_t s) {
+hipError_t launch_np(const SelectiveArgs& args, int64_t batch, hipStream_t s) {
+  SelectiveArgs a = args;
+  constexpr int TT = tile_tokens(NP), PER = TT * NP / kThreads, PK = TT * kChannels / kThreads;
+  // whole packs: widths, strides and bases in multiples of them (a pack of
+  // more than 16 bytes is aligned to 16)
+  auto whole = [](const void* p, size_t elem, int v, const Stride& st) {
+    const size_t bytes = v * elem < 16 ? v * elem : 16;
+    return reinterpret_cast<uintptr_t>(p) % bytes == 0 && st.token % v == 0 && st.batch % v == 0;
+  };
+  const bool bc = a.N % PER == 0 && whole(a.B, sizeof(TIO), PER, a.bs) && whole(a.C, sizeof(TIO), PER, a.cs);
+  a.whole_in = bc && a.epg % PK == 0 && whole(a.x, sizeof(TIO), PK, a.xs) && whole(a.dt, sizeof(TDT), PK, a.ds) &&
+              (a.z == nullptr || whole(a.z, sizeof(TIO), PK, a.zs));
+  a.whole_y = a.epg % PK == 0 && whole(a.y, sizeof(TIO), PK, Stride{a.E, a.L * a.E});
   const unsigned tiles = (unsigned)(a.tiles * (a.E / a.epg));
   if (a.nseg > 1) {
     selective_scan_kernel<TIO, TDT, NP, false><<<dim3(tiles, (unsigned)(a.nseg - 1), (unsigned)batch), kThreads, 0, s>>>(a);

@@ -32,7 +32,10 @@ struct SelectiveArgs {
   float* ends;       // [batch, nseg, E, padded N]: the segments' end states
   float* dsums;      // [batch, nseg, E]: their sums of dt
   float* init_copy;  // as ends: initial states that the final states overwrite, else nullptr
-  int epg, tiles;    // channels per group, workgroups per group (set at launch)
+  // set at launch: channels per group, workgroups per group, and which rows
+  // can be taken in whole packs
+  int epg, tiles;
+  bool whole_in, whole_y;
 };
 struct SelectiveCut {
   int64_t nseg, len;
@@ -156,8 +159,9 @@ template <> struct Elem<__hip_bfloat16> {
   static __device__ __forceinline__ uint16_t bits(float v) { return bf16_bits(v); }
 };
 
-// V consecutive elements: one access of V elements where VEC, else V of one.
-template <typename T, int V> struct alignas(V * sizeof(T)) Pack {
+// V consecutive elements (a power of two): aligned accesses of up to 16 bytes
+// where VEC, else V of one element.
+template <typename T, int V> struct alignas(V * sizeof(T) < 16 ? V * sizeof(T) : 16) Pack {
   typename Elem<T>::raw v[V];
 };
 template <typename T, int V, bool VEC>
