@@ -7,6 +7,7 @@ built, every call raises -- there is no fallback implementation.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -107,10 +108,7 @@ class SSDDesc(ctypes.Structure):
     ]
 
 
-class Stride(ctypes.Structure):
-    _fields_ = [("token", ctypes.c_int64), ("batch", ctypes.c_int64)]
-
-
+# (the C structs' pairs of strides, token and batch, are laid out flat here)
 class SelectiveDesc(ctypes.Structure):
     _fields_ = [
         ("batch", ctypes.c_int64),
@@ -125,11 +123,16 @@ class SelectiveDesc(ctypes.Structure):
         ("dt_clamp", ctypes.c_int32),
         ("dt_min", ctypes.c_float),
         ("dt_max", ctypes.c_float),
-        ("x_stride", Stride),
-        ("dt_stride", Stride),
-        ("z_stride", Stride),
-        ("B_stride", Stride),
-        ("C_stride", Stride),
+        ("x_token", ctypes.c_int64),
+        ("x_batch", ctypes.c_int64),
+        ("dt_token", ctypes.c_int64),
+        ("dt_batch", ctypes.c_int64),
+        ("z_token", ctypes.c_int64),
+        ("z_batch", ctypes.c_int64),
+        ("B_token", ctypes.c_int64),
+        ("B_batch", ctypes.c_int64),
+        ("C_token", ctypes.c_int64),
+        ("C_batch", ctypes.c_int64),
     ]
 
 
@@ -138,11 +141,14 @@ class Conv1dDesc(ctypes.Structure):
         ("batch", ctypes.c_int64),
         ("seqlen", ctypes.c_int64),
         ("channels", ctypes.c_int64),
-        ("out_channels", ctypes.c_int64 * 3),
+        ("out0", ctypes.c_int64),
+        ("out1", ctypes.c_int64),
+        ("out2", ctypes.c_int64),
         ("conv_width", ctypes.c_int32),
         ("silu", ctypes.c_int32),
         ("io_dtype", ctypes.c_int32),
-        ("x_stride", Stride),
+        ("x_token", ctypes.c_int64),
+        ("x_batch", ctypes.c_int64),
     ]
 
 
@@ -157,8 +163,10 @@ class GroupNormDesc(ctypes.Structure):
         ("gate_first", ctypes.c_int32),
         ("silu", ctypes.c_int32),
         ("eps", ctypes.c_float),
-        ("x_stride", Stride),
-        ("z_stride", Stride),
+        ("x_token", ctypes.c_int64),
+        ("x_batch", ctypes.c_int64),
+        ("z_token", ctypes.c_int64),
+        ("z_batch", ctypes.c_int64),
     ]
 
 
@@ -661,10 +669,12 @@ def conv1d_split(xbc, weight, bias=None, *, nheads, headdim, ngroups, dstate, si
 # ---- the layer operators around the scan -------------------------------------
 #
 # Inputs may be views of wider buffers (rows of contiguous channels, any
-# distance between tokens and batch rows); a call for one token is short, so
-# the checks below are kept few.
+# distance between tokens and batch rows). A call for one token takes a few
+# microseconds on the GPU, so what the host does for it is kept short: one
+# look at each tensor, one descriptor, the raw handle of the current stream.
 
 _IO = {torch.float32: SSD_DTYPE_F32, torch.bfloat16: SSD_DTYPE_BF16}
+_F32, _I32 = torch.float32, torch.int32
 
 
 def _io(t, name):
@@ -672,74 +682,6 @@ def _io(t, name):
     if code is None:
         raise TypeError(f"{name}: unsupported io dtype {t.dtype}")
     return code
-
-
-def _rows(t, name, dtype, device, shape):
-    """Stride of a strided input of ``shape`` = (batch, tokens, channels..),
-    or (batch, channels..) with ``tokens`` None: channels contiguous."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    return t.stride()
-
-
-def _inner(st, shape, lead, name):
-    """The width of a row whose trailing dimensions are contiguous."""
-    width = 1
-    for i in range(len(shape) - 1, lead - 1, -1):
-        if shape[i] != 1 and st[i] != width:
-            raise ValueError(f"{name}: the channels of a token must be contiguous")
-        width *= shape[i]
-    return width
-
-
-def _stride_of(t, name, dtype, device, shape, lead=2):
-    st = _rows(t, name, dtype, device, shape)
-    width = _inner(st, shape, lead, name)
-    batch = st[0] if shape[0] > 1 else 0
-    token = (st[1] if shape[1] > 1 else 0) if lead == 2 else 0
-    # (0 stands for dense, so a dimension repeated by expand() is refused here)
-    if (shape[0] > 1 and batch < width) or (lead == 2 and shape[1] > 1 and token < width):
-        raise ValueError(f"{name}: tokens must not overlap (an expanded dimension needs a copy)")
-    if token == 0 and batch != 0:
-        token = width
-    elif batch == 0 and token != 0:
-        batch = (shape[1] - 1) * token + width if lead == 2 else width
-    return Stride(token, batch)
-
-
-def _vec(t, name, device, shape):
-    """A dense fp32 argument, or None."""
-    if t is None:
-        return None
-    if t.dtype != torch.float32:
-        raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
-    if t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of shape {shape} on {device}")
-    return t.data_ptr()
-
-
-def _out(t, name, dtype, device, shape):
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} on {device}")
-    return t
-
-
-def _ints(t, name, device, numel=None):
-    if t is None:
-        return None
-    if t.dtype != torch.int32:
-        raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
-    if t.device != device or t.dim() != 1 or not t.is_contiguous() or (numel is not None and t.numel() != numel):
-        raise ValueError(f"{name} must be a contiguous vector{'' if numel is None else f' of {numel}'} on {device}")
-    return t.data_ptr()
 
 
 def _dim(t, name, n):
@@ -751,28 +693,67 @@ def _dim(t, name, n):
         raise ValueError(f"{name} must have {n} dimensions, got {t.dim()}")
 
 
-class _On:
-    """Device and stream of one call: outputs and workspaces allocated inside
-    belong to ``stream``, so their memory is not handed out again before the
-    kernels that use it have run."""
+def _strides(t, name, dtype, device, shape, lead):
+    """(token, batch) stride of a strided input of ``shape`` = (batch, tokens,
+    channels..) with ``lead`` 2, or (batch, channels..) with ``lead`` 1; 0
+    stands for dense."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.is_contiguous():
+        return 0, 0
+    st = t.stride()
+    width = 1
+    for i in range(len(shape) - 1, lead - 1, -1):
+        if shape[i] != 1 and st[i] != width:
+            raise ValueError(f"{name}: the channels of a token must be contiguous")
+        width *= shape[i]
+    rows = shape[1] if lead == 2 else 1
+    token = st[1] if rows > 1 else width
+    batch = st[0] if shape[0] > 1 else (rows - 1) * token + width
+    if token < width or batch < width:
+        raise ValueError(f"{name}: tokens must not overlap (an expanded dimension needs a copy)")
+    return token, batch
 
-    __slots__ = ("guards", "handle")
+
+def _dense(t, name, device, shape, dtype=_F32):
+    """Address of a dense argument, None for one that is not given."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _out(t, name, dtype, device, shape):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _dense(t, name, device, shape, dtype)
+    return t
+
+
+def _offsets(cu_seqlens, device):
+    if cu_seqlens is None or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must hold num_seqs + 1 offsets, num_seqs >= 1")
+    return _dense(cu_seqlens, "cu_seqlens", device, cu_seqlens.shape, _I32), cu_seqlens.numel() - 1
+
+
+class _On:
+    """Makes a tensor's device and the given stream the current ones. Outputs
+    and workspaces allocated inside then belong to that stream, so their
+    memory is not handed out again before the kernels that use it have run."""
 
     def __init__(self, device, stream):
-        self.guards = []
-        if device.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(device))
-        if stream is None:
-            self.handle = torch.cuda.current_stream(device).cuda_stream
-        else:
-            self.handle = stream.cuda_stream
-            if stream != torch.cuda.current_stream(device):
-                self.guards.append(torch.cuda.stream(stream))
+        self.guards = [torch.cuda.device(device)] + ([] if stream is None else [torch.cuda.stream(stream)])
 
     def __enter__(self):
         for g in self.guards:
             g.__enter__()
-        return self.handle
 
     def __exit__(self, *exc):
         for g in reversed(self.guards):
@@ -780,37 +761,41 @@ class _On:
         return False
 
 
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _on(device, stream):
+    if stream is None and device.index == torch.cuda.current_device():
+        return _HERE_ALREADY
+    return _On(device, stream)
+
+
+def _current(device):
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _selective_desc(x, dt, A, B, C, z, dt_pre, lead):
     dev, io = x.device, x.dtype
-    shape = tuple(x.shape)
+    shape = x.shape
     E = shape[-1]
     _dim(A, "A", 2)
-    N = A.shape[1]
     _dim(B, "B", lead + 2)
-    _dim(C, "C", lead + 2)
-    _dim(dt, "dt", lead + 1)
-    G = B.shape[lead]
-    bc = shape[:lead] + (G, N)
-    d = SelectiveDesc()
-    d.batch, d.seqlen, d.channels, d.dstate, d.ngroups = shape[0], shape[1] if lead == 2 else 1, E, N, G
-    d.io_dtype = _io(x, "x")
-    if dt.dtype not in (torch.float32, io):
-        raise TypeError(f"dt must be torch.float32 or {io}, got {dt.dtype}")
-    d.dt_dtype = _IO[dt.dtype]
-    d.x_stride = _stride_of(x, "x", io, dev, shape, lead)
-    d.dt_stride = _stride_of(dt, "dt", dt.dtype, dev, shape, lead)
-    d.B_stride = _stride_of(B, "B", io, dev, bc, lead)
-    d.C_stride = _stride_of(C, "C", io, dev, bc, lead)
-    if z is not None:
-        _dim(z, "z", lead + 1)
-        d.z_stride = _stride_of(z, "z", io, dev, shape, lead)
+    N, G = A.shape[1], B.shape[lead]
+    bc = (*shape[:lead], G, N)
+    ddt = dt.dtype
+    if ddt != _F32 and ddt != io:
+        raise TypeError(f"dt must be torch.float32 or {io}, got {ddt}")
+    bias, softplus, clamp, lo, hi = None, 0, 0, 0.0, 0.0
     if dt_pre:
-        d.dt_bias = _vec(dt_pre.get("bias"), "dt bias", dev, (E,))
-        d.dt_softplus = 1 if dt_pre.get("softplus") else 0
+        bias = _dense(dt_pre.get("bias"), "dt bias", dev, (E,))
+        softplus = 1 if dt_pre.get("softplus") else 0
         limit = dt_pre.get("limit")
         if limit is not None:
-            d.dt_clamp, d.dt_min, d.dt_max = 1, float(limit[0]), float(limit[1])
-    return d
+            clamp, lo, hi = 1, float(limit[0]), float(limit[1])
+    return SelectiveDesc(shape[0], shape[1] if lead == 2 else 1, E, N, G, _io(x, "x"), _IO[ddt], bias, softplus, clamp,
+                         lo, hi, *_strides(x, "x", io, dev, shape, lead), *_strides(dt, "dt", ddt, dev, shape, lead),
+                         *((0, 0) if z is None else _strides(z, "z", io, dev, shape, lead)),
+                         *_strides(B, "B", io, dev, bc, lead), *_strides(C, "C", io, dev, bc, lead))
 
 
 def _data(t):
@@ -829,14 +814,14 @@ def _selective_prompts(x, dt, A, B, C, D, z, cu, S, init, y, final, want_final, 
     d = _selective_desc(x, dt, A, B, C, z, dt_pre, 2)
     E, N = d.channels, d.dstate
     states = (S if S else d.batch, E, N)
-    Ap, Dp = _vec(A, "A", dev, (E, N)), _vec(D, "D", dev, (E,))
-    ip = _vec(init, "init_states" if S else "init_state", dev, states)
+    Ap, Dp = _dense(A, "A", dev, (E, N)), _dense(D, "D", dev, (E,))
+    ip = _dense(init, "init_states" if S else "init_state", dev, states)
     lib = load_library()
-    with _On(dev, stream) as sp:
+    need = selective_scan_workspace_bytes(d, S)
+    with _on(dev, stream):
         y = _out(y, "y", x.dtype, dev, x.shape)
         if final is not None or want_final:
-            final = _out(final, "final_states" if S else "final_state", torch.float32, dev, states)
-        need = selective_scan_workspace_bytes(d, S)
+            final = _out(final, "final_states" if S else "final_state", _F32, dev, states)
         if workspace is None:
             if need:
                 workspace = torch.empty(need, dtype=torch.uint8, device=dev)
@@ -846,12 +831,12 @@ def _selective_prompts(x, dt, A, B, C, D, z, cu, S, init, y, final, want_final, 
         if S:
             st = lib.ssd_selective_scan_varlen(ctypes.byref(d), cu, S, x.data_ptr(), dt.data_ptr(), Ap, B.data_ptr(),
                                                C.data_ptr(), Dp, _data(z), ip, y.data_ptr(), _data(final),
-                                               _data(workspace), size, sp)
-            _check(st, "ssd_selective_scan_varlen")
+                                               _data(workspace), size, _current(dev))
         else:
             st = lib.ssd_selective_scan(ctypes.byref(d), x.data_ptr(), dt.data_ptr(), Ap, B.data_ptr(), C.data_ptr(),
-                                        Dp, _data(z), ip, y.data_ptr(), _data(final), _data(workspace), size, sp)
-            _check(st, "ssd_selective_scan")
+                                        Dp, _data(z), ip, y.data_ptr(), _data(final), _data(workspace), size,
+                                        _current(dev))
+    _check(st, "ssd_selective_scan_varlen" if S else "ssd_selective_scan")
     return y, final
 
 
@@ -871,6 +856,12 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, init_state=None, *, return_fi
                               workspace, dt_pre, stream)
 
 
+def _packed(x):
+    _dim(x, "x", 3)
+    if x.shape[0] != 1:
+        raise ValueError("packed sequences: x must be [1, T, channels]")
+
+
 def selective_scan_varlen(x, dt, A, B, C, D=None, z=None, *, cu_seqlens, init_states=None,
                           return_final_states: bool = True, y=None, final_states=None, workspace=None, dt_pre=None,
                           stream=None):
@@ -878,14 +869,10 @@ def selective_scan_varlen(x, dt, A, B, C, D=None, z=None, *, cu_seqlens, init_st
     [1, T, G, N], sequence s being tokens [cu_seqlens[s], cu_seqlens[s+1])
     (int32 device tensor [S+1]). Returns (y, final_states [S, E, N] or None).
     Where cu_seqlens ends before T, y of the tokens behind it is not written."""
-    _dim(x, "x", 3)
-    if x.shape[0] != 1:
-        raise ValueError("packed sequences: x must be [1, T, E]")
-    cu = _ints(cu_seqlens, "cu_seqlens", x.device)
-    if cu is None or cu_seqlens.numel() < 2:
-        raise ValueError("cu_seqlens must hold num_seqs + 1 offsets, num_seqs >= 1")
-    return _selective_prompts(x, dt, A, B, C, D, z, cu, cu_seqlens.numel() - 1, init_states, y, final_states,
-                              return_final_states, workspace, dt_pre, stream)
+    _packed(x)
+    cu, S = _offsets(cu_seqlens, x.device)
+    return _selective_prompts(x, dt, A, B, C, D, z, cu, S, init_states, y, final_states, return_final_states,
+                              workspace, dt_pre, stream)
 
 
 def selective_step(x, dt, A, B, C, D, z, state, *, state_slots=None, y=None, dt_pre=None, stream=None):
@@ -895,34 +882,29 @@ def selective_step(x, dt, A, B, C, D, z, state, *, state_slots=None, y=None, dt_
     outside the pool, or one that an earlier row has, is left alone. Returns
     y [b, E] (pass ``y`` to keep what such rows held)."""
     _dim(x, "x", 2)
-    dev = x.device
+    dev, shape = x.device, x.shape
     d = _selective_desc(x, dt, A, B, C, z, dt_pre, 1)
-    E, N = d.channels, d.dstate
     _dim(state, "state", 3)
+    E, N = A.shape
     n = state.shape[0]
-    sp, Ap, Dp = _vec(state, "state", dev, (n, E, N)), _vec(A, "A", dev, (E, N)), _vec(D, "D", dev, (E,))
-    slots = _ints(state_slots, "state_slots", dev, d.batch)
-    with _On(dev, stream) as handle:
-        y = _out(y, "y", x.dtype, dev, x.shape)
+    sp, Ap, Dp = _dense(state, "state", dev, (n, E, N)), _dense(A, "A", dev, (shape[1], N)), _dense(D, "D", dev, (E,))
+    slots = _dense(state_slots, "state_slots", dev, shape[:1], _I32)
+    with _on(dev, stream):
+        y = _out(y, "y", x.dtype, dev, shape)
         st = load_library().ssd_selective_step(ctypes.byref(d), x.data_ptr(), dt.data_ptr(), Ap, B.data_ptr(),
-                                               C.data_ptr(), Dp, _data(z), sp, slots, n, y.data_ptr(), handle)
+                                               C.data_ptr(), Dp, _data(z), sp, slots, n, y.data_ptr(), _current(dev))
     _check(st, "ssd_selective_step")
     return y
 
 
 def _conv_desc(x, weight, widths, silu, lead):
-    dev = x.device
-    shape = tuple(x.shape)
+    shape = x.shape
     _dim(weight, "weight", 2)
     CH, K = weight.shape
     if CH != shape[-1]:
         raise ValueError(f"weight must have shape ({shape[-1]}, K), got {tuple(weight.shape)}")
-    d = Conv1dDesc()
-    d.batch, d.seqlen, d.channels = shape[0], shape[1] if lead == 2 else 1, CH
-    d.out_channels[0], d.out_channels[1], d.out_channels[2] = widths
-    d.conv_width, d.silu, d.io_dtype = K, 1 if silu else 0, _io(x, "x")
-    d.x_stride = _stride_of(x, "x", x.dtype, dev, shape, lead)
-    return d
+    return Conv1dDesc(shape[0], shape[1] if lead == 2 else 1, CH, *widths, K, 1 if silu else 0, _io(x, "x"),
+                      *_strides(x, "x", x.dtype, x.device, shape, lead))
 
 
 def _split_widths(CH, nheads, headdim, ngroups, dstate):
@@ -932,17 +914,17 @@ def _split_widths(CH, nheads, headdim, ngroups, dstate):
 
 
 def _conv_prompts(x, weight, bias, widths, shapes, outs, cu, S, state_in, state_out, silu, stream):
-    dev = x.device
+    dev, io = x.device, x.dtype
     d = _conv_desc(x, weight, widths, silu, 2)
-    CH, K = d.channels, d.conv_width
-    states = (S if S else d.batch, CH, K - 1)
-    wp, bp = _vec(weight, "weight", dev, (CH, K)), _vec(bias, "bias", dev, (CH,))
+    CH, K = weight.shape
+    states = (S if S else x.shape[0], CH, K - 1)
+    wp, bp = _dense(weight, "weight", dev, (CH, K)), _dense(bias, "bias", dev, (CH,))
     name = "conv_states" if S else "conv_state"
-    ip, op = _vec(state_in, name + "_in", dev, states), _vec(state_out, name + "_out", dev, states)
-    with _On(dev, stream) as handle:
-        outs = [_out(o, "y", x.dtype, dev, s) for o, s in zip(outs, shapes)]
+    ip, op = _dense(state_in, name + "_in", dev, states), _dense(state_out, name + "_out", dev, states)
+    with _on(dev, stream):
+        outs = [_out(o, "y", io, dev, s) for o, s in zip(outs, shapes)]
         ptrs = [o.data_ptr() for o in outs] + [None] * (3 - len(outs))
-        st = load_library().ssd_conv1d(ctypes.byref(d), cu, S, x.data_ptr(), wp, bp, ip, op, *ptrs, handle)
+        st = load_library().ssd_conv1d(ctypes.byref(d), cu, S, x.data_ptr(), wp, bp, ip, op, *ptrs, _current(dev))
     _check(st, "ssd_conv1d")
     return outs
 
@@ -957,22 +939,13 @@ def conv1d(x, weight, bias=None, *, silu=True, conv_state_in=None, conv_state_ou
                          conv_state_out, silu, stream)[0]
 
 
-def _packed(x, cu_seqlens):
-    _dim(x, "x", 3)
-    if x.shape[0] != 1:
-        raise ValueError("packed sequences: x must be [1, T, CH]")
-    cu = _ints(cu_seqlens, "cu_seqlens", x.device)
-    if cu is None or cu_seqlens.numel() < 2:
-        raise ValueError("cu_seqlens must hold num_seqs + 1 offsets, num_seqs >= 1")
-    return cu, cu_seqlens.numel() - 1
-
-
 def conv1d_varlen(x, weight, bias=None, *, cu_seqlens, silu=True, conv_states_in=None, conv_states_out=None, y=None,
                   stream=None):
     """``conv1d`` over packed sequences x [1, T, CH]: sequence s is tokens
     [cu_seqlens[s], cu_seqlens[s+1]) (int32 device tensor [S+1]), its states
     row s of ``conv_states_in`` and ``conv_states_out`` [S, CH, K-1]."""
-    cu, S = _packed(x, cu_seqlens)
+    _packed(x)
+    cu, S = _offsets(cu_seqlens, x.device)
     return _conv_prompts(x, weight, bias, (x.shape[2], 0, 0), [x.shape], [y], cu, S, conv_states_in,
                          conv_states_out, silu, stream)[0]
 
@@ -981,7 +954,8 @@ def conv1d_split_varlen(xbc, weight, bias=None, *, cu_seqlens, nheads, headdim, 
                         conv_states_in=None, conv_states_out=None, stream=None):
     """``conv1d_split`` over packed sequences: xbc [1, T, H*P + 2*G*N] into
     the x [1, T, H, P], B and C [1, T, G, N] that ``forward_varlen`` reads."""
-    cu, S = _packed(xbc, cu_seqlens)
+    _packed(xbc)
+    cu, S = _offsets(cu_seqlens, xbc.device)
     T = xbc.shape[1]
     widths = _split_widths(xbc.shape[2], nheads, headdim, ngroups, dstate)
     shapes = [(1, T, nheads, headdim), (1, T, ngroups, dstate), (1, T, ngroups, dstate)]
@@ -990,17 +964,18 @@ def conv1d_split_varlen(xbc, weight, bias=None, *, cu_seqlens, nheads, headdim, 
 
 
 def _conv_token(x, weight, bias, widths, shapes, outs, conv_state, state_slots, silu, stream):
-    dev = x.device
+    dev, io = x.device, x.dtype
     d = _conv_desc(x, weight, widths, silu, 1)
-    CH, K = d.channels, d.conv_width
+    CH, K = weight.shape
     _dim(conv_state, "conv_state", 3)
     n = conv_state.shape[0]
-    wp, bp = _vec(weight, "weight", dev, (CH, K)), _vec(bias, "bias", dev, (CH,))
-    cp, slots = _vec(conv_state, "conv_state", dev, (n, CH, K - 1)), _ints(state_slots, "state_slots", dev, d.batch)
-    with _On(dev, stream) as handle:
-        outs = [_out(o, "y", x.dtype, dev, s) for o, s in zip(outs, shapes)]
+    wp, bp = _dense(weight, "weight", dev, (CH, K)), _dense(bias, "bias", dev, (CH,))
+    cp = _dense(conv_state, "conv_state", dev, (n, CH, K - 1))
+    slots = _dense(state_slots, "state_slots", dev, x.shape[:1], _I32)
+    with _on(dev, stream):
+        outs = [_out(o, "y", io, dev, s) for o, s in zip(outs, shapes)]
         ptrs = [o.data_ptr() for o in outs] + [None] * (3 - len(outs))
-        st = load_library().ssd_conv1d_step(ctypes.byref(d), x.data_ptr(), wp, bp, cp, slots, n, *ptrs, handle)
+        st = load_library().ssd_conv1d_step(ctypes.byref(d), x.data_ptr(), wp, bp, cp, slots, n, *ptrs, _current(dev))
     _check(st, "ssd_conv1d_step")
     return outs
 
@@ -1032,25 +1007,25 @@ def group_norm(x, weight=None, bias=None, z=None, *, ngroups=1, eps=1e-5, center
     False gives the root-mean-square form. ``z`` (like x) gates with silu(z),
     before the norm with ``gate_first``, else behind it; ``silu`` applies the
     SiLU to the result instead."""
-    if not 1 <= x.dim() <= 3:
+    rank = x.dim()
+    if not 1 <= rank <= 3:
         raise ValueError("x must have 1 to 3 dimensions")
-    _dim(x, "x", x.dim())
-    dev, io = x.device, x.dtype
-    shape = tuple(x.shape)
-    if z is not None and tuple(z.shape) != shape:
-        raise ValueError(f"z must have shape {shape}, got {tuple(z.shape)}")
-    lead = (1,) * (3 - len(shape))
-    d = GroupNormDesc()
-    s3 = lead + shape
-    d.batch, d.rows, d.channels, d.ngroups = s3[0], s3[1], s3[2], int(ngroups)
-    d.io_dtype, d.center, d.gate_first, d.silu = _io(x, "x"), int(bool(center)), int(bool(gate_first)), int(bool(silu))
-    d.eps = float(eps)
-    d.x_stride = _stride_of(x.view(s3) if lead else x, "x", io, dev, s3)
-    if z is not None:
-        d.z_stride = _stride_of(z.view(s3) if lead else z, "z", io, dev, s3)
-    wp, bp = _vec(weight, "weight", dev, (s3[2],)), _vec(bias, "bias", dev, (s3[2],))
-    with _On(dev, stream) as handle:
+    _dim(x, "x", rank)
+    dev, io, shape = x.device, x.dtype, x.shape
+    if z is not None and z.shape != shape:
+        raise ValueError(f"z must have shape {tuple(shape)}, got {tuple(z.shape)}")
+    x3, z3 = x, z
+    if rank != 3:
+        x3 = x.view((1,) * (3 - rank) + tuple(shape))
+        z3 = None if z is None else z.view(x3.shape)
+    b, rows, C = x3.shape
+    d = GroupNormDesc(b, rows, C, int(ngroups), _io(x, "x"), 1 if center else 0, 1 if gate_first else 0,
+                      1 if silu else 0, float(eps), *_strides(x3, "x", io, dev, x3.shape, 2),
+                      *((0, 0) if z is None else _strides(z3, "z", io, dev, x3.shape, 2)))
+    wp, bp = _dense(weight, "weight", dev, (C,)), _dense(bias, "bias", dev, (C,))
+    with _on(dev, stream):
         out = _out(out, "out", io, dev, shape)
-        st = load_library().ssd_group_norm(ctypes.byref(d), x.data_ptr(), wp, bp, _data(z), out.data_ptr(), handle)
+        st = load_library().ssd_group_norm(ctypes.byref(d), x.data_ptr(), wp, bp, _data(z), out.data_ptr(),
+                                           _current(dev))
     _check(st, "ssd_group_norm")
     return out

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import mamba_ssd_scan_fwd_amd as ssd
-from mamba_ssd_scan_fwd_amd.binding import Conv1dDesc, GroupNormDesc, SelectiveDesc, Stride
+from mamba_ssd_scan_fwd_amd.binding import Conv1dDesc, GroupNormDesc, SelectiveDesc
 
 OK, NULLP, SHAPE, UNSUP, ALIGN, WS, ALIAS = range(7)
 BASE = 0x7F0000000000  # fake device addresses: never dereferenced
@@ -20,9 +20,20 @@ def lib():
     return ssd.load_library()
 
 
+class Stride(tuple):
+    """(token, batch) of a descriptor's stride."""
+
+    def __new__(cls, token, batch):
+        return super().__new__(cls, (token, batch))
+
+
 def fill(d, kw):
     for k, v in kw.items():
-        setattr(d, k, v)
+        if isinstance(v, Stride):
+            setattr(d, k.replace("stride", "token"), v[0])
+            setattr(d, k.replace("stride", "batch"), v[1])
+        else:
+            setattr(d, k, v)
     return d
 
 
@@ -33,7 +44,7 @@ def sel(**kw):
 def conv(**kw):
     widths = kw.pop("out_channels", (64, 0, 0))
     d = fill(Conv1dDesc(batch=2, seqlen=100, channels=64, conv_width=4, silu=1, io_dtype=1), kw)
-    d.out_channels[:] = widths
+    d.out0, d.out1, d.out2 = widths
     return d
 
 
@@ -264,21 +275,20 @@ def test_binding_refuses_host_tensors_and_wrong_ranks():
 
 
 def test_strides_of_views():
-    from mamba_ssd_scan_fwd_amd.binding import _stride_of
+    from mamba_ssd_scan_fwd_amd.binding import _strides
 
     def of(t, lead=2):
-        s = _stride_of(t, "t", t.dtype, t.device, tuple(t.shape), lead)
-        return s.token, s.batch
+        return _strides(t, "t", t.dtype, t.device, t.shape, lead)
 
     wide = torch.zeros(3, 10, 20)
-    assert of(wide) == (20, 200)
+    assert of(wide) == (0, 0)  # dense
     assert of(wide[:, :, 5:12]) == (20, 200)
     assert of(wide[:, 2:6]) == (20, 200)
     assert of(wide[:, ::2]) == (40, 200)
     assert of(wide.transpose(0, 1)) == (200, 20)
-    assert of(wide[:1]) == (20, 200)
+    assert of(wide[:1]) == (0, 0)
     assert of(wide[:, :1]) == (20, 200)
-    assert of(wide[:1, :1]) == (0, 0)
+    assert of(wide[:1, :, :4]) == (20, 184)
     assert of(wide[:, 3], 1) == (20, 200)
     assert of(wide[:, :, 4:12].unflatten(2, (2, 4))) == (20, 200)
     for bad in (wide[:, :, ::2], wide.transpose(1, 2), wide[:, :, 4:12].unflatten(2, (2, 4))[..., :3],
@@ -287,3 +297,11 @@ def test_strides_of_views():
             of(bad)
     with pytest.raises(ValueError):
         of(wide[:1, 0].expand(3, 20), 1)
+
+
+def test_structs_are_as_long_as_the_headers():
+    # 5 sizes, 2 types, pointer, 2 flags, 2 limits, 5 pairs of strides; 6
+    # sizes, 3 ints (padded), 1 pair; 4 sizes, 4 ints, eps (padded), 2 pairs
+    assert ctypes.sizeof(SelectiveDesc) == 40 + 8 + 8 + 8 + 8 + 80
+    assert ctypes.sizeof(Conv1dDesc) == 48 + 16 + 16
+    assert ctypes.sizeof(GroupNormDesc) == 32 + 16 + 8 + 32
