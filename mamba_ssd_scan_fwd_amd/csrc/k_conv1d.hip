@@ -18,7 +18,7 @@ namespace ssd {
 namespace {
 
 constexpr int kThreads = 64;
-constexpr int kU = 8;  // tokens whose loads are issued together
+constexpr int kU = 4;  // tokens whose loads are issued together
 
 // The output that holds channel ch: its base for row 0 and its row length.
 // (V channels never straddle outputs: the widths are multiples of V.)
@@ -52,45 +52,74 @@ __global__ __launch_bounds__(kThreads) void conv1d_kernel(const Conv1dArgs a) {
   TIO* out = output_of<TIO>(a.out, a.width, cc, os);
   out += b * a.L * os;
 
+  // The V channels' weights, and their carried states, are blocks of K V and
+  // (K - 1) V consecutive floats, channel by channel, taken V at a time.
   float w[K][V], bias[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    bias[v] = a.bias != nullptr ? a.bias[cc + v] : 0.f;
+  for (int k = 0; k < K; ++k) {
+    const Pack<float, V> p = load_pack<float, V, VEC>(a.w + cc * K + k * V, V);
 #pragma unroll
-    for (int k = 0; k < K; ++k) w[k][v] = a.w[(cc + v) * K + k];
+    for (int v = 0; v < V; ++v) w[(k * V + v) % K][(k * V + v) / K] = p.v[v];
   }
-  // input j of the K - 1 that row's carried state holds (zeros without one)
-  auto carried = [&](int64_t row, int j, float (&f)[V]) {
+  {
+    const Pack<float, V> p = load_pack<float, V, VEC>(a.bias != nullptr ? a.bias + cc : a.w, V);
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      f[v] = a.state_in != nullptr ? a.state_in[(row * a.CH + cc + v) * H + j] : 0.f;
+    for (int v = 0; v < V; ++v) bias[v] = a.bias != nullptr ? p.v[v] : 0.f;
+  }
+  // the K - 1 inputs that row's carried state holds (zeros without one)
+  auto carried = [&](int64_t row, float (&f)[H][V]) {
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+      Pack<float, V> p = {};
+      if (a.state_in != nullptr) p = load_pack<float, V, VEC>(a.state_in + (row * a.CH + cc) * H + j * V, V);
+#pragma unroll
+      for (int v = 0; v < V; ++v) f[(j * V + v) % H][(j * V + v) / H] = p.v[v];
+    }
   };
   auto keep = [&](int64_t row, const float (&hist)[H][V]) {
     if (!mine) return;
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j)
+    for (int j = 0; j < K - 1; ++j) {
+      float f[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) a.state_out[(row * a.CH + cc + v) * H + j] = hist[j][v];
+      for (int v = 0; v < V; ++v) f[v] = hist[(j * V + v) % H][(j * V + v) / H];
+      store_pack<float, V, VEC>(a.state_out + (row * a.CH + cc) * H + j * V, f, V);
+    }
   };
 
   // Tokens [r0, r1) of the sequence `row` that began at `first`.
   auto walk = [&](int64_t row, int64_t first, int64_t r0, int64_t r1, bool ends) {
-    float hist[H][V];
-#pragma unroll
-    for (int j = 0; j < K - 1; ++j) {
-      const int64_t t = r0 - (K - 1) + j;
-      if (t >= first) {
-        const Pack<TIO, V> p = load_pack<TIO, V, VEC>(in + t * a.xs.token, V);
-#pragma unroll
-        for (int v = 0; v < V; ++v) hist[j][v] = Elem<TIO>::f32(p.v[v]);
-      } else {
-        carried(row, (int)(t - first) + K - 1, hist[j]);
-      }
-    }
-    Pack<TIO, V> nxt[kU];
+    // (all loads first: the tokens before r0, or the run's first in their place)
+    Pack<TIO, V> nxt[kU], before[H];
 #pragma unroll
     for (int u = 0; u < kU; ++u)
       nxt[u] = load_pack<TIO, V, VEC>(in + (r0 + u < r1 ? r0 + u : r1 - 1) * a.xs.token, V);
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+      const int64_t t = r0 - (K - 1) + j;
+      before[j] = load_pack<TIO, V, VEC>(in + (t >= first ? t : r0) * a.xs.token, V);
+    }
+    float hist[H][V];
+    // of the carried state, inputs r0 - first .. K - 2 still lie before r0
+    const int64_t d = r0 - first;
+    if (d < K - 1) {
+      float old[H][V];
+      carried(row, old);
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          hist[j][v] = Elem<TIO>::f32(before[j].v[v]);
+#pragma unroll
+          for (int i = j; i < K - 1; ++i)
+            if (j + d == i) hist[j][v] = old[i][v];
+        }
+    } else {
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+        for (int v = 0; v < V; ++v) hist[j][v] = Elem<TIO>::f32(before[j].v[v]);
+    }
     for (int64_t tb = r0; tb < r1; tb += kU) {
       Pack<TIO, V> cur[kU];
 #pragma unroll
@@ -147,8 +176,7 @@ __global__ __launch_bounds__(kThreads) void conv1d_kernel(const Conv1dArgs a) {
         const int k = __builtin_ctzll(empty);
         empty &= empty - 1;
         float hist[H][V];
-#pragma unroll
-        for (int j = 0; j < K - 1; ++j) carried(r + k, j, hist[j]);
+        carried(r + k, hist);
         keep(r + k, hist);
       }
     }
@@ -242,7 +270,8 @@ template <typename TIO, int K>
 hipError_t launch_conv_k(const Conv1dArgs& args, int64_t batch, hipStream_t s) {
   constexpr int W = 16 / sizeof(TIO);
   Conv1dArgs a = args;
-  const bool vec = whole_packs<W, TIO>(a, a.xs.token, a.xs.batch);
+  const bool vec = whole_packs<W, TIO>(a, a.xs.token, a.xs.batch) && on16(a.w) && on16(a.bias) && on16(a.state_in) &&
+                   on16(a.state_out);
   const int64_t gx = (a.CH + kThreads * (vec ? W : 1) - 1) / (kThreads * (vec ? W : 1));
   // short tiles while they are needed to fill the card, then long ones, whose
   // K - 1 repeated rows weigh less

@@ -53,8 +53,8 @@ __global__ __launch_bounds__(kThreads) void selective_step_kernel(const Selectiv
     if (row0 + k >= a.batch || slot[k] < 0 || slot[k] >= a.nslots) slot[k] = -1;
     const int64_t from = slot[k] < 0 ? 0 : slot[k];
     h[k] = load_pack<float, 4, VEC>(a.state + (from * a.E + e) * a.N + nc, nn);
-    bv[k] = load_pack<TIO, 4, false>(static_cast<const TIO*>(a.B) + r * a.bs + (int64_t)g * a.N + nc, nn);
-    cv[k] = load_pack<TIO, 4, false>(static_cast<const TIO*>(a.C) + r * a.cs + (int64_t)g * a.N + nc, nn);
+    bv[k] = load_pack<TIO, 4, VEC>(static_cast<const TIO*>(a.B) + r * a.bs + (int64_t)g * a.N + nc, nn);
+    cv[k] = load_pack<TIO, 4, VEC>(static_cast<const TIO*>(a.C) + r * a.cs + (int64_t)g * a.N + nc, nn);
     xv[k] = reinterpret_cast<const RX*>(a.x)[r * a.xs + e];
     dv[k] = reinterpret_cast<const typename Elem<TDT>::raw*>(a.dt)[r * a.ds + e];
     zv[k] = reinterpret_cast<const RX*>(zp)[r * zs + e];
@@ -92,8 +92,10 @@ __global__ __launch_bounds__(kThreads) void selective_step_kernel(const Selectiv
 template <typename TIO, typename TDT, int NP>
 hipError_t launch_np(const SelectiveStepArgs& a, hipStream_t s) {
   const unsigned gx = (unsigned)((a.E + kThreads / (NP / 4) - 1) / (kThreads / (NP / 4)));
-  // 16-byte accesses: whole quarters of every row of A and of the states
-  const bool vec = a.N % 4 == 0 && reinterpret_cast<uintptr_t>(a.A) % 16 == 0 && reinterpret_cast<uintptr_t>(a.state) % 16 == 0;
+  // whole groups of four states in every row of A, B, C and of the pool
+  auto on = [](const void* p, size_t b) { return reinterpret_cast<uintptr_t>(p) % b == 0; };
+  const bool vec = a.N % 4 == 0 && on(a.A, 16) && on(a.state, 16) && on(a.B, 4 * sizeof(TIO)) &&
+                   on(a.C, 4 * sizeof(TIO)) && a.bs % 4 == 0 && a.cs % 4 == 0;
   auto go = [&](auto kern, int rows) {
     kern<<<dim3(gx, (unsigned)((a.batch + rows - 1) / rows)), kThreads, 0, s>>>(a);
     return hipGetLastError();
