@@ -247,46 +247,40 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
       if constexpr (OUT) zn.put(zl[buf] + at);
     };
 
-    fetch(left);
-    buf ^= 1;
-    stage(left, buf);
-    __syncthreads();
-    for (; left > 0; left -= TT) {
-      // the older of two waves on a SIMD would otherwise run at its own pace
-      // and leave the other to finish alone, at half of the SIMD's rate
-      if ((left / TT ^ wave_slot) & 1) __builtin_amdgcn_s_setprio(2);
-      else __builtin_amdgcn_s_setprio(0);
-      if (left > TT) fetch(left - TT);
-      // step sizes and inputs of this lane's tokens; behind the run a step of
-      // zero leaves the state as it is
-      RX* xq = xl[buf] + q * kPitch + tid / 4;
-      const RD* dq = dl[buf] + q * kPitch + tid / 4;
-      float dv[GR], xv[GR];
+    // NG groups of four tokens from group i0 of the tile on. TAIL: the run may
+    // end among them; behind it a step of zero leaves the state as it is.
+    auto groups = [&](auto ng, auto tail, int i0) {
+      constexpr int NG = decltype(ng)::value;
+      constexpr bool TAIL = decltype(tail)::value;
+      const int at0 = (4 * i0 + q) * kPitch + tid / 4;
+      RX* xq = xl[buf] + at0;
+      const RD* dq = dl[buf] + at0;
+      float dv[NG], xv[NG];
 #pragma unroll
-      for (int i = 0; i < GR; ++i) {
+      for (int i = 0; i < NG; ++i) {
         dv[i] = Elem<TDT>::f32(dq[4 * i * kPitch]) + bias;
         xv[i] = Elem<TIO>::f32(xq[4 * i * kPitch]);
       }
       if (a.dto.softplus) {
 #pragma unroll
-        for (int i = 0; i < GR; ++i) dv[i] = softplus_f32(dv[i]);
+        for (int i = 0; i < NG; ++i) dv[i] = softplus_f32(dv[i]);
       }
       if (a.dto.clamp) {
 #pragma unroll
-        for (int i = 0; i < GR; ++i) dv[i] = fminf(fmaxf(dv[i], a.dto.lo), a.dto.hi);
+        for (int i = 0; i < NG; ++i) dv[i] = fminf(fmaxf(dv[i], a.dto.lo), a.dto.hi);
       }
-      if (left < TT) {
+      if constexpr (TAIL) {
 #pragma unroll
-        for (int i = 0; i < GR; ++i) {
-          const bool in = 4 * i + q < left;
+        for (int i = 0; i < NG; ++i) {
+          const bool in = 4 * (i0 + i) + q < left;
           dv[i] = in ? dv[i] : 0.f;
           xv[i] = in ? xv[i] : 0.f;
         }
       }
-      const float4* row = bc4[buf] + q;
-      float yv[OUT ? GR : 1], uv[GR];
+      const float4* row = bc4[buf] + 4 * i0 * (ROW / 4) + q;
+      float yv[OUT ? NG : 1], uv[NG];
 #pragma unroll
-      for (int i = 0; i < GR; ++i) {
+      for (int i = 0; i < NG; ++i) {
         uv[i] = dv[i] * xv[i];
         if constexpr (OUT) yv[i] = Dv * xv[i];
         else dsum += dv[i];
@@ -309,13 +303,13 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
         for (int k = 0; k < 4; ++k) dec[w % 2][k] = __builtin_amdgcn_exp2f(d * A2[4 * v + k]);
       };
       read(0);
-      read(1);
+      if (4 * NG * VU > 1) read(1);
       decay(0);
 #pragma unroll
-      for (int w = 0; w < TT * VU; ++w) {
+      for (int w = 0; w < 4 * NG * VU; ++w) {
         const int tk = w / VU, v = w % VU, i = tk / 4, j = tk % 4;
-        if (w + 2 < TT * VU) read(w + 2);
-        if (w + 1 < TT * VU) decay(w + 1);
+        if (w + 2 < 4 * NG * VU) read(w + 2);
+        if (w + 1 < 4 * NG * VU) decay(w + 1);
         const float u = quad_bcast_of(j, uv[i]);
         const float4 bv = bq[w % 3], cv = cq[OUT ? w % 3 : 0];
         const float bb[4] = {bv.x, bv.y, bv.z, bv.w}, cc[4] = {cv.x, cv.y, cv.z, cv.w};
@@ -340,17 +334,36 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
       for (int s = 0; s < SPL; ++s) asm volatile("" : "+v"(h[s]));
       // the next tile's loads are all that is in flight here; y's stores, below,
       // then have the whole of the next tile to land
-      if (left > TT) stage(left - TT, buf ^ 1);
+      if (NG == GR && left > TT) stage(left - TT, buf ^ 1);
       if constexpr (OUT) {
         if (a.z != nullptr) {
-          const RX* zq = zl[buf] + q * kPitch + tid / 4;
+          const RX* zq = zl[buf] + at0;
 #pragma unroll
-          for (int i = 0; i < GR; ++i) yv[i] *= silu_f32(Elem<TIO>::f32(zq[4 * i * kPitch]));
+          for (int i = 0; i < NG; ++i) yv[i] *= silu_f32(Elem<TIO>::f32(zq[4 * i * kPitch]));
         }
-        // y takes the places of x, which no other lane reads; then each lane
-        // writes PK channels of a token of its wave's 16
+        // y takes the places of x, which no other lane reads
 #pragma unroll
-        for (int i = 0; i < GR; ++i) xq[4 * i * kPitch] = Elem<TIO>::bits(yv[i]);
+        for (int i = 0; i < NG; ++i) xq[4 * i * kPitch] = Elem<TIO>::bits(yv[i]);
+      }
+    };
+
+    fetch(left);
+    buf ^= 1;
+    stage(left, buf);
+    __syncthreads();
+    for (; left > 0; left -= TT) {
+      // the older of two waves on a SIMD would otherwise run at its own pace
+      // and leave the other to finish alone, at half of the SIMD's rate
+      if ((left / TT ^ wave_slot) & 1) __builtin_amdgcn_s_setprio(2);
+      else __builtin_amdgcn_s_setprio(0);
+      if (left > TT) fetch(left - TT);
+      if (left >= TT) {
+        groups(std::integral_constant<int, GR>{}, std::false_type{}, 0);
+      } else {
+        for (int i = 0; 4 * i < left; ++i) groups(std::integral_constant<int, 1>{}, std::true_type{}, i);
+      }
+      if constexpr (OUT) {
+        // each lane writes PK channels of a token of its wave's 16
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
