@@ -693,16 +693,21 @@ def _dim(t, name, n):
         raise ValueError(f"{name} must have {n} dimensions, got {t.dim()}")
 
 
+def _unlike(t, name, dtype, device, shape):
+    """Raises for the first thing in which ``t`` is not as it has to be."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
 def _strides(t, name, dtype, device, shape, lead):
     """(token, batch) stride of a strided input of ``shape`` = (batch, tokens,
     channels..) with ``lead`` 2, or (batch, channels..) with ``lead`` 1; 0
     stands for dense."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype or t.shape != shape or t.device != device:
+        _unlike(t, name, dtype, device, shape)
     if t.is_contiguous():
         return 0, 0
     st = t.stride()
@@ -723,22 +728,21 @@ def _dense(t, name, device, shape, dtype=_F32):
     """Address of a dense argument, None for one that is not given."""
     if t is None:
         return None
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} on {device}")
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+        _unlike(t, name, dtype, device, shape)
     return t.data_ptr()
 
 
-def _out(t, name, dtype, device, shape):
+def _out(t, name, like, shape):
+    """The output given, or a new dense one of ``like``'s type and device."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _dense(t, name, device, shape, dtype)
+        return like.new_empty(shape)
+    _dense(t, name, like.device, shape, like.dtype)
     return t
 
 
 def _offsets(cu_seqlens, device):
-    if cu_seqlens is None or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
         raise ValueError("cu_seqlens must hold num_seqs + 1 offsets, num_seqs >= 1")
     return _dense(cu_seqlens, "cu_seqlens", device, cu_seqlens.shape, _I32), cu_seqlens.numel() - 1
 
@@ -770,6 +774,18 @@ def _on(device, stream):
     return _On(device, stream)
 
 
+def _used_on(stream, device, *tensors):
+    """After a call on ``stream``: inputs that belong to the caller's stream,
+    and outputs that belong to this one, are in use on both."""
+    here = torch.cuda.current_stream(device)
+    if stream == here:
+        return
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+            t.record_stream(here)
+
+
 def _current(device):
     return torch._C._cuda_getCurrentRawStream(device.index)
 
@@ -783,7 +799,7 @@ def _selective_desc(x, dt, A, B, C, z, dt_pre, lead):
     N, G = A.shape[1], B.shape[lead]
     bc = (*shape[:lead], G, N)
     ddt = dt.dtype
-    if ddt != _F32 and ddt != io:
+    if ddt is not _F32 and ddt is not io:
         raise TypeError(f"dt must be torch.float32 or {io}, got {ddt}")
     bias, softplus, clamp, lo, hi = None, 0, 0, 0.0, 0.0
     if dt_pre:
@@ -792,10 +808,13 @@ def _selective_desc(x, dt, A, B, C, z, dt_pre, lead):
         limit = dt_pre.get("limit")
         if limit is not None:
             clamp, lo, hi = 1, float(limit[0]), float(limit[1])
+    xt, xb = _strides(x, "x", io, dev, shape, lead)
+    dtt, dtb = _strides(dt, "dt", ddt, dev, shape, lead)
+    zt, zb = (0, 0) if z is None else _strides(z, "z", io, dev, shape, lead)
+    bt, bb = _strides(B, "B", io, dev, bc, lead)
+    ct, cb = _strides(C, "C", io, dev, bc, lead)
     return SelectiveDesc(shape[0], shape[1] if lead == 2 else 1, E, N, G, _io(x, "x"), _IO[ddt], bias, softplus, clamp,
-                         lo, hi, *_strides(x, "x", io, dev, shape, lead), *_strides(dt, "dt", ddt, dev, shape, lead),
-                         *((0, 0) if z is None else _strides(z, "z", io, dev, shape, lead)),
-                         *_strides(B, "B", io, dev, bc, lead), *_strides(C, "C", io, dev, bc, lead))
+                         lo, hi, xt, xb, dtt, dtb, zt, zb, bt, bb, ct, cb)
 
 
 def _data(t):
@@ -809,8 +828,9 @@ def selective_scan_workspace_bytes(desc: SelectiveDesc, num_seqs: int = 0) -> in
     return int(n.value)
 
 
-def _selective_prompts(x, dt, A, B, C, D, z, cu, S, init, y, final, want_final, workspace, dt_pre, stream):
+def _selective_prompts(x, dt, A, B, C, D, z, cu_seqlens, init, y, final, want_final, workspace, dt_pre, stream):
     dev = x.device
+    cu, S = (None, 0) if cu_seqlens is None else _offsets(cu_seqlens, dev)
     d = _selective_desc(x, dt, A, B, C, z, dt_pre, 2)
     E, N = d.channels, d.dstate
     states = (S if S else d.batch, E, N)
@@ -819,9 +839,9 @@ def _selective_prompts(x, dt, A, B, C, D, z, cu, S, init, y, final, want_final, 
     lib = load_library()
     need = selective_scan_workspace_bytes(d, S)
     with _on(dev, stream):
-        y = _out(y, "y", x.dtype, dev, x.shape)
+        y = _out(y, "y", x, x.shape)
         if final is not None or want_final:
-            final = _out(final, "final_states" if S else "final_state", _F32, dev, states)
+            final = _out(final, "final_states" if S else "final_state", A, states)
         if workspace is None:
             if need:
                 workspace = torch.empty(need, dtype=torch.uint8, device=dev)
@@ -837,6 +857,8 @@ def _selective_prompts(x, dt, A, B, C, D, z, cu, S, init, y, final, want_final, 
                                         Dp, _data(z), ip, y.data_ptr(), _data(final), _data(workspace), size,
                                         _current(dev))
     _check(st, "ssd_selective_scan_varlen" if S else "ssd_selective_scan")
+    if stream is not None:
+        _used_on(stream, dev, x, dt, A, B, C, D, z, init, y, final, workspace, cu_seqlens, (dt_pre or {}).get("bias"))
     return y, final
 
 
@@ -852,14 +874,16 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, init_state=None, *, return_fi
     ``forward``, its bias [E]. ``final_state`` may be ``init_state``.
     """
     _dim(x, "x", 3)
-    return _selective_prompts(x, dt, A, B, C, D, z, None, 0, init_state, y, final_state, return_final_state,
+    return _selective_prompts(x, dt, A, B, C, D, z, None, init_state, y, final_state, return_final_state,
                               workspace, dt_pre, stream)
 
 
-def _packed(x):
+def _packed(x, cu_seqlens):
     _dim(x, "x", 3)
     if x.shape[0] != 1:
         raise ValueError("packed sequences: x must be [1, T, channels]")
+    if cu_seqlens is None:
+        raise ValueError("cu_seqlens is required")
 
 
 def selective_scan_varlen(x, dt, A, B, C, D=None, z=None, *, cu_seqlens, init_states=None,
@@ -869,9 +893,8 @@ def selective_scan_varlen(x, dt, A, B, C, D=None, z=None, *, cu_seqlens, init_st
     [1, T, G, N], sequence s being tokens [cu_seqlens[s], cu_seqlens[s+1])
     (int32 device tensor [S+1]). Returns (y, final_states [S, E, N] or None).
     Where cu_seqlens ends before T, y of the tokens behind it is not written."""
-    _packed(x)
-    cu, S = _offsets(cu_seqlens, x.device)
-    return _selective_prompts(x, dt, A, B, C, D, z, cu, S, init_states, y, final_states, return_final_states,
+    _packed(x, cu_seqlens)
+    return _selective_prompts(x, dt, A, B, C, D, z, cu_seqlens, init_states, y, final_states, return_final_states,
                               workspace, dt_pre, stream)
 
 
@@ -890,10 +913,12 @@ def selective_step(x, dt, A, B, C, D, z, state, *, state_slots=None, y=None, dt_
     sp, Ap, Dp = _dense(state, "state", dev, (n, E, N)), _dense(A, "A", dev, (shape[1], N)), _dense(D, "D", dev, (E,))
     slots = _dense(state_slots, "state_slots", dev, shape[:1], _I32)
     with _on(dev, stream):
-        y = _out(y, "y", x.dtype, dev, shape)
+        y = _out(y, "y", x, shape)
         st = load_library().ssd_selective_step(ctypes.byref(d), x.data_ptr(), dt.data_ptr(), Ap, B.data_ptr(),
                                                C.data_ptr(), Dp, _data(z), sp, slots, n, y.data_ptr(), _current(dev))
     _check(st, "ssd_selective_step")
+    if stream is not None:
+        _used_on(stream, dev, x, dt, A, B, C, D, z, state, state_slots, y, (dt_pre or {}).get("bias"))
     return y
 
 
@@ -913,8 +938,9 @@ def _split_widths(CH, nheads, headdim, ngroups, dstate):
     return nheads * headdim, ngroups * dstate, ngroups * dstate
 
 
-def _conv_prompts(x, weight, bias, widths, shapes, outs, cu, S, state_in, state_out, silu, stream):
-    dev, io = x.device, x.dtype
+def _conv_prompts(x, weight, bias, widths, shapes, outs, cu_seqlens, state_in, state_out, silu, stream):
+    dev = x.device
+    cu, S = (None, 0) if cu_seqlens is None else _offsets(cu_seqlens, dev)
     d = _conv_desc(x, weight, widths, silu, 2)
     CH, K = weight.shape
     states = (S if S else x.shape[0], CH, K - 1)
@@ -922,10 +948,12 @@ def _conv_prompts(x, weight, bias, widths, shapes, outs, cu, S, state_in, state_
     name = "conv_states" if S else "conv_state"
     ip, op = _dense(state_in, name + "_in", dev, states), _dense(state_out, name + "_out", dev, states)
     with _on(dev, stream):
-        outs = [_out(o, "y", io, dev, s) for o, s in zip(outs, shapes)]
+        outs = [_out(o, "y", x, s) for o, s in zip(outs, shapes)]
         ptrs = [o.data_ptr() for o in outs] + [None] * (3 - len(outs))
         st = load_library().ssd_conv1d(ctypes.byref(d), cu, S, x.data_ptr(), wp, bp, ip, op, *ptrs, _current(dev))
     _check(st, "ssd_conv1d")
+    if stream is not None:
+        _used_on(stream, dev, x, weight, bias, state_in, state_out, cu_seqlens, *outs)
     return outs
 
 
@@ -935,7 +963,7 @@ def conv1d(x, weight, bias=None, *, silu=True, conv_state_in=None, conv_state_ou
     optional SiLU. ``conv_state_in`` and ``conv_state_out`` [b, CH, K-1] fp32
     hold the inputs before the first token and the last ones. Returns y."""
     _dim(x, "x", 3)
-    return _conv_prompts(x, weight, bias, (x.shape[2], 0, 0), [x.shape], [y], None, 0, conv_state_in,
+    return _conv_prompts(x, weight, bias, (x.shape[2], 0, 0), [x.shape], [y], None, conv_state_in,
                          conv_state_out, silu, stream)[0]
 
 
@@ -944,9 +972,8 @@ def conv1d_varlen(x, weight, bias=None, *, cu_seqlens, silu=True, conv_states_in
     """``conv1d`` over packed sequences x [1, T, CH]: sequence s is tokens
     [cu_seqlens[s], cu_seqlens[s+1]) (int32 device tensor [S+1]), its states
     row s of ``conv_states_in`` and ``conv_states_out`` [S, CH, K-1]."""
-    _packed(x)
-    cu, S = _offsets(cu_seqlens, x.device)
-    return _conv_prompts(x, weight, bias, (x.shape[2], 0, 0), [x.shape], [y], cu, S, conv_states_in,
+    _packed(x, cu_seqlens)
+    return _conv_prompts(x, weight, bias, (x.shape[2], 0, 0), [x.shape], [y], cu_seqlens, conv_states_in,
                          conv_states_out, silu, stream)[0]
 
 
@@ -954,17 +981,16 @@ def conv1d_split_varlen(xbc, weight, bias=None, *, cu_seqlens, nheads, headdim, 
                         conv_states_in=None, conv_states_out=None, stream=None):
     """``conv1d_split`` over packed sequences: xbc [1, T, H*P + 2*G*N] into
     the x [1, T, H, P], B and C [1, T, G, N] that ``forward_varlen`` reads."""
-    _packed(xbc)
-    cu, S = _offsets(cu_seqlens, xbc.device)
+    _packed(xbc, cu_seqlens)
     T = xbc.shape[1]
     widths = _split_widths(xbc.shape[2], nheads, headdim, ngroups, dstate)
     shapes = [(1, T, nheads, headdim), (1, T, ngroups, dstate), (1, T, ngroups, dstate)]
-    return tuple(_conv_prompts(xbc, weight, bias, widths, shapes, [None] * 3, cu, S, conv_states_in,
+    return tuple(_conv_prompts(xbc, weight, bias, widths, shapes, [None] * 3, cu_seqlens, conv_states_in,
                                conv_states_out, silu, stream))
 
 
 def _conv_token(x, weight, bias, widths, shapes, outs, conv_state, state_slots, silu, stream):
-    dev, io = x.device, x.dtype
+    dev = x.device
     d = _conv_desc(x, weight, widths, silu, 1)
     CH, K = weight.shape
     _dim(conv_state, "conv_state", 3)
@@ -973,10 +999,12 @@ def _conv_token(x, weight, bias, widths, shapes, outs, conv_state, state_slots, 
     cp = _dense(conv_state, "conv_state", dev, (n, CH, K - 1))
     slots = _dense(state_slots, "state_slots", dev, x.shape[:1], _I32)
     with _on(dev, stream):
-        outs = [_out(o, "y", io, dev, s) for o, s in zip(outs, shapes)]
+        outs = [_out(o, "y", x, s) for o, s in zip(outs, shapes)]
         ptrs = [o.data_ptr() for o in outs] + [None] * (3 - len(outs))
         st = load_library().ssd_conv1d_step(ctypes.byref(d), x.data_ptr(), wp, bp, cp, slots, n, *ptrs, _current(dev))
     _check(st, "ssd_conv1d_step")
+    if stream is not None:
+        _used_on(stream, dev, x, weight, bias, conv_state, state_slots, *outs)
     return outs
 
 
@@ -1024,8 +1052,10 @@ def group_norm(x, weight=None, bias=None, z=None, *, ngroups=1, eps=1e-5, center
                       *((0, 0) if z is None else _strides(z3, "z", io, dev, x3.shape, 2)))
     wp, bp = _dense(weight, "weight", dev, (C,)), _dense(bias, "bias", dev, (C,))
     with _on(dev, stream):
-        out = _out(out, "out", io, dev, shape)
+        out = _out(out, "out", x, shape)
         st = load_library().ssd_group_norm(ctypes.byref(d), x.data_ptr(), wp, bp, _data(z), out.data_ptr(),
                                            _current(dev))
     _check(st, "ssd_group_norm")
+    if stream is not None:
+        _used_on(stream, dev, x, weight, bias, z, out)
     return out

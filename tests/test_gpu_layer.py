@@ -522,3 +522,194 @@ def test_layer_operators_replay_from_a_captured_graph():
         eager = run()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, eager))
+
+
+def test_every_operator_takes_a_stream():
+    s = Selective(1, 40, 64, 16, io="bf16", dt="bf16", seed=34)
+    kw, h0, _ = s.to(DEV)
+    one = {k: (v[:, 0] if k in ("x", "dt", "z", "B", "C") else v) for k, v in kw.items()}
+    g = torch.Generator().manual_seed(35)
+    w, conv = torch.randn((64, 4), generator=g).to(DEV), torch.randn((1, 64, 3), generator=g).to(DEV)
+    cu = torch.tensor([0, 7, 40], dtype=torch.int32, device=DEV)
+
+    def run(**on):
+        st, cs = h0.clone(), conv.clone()
+        torch.cuda.synchronize()
+        out = [ssd.selective_scan_varlen(cu_seqlens=cu, **kw, **on)[0], ssd.selective_step(state=st, **one, **on),
+               ssd.conv1d(kw["x"], w, **on), ssd.conv1d_varlen(kw["x"], w, cu_seqlens=cu, **on),
+               ssd.conv1d_step(one["x"], w, None, cs, **on), ssd.group_norm(kw["x"], **on)]
+        torch.cuda.synchronize()
+        return [*out, st, cs]
+
+    note("[gpu] every layer operator with a stream argument")
+    side = torch.cuda.Stream()
+    for a, b in zip(run(), run(stream=side)):
+        assert torch.equal(a, b)
+
+
+# ---- far offsets, alignment, odd shapes --------------------------------------------------
+
+
+def test_rows_far_apart():
+    """Token strides that take the last rows past 2^32 bytes and 2^31 elements."""
+    L, E, N, far = 1100, 64, 16, (1 << 21) + 24
+    s = Selective(1, L, E, N, io="bf16", dt="bf16", seed=41)
+    kw, h0, _ = s.to(DEV)
+    note("[gpu] rows more than 2^32 bytes apart")
+    base = torch.empty(L * far, dtype=torch.bfloat16, device=DEV)
+    wide = base.view(1, L, far)
+    moved = dict(kw)
+    at = 0
+    for k in ("x", "dt", "z"):
+        wide[:, :, at:at + E] = kw[k]
+        moved[k] = wide[:, :, at:at + E]
+        at += E + 8
+    for k in ("B", "C"):
+        wide[:, :, at:at + N] = kw[k][:, :, 0]
+        moved[k] = wide[:, :, at:at + N].unsqueeze(2)
+        at += N + 8
+    want = ssd.selective_scan(init_state=h0, **kw)
+    got = ssd.selective_scan(init_state=h0, **moved)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    w = torch.randn((E, 4), generator=torch.Generator().manual_seed(1)).to(DEV)
+    assert torch.equal(ssd.conv1d(kw["x"], w), ssd.conv1d(moved["x"], w))
+    assert torch.equal(ssd.group_norm(kw["x"], None, None, kw["z"], ngroups=2),
+                       ssd.group_norm(moved["x"], None, None, moved["z"], ngroups=2))
+
+
+def test_slots_behind_two_to_the_31_elements():
+    E, N, K = 8192, 16, 4
+    pool = (1 << 31) // (E * N) + 3
+    s = Selective(2, 1, E, N, io="bf16", dt="bf16", seed=42)
+    kw, h0, _ = s.to(DEV)
+    one = {k: (v[:, 0] if k in ("x", "dt", "z", "B", "C") else v) for k, v in kw.items()}
+    note("[gpu] state pool of more than 2^31 elements")
+    state = torch.zeros((pool, E, N), device=DEV)
+    slots = torch.tensor([pool - 1, 1], dtype=torch.int32, device=DEV)
+    state[slots.long()] = h0
+    y = ssd.selective_step(state=state, state_slots=slots, **one)
+    yr, yb, hr, hb = s.reference()
+    within(y, yr[:, 0], yb[:, 0], "y")
+    within(state[slots.long()], hr, hb, "state")
+    assert not state[pool - 2].any() and not state[0].any()
+    del state
+    pool = (1 << 31) // (E * (K - 1)) + 3
+    conv = torch.zeros((pool, E, K - 1), device=DEV)
+    slots = torch.tensor([1, pool - 1], dtype=torch.int32, device=DEV)
+    x, w, bv, g = conv_inputs(2, 1, E, K, "bf16", 43, False)
+    before = torch.randn((2, E, K - 1), generator=g)
+    conv[slots.long()] = before.to(DEV)
+    y = ssd.conv1d_step(x[:, 0].to(DEV), w.to(DEV), bv.to(DEV), conv, state_slots=slots)
+    want, bound, last = conv_reference(np64(x), np64(w), np64(bv), True, np64(before), [(i, 0, 1) for i in range(2)],
+                                       torch.bfloat16)
+    within(y, want[:, 0], bound[:, 0], "y")
+    assert np.array_equal(np64(conv[slots.long()]), last)
+    assert not conv[pool - 2].any()
+
+
+@pytest.mark.parametrize("io", ["fp32", "bf16"])
+def test_unaligned_views_give_the_same_bits(io):
+    """The element-wise accesses compute what the wide ones do."""
+    b, L, E, N = 2, 70, 128, 16
+    s = Selective(b, L, E, N, io=io, dt=io, seed=44)
+    kw, h0, _ = s.to(DEV)
+    note(f"[gpu] unaligned views {io}")
+
+    def shifted(t, by):
+        wide = torch.zeros((*t.shape[:2], t[0, 0].numel() + 9), dtype=t.dtype, device=DEV)
+        flat = t.flatten(2)
+        wide[..., by:by + flat.shape[2]] = flat
+        return wide[..., by:by + flat.shape[2]].view(t.shape) if t.dim() == 3 else \
+            wide[..., by:by + flat.shape[2]].unflatten(2, t.shape[2:])
+
+    off = {k: (shifted(v, 3) if k in ("x", "dt", "z", "B", "C") else v) for k, v in kw.items()}
+    want, got = ssd.selective_scan(init_state=h0, **kw), ssd.selective_scan(init_state=h0, **off)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    first = lambda d: {k: (v[:, 0] if k in ("x", "dt", "z", "B", "C") else v) for k, v in d.items()}  # noqa: E731
+    s1, s2 = h0.clone(), h0.clone()
+    assert torch.equal(ssd.selective_step(state=s1, **first(kw)), ssd.selective_step(state=s2, **first(off)))
+    assert torch.equal(s1, s2)
+    w = torch.randn((E, 4), generator=torch.Generator().manual_seed(2)).to(DEV)
+    c1, c2 = (torch.zeros((b, E, 3), device=DEV) for _ in range(2))
+    assert torch.equal(ssd.conv1d(kw["x"], w, conv_state_out=c1), ssd.conv1d(off["x"], w, conv_state_out=c2))
+    assert torch.equal(c1, c2)
+    assert torch.equal(ssd.conv1d_step(kw["x"][:, 1], w, None, c1), ssd.conv1d_step(off["x"][:, 1], w, None, c2))
+    assert torch.equal(c1, c2)
+    assert torch.equal(ssd.group_norm(kw["x"], None, None, kw["z"]), ssd.group_norm(off["x"], None, None, off["z"]))
+
+
+@pytest.mark.parametrize("lens", [[1] * 200, [1, 2, 3, 0] * 40, [0, 0, 777, 0], [300, 1, 1, 1, 300], [2] * 64 + [500]])
+def test_many_short_and_a_few_long_sequences(lens):
+    T = sum(lens)
+    s = Selective(1, T, 66, 16, lens=lens, io="bf16", dt="bf16", seed=T)
+    kw, h0, cu = s.to(DEV)
+    note(f"[gpu] packed: {len(lens)} sequences, {T} tokens")
+    state = h0.clone()
+    y, _ = ssd.selective_scan_varlen(cu_seqlens=cu, init_states=state, final_states=state, **kw)
+    yr, yb, hr, hb = s.reference()
+    within(y, yr, yb, "y")
+    within(state, hr, hb, "final_states")
+    w = torch.randn((66, 4), generator=torch.Generator().manual_seed(3))
+    c0 = torch.randn((len(lens), 66, 3), generator=torch.Generator().manual_seed(4))
+    out = torch.empty((len(lens), 66, 3), device=DEV)
+    yc = ssd.conv1d_varlen(kw["x"], w.to(DEV), cu_seqlens=cu, conv_states_in=c0.to(DEV), conv_states_out=out)
+    ends = np.cumsum(lens)
+    want, bound, last = conv_reference(np64(s.x), np64(w), None, True, np64(c0),
+                                       [(0, int(e) - n, int(e)) for n, e in zip(lens, ends)], torch.bfloat16)
+    within(yc, want, bound, "conv")
+    assert np.array_equal(np64(out), last)
+
+
+@pytest.mark.parametrize("cu", [[0, 50, 30, 100], [0, 1 << 30, 100], [-5, 40, 100], [20, 60, 80], [0, 0, 0], [100, 0, 100]])
+def test_bad_offsets_stay_inside(cu):
+    """Arrays of offsets that are no such thing: any values, but no access
+    outside (y, states and what surrounds them)."""
+    E, N, L, S = 48, 16, 100, len(cu) - 1
+    s = Selective(1, L, E, N, init=False, seed=45)
+    kw, _, _ = s.to(DEV)
+    c = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    note(f"[gpu] bad offsets {cu}")
+    guard = 4096
+    ybuf = torch.full((2 * guard + L * E,), 9.0, device=DEV)
+    fbuf = torch.full((2 * guard + S * E * N,), 9.0, device=DEV)
+    y = ybuf[guard:guard + L * E].view(1, L, E)
+    f = fbuf[guard:guard + S * E * N].view(S, E, N)
+    ssd.selective_scan_varlen(cu_seqlens=c, y=y, final_states=f, **kw)
+    w = torch.ones((E, 4), device=DEV)
+    cbuf = torch.full((2 * guard + S * E * 3,), 9.0, device=DEV)
+    ssd.conv1d_varlen(kw["x"], w, cu_seqlens=c, y=y, conv_states_out=cbuf[guard:guard + S * E * 3].view(S, E, 3))
+    torch.cuda.synchronize()
+    for buf in (ybuf, fbuf, cbuf):
+        assert (buf[:guard] == 9.0).all() and (buf[-guard:] == 9.0).all()
+
+
+def test_group_norm_of_rows_without_spread():
+    """A constant row (variance 0) and one of infinities: what the formula gives."""
+    x = torch.zeros((4, 256), device=DEV)
+    x[1], x[2], x[3, 7] = 3.0, float("inf"), float("nan")
+    note("[gpu] group norm of constant and non-finite rows")
+    b = torch.full((256,), 0.5, device=DEV)
+    o = ssd.group_norm(x, None, b)
+    assert torch.equal(o[:2], torch.full((2, 256), 0.5, device=DEV))
+    assert torch.isnan(o[2:]).all()
+    o = ssd.group_norm(x, center=False)
+    assert torch.equal(o[0], torch.zeros(256, device=DEV))
+    want = 3.0 / np.sqrt(9.0 + 1e-5)
+    assert (np64(o[1]) - want).max() <= 6 * U * want
+    assert torch.isnan(o[2:]).all()
+
+
+def test_selective_scan_of_zero_steps_and_long_decays():
+    """dt = 0 carries the state over unchanged; a decay of exp(-large) forgets it."""
+    b, L, E, N = 1, 90, 64, 16
+    s = Selective(b, L, E, N, skip=False, gate=False, pre=False, seed=46)
+    kw, h0, _ = s.to(DEV)
+    note("[gpu] selective scan: zero steps, infinite decays")
+    kw["dt"].zero_()
+    y, h = ssd.selective_scan(init_state=h0, **kw)
+    assert torch.equal(h, h0)
+    kw["dt"].fill_(1.0e4)
+    y, h = ssd.selective_scan(init_state=h0, **kw)
+    # every decay is exp(-1e4 |A|) = 0: only the last token is left
+    want = 1.0e4 * np64(kw["x"][0, -1])[:, None] * np64(kw["B"][0, -1])
+    within(h[0], want, 3 * U * np.abs(want), "final_state")
