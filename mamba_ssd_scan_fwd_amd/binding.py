@@ -1,4 +1,5 @@
-"""ctypes binding of libssd.so: argument marshalling only.
+"""Binding of libssd.so (ctypes; the layer operators' calls through the compiled
+``_marshal``): argument marshalling only.
 
 PyTorch provides device memory and the current stream; every step of the
 computation runs in the library's HIP kernels. If the library has not been
@@ -7,7 +8,6 @@ built, every call raises -- there is no fallback implementation.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -670,81 +670,28 @@ def conv1d_split(xbc, weight, bias=None, *, nheads, headdim, ngroups, dstate, si
 #
 # Inputs may be views of wider buffers (rows of contiguous channels, any
 # distance between tokens and batch rows). A call for one token takes a few
-# microseconds on the GPU, so what the host does for it is kept short: one
-# look at each tensor, one descriptor, the raw handle of the current stream.
+# microseconds on the GPU, so its marshalling is compiled (csrc_py/marshal.cpp):
+# the checks of the tensors, the outputs and the descriptor.
 
-_IO = {torch.float32: SSD_DTYPE_F32, torch.bfloat16: SSD_DTYPE_BF16}
-_F32, _I32 = torch.float32, torch.int32
-
-
-def _io(t, name):
-    code = _IO.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name}: unsupported io dtype {t.dtype}")
-    return code
+_native = None
 
 
-def _dim(t, name, n):
-    if t is None:
-        raise ValueError(f"{name} is required")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.dim() != n:
-        raise ValueError(f"{name} must have {n} dimensions, got {t.dim()}")
-
-
-def _unlike(t, name, dtype, device, shape):
-    """Raises for the first thing in which ``t`` is not as it has to be."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
-
-
-def _strides(t, name, dtype, device, shape, lead):
-    """(token, batch) stride of a strided input of ``shape`` = (batch, tokens,
-    channels..) with ``lead`` 2, or (batch, channels..) with ``lead`` 1; 0
-    stands for dense."""
-    if t.dtype != dtype or t.shape != shape or t.device != device:
-        _unlike(t, name, dtype, device, shape)
-    if t.is_contiguous():
-        return 0, 0
-    st = t.stride()
-    width = 1
-    for i in range(len(shape) - 1, lead - 1, -1):
-        if shape[i] != 1 and st[i] != width:
-            raise ValueError(f"{name}: the channels of a token must be contiguous")
-        width *= shape[i]
-    rows = shape[1] if lead == 2 else 1
-    token = st[1] if rows > 1 else width
-    batch = st[0] if shape[0] > 1 else (rows - 1) * token + width
-    if token < width or batch < width:
-        raise ValueError(f"{name}: tokens must not overlap (an expanded dimension needs a copy)")
-    return token, batch
-
-
-def _dense(t, name, device, shape, dtype=_F32):
-    """Address of a dense argument, None for one that is not given."""
-    if t is None:
-        return None
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
-        _unlike(t, name, dtype, device, shape)
-    return t.data_ptr()
-
-
-def _out(t, name, like, shape):
-    """The output given, or a new dense one of ``like``'s type and device."""
-    if t is None:
-        return like.new_empty(shape)
-    _dense(t, name, like.device, shape, like.dtype)
-    return t
-
-
-def _offsets(cu_seqlens, device):
-    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
-        raise ValueError("cu_seqlens must hold num_seqs + 1 offsets, num_seqs >= 1")
-    return _dense(cu_seqlens, "cu_seqlens", device, cu_seqlens.shape, _I32), cu_seqlens.numel() - 1
+def _marshal():
+    """The compiled marshalling, bound to the loaded library."""
+    global _native
+    if _native is None:
+        lib = load_library()
+        try:
+            from . import _marshal as m
+        except ImportError as e:
+            raise RuntimeError("the _marshal extension is missing; build it with "
+                               "`python -m mamba_ssd_scan_fwd_amd.build`") from e
+        at = [ctypes.cast(getattr(lib, "ssd_" + n), ctypes.c_void_p).value
+              for n in ("selective_scan_workspace_bytes", "selective_scan", "selective_scan_varlen", "selective_step",
+                        "conv1d", "conv1d_step", "group_norm")]
+        m.bind(*at, SSDError)
+        _native = m
+    return _native
 
 
 class _On:
@@ -765,60 +712,38 @@ class _On:
         return False
 
 
-_HERE_ALREADY = contextlib.nullcontext()
-
-
-def _on(device, stream):
-    if stream is None and device.index == torch.cuda.current_device():
-        return _HERE_ALREADY
-    return _On(device, stream)
-
-
-def _used_on(stream, device, *tensors):
+def _used_on(stream, device, tensors):
     """After a call on ``stream``: inputs that belong to the caller's stream,
     and outputs that belong to this one, are in use on both."""
     here = torch.cuda.current_stream(device)
     if stream == here:
         return
     for t in tensors:
-        if t is not None:
+        if isinstance(t, torch.Tensor):
             t.record_stream(stream)
             t.record_stream(here)
 
 
-def _current(device):
-    return torch._C._cuda_getCurrentRawStream(device.index)
+def _run(name, stream, *args):
+    """One call of the compiled marshalling, args[0] being x: on the current
+    stream of x's device, or on ``stream``."""
+    fn = getattr(_marshal(), name)
+    dev = args[0].device
+    if dev.index is None:
+        return fn(*args, 0)  # a host tensor: refused there
+    if stream is None and dev.index == torch.cuda.current_device():
+        return fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    with _On(dev, stream):
+        out = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if stream is not None:
+        _used_on(stream, dev, args + (out if isinstance(out, tuple) else (out,)))
+    return out
 
 
-def _selective_desc(x, dt, A, B, C, z, dt_pre, lead):
-    dev, io = x.device, x.dtype
-    shape = x.shape
-    E = shape[-1]
-    _dim(A, "A", 2)
-    _dim(B, "B", lead + 2)
-    N, G = A.shape[1], B.shape[lead]
-    bc = (*shape[:lead], G, N)
-    ddt = dt.dtype
-    if ddt is not _F32 and ddt is not io:
-        raise TypeError(f"dt must be torch.float32 or {io}, got {ddt}")
-    bias, softplus, clamp, lo, hi = None, 0, 0, 0.0, 0.0
-    if dt_pre:
-        bias = _dense(dt_pre.get("bias"), "dt bias", dev, (E,))
-        softplus = 1 if dt_pre.get("softplus") else 0
-        limit = dt_pre.get("limit")
-        if limit is not None:
-            clamp, lo, hi = 1, float(limit[0]), float(limit[1])
-    xt, xb = _strides(x, "x", io, dev, shape, lead)
-    dtt, dtb = _strides(dt, "dt", ddt, dev, shape, lead)
-    zt, zb = (0, 0) if z is None else _strides(z, "z", io, dev, shape, lead)
-    bt, bb = _strides(B, "B", io, dev, bc, lead)
-    ct, cb = _strides(C, "C", io, dev, bc, lead)
-    return SelectiveDesc(shape[0], shape[1] if lead == 2 else 1, E, N, G, _io(x, "x"), _IO[ddt], bias, softplus, clamp,
-                         lo, hi, xt, xb, dtt, dtb, zt, zb, bt, bb, ct, cb)
-
-
-def _data(t):
-    return None if t is None else t.data_ptr()
+def _pre(dt_pre):
+    if not dt_pre:
+        return None, False, None
+    return dt_pre.get("bias"), dt_pre.get("softplus", False), dt_pre.get("limit")
 
 
 def selective_scan_workspace_bytes(desc: SelectiveDesc, num_seqs: int = 0) -> int:
@@ -826,40 +751,6 @@ def selective_scan_workspace_bytes(desc: SelectiveDesc, num_seqs: int = 0) -> in
     _check(load_library().ssd_selective_scan_workspace_bytes(ctypes.byref(desc), num_seqs, ctypes.byref(n)),
            "ssd_selective_scan_workspace_bytes")
     return int(n.value)
-
-
-def _selective_prompts(x, dt, A, B, C, D, z, cu_seqlens, init, y, final, want_final, workspace, dt_pre, stream):
-    dev = x.device
-    cu, S = (None, 0) if cu_seqlens is None else _offsets(cu_seqlens, dev)
-    d = _selective_desc(x, dt, A, B, C, z, dt_pre, 2)
-    E, N = d.channels, d.dstate
-    states = (S if S else d.batch, E, N)
-    Ap, Dp = _dense(A, "A", dev, (E, N)), _dense(D, "D", dev, (E,))
-    ip = _dense(init, "init_states" if S else "init_state", dev, states)
-    lib = load_library()
-    need = selective_scan_workspace_bytes(d, S)
-    with _on(dev, stream):
-        y = _out(y, "y", x, x.shape)
-        if final is not None or want_final:
-            final = _out(final, "final_states" if S else "final_state", A, states)
-        if workspace is None:
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        elif not workspace.is_contiguous() or workspace.device != dev or workspace.nbytes < need:
-            raise ValueError(f"workspace needs {need} contiguous bytes on {dev}")
-        size = 0 if workspace is None else workspace.nbytes
-        if S:
-            st = lib.ssd_selective_scan_varlen(ctypes.byref(d), cu, S, x.data_ptr(), dt.data_ptr(), Ap, B.data_ptr(),
-                                               C.data_ptr(), Dp, _data(z), ip, y.data_ptr(), _data(final),
-                                               _data(workspace), size, _current(dev))
-        else:
-            st = lib.ssd_selective_scan(ctypes.byref(d), x.data_ptr(), dt.data_ptr(), Ap, B.data_ptr(), C.data_ptr(),
-                                        Dp, _data(z), ip, y.data_ptr(), _data(final), _data(workspace), size,
-                                        _current(dev))
-    _check(st, "ssd_selective_scan_varlen" if S else "ssd_selective_scan")
-    if stream is not None:
-        _used_on(stream, dev, x, dt, A, B, C, D, z, init, y, final, workspace, cu_seqlens, (dt_pre or {}).get("bias"))
-    return y, final
 
 
 def selective_scan(x, dt, A, B, C, D=None, z=None, init_state=None, *, return_final_state: bool = True, y=None,
@@ -873,17 +764,14 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, init_state=None, *, return_fi
     x, dt, z, B and C may be views of wider buffers. ``dt_pre`` as for
     ``forward``, its bias [E]. ``final_state`` may be ``init_state``.
     """
-    _dim(x, "x", 3)
-    return _selective_prompts(x, dt, A, B, C, D, z, None, init_state, y, final_state, return_final_state,
-                              workspace, dt_pre, stream)
+    return _run("selective_prompts", stream, x, dt, A, B, C, D, z, None, init_state, y, final_state,
+                return_final_state, workspace, *_pre(dt_pre))[:2]
 
 
-def _packed(x, cu_seqlens):
-    _dim(x, "x", 3)
-    if x.shape[0] != 1:
-        raise ValueError("packed sequences: x must be [1, T, channels]")
+def _offsets(cu_seqlens):
     if cu_seqlens is None:
         raise ValueError("cu_seqlens is required")
+    return cu_seqlens
 
 
 def selective_scan_varlen(x, dt, A, B, C, D=None, z=None, *, cu_seqlens, init_states=None,
@@ -893,9 +781,8 @@ def selective_scan_varlen(x, dt, A, B, C, D=None, z=None, *, cu_seqlens, init_st
     [1, T, G, N], sequence s being tokens [cu_seqlens[s], cu_seqlens[s+1])
     (int32 device tensor [S+1]). Returns (y, final_states [S, E, N] or None).
     Where cu_seqlens ends before T, y of the tokens behind it is not written."""
-    _packed(x, cu_seqlens)
-    return _selective_prompts(x, dt, A, B, C, D, z, cu_seqlens, init_states, y, final_states, return_final_states,
-                              workspace, dt_pre, stream)
+    return _run("selective_prompts", stream, x, dt, A, B, C, D, z, _offsets(cu_seqlens), init_states, y, final_states,
+                return_final_states, workspace, *_pre(dt_pre))[:2]
 
 
 def selective_step(x, dt, A, B, C, D, z, state, *, state_slots=None, y=None, dt_pre=None, stream=None):
@@ -904,57 +791,7 @@ def selective_step(x, dt, A, B, C, D, z, state, *, state_slots=None, y=None, dt_
     ``state_slots[b]`` (int32 [b]; slot b without it); a row with a slot
     outside the pool, or one that an earlier row has, is left alone. Returns
     y [b, E] (pass ``y`` to keep what such rows held)."""
-    _dim(x, "x", 2)
-    dev, shape = x.device, x.shape
-    d = _selective_desc(x, dt, A, B, C, z, dt_pre, 1)
-    _dim(state, "state", 3)
-    E, N = A.shape
-    n = state.shape[0]
-    sp, Ap, Dp = _dense(state, "state", dev, (n, E, N)), _dense(A, "A", dev, (shape[1], N)), _dense(D, "D", dev, (E,))
-    slots = _dense(state_slots, "state_slots", dev, shape[:1], _I32)
-    with _on(dev, stream):
-        y = _out(y, "y", x, shape)
-        st = load_library().ssd_selective_step(ctypes.byref(d), x.data_ptr(), dt.data_ptr(), Ap, B.data_ptr(),
-                                               C.data_ptr(), Dp, _data(z), sp, slots, n, y.data_ptr(), _current(dev))
-    _check(st, "ssd_selective_step")
-    if stream is not None:
-        _used_on(stream, dev, x, dt, A, B, C, D, z, state, state_slots, y, (dt_pre or {}).get("bias"))
-    return y
-
-
-def _conv_desc(x, weight, widths, silu, lead):
-    shape = x.shape
-    _dim(weight, "weight", 2)
-    CH, K = weight.shape
-    if CH != shape[-1]:
-        raise ValueError(f"weight must have shape ({shape[-1]}, K), got {tuple(weight.shape)}")
-    return Conv1dDesc(shape[0], shape[1] if lead == 2 else 1, CH, *widths, K, 1 if silu else 0, _io(x, "x"),
-                      *_strides(x, "x", x.dtype, x.device, shape, lead))
-
-
-def _split_widths(CH, nheads, headdim, ngroups, dstate):
-    if CH != nheads * headdim + 2 * ngroups * dstate:
-        raise ValueError("xbc channels must be H*P + 2*G*N")
-    return nheads * headdim, ngroups * dstate, ngroups * dstate
-
-
-def _conv_prompts(x, weight, bias, widths, shapes, outs, cu_seqlens, state_in, state_out, silu, stream):
-    dev = x.device
-    cu, S = (None, 0) if cu_seqlens is None else _offsets(cu_seqlens, dev)
-    d = _conv_desc(x, weight, widths, silu, 2)
-    CH, K = weight.shape
-    states = (S if S else x.shape[0], CH, K - 1)
-    wp, bp = _dense(weight, "weight", dev, (CH, K)), _dense(bias, "bias", dev, (CH,))
-    name = "conv_states" if S else "conv_state"
-    ip, op = _dense(state_in, name + "_in", dev, states), _dense(state_out, name + "_out", dev, states)
-    with _on(dev, stream):
-        outs = [_out(o, "y", x, s) for o, s in zip(outs, shapes)]
-        ptrs = [o.data_ptr() for o in outs] + [None] * (3 - len(outs))
-        st = load_library().ssd_conv1d(ctypes.byref(d), cu, S, x.data_ptr(), wp, bp, ip, op, *ptrs, _current(dev))
-    _check(st, "ssd_conv1d")
-    if stream is not None:
-        _used_on(stream, dev, x, weight, bias, state_in, state_out, cu_seqlens, *outs)
-    return outs
+    return _run("selective_step", stream, x, dt, A, B, C, D, z, state, state_slots, y, *_pre(dt_pre))
 
 
 def conv1d(x, weight, bias=None, *, silu=True, conv_state_in=None, conv_state_out=None, y=None, stream=None):
@@ -962,9 +799,7 @@ def conv1d(x, weight, bias=None, *, silu=True, conv_state_in=None, conv_state_ou
     view of a wider buffer or dense), weight [CH, K] fp32, K in 1..4, with an
     optional SiLU. ``conv_state_in`` and ``conv_state_out`` [b, CH, K-1] fp32
     hold the inputs before the first token and the last ones. Returns y."""
-    _dim(x, "x", 3)
-    return _conv_prompts(x, weight, bias, (x.shape[2], 0, 0), [x.shape], [y], None, conv_state_in,
-                         conv_state_out, silu, stream)[0]
+    return _run("conv_prompts", stream, x, weight, bias, None, silu, None, conv_state_in, conv_state_out, y)
 
 
 def conv1d_varlen(x, weight, bias=None, *, cu_seqlens, silu=True, conv_states_in=None, conv_states_out=None, y=None,
@@ -972,48 +807,23 @@ def conv1d_varlen(x, weight, bias=None, *, cu_seqlens, silu=True, conv_states_in
     """``conv1d`` over packed sequences x [1, T, CH]: sequence s is tokens
     [cu_seqlens[s], cu_seqlens[s+1]) (int32 device tensor [S+1]), its states
     row s of ``conv_states_in`` and ``conv_states_out`` [S, CH, K-1]."""
-    _packed(x, cu_seqlens)
-    return _conv_prompts(x, weight, bias, (x.shape[2], 0, 0), [x.shape], [y], cu_seqlens, conv_states_in,
-                         conv_states_out, silu, stream)[0]
+    return _run("conv_prompts", stream, x, weight, bias, None, silu, _offsets(cu_seqlens), conv_states_in,
+                conv_states_out, y)
 
 
 def conv1d_split_varlen(xbc, weight, bias=None, *, cu_seqlens, nheads, headdim, ngroups, dstate, silu=True,
                         conv_states_in=None, conv_states_out=None, stream=None):
     """``conv1d_split`` over packed sequences: xbc [1, T, H*P + 2*G*N] into
     the x [1, T, H, P], B and C [1, T, G, N] that ``forward_varlen`` reads."""
-    _packed(xbc, cu_seqlens)
-    T = xbc.shape[1]
-    widths = _split_widths(xbc.shape[2], nheads, headdim, ngroups, dstate)
-    shapes = [(1, T, nheads, headdim), (1, T, ngroups, dstate), (1, T, ngroups, dstate)]
-    return tuple(_conv_prompts(xbc, weight, bias, widths, shapes, [None] * 3, cu_seqlens, conv_states_in,
-                               conv_states_out, silu, stream))
-
-
-def _conv_token(x, weight, bias, widths, shapes, outs, conv_state, state_slots, silu, stream):
-    dev = x.device
-    d = _conv_desc(x, weight, widths, silu, 1)
-    CH, K = weight.shape
-    _dim(conv_state, "conv_state", 3)
-    n = conv_state.shape[0]
-    wp, bp = _dense(weight, "weight", dev, (CH, K)), _dense(bias, "bias", dev, (CH,))
-    cp = _dense(conv_state, "conv_state", dev, (n, CH, K - 1))
-    slots = _dense(state_slots, "state_slots", dev, x.shape[:1], _I32)
-    with _on(dev, stream):
-        outs = [_out(o, "y", x, s) for o, s in zip(outs, shapes)]
-        ptrs = [o.data_ptr() for o in outs] + [None] * (3 - len(outs))
-        st = load_library().ssd_conv1d_step(ctypes.byref(d), x.data_ptr(), wp, bp, cp, slots, n, *ptrs, _current(dev))
-    _check(st, "ssd_conv1d_step")
-    if stream is not None:
-        _used_on(stream, dev, x, weight, bias, conv_state, state_slots, *outs)
-    return outs
+    return _run("conv_prompts", stream, xbc, weight, bias, (nheads, headdim, ngroups, dstate), silu,
+                _offsets(cu_seqlens), conv_states_in, conv_states_out, None)
 
 
 def conv1d_step(x, weight, bias, conv_state, *, silu=True, state_slots=None, y=None, stream=None):
     """``conv1d`` at one token: x [b, CH], ``conv_state`` [slots, CH, K-1]
     fp32 moved on in place. ``state_slots`` as for ``selective_step``.
     Returns y [b, CH]."""
-    _dim(x, "x", 2)
-    return _conv_token(x, weight, bias, (x.shape[1], 0, 0), [x.shape], [y], conv_state, state_slots, silu, stream)[0]
+    return _run("conv_token", stream, x, weight, bias, None, silu, conv_state, state_slots, y)
 
 
 def conv1d_split_step(xbc, weight, bias, conv_state, *, nheads, headdim, ngroups, dstate, silu=True,
@@ -1021,11 +831,8 @@ def conv1d_split_step(xbc, weight, bias, conv_state, *, nheads, headdim, ngroups
     """``conv1d_split`` at one token: xbc [b, H*P + 2*G*N] into the x
     [b, H, P], B and C [b, G, N] that ``decode_step`` reads; ``conv_state`` and
     ``state_slots`` as for ``conv1d_step``."""
-    _dim(xbc, "xbc", 2)
-    b = xbc.shape[0]
-    widths = _split_widths(xbc.shape[1], nheads, headdim, ngroups, dstate)
-    shapes = [(b, nheads, headdim), (b, ngroups, dstate), (b, ngroups, dstate)]
-    return tuple(_conv_token(xbc, weight, bias, widths, shapes, [None] * 3, conv_state, state_slots, silu, stream))
+    return _run("conv_token", stream, xbc, weight, bias, (nheads, headdim, ngroups, dstate), silu, conv_state,
+                state_slots, None)
 
 
 def group_norm(x, weight=None, bias=None, z=None, *, ngroups=1, eps=1e-5, center=True, gate_first=False, silu=False,
@@ -1035,27 +842,4 @@ def group_norm(x, weight=None, bias=None, z=None, *, ngroups=1, eps=1e-5, center
     False gives the root-mean-square form. ``z`` (like x) gates with silu(z),
     before the norm with ``gate_first``, else behind it; ``silu`` applies the
     SiLU to the result instead."""
-    rank = x.dim()
-    if not 1 <= rank <= 3:
-        raise ValueError("x must have 1 to 3 dimensions")
-    _dim(x, "x", rank)
-    dev, io, shape = x.device, x.dtype, x.shape
-    if z is not None and z.shape != shape:
-        raise ValueError(f"z must have shape {tuple(shape)}, got {tuple(z.shape)}")
-    x3, z3 = x, z
-    if rank != 3:
-        x3 = x.view((1,) * (3 - rank) + tuple(shape))
-        z3 = None if z is None else z.view(x3.shape)
-    b, rows, C = x3.shape
-    d = GroupNormDesc(b, rows, C, int(ngroups), _io(x, "x"), 1 if center else 0, 1 if gate_first else 0,
-                      1 if silu else 0, float(eps), *_strides(x3, "x", io, dev, x3.shape, 2),
-                      *((0, 0) if z is None else _strides(z3, "z", io, dev, x3.shape, 2)))
-    wp, bp = _dense(weight, "weight", dev, (C,)), _dense(bias, "bias", dev, (C,))
-    with _on(dev, stream):
-        out = _out(out, "out", x, shape)
-        st = load_library().ssd_group_norm(ctypes.byref(d), x.data_ptr(), wp, bp, _data(z), out.data_ptr(),
-                                           _current(dev))
-    _check(st, "ssd_group_norm")
-    if stream is not None:
-        _used_on(stream, dev, x, weight, bias, z, out)
-    return out
+    return _run("group_norm", stream, x, weight, bias, z, ngroups, eps, center, gate_first, silu, out)

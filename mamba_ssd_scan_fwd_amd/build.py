@@ -3,8 +3,10 @@
 Usage: python -m mamba_ssd_scan_fwd_amd.build [-j JOBS] [--verbose]
 
 Every source under csrc/ is compiled to an object in ``_build/`` (in
-parallel), then linked into ``mamba_ssd_scan_fwd_amd/libssd.so``. The build
-always recompiles; it never needs a GPU (hipcc cross-compiles for gfx950).
+parallel), then linked into ``mamba_ssd_scan_fwd_amd/libssd.so``. The Python
+extension ``_marshal`` (csrc_py/: argument marshalling of the layer operators,
+host code only) is built beside it with the host compiler. The build always
+recompiles; it never needs a GPU (hipcc cross-compiles for gfx950).
 
 ``--host-sanitize`` builds a second copy, ``_build/libssd_host_san.so``, whose
 host code (argument validation, planning, launch set-up) is instrumented with
@@ -26,6 +28,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -85,12 +88,44 @@ def _compile(src: str, verbose: bool, sanitize: bool = False) -> str:
     return obj
 
 
+MARSHAL = os.path.join(PKG, "_marshal" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+
+
+def build_marshal(verbose: bool = False) -> str:
+    """Compile the marshalling extension against the installed PyTorch."""
+    import torch
+    from torch.utils import cpp_extension
+
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        raise RuntimeError("g++ not found: a host C++ compiler is required to build _marshal")
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = MARSHAL + ".tmp"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f for p in cpp_extension.include_paths() for f in ("-isystem", p)),
+           "-isystem", sysconfig.get_paths()["include"], os.path.join(PKG, "csrc_py", "marshal.cpp"), "-o", tmp,
+           f"-L{libs}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compile failed: marshal.cpp\n{r.stdout}\n{r.stderr}")
+    if verbose and r.stderr.strip():
+        print(r.stderr, file=sys.stderr)
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build(jobs: int | None = None, verbose: bool = False, host_sanitize: bool = False) -> str:
     os.makedirs(SAN_BUILD if host_sanitize else BUILD, exist_ok=True)
     srcs = sources()
     jobs = jobs or min(len(srcs), max(1, min(os.cpu_count() or 1, 16)))
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        marshal = None if host_sanitize else ex.submit(build_marshal, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose, host_sanitize), srcs))
+        if marshal is not None:
+            marshal.result()
     out = SAN_LIB if host_sanitize else LIB
     tmp = out + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *(HOST_SAN if host_sanitize else []), "-o", tmp,

@@ -259,6 +259,7 @@ def test_workspace_follows_the_cut_of_the_time_axis():
 
 
 def test_binding_refuses_host_tensors_and_wrong_ranks():
+    lib()
     x = torch.zeros(2, 8, 16)
     with pytest.raises(ValueError, match="device tensor"):
         ssd.selective_scan(x, x, torch.zeros(16, 4), x, x)
@@ -275,10 +276,12 @@ def test_binding_refuses_host_tensors_and_wrong_ranks():
 
 
 def test_strides_of_views():
-    from mamba_ssd_scan_fwd_amd.binding import _strides
+    from mamba_ssd_scan_fwd_amd.binding import _marshal
+
+    lib()
 
     def of(t, lead=2):
-        return _strides(t, "t", t.dtype, t.device, t.shape, lead)
+        return _marshal().strides(t, lead)
 
     wide = torch.zeros(3, 10, 20)
     assert of(wide) == (0, 0)  # dense
