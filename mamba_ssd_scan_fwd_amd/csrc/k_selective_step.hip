@@ -52,7 +52,9 @@ __global__ __launch_bounds__(kThreads) void selective_step_kernel(const Selectiv
     slot[k] = a.slots != nullptr ? a.slots[r] : r;
     if (row0 + k >= a.batch || slot[k] < 0 || slot[k] >= a.nslots) slot[k] = -1;
     const int64_t from = slot[k] < 0 ? 0 : slot[k];
-    h[k] = load_pack<float, 4, VEC>(a.state + (from * a.E + e) * a.N + nc, nn);
+    const float* hp = a.state + (from * a.E + e) * a.N + nc;
+    if (VEC && a.stream) h[k] = load_stream(reinterpret_cast<const Pack<float, 4>*>(hp));
+    else h[k] = load_pack<float, 4, VEC>(hp, nn);
     bv[k] = load_pack<TIO, 4, VEC>(static_cast<const TIO*>(a.B) + r * a.bs + (int64_t)g * a.N + nc, nn);
     cv[k] = load_pack<TIO, 4, VEC>(static_cast<const TIO*>(a.C) + r * a.cs + (int64_t)g * a.N + nc, nn);
     xv[k] = reinterpret_cast<const RX*>(a.x)[r * a.xs + e];
@@ -79,7 +81,11 @@ __global__ __launch_bounds__(kThreads) void selective_step_kernel(const Selectiv
 #pragma unroll
     for (int off = LPC / 2; off > 0; off >>= 1) p += __shfl_xor(p, off, LPC);
     if (slot[k] >= 0 && mine) {
-      if (nn > 0) store_pack<float, 4, VEC>(a.state + (slot[k] * a.E + e) * a.N + n0, hn, nn);
+      float* hp = a.state + (slot[k] * a.E + e) * a.N + n0;
+      if (nn > 0) {
+        if (VEC && a.stream) store_stream(reinterpret_cast<Pack<float, 4>*>(hp), Pack<float, 4>{{hn[0], hn[1], hn[2], hn[3]}});
+        else store_pack<float, 4, VEC>(hp, hn, nn);
+      }
       if (sub == 0) {
         float y = fmaf(Dv, x, p);
         if (a.z != nullptr) y *= silu_f32(Elem<TIO>::f32(zv[k]));
@@ -90,7 +96,15 @@ __global__ __launch_bounds__(kThreads) void selective_step_kernel(const Selectiv
 }
 
 template <typename TIO, typename TDT, int NP>
-hipError_t launch_np(const SelectiveStepArgs& a, hipStream_t s) {
+hipError_t launch_np(const SelectiveStepArgs& args, hipStream_t s) {
+  SelectiveStepArgs a = args;
+  // A layer's states are next used a token later, behind those of all other
+  // layers. From a quarter of the memory-side cache on they are not kept in it
+  // (non-temporal): 256 rows of 8192 x 16 (128 MiB), three layers in turn, 57 ->
+  // 52 us, 128 rows of twelve layers 31 -> 28 us. That costs a program of one
+  // layer, whose states would stay there (44 -> 52, 24 -> 27 us), and from 64
+  // rows down it would cost three layers too (13.8 -> 15.7 us).
+  a.stream = a.batch * a.E * a.N * (int64_t)sizeof(float) >= kMemorySideCache / 4;
   const unsigned gx = (unsigned)((a.E + kThreads / (NP / 4) - 1) / (kThreads / (NP / 4)));
   // whole groups of four states in every row of A, B, C and of the pool
   auto on = [](const void* p, size_t b) { return reinterpret_cast<uintptr_t>(p) % b == 0; };

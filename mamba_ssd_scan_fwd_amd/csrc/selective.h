@@ -61,6 +61,7 @@ struct SelectiveStepArgs {
   int64_t batch;
   int E, N, G;
   DtOpts dto;
+  bool stream;                     // states past the memory-side cache (set at launch)
 };
 hipError_t launch_selective_step(const SelectiveStepArgs& a, int io, int dt, hipStream_t s);
 
@@ -109,9 +110,12 @@ struct GroupNormArgs {
   int C, G;
   float eps;
   int center, gate_first, silu;
+  bool stream;                     // read past the memory-side cache (set at launch)
 };
 constexpr int64_t kGroupNormMaxGroup = 16384;  // channels per group
 hipError_t launch_group_norm(const GroupNormArgs& a, int io, hipStream_t s);
+
+constexpr int64_t kMemorySideCache = int64_t(256) << 20;  // bytes, on MI355X
 
 #ifdef __HIPCC__
 // ---- device helpers --------------------------------------------------------------
@@ -189,6 +193,18 @@ __device__ __forceinline__ void store_pack(T* p, const float (&f)[V], int n) {
     for (int i = 0; i < V; ++i)
       if (i < n) reinterpret_cast<R*>(p)[i] = Elem<T>::bits(f[i]);
   }
+}
+
+// 16-byte packs that are not expected to be read again soon: past the caches.
+template <typename P> __device__ __forceinline__ P load_stream(const P* p) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  static_assert(sizeof(P) == 16, "one 16-byte access");
+  return __builtin_bit_cast(P, __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p)));
+}
+template <typename P> __device__ __forceinline__ void store_stream(P* p, const P& v) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  static_assert(sizeof(P) == 16, "one 16-byte access");
+  __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4*>(p));
 }
 
 // Offset i of a packed batch, clamped into [0, T].
