@@ -295,7 +295,7 @@ hipError_t launch_step_k(const Conv1dStepArgs& a, hipStream_t s) {
   };
   if (!vec) return go(conv1d_step_kernel<TIO, K, 1, 1>, 1);
   // several rows a workgroup share the weights once that leaves the card full
-  return gx * a.batch >= 4 * 512 ? go(conv1d_step_kernel<TIO, K, 4, 4>, 4) : go(conv1d_step_kernel<TIO, K, 4, 1>, 1);
+  return gx * a.batch >= 4 * 512 ? go(conv1d_step_kernel<TIO, K, 4, 2>, 2) : go(conv1d_step_kernel<TIO, K, 4, 1>, 1);
 }
 
 }  // namespace

@@ -194,9 +194,9 @@ template <typename TIO>
 hipError_t launch_io(const GroupNormArgs& args, hipStream_t s) {
   GroupNormArgs a = args;
   // Inputs and output that do not fit the memory-side cache together are read
-  // past it (non-temporal), which leaves it to the output's writes: 384 MB 80 ->
-  // 71 us. Below, part of the inputs may still lie there from the operator that
-  // wrote them: 192 MB 36 us from the cache, 40 us past it.
+  // past it (non-temporal), which leaves it to the output's writes: 384 MB 78 ->
+  // 66 us. Below, part of the inputs may still lie there from the operator that
+  // wrote them: 96 MB 19.4 us from the cache, 21.0 us past it.
   a.stream = a.batch * a.rows * a.C * (int64_t)sizeof(TIO) * (a.z != nullptr ? 3 : 2) > kMemorySideCache;
   constexpr int V = 16 / sizeof(TIO);
   auto on = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
