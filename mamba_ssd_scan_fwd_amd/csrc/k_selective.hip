@@ -352,9 +352,12 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
     stage(left, buf);
     __syncthreads();
     for (; left > 0; left -= TT) {
-      // the older of two waves on a SIMD would otherwise run at its own pace
-      // and leave the other to finish alone, at half of the SIMD's rate
-      if ((left / TT ^ wave_slot) & 1) __builtin_amdgcn_s_setprio(2);
+      // The older of two waves on a SIMD would otherwise run at its own pace
+      // and leave the other to finish alone, at half of the SIMD's rate. They
+      // take turns instead, by the clock: every 2^15 cycles (8 x 2048 tokens,
+      // 4096 channels: no turns 297 us, a turn a tile 283, 2^15 cycles 276, 2^19
+      // 295; short runs want them no longer: packed 143, 143, 142, 150 us).
+      if (((uint32_t)(__builtin_amdgcn_s_memtime() >> 15) ^ wave_slot) & 1) __builtin_amdgcn_s_setprio(2);
       else __builtin_amdgcn_s_setprio(0);
       if (left > TT) fetch(left - TT);
       if (left >= TT) {

@@ -127,16 +127,16 @@ __device__ __forceinline__ float silu_f32(float z) {
   return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-z * kLog2e));
 }
 
-// log(1 + e^v) from the hardware's log2 and exp2. With w = 1 + e rounded,
-// log(w) e / (w - 1) corrects the rounding of w to first order, so the result
-// keeps its relative accuracy where e is small (dt near 0.001 is the usual
-// range); v itself above 20, as dt_pre does.
+// log(1 + e^v) from the hardware's log2 and exp2. w = 1 + e is rounded; what
+// the rounding lost, c, is added to first order as c / w, so the result keeps its
+// relative accuracy where e is small (dt near 0.001 is the usual range). v
+// itself above 20, as dt_pre does.
 __device__ __forceinline__ float softplus_f32(float v) {
   const float e = __builtin_amdgcn_exp2f(v * kLog2e);
   const float w = 1.f + e;
-  const float r = __builtin_amdgcn_logf(w) * (0.69314718055994530942f * e) * __builtin_amdgcn_rcpf(w - 1.f);
-  const float s = w == 1.f ? e : r;
-  return v > 20.f ? v : s;
+  const float c = e - (w - 1.f);
+  const float r = fmaf(__builtin_amdgcn_logf(w), 0.69314718055994530942f, c * __builtin_amdgcn_rcpf(w));
+  return v > 20.f ? v : r;
 }
 __device__ __forceinline__ float step_size(float v, float bias, const DtOpts& o) {
   v += bias;
