@@ -91,15 +91,15 @@ ssd_status_t plan_scan(const ssd_selective_desc_t* d, int64_t nseq, SelectivePla
   const ssd_status_t st = plan_selective(d, nseq, p);
   if (st != SSD_OK) return st;
   if (d->batch > kMaxGridZ) return SSD_ERR_BAD_SHAPE;
-  const SelectiveCut c = selective_scan_segments(d->batch, d->seqlen, d->channels, d->ngroups, nseq);
+  const SelectiveCut c = selective_scan_cut(d->batch, d->seqlen, d->channels, d->ngroups, nseq);
   p->cut = c;
   p->ends_off = p->dsums_off = p->copy_off = p->total = 0;
-  if (c.nseg > 1) {
+  if (c.n > 1) {
     const int64_t per = d->channels * selective_padded_states(d->dstate);
-    if (d->batch * c.nseg > kMaxElems / per) return SSD_ERR_BAD_SHAPE;
-    const size_t ends = size_t(d->batch * c.nseg * per) * sizeof(float);
+    if (d->batch * c.n > kMaxElems / per) return SSD_ERR_BAD_SHAPE;
+    const size_t ends = size_t(d->batch * c.n * per) * sizeof(float);
     p->dsums_off = align_up(ends, kWsAlign);
-    p->copy_off = align_up(p->dsums_off + size_t(d->batch * c.nseg * d->channels) * sizeof(float), kWsAlign);
+    p->copy_off = align_up(p->dsums_off + size_t(d->batch * c.n * d->channels) * sizeof(float), kWsAlign);
     p->total = p->copy_off + align_up(ends, kWsAlign);
   }
   return SSD_OK;
@@ -143,12 +143,11 @@ ssd_status_t run_scan(SelectivePlan& p, const int32_t* cu, const void* x, const 
   a.x = x, a.dt = dt, a.B = B, a.C = C, a.z = z, a.A = A, a.D = D, a.init = init, a.y = y;
   a.final_state = final_state;
   a.cu = cu;
-  a.seg_len = p.cut.len;
-  a.nseg = (int)p.cut.nseg;
+  a.cut = p.cut;
   char* wc = static_cast<char*>(w);
   a.ends = reinterpret_cast<float*>(wc + p.ends_off);
   a.dsums = reinterpret_cast<float*>(wc + p.dsums_off);
-  a.init_copy = init != nullptr && init == final_state && a.nseg > 1 ? reinterpret_cast<float*>(wc + p.copy_off) : nullptr;
+  a.init_copy = init != nullptr && init == final_state && a.cut.n > 1 ? reinterpret_cast<float*>(wc + p.copy_off) : nullptr;
   hipError_t e = launch_selective_scan(a, p.io, p.dt, p.batch, s);
   if (owned) {
     const hipError_t fe = hipFreeAsync(w, s);

@@ -28,7 +28,7 @@
 // output, from the state folded together from the segments before:
 //     h <- exp(A sum_j d) h + end_j.
 // That doubles most of the arithmetic, so it is done only below a wave count
-// (selective_scan_segments). No workgroup waits for another.
+// (selective_scan_cut). No workgroup waits for another.
 //
 // Packed sequences use the same segments of the packed stream; a segment's
 // walk is a list of runs, one for each sequence with tokens in it, each
@@ -137,9 +137,11 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
   const bool mine = cg < a.epg;
   const int e = g * a.epg + (mine ? cg : a.epg - 1);
   const int64_t b = blockIdx.z;
-  const int seg = blockIdx.y;
-  const int64_t s0 = (int64_t)seg * a.seg_len;
-  const int64_t s1 = s0 + a.seg_len < a.L ? s0 + a.seg_len : a.L;
+  // the piece of the time axis this workgroup begins with, and its tokens:
+  // one piece, or with output a segment of them
+  const int seg = OUT ? blockIdx.y * a.cut.pieces : blockIdx.y;
+  const int64_t s0 = (int64_t)seg * a.cut.len, want = (int64_t)a.cut.len * (OUT ? a.cut.pieces : 1);
+  const int64_t s1 = s0 + want < a.L ? s0 + want : a.L;
 
   const TIO* xb = static_cast<const TIO*>(a.x) + b * a.xs.batch + (int64_t)g * a.epg;
   const TDT* db = static_cast<const TDT*>(a.dt) + b * a.ds.batch + (int64_t)g * a.epg;
@@ -182,7 +184,7 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
   };
   // workspace states: [batch, segment, E, NP]
   auto ws_at = [&](float* base, int64_t j, int i) {
-    return reinterpret_cast<float4*>(base + (((b * a.nseg + j) * a.E + e) * NP + i * 16 + q * 4));
+    return reinterpret_cast<float4*>(base + (((b * a.cut.n + j) * a.E + e) * NP + i * 16 + q * 4));
   };
   auto ws_store = [&](float* base) {
     if (!mine) return;
@@ -413,7 +415,7 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
     ws_store(a.ends);
     dsum += quad_xor<1>(dsum);
     dsum += quad_xor<2>(dsum);
-    if (mine && q == 0) a.dsums[(b * a.nseg + seg) * a.E + e] = dsum;
+    if (mine && q == 0) a.dsums[(b * a.cut.n + seg) * a.E + e] = dsum;
   } else {
     // the state that enters at the segment's start, for a sequence that
     // began in segment j0
@@ -424,7 +426,7 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
         h[4 * i] = v.x, h[4 * i + 1] = v.y, h[4 * i + 2] = v.z, h[4 * i + 3] = v.w;
       }
       for (int64_t j = j0 + 1; j < seg; ++j) {
-        const float ds = a.dsums[(b * a.nseg + j) * a.E + e];
+        const float ds = a.dsums[(b * a.cut.n + j) * a.E + e];
 #pragma unroll
         for (int i = 0; i < SPL / 4; ++i) {
           const float4 v = *ws_at(a.ends, j, i);
@@ -435,13 +437,13 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
         }
       }
     };
-    auto begin = [&](int64_t row, bool goes_on) {
+    auto begin = [&](int64_t row, int64_t piece, bool goes_on) {
       if (goes_on && a.init_copy != nullptr) {
         // the final state of this sequence may be written over its initial
         // state by another workgroup of this launch: take the kept copy
 #pragma unroll
         for (int i = 0; i < SPL / 4; ++i) {
-          const float4 v = *ws_at(a.init_copy, seg, i);
+          const float4 v = *ws_at(a.init_copy, piece, i);
           h[4 * i] = v.x, h[4 * i + 1] = v.y, h[4 * i + 2] = v.z, h[4 * i + 3] = v.w;
         }
       } else {
@@ -457,7 +459,7 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
       const int64_t last = packed ? seq_offset(a.cu, row + 1, a.L) : a.L;
       if (last <= pos || first > pos) continue;
       const int64_t r1 = last < s1 ? last : s1;
-      if (first < s0) enter(first / a.seg_len); else begin(row, last > s1);
+      if (first < s0) enter(first / a.cut.len); else begin(row, first / a.cut.len, last > s1);
       walk(pos, r1);
       if (last <= s1 && a.final_state != nullptr) store_state(a.final_state, row);
       pos = r1;
@@ -465,7 +467,7 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
     if (packed && a.final_state != nullptr) {
       // sequences without tokens keep their state: this segment's share of them
       const int lane = tid & 63;
-      for (int64_t r = (int64_t)seg * 64; r < a.nseq; r += (int64_t)a.nseg * 64) {
+      for (int64_t r = (int64_t)blockIdx.y * 64; r < a.nseq; r += (int64_t)gridDim.y * 64) {
         const int64_t i = r + lane < a.nseq ? r + lane : a.nseq - 1;
         uint64_t empty = __ballot(r + lane < a.nseq && seq_offset(a.cu, i + 1, a.L) <= seq_offset(a.cu, i, a.L));
         while (empty != 0) {
@@ -494,12 +496,14 @@ hipError_t launch_np(const SelectiveArgs& args, int64_t batch, hipStream_t s) {
               (a.z == nullptr || whole(a.z, sizeof(TIO), PK, a.zs));
   a.whole_y = a.epg % PK == 0 && whole(a.y, sizeof(TIO), PK, Stride{a.E, a.L * a.E});
   const unsigned tiles = (unsigned)(a.tiles * (a.E / a.epg));
-  if (a.nseg > 1) {
-    selective_scan_kernel<TIO, TDT, NP, false><<<dim3(tiles, (unsigned)(a.nseg - 1), (unsigned)batch), kThreads, 0, s>>>(a);
+  const int segments = (a.cut.n + a.cut.pieces - 1) / a.cut.pieces;
+  if (segments > 1) {
+    selective_scan_kernel<TIO, TDT, NP, false>
+        <<<dim3(tiles, (unsigned)((segments - 1) * a.cut.pieces), (unsigned)batch), kThreads, 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  selective_scan_kernel<TIO, TDT, NP, true><<<dim3(tiles, (unsigned)a.nseg, (unsigned)batch), kThreads, 0, s>>>(a);
+  selective_scan_kernel<TIO, TDT, NP, true><<<dim3(tiles, (unsigned)segments, (unsigned)batch), kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -516,25 +520,28 @@ hipError_t launch_io(const SelectiveArgs& a, int64_t batch, hipStream_t s) {
 
 }  // namespace
 
-SelectiveCut selective_scan_segments(int64_t batch, int64_t L, int64_t E, int64_t G, int64_t nseq) {
+SelectiveCut selective_scan_cut(int64_t batch, int64_t L, int64_t E, int64_t G, int64_t nseq) {
   const int64_t tiles = (E / G + kChannels - 1) / kChannels * G;
   const int64_t waves = tiles * 4 * batch;
   // one wave a SIMD keeps the vector units busy enough that walking the
   // tokens twice would cost more; below that, aim at two waves a SIMD
   const int64_t full = 1024;
-  int64_t want = waves >= full ? 1 : (2 * full + waves - 1) / waves;
+  const int64_t want = waves >= full ? 1 : (2 * full + waves - 1) / waves;
   int64_t len = (L + want - 1) / want;
   if (nseq > 0 && 4 * L / nseq < len) len = 4 * L / nseq;
   if (len < 64) len = 64;
-  len = (len + 31) / 32 * 32;
-  SelectiveCut c;
-  c.nseg = (L + len - 1) / len;
-  if (c.nseg > 65535) {
-    len = ((L + 65534) / 65535 + 31) / 32 * 32;
-    c.nseg = (L + len - 1) / len;
-  }
-  c.len = len;
-  return c;
+  if (len >= L) return SelectiveCut{1, L, 1};
+  // The first walk needs half the registers of the second, so it has room for
+  // more waves: a quarter of a segment each (16384 tokens of 4096 channels 464
+  // -> 442 us). Packed sequences keep whole segments: every piece may end in
+  // the middle of a run (37 sequences in 8197 tokens 142 -> 154 us).
+  int64_t pieces = nseq > 0 ? 1 : 4;
+  int64_t unit = 32 * pieces;  // whole tiles
+  len = (len + unit - 1) / unit * unit;
+  while (L > len * 16384) len *= 2;  // pieces along grid.y
+  if (len >= L) return SelectiveCut{1, L, 1};
+  len /= pieces;
+  return SelectiveCut{(int)((L + len - 1) / len), len, (int)pieces};
 }
 
 hipError_t launch_selective_scan(const SelectiveArgs& args, int io, int dt, int64_t batch, hipStream_t s) {

@@ -15,6 +15,15 @@ struct Stride {
 };
 
 // ---- selective scan ----------------------------------------------------------
+// The cut of the time axis: n pieces of len tokens, `pieces` of them to a
+// segment of the second walk. n = 1: one walk over all tokens.
+struct SelectiveCut {
+  int n;
+  int64_t len;
+  int pieces;
+};
+SelectiveCut selective_scan_cut(int64_t batch, int64_t L, int64_t E, int64_t G, int64_t nseq);
+
 struct SelectiveArgs {
   const void *x, *dt, *B, *C, *z;  // z nullable
   const float *A, *D, *init;       // D, init nullable
@@ -26,19 +35,15 @@ struct SelectiveArgs {
   const int32_t* cu;               // packed: sequence offsets [nseq + 1], else nullptr
   int64_t nseq;
   DtOpts dto;
-  // the cut of the time axis, and the workspace when nseg > 1
-  int64_t seg_len;
-  int nseg;
-  float* ends;       // [batch, nseg, E, padded N]: the segments' end states
-  float* dsums;      // [batch, nseg, E]: their sums of dt
+  SelectiveCut cut;
+  // the workspace when cut.n > 1
+  float* ends;       // [batch, cut.n, E, padded N]: the pieces' end states
+  float* dsums;      // [batch, cut.n, E]: their sums of dt
   float* init_copy;  // as ends: initial states that the final states overwrite, else nullptr
   // set at launch: channels per group, workgroups per group, and which rows
   // can be taken in whole packs
   int epg, tiles;
   bool whole_in, whole_y;
-};
-struct SelectiveCut {
-  int64_t nseg, len;
 };
 // States per channel as the kernels hold them: the next of 16, 32, .. 256.
 inline int selective_padded_states(int64_t N) {
@@ -46,7 +51,6 @@ inline int selective_padded_states(int64_t N) {
   while (np < N) np *= 2;
   return np;
 }
-SelectiveCut selective_scan_segments(int64_t batch, int64_t L, int64_t E, int64_t G, int64_t nseq);
 hipError_t launch_selective_scan(const SelectiveArgs& a, int io, int dt, int64_t batch, hipStream_t s);
 
 // The recurrence at one token, states in slots.
