@@ -523,10 +523,12 @@ hipError_t launch_io(const SelectiveArgs& a, int64_t batch, hipStream_t s) {
 SelectiveCut selective_scan_cut(int64_t batch, int64_t L, int64_t E, int64_t G, int64_t nseq) {
   const int64_t tiles = (E / G + kChannels - 1) / kChannels * G;
   const int64_t waves = tiles * 4 * batch;
-  // one wave a SIMD keeps the vector units busy enough that walking the
-  // tokens twice would cost more; below that, aim at two waves a SIMD
-  const int64_t full = 1024;
-  const int64_t want = waves >= full ? 1 : (2 * full + waves - 1) / waves;
+  // As many segments as two waves a SIMD allow: one walk takes the same time
+  // for 1025 waves as for 2048, and for 1 as for 1024. 4096 tokens of 4096
+  // channels, batch 2 (512 waves): 392 us in one walk, 224 in four segments;
+  // batch 4: 395 and 371 in two; batch 6: 534 and, as two, 619.
+  const int64_t full = 2048;
+  const int64_t want = 2 * waves > full ? 1 : full / waves;
   int64_t len = (L + want - 1) / want;
   if (nseq > 0 && 4 * L / nseq < len) len = 4 * L / nseq;
   if (len < 64) len = 64;
