@@ -37,7 +37,8 @@ __device__ __forceinline__ TIO* output_of(void* const (&out)[3], const int (&wid
   return static_cast<TIO*>(out[o]) + ch;
 }
 
-template <typename TIO, int K, int V>
+// STREAM: the inputs are read past the memory-side cache.
+template <typename TIO, int K, int V, bool STREAM>
 __global__ __launch_bounds__(kThreads) void conv1d_kernel(const Conv1dArgs a) {
   constexpr int H = K > 1 ? K - 1 : 1;
   constexpr bool VEC = V > 1;
@@ -87,17 +88,24 @@ __global__ __launch_bounds__(kThreads) void conv1d_kernel(const Conv1dArgs a) {
     }
   };
 
+  // V inputs of token t
+  auto input = [&](int64_t t) {
+    const TIO* p = in + t * a.xs.token;
+    if constexpr (STREAM) return load_stream(reinterpret_cast<const Pack<TIO, V>*>(p));
+    else return load_pack<TIO, V, VEC>(p, V);
+  };
+
   // Tokens [r0, r1) of the sequence `row` that began at `first`.
   auto walk = [&](int64_t row, int64_t first, int64_t r0, int64_t r1, bool ends) {
     // (all loads first: the tokens before r0, or the run's first in their place)
     Pack<TIO, V> nxt[kU], before[H];
 #pragma unroll
     for (int u = 0; u < kU; ++u)
-      nxt[u] = load_pack<TIO, V, VEC>(in + (r0 + u < r1 ? r0 + u : r1 - 1) * a.xs.token, V);
+      nxt[u] = input(r0 + u < r1 ? r0 + u : r1 - 1);
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
       const int64_t t = r0 - (K - 1) + j;
-      before[j] = load_pack<TIO, V, VEC>(in + (t >= first ? t : r0) * a.xs.token, V);
+      before[j] = input(t >= first ? t : r0);
     }
     float hist[H][V];
     // of the carried state, inputs r0 - first .. K - 2 still lie before r0
@@ -127,7 +135,7 @@ __global__ __launch_bounds__(kThreads) void conv1d_kernel(const Conv1dArgs a) {
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const int64_t t = tb + kU + u;
-        nxt[u] = load_pack<TIO, V, VEC>(in + (t < r1 ? t : r1 - 1) * a.xs.token, V);
+        nxt[u] = input(t < r1 ? t : r1 - 1);
       }
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
@@ -277,11 +285,19 @@ hipError_t launch_conv_k(const Conv1dArgs& args, int64_t batch, hipStream_t s) {
   // K - 1 repeated rows weigh less
   int64_t tile = 64;
   while (tile > 8 && gx * batch * ((a.L + tile - 1) / tile) < 2048) tile /= 2;
+  // Where the input would drive the output, which the next operator reads, out
+  // of the memory-side cache, it is read past the cache (non-temporal): 128 MiB of
+  // both 27.7 -> 26.9 us, 256 MiB 56 -> 48 us. Smaller ones may lie there
+  // themselves (64 MiB: 14.8 us, past it 16.8), and an output as large as the
+  // cache is lost either way (512 MiB: 111 us, past it 114).
+  const int64_t out_bytes = batch * a.L * a.CH * (int64_t)sizeof(TIO);
+  const bool stream = 2 * out_bytes >= kMemorySideCache / 2 && out_bytes < kMemorySideCache;
   if ((a.L + tile - 1) / tile > 65535) tile = (a.L + 65534) / 65535;
   a.tile = (int)tile;
   const dim3 grid((unsigned)gx, (unsigned)((a.L + tile - 1) / tile), (unsigned)batch);
-  if (vec) conv1d_kernel<TIO, K, W><<<grid, kThreads, 0, s>>>(a);
-  else conv1d_kernel<TIO, K, 1><<<grid, kThreads, 0, s>>>(a);
+  if (vec && stream) conv1d_kernel<TIO, K, W, true><<<grid, kThreads, 0, s>>>(a);
+  else if (vec) conv1d_kernel<TIO, K, W, false><<<grid, kThreads, 0, s>>>(a);
+  else conv1d_kernel<TIO, K, 1, false><<<grid, kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 

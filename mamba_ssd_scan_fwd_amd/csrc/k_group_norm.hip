@@ -193,11 +193,11 @@ hipError_t launch_z(const GroupNormArgs& a, hipStream_t s) {
 template <typename TIO>
 hipError_t launch_io(const GroupNormArgs& args, hipStream_t s) {
   GroupNormArgs a = args;
-  // Inputs and output that do not fit the memory-side cache together are read
-  // past it (non-temporal), which leaves it to the output's writes: 384 MB 78 ->
-  // 66 us. Below, part of the inputs may still lie there from the operator that
-  // wrote them: 96 MB 19.4 us from the cache, 21.0 us past it.
-  a.stream = a.batch * a.rows * a.C * (int64_t)sizeof(TIO) * (a.z != nullptr ? 3 : 2) > kMemorySideCache;
+  // Inputs and output beyond half the memory-side cache: the inputs are read past
+  // it (non-temporal), which leaves it to the output, 192 MB 40 -> 35 us, 384 MB
+  // 79 -> 67, 768 MB 157 -> 152. Smaller ones are better off in it (96 MB 20.8 us,
+  // past it 21.6; 19.4 and 21.0 where the inputs lie there already).
+  a.stream = a.batch * a.rows * a.C * (int64_t)sizeof(TIO) * (a.z != nullptr ? 3 : 2) > kMemorySideCache / 2;
   constexpr int V = 16 / sizeof(TIO);
   auto on = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
   // 16-byte accesses: groups, row strides and bases in whole packs
