@@ -7,7 +7,11 @@
 // alignment allows) and walks a tile of tokens with the K - 1 inputs before
 // it in registers, kU tokens' loads in flight ahead of the ones in use. Each
 // input is read once, plus K - 1 rows at the start of a tile, and the work
-// per element is far below what the memory traffic costs.
+// per element is far below what the memory traffic costs. Eight bf16 channels and
+// four tokens ahead: 8 x 2048 x 4096 47 us (5.7 TB/s; a copy of the same bytes
+// takes 50); eight tokens ahead leave two waves a SIMD (55 -> 51 us, with scalar
+// weight loads). 8197 packed tokens of 4352 channels: 34 us, 4.2 TB/s, the
+// start of each run (offsets, carried state, first rows) being waited for.
 //
 // Packed sequences cut the packed stream into the same tiles: a tile is a
 // list of runs, one for each sequence with tokens in it, and a run starts
@@ -193,7 +197,9 @@ __global__ __launch_bounds__(kThreads) void conv1d_kernel(const Conv1dArgs a) {
 
 // One token per row: V channels to a thread, their K - 1 old inputs read and
 // written as one block of V (K - 1) floats. Rows without a slot of their own
-// (negative, behind the pool, or named by an earlier row) are padding.
+// (negative, behind the pool, or named by an earlier row) are padding. 256 rows
+// of 8192 channels: 13.0 us, 4.5 TB/s (rows a workgroup: 1 13.5, 2 13.0, 4 13.6, 8
+// 14.3); one row of 4352 channels 2.8 us.
 constexpr int kStepThreads = 256;
 
 template <typename TIO, int K, int V, int R>

@@ -7,19 +7,30 @@
 //
 // A product with the decays of every (e, n) has no matrix form over tokens, so
 // this is vector work: per token, channel and state one exp2, two products
-// and two fused adds. Memory (x, dt, z and y once) stays well below that.
+// and two fused adds: for 64 lanes 4 x 4 + 8 = 24 cycles of a SIMD (a wave's
+// exp2 takes 8 cycles and keeps other waves' arithmetic waiting, measured).
+// Memory (x, dt, z and y once) stays well below that.
 //
 // Layout: four lanes share a channel, each holding a quarter of its states in
 // registers for the whole walk over the tokens; a workgroup of four waves
 // takes 64 channels of one group, so a token's row of a bf16 array is one
-// 128-byte line. Tokens go in groups of four: lane q of the quad loads x, dt
-// and z of token 4i + q and computes its softplus, dt x, gate and store alone
-// (nothing is done four times), and the four tokens' dt and dt x reach the
-// quad by DPP broadcasts. The four partial sums of y are exchanged in one
-// transposing reduction (three adds), which leaves token 4i + q's sum in lane
-// q. B and C are the same for all channels of a group: they are converted to
-// fp32 once per tile into LDS (two buffers, one barrier a tile), whence the
-// four quarters read 16 bytes each, without bank conflicts.
+// 128-byte line. Tokens go in groups of four: lane q of the quad takes x, dt
+// and z of token 4i + q and computes its softplus, dt x and gate alone (nothing
+// is done four times), and the four tokens' dt and dt x reach the quad by DPP
+// broadcasts. The four partial sums of y are exchanged in one transposing
+// reduction (three adds), which leaves token 4i + q's sum in lane q.
+//
+// Tiles of 32 tokens (fewer with more states) go through LDS, two buffers and
+// one barrier a tile: x, dt and z as they are, in 16-byte accesses, and B and
+// C, the same for all channels of a group, converted to fp32, whence the four
+// quarters read 16 bytes each. The next tile's loads are issued at the start of
+// a tile and written to LDS before y is stored, so that no wait for a load is
+// also a wait for a store.
+//
+// Measured (8 x 2048 tokens, 4096 channels, 16 states, bf16, gate): 274 us, the
+// vector units busy 85% of the time; 31 instructions a token and wave, of which
+// the 20 above are the states' and 9 the step sizes, gates and moves. The
+// arithmetic of the 20 alone takes about 180 us, a copy of the same bytes 100.
 //
 // The time axis: where batch rows and channels are too few waves for the
 // card, the tokens are cut into segments. A first launch walks each segment

@@ -8,7 +8,11 @@
 // where N allows it), padded N / 4 lanes to a channel; a workgroup keeps its
 // channels' A for up to kRows rows of the batch, since A is as large as one
 // row's state and would otherwise double what L2 has to deliver. All rows'
-// loads are issued before the first is used.
+// loads are issued before the first is used. B and C in one access each took
+// the kernel from 82 to 57 us (256 rows of 8192 channels): element by element
+// they were half of all load instructions. Rows a workgroup: 1 68 us, 2 59, 4 57,
+// 8 60. With the states past the cache (below) 51 us, 5.5 TB/s of 6.0 that an
+// update in place reaches; one row of 4096 channels 3.1 us.
 //
 // A row whose slot is negative or behind the pool is padding: nothing is
 // read or written for it. Where a slot is named twice the first row has it
