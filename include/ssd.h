@@ -437,8 +437,7 @@ SSD_API ssd_status_t ssd_decode_step(const ssd_desc_t* desc, const void* x, cons
  *    buffers and time-major arrays are read in place. A stride of 0 means
  *    dense. Rows may not overlap (strides >= the row's width; a token stride
  *    is below 2^22). Outputs and states are dense.
- *  - Base pointers need the alignment of their elements only; 16-byte aligned
- *    bases, widths and strides are read in 16-byte accesses.
+ *  - Base pointers need the alignment of their elements only.
  *  - The stream's device must be the current device.
  */
 typedef struct {

@@ -3,8 +3,8 @@
 //     y[t][ch] = act(bias[ch] + sum_{k<K} w[ch][k] in[t - (K-1) + k][ch])
 // where in[] before a sequence's first token is its carried state.
 //
-// Prompts: each thread owns V consecutive channels (16 bytes of a row where
-// alignment allows) and walks a tile of tokens with the K - 1 inputs before
+// Prompts: each thread owns V consecutive channels (16 bytes of a row, at any
+// address; one where outputs share such a pack) and walks a tile of tokens with the K - 1 inputs before
 // it in registers, kU tokens' loads in flight ahead of the ones in use. Each
 // input is read once, plus K - 1 rows at the start of a tile, and the work
 // per element is far below what the memory traffic costs. Eight bf16 channels and
@@ -45,10 +45,11 @@ __device__ __forceinline__ TIO* output_of(void* const (&out)[3], const int (&wid
 template <typename TIO, int K, int V, bool STREAM>
 __global__ __launch_bounds__(kThreads) void conv1d_kernel(const Conv1dArgs a) {
   constexpr int H = K > 1 ? K - 1 : 1;
-  constexpr bool VEC = V > 1;
   const int ch = V * (blockIdx.x * kThreads + threadIdx.x);
   const bool mine = ch < a.CH;
-  const int cc = mine ? ch : 0;
+  // (the last pack ends with the channels; where it overlaps the one before,
+  // both write the same values)
+  const int cc = !mine ? 0 : ch + V <= a.CH ? ch : a.CH - V;
   const int64_t b = blockIdx.z;
   const int64_t t0 = (int64_t)blockIdx.y * a.tile;
   const int64_t t1 = t0 + a.tile < a.L ? t0 + a.tile : a.L;
@@ -62,12 +63,12 @@ __global__ __launch_bounds__(kThreads) void conv1d_kernel(const Conv1dArgs a) {
   float w[K][V], bias[V];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const Pack<float, V> p = load_pack<float, V, VEC>(a.w + cc * K + k * V, V);
+    const Pack<float, V> p = load_pack<float, V>(a.w + cc * K + k * V);
 #pragma unroll
     for (int v = 0; v < V; ++v) w[(k * V + v) % K][(k * V + v) / K] = p.v[v];
   }
   {
-    const Pack<float, V> p = load_pack<float, V, VEC>(a.bias != nullptr ? a.bias + cc : a.w, V);
+    const Pack<float, V> p = load_pack<float, V>(a.bias != nullptr ? a.bias + cc : a.w);
 #pragma unroll
     for (int v = 0; v < V; ++v) bias[v] = a.bias != nullptr ? p.v[v] : 0.f;
   }
@@ -76,7 +77,7 @@ __global__ __launch_bounds__(kThreads) void conv1d_kernel(const Conv1dArgs a) {
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
       Pack<float, V> p = {};
-      if (a.state_in != nullptr) p = load_pack<float, V, VEC>(a.state_in + (row * a.CH + cc) * H + j * V, V);
+      if (a.state_in != nullptr) p = load_pack<float, V>(a.state_in + (row * a.CH + cc) * H + j * V);
 #pragma unroll
       for (int v = 0; v < V; ++v) f[(j * V + v) % H][(j * V + v) / H] = p.v[v];
     }
@@ -88,15 +89,15 @@ __global__ __launch_bounds__(kThreads) void conv1d_kernel(const Conv1dArgs a) {
       float f[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) f[v] = hist[(j * V + v) % H][(j * V + v) / H];
-      store_pack<float, V, VEC>(a.state_out + (row * a.CH + cc) * H + j * V, f, V);
+      store_pack<float, V>(a.state_out + (row * a.CH + cc) * H + j * V, f);
     }
   };
 
   // V inputs of token t
   auto input = [&](int64_t t) {
     const TIO* p = in + t * a.xs.token;
-    if constexpr (STREAM) return load_stream(reinterpret_cast<const Pack<TIO, V>*>(p));
-    else return load_pack<TIO, V, VEC>(p, V);
+    if constexpr (STREAM) return load_stream<TIO, V>(p);
+    else return load_pack<TIO, V>(p);
   };
 
   // Tokens [r0, r1) of the sequence `row` that began at `first`.
@@ -157,7 +158,7 @@ __global__ __launch_bounds__(kThreads) void conv1d_kernel(const Conv1dArgs a) {
             for (int k = 0; k + 1 < K - 1; ++k) hist[k][v] = hist[k + 1][v];
             hist[H - 1][v] = now;
           }
-          if (mine) store_pack<TIO, V, VEC>(out + (tb + u) * os, z, V);
+          if (mine) store_pack<TIO, V>(out + (tb + u) * os, z);
         }
       }
     }
@@ -202,21 +203,27 @@ __global__ __launch_bounds__(kThreads) void conv1d_kernel(const Conv1dArgs a) {
 // 14.3); one row of 4352 channels 2.8 us.
 constexpr int kStepThreads = 256;
 
-template <typename TIO, int K, int V, int R>
+// PART: the last thread of a row has fewer than V channels.
+template <typename TIO, int K, int V, int R, bool PART>
 __global__ __launch_bounds__(kStepThreads) void conv1d_step_kernel(const Conv1dStepArgs a) {
   constexpr int H = K > 1 ? K - 1 : 1;
-  constexpr bool VEC = V > 1;
   const int ch = V * (blockIdx.x * kStepThreads + threadIdx.x);
   const bool mine = ch < a.CH;
   const int cc = mine ? ch : 0;
+  const int n = a.CH - cc < V ? a.CH - cc : V;  // channels there: fewer at the end of a row
+  // V of the n K weights or n H inputs of a lane's channels, from the j V-th on
+  auto block = [&](const float* p, int per, int j) {
+    const int there = n * per - j * V;
+    return load_pack<float, V, PART>(PART && there <= 0 ? p : p + j * V, there);
+  };
   const int64_t row0 = (int64_t)blockIdx.y * R;
   int os;
   TIO* out = output_of<TIO>(a.out, a.width, cc, os);
 
   Pack<float, V> w[K], bias;
 #pragma unroll
-  for (int k = 0; k < K; ++k) w[k] = load_pack<float, V, VEC>(a.w + cc * K + k * V, V);
-  bias = load_pack<float, V, false>(a.bias != nullptr ? a.bias + cc : a.w, V);
+  for (int k = 0; k < K; ++k) w[k] = block(a.w + cc * K, K, k);
+  bias = load_pack<float, V, PART>(a.bias != nullptr ? a.bias + cc : a.w + cc * K, n);
   Pack<float, V> old[R][H];
   Pack<TIO, V> xv[R];
   int64_t slot[R];
@@ -229,9 +236,9 @@ __global__ __launch_bounds__(kStepThreads) void conv1d_step_kernel(const Conv1dS
     if constexpr (K > 1) {
 #pragma unroll
       for (int j = 0; j < K - 1; ++j)
-        old[r][j] = load_pack<float, V, VEC>(a.state + (from * a.CH + cc) * H + j * V, V);
+        old[r][j] = block(a.state + (from * a.CH + cc) * H, H, j);
     }
-    xv[r] = load_pack<TIO, V, VEC>(static_cast<const TIO*>(a.x) + row * a.xs + cc, V);
+    xv[r] = load_pack<TIO, V, PART>(static_cast<const TIO*>(a.x) + row * a.xs + cc, n);
   }
   if (a.slots != nullptr) {
     const uint32_t again = repeated_slots<R, kStepThreads>(a.slots, row0, a.batch);
@@ -261,31 +268,27 @@ __global__ __launch_bounds__(kStepThreads) void conv1d_step_kernel(const Conv1dS
     if constexpr (K > 1) {
 #pragma unroll
       for (int j = 0; j < K - 1; ++j)
-        store_pack<float, V, VEC>(a.state + (slot[r] * a.CH + cc) * H + j * V, kept[j], V);
+        store_pack<float, V, PART>(a.state + (slot[r] * a.CH + cc) * H + j * V, kept[j], n * H - j * V);
     }
-    store_pack<TIO, V, VEC>(out + (row0 + r) * os, z, V);
+    store_pack<TIO, V, PART>(out + (row0 + r) * os, z, n);
   }
 }
 
-bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
-
-// Whether rows of CH channels can be taken V at a time in accesses of
-// V elements: outputs' widths, row strides and bases all multiples of that.
-template <int V, typename TIO, typename Args>
-bool whole_packs(const Args& a, int64_t token, int64_t batch) {
-  const size_t bytes = V * sizeof(TIO);
-  if (token % V || batch % V || reinterpret_cast<uintptr_t>(a.x) % bytes) return false;
-  for (int i = 0; i < 3; ++i)
-    if (a.width[i] % V || reinterpret_cast<uintptr_t>(a.out[i]) % bytes) return false;
-  return true;
+// Whether no V consecutive channels from a multiple of V on, nor the last V,
+// belong to two outputs.
+template <int V, typename Args> bool whole_packs(const Args& a) {
+  int last = 2;
+  while (last > 0 && a.width[last] == 0) --last;
+  for (int i = 0; i < last; ++i)
+    if (a.width[i] % V) return false;
+  return a.width[last] >= V;
 }
 
 template <typename TIO, int K>
 hipError_t launch_conv_k(const Conv1dArgs& args, int64_t batch, hipStream_t s) {
   constexpr int W = 16 / sizeof(TIO);
   Conv1dArgs a = args;
-  const bool vec = whole_packs<W, TIO>(a, a.xs.token, a.xs.batch) && on16(a.w) && on16(a.bias) && on16(a.state_in) &&
-                   on16(a.state_out);
+  const bool vec = whole_packs<W>(a);
   const int64_t gx = (a.CH + kThreads * (vec ? W : 1) - 1) / (kThreads * (vec ? W : 1));
   // short tiles while they are needed to fill the card, then long ones, whose
   // K - 1 repeated rows weigh less
@@ -309,15 +312,16 @@ hipError_t launch_conv_k(const Conv1dArgs& args, int64_t batch, hipStream_t s) {
 
 template <typename TIO, int K>
 hipError_t launch_step_k(const Conv1dStepArgs& a, hipStream_t s) {
-  const bool vec = whole_packs<4, TIO>(a, a.xs, 0) && on16(a.state) && on16(a.w);
+  const bool vec = whole_packs<4>(a);
   const int64_t gx = (a.CH + kStepThreads * (vec ? 4 : 1) - 1) / (kStepThreads * (vec ? 4 : 1));
   auto go = [&](auto kern, int rows) {
     kern<<<dim3((unsigned)gx, (unsigned)((a.batch + rows - 1) / rows)), kStepThreads, 0, s>>>(a);
     return hipGetLastError();
   };
-  if (!vec) return go(conv1d_step_kernel<TIO, K, 1, 1>, 1);
+  if (!vec) return go(conv1d_step_kernel<TIO, K, 1, 1, false>, 1);
+  if (a.CH % 4 != 0) return go(conv1d_step_kernel<TIO, K, 4, 1, true>, 1);
   // several rows a workgroup share the weights once that leaves the card full
-  return gx * a.batch >= 4 * 512 ? go(conv1d_step_kernel<TIO, K, 4, 2>, 2) : go(conv1d_step_kernel<TIO, K, 4, 1>, 1);
+  return gx * a.batch >= 4 * 512 ? go(conv1d_step_kernel<TIO, K, 4, 2, false>, 2) : go(conv1d_step_kernel<TIO, K, 4, 1, false>, 1);
 }
 
 }  // namespace

@@ -22,7 +22,7 @@
 namespace ssd {
 namespace {
 
-template <typename TIO, int V, int M, bool VEC, int T, bool Z>
+template <typename TIO, int V, int M, bool WHOLE, int T, bool Z>
 __global__ __launch_bounds__(T > 64 ? T : 256) void group_norm_kernel(const GroupNormArgs a) {
   constexpr int THREADS = T > 64 ? T : 256;
   constexpr int TEAMS = THREADS / T;  // teams per workgroup
@@ -38,18 +38,24 @@ __global__ __launch_bounds__(T > 64 ? T : 256) void group_norm_kernel(const Grou
   const float inv = 1.f / (float)S;
   int par = 0;
 
-  int at[M], nn[M];  // this lane's packs: first channel, channels present
+  // This lane's packs: first channel, and which of its elements count. WHOLE:
+  // groups of V channels and more; the last pack of a group ends with it, and
+  // where it overlaps the one before (skip > 0) both write the same values.
+  // Otherwise the one pack of a small group, of which nn elements are there.
+  int at[M], nn[M], skip[M];
 #pragma unroll
   for (int m = 0; m < M; ++m) {
-    const int c = (m * T + lane) * V;
-    nn[m] = S - c < 0 ? 0 : S - c > V ? V : S - c;
-    at[m] = g * S + (nn[m] > 0 ? c : 0);
+    const int c = (m * T + lane) * V, from = WHOLE && c + V > S ? S - V : c;
+    nn[m] = c >= S ? 0 : S - from < V ? S - from : V;
+    skip[m] = c - from;
+    at[m] = g * S + (nn[m] > 0 ? from : 0);
   }
+  auto counts = [&](int m, int v) { return v < nn[m] && v >= skip[m]; };
   constexpr bool HOLD = T < 1024;
   // weights and offsets of pack m (any valid address stands in for none)
   auto weights = [&](int m, float (&w)[V], float (&bias)[V]) {
-    const Pack<float, V> wp = load_pack<float, V, VEC>(a.w != nullptr ? a.w + at[m] : a.bias + at[m], nn[m]);
-    const Pack<float, V> bp = load_pack<float, V, VEC>(a.bias != nullptr ? a.bias + at[m] : a.w + at[m], nn[m]);
+    const Pack<float, V> wp = load_pack<float, V, !WHOLE>(a.w != nullptr ? a.w + at[m] : a.bias + at[m], nn[m]);
+    const Pack<float, V> bp = load_pack<float, V, !WHOLE>(a.bias != nullptr ? a.bias + at[m] : a.w + at[m], nn[m]);
 #pragma unroll
     for (int v = 0; v < V; ++v) w[v] = a.w != nullptr ? wp.v[v] : 1.f, bias[v] = a.bias != nullptr ? bp.v[v] : 0.f;
   };
@@ -71,12 +77,12 @@ __global__ __launch_bounds__(T > 64 ? T : 256) void group_norm_kernel(const Grou
     const TIO* zp = static_cast<const TIO*>(a.z) + b * a.zs.batch + t * a.zs.token;
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-      if (VEC && a.stream) {
-        xn[m] = load_stream(reinterpret_cast<const Pack<TIO, V>*>(xp + at[m]));
-        if constexpr (Z) zn[m] = load_stream(reinterpret_cast<const Pack<TIO, V>*>(zp + at[m]));
+      if (WHOLE && a.stream) {
+        xn[m] = load_stream<TIO, V>(xp + at[m]);
+        if constexpr (Z) zn[m] = load_stream<TIO, V>(zp + at[m]);
       } else {
-        xn[m] = load_pack<TIO, V, VEC>(xp + at[m], nn[m]);
-        if constexpr (Z) zn[m] = load_pack<TIO, V, VEC>(zp + at[m], nn[m]);
+        xn[m] = load_pack<TIO, V, !WHOLE>(xp + at[m], nn[m]);
+        if constexpr (Z) zn[m] = load_pack<TIO, V, !WHOLE>(zp + at[m], nn[m]);
       }
     }
   };
@@ -120,7 +126,7 @@ __global__ __launch_bounds__(T > 64 ? T : 256) void group_norm_kernel(const Grou
       for (int m = 0; m < M; ++m)
 #pragma unroll
         for (int v = 0; v < V; ++v)
-          if (v < nn[m]) mu += x[m][v];
+          if (counts(m, v)) mu += x[m][v];
       mu = team_sum(mu) * inv;
     }
     float sq = 0.f;
@@ -129,7 +135,7 @@ __global__ __launch_bounds__(T > 64 ? T : 256) void group_norm_kernel(const Grou
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         x[m][v] -= mu;
-        if (v < nn[m]) sq = fmaf(x[m][v], x[m][v], sq);
+        if (counts(m, v)) sq = fmaf(x[m][v], x[m][v], sq);
       }
     const float var = team_sum(sq) * inv + a.eps;
     // one Newton step on the hardware's reciprocal root (1 ulp)
@@ -153,13 +159,13 @@ __global__ __launch_bounds__(T > 64 ? T : 256) void group_norm_kernel(const Grou
           if (a.silu) o[v] = silu_f32(o[v]);
         }
       }
-      if (nn[m] > 0) store_pack<TIO, V, VEC>(static_cast<TIO*>(a.out) + r * a.C + at[m], o, nn[m]);
+      if (nn[m] > 0) store_pack<TIO, V, !WHOLE>(static_cast<TIO*>(a.out) + r * a.C + at[m], o, nn[m]);
     }
     if (!HOLD && r + step < rows) fetch(r + step);
   }
 }
 
-template <typename TIO, bool VEC, bool Z>
+template <typename TIO, bool Z>
 hipError_t launch_z(const GroupNormArgs& a, hipStream_t s) {
   constexpr int V = 16 / sizeof(TIO);
   const int64_t S = a.C / a.G, packs = (S + V - 1) / V, rows = a.batch * a.rows;
@@ -182,16 +188,17 @@ hipError_t launch_z(const GroupNormArgs& a, hipStream_t s) {
     kern<<<dim3((unsigned)blocks), threads, 0, s>>>(a);
     return hipGetLastError();
   };
-  if (packs <= 8) return go(group_norm_kernel<TIO, V, 1, VEC, 8, Z>, 8);
-  if (packs <= 16) return go(group_norm_kernel<TIO, V, 1, VEC, 16, Z>, 16);
-  if (packs <= 32) return go(group_norm_kernel<TIO, V, 1, VEC, 32, Z>, 32);
-  if (packs <= 64) return go(group_norm_kernel<TIO, V, 1, VEC, 64, Z>, 64);
-  if (packs <= 128) return go(group_norm_kernel<TIO, V, 2, VEC, 64, Z>, 64);
-  if (packs <= 256) return go(group_norm_kernel<TIO, V, 1, VEC, 256, Z>, 256);
-  if (packs <= 512) return go(group_norm_kernel<TIO, V, 2, VEC, 256, Z>, 256);
-  if (packs <= 1024) return go(group_norm_kernel<TIO, V, 4, VEC, 256, Z>, 256);
+  if (S < V) return go(group_norm_kernel<TIO, V, 1, false, 8, Z>, 8);
+  if (packs <= 8) return go(group_norm_kernel<TIO, V, 1, true, 8, Z>, 8);
+  if (packs <= 16) return go(group_norm_kernel<TIO, V, 1, true, 16, Z>, 16);
+  if (packs <= 32) return go(group_norm_kernel<TIO, V, 1, true, 32, Z>, 32);
+  if (packs <= 64) return go(group_norm_kernel<TIO, V, 1, true, 64, Z>, 64);
+  if (packs <= 128) return go(group_norm_kernel<TIO, V, 2, true, 64, Z>, 64);
+  if (packs <= 256) return go(group_norm_kernel<TIO, V, 1, true, 256, Z>, 256);
+  if (packs <= 512) return go(group_norm_kernel<TIO, V, 2, true, 256, Z>, 256);
+  if (packs <= 1024) return go(group_norm_kernel<TIO, V, 4, true, 256, Z>, 256);
   constexpr int M = (int)(kGroupNormMaxGroup / 1024 / V);
-  return go(group_norm_kernel<TIO, V, M, VEC, 1024, Z>, 1024);
+  return go(group_norm_kernel<TIO, V, M, true, 1024, Z>, 1024);
 }
 
 template <typename TIO>
@@ -202,13 +209,7 @@ hipError_t launch_io(const GroupNormArgs& args, hipStream_t s) {
   // 79 -> 67, 768 MB 157 -> 152. Smaller ones are better off in it (96 MB 20.8 us,
   // past it 21.6; 19.4 and 21.0 where the inputs lie there already).
   a.stream = a.batch * a.rows * a.C * (int64_t)sizeof(TIO) * (a.z != nullptr ? 3 : 2) > kMemorySideCache / 2;
-  constexpr int V = 16 / sizeof(TIO);
-  auto on = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
-  // 16-byte accesses: groups, row strides and bases in whole packs
-  const bool vec = (a.C / a.G) % V == 0 && on(a.w) && on(a.bias) && a.xs.token % V == 0 && a.xs.batch % V == 0 && on(a.x) && on(a.out) &&
-                   (a.z == nullptr || (a.zs.token % V == 0 && a.zs.batch % V == 0 && on(a.z)));
-  if (a.z != nullptr) return vec ? launch_z<TIO, true, true>(a, s) : launch_z<TIO, false, true>(a, s);
-  return vec ? launch_z<TIO, true, false>(a, s) : launch_z<TIO, false, false>(a, s);
+  return a.z != nullptr ? launch_z<TIO, true>(a, s) : launch_z<TIO, false>(a, s);
 }
 
 }  // namespace

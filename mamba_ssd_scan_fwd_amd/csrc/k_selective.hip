@@ -46,6 +46,8 @@
 // beginning from its own state, so nothing of one sequence meets another.
 #include "selective.h"
 
+#include <cfloat>
+
 namespace ssd {
 namespace {
 
@@ -89,7 +91,7 @@ template <typename T, int V> struct Words {
 
 // Elements at `row` (of the wave) + `off` bytes from p, of which n are there
 // (at least one; the first stands in for the others), in accesses of up to
-// 16 bytes where WHOLE.
+// 16 bytes, at any address, where WHOLE says that all are.
 template <bool WHOLE, typename T, int V>
 __device__ __forceinline__ void load_row(Words<T, V>& r, const T* p, uint64_t row, uint32_t off, int n) {
   using W = Words<T, V>;
@@ -97,7 +99,7 @@ __device__ __forceinline__ void load_row(Words<T, V>& r, const T* p, uint64_t ro
   if constexpr (W::BYTES == 2) {
     r.w[0] = *reinterpret_cast<const uint16_t*>(at);
   } else if constexpr (WHOLE) {
-    r = __builtin_bit_cast(W, *reinterpret_cast<const Pack<float, W::N>*>(at));
+    __builtin_memcpy(&r, at, sizeof(r));
   } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int k = 0; k < V; ++k) r.w[k] = reinterpret_cast<const uint32_t*>(at)[k < n ? k : 0];
@@ -173,6 +175,8 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
   for (int s = 0; s < SPL; ++s) {
     const int n = (s / 4) * 16 + q * 4 + s % 4;
     A2[s] = n < a.N ? a.A[(int64_t)e * a.N + n] * kLog2e : 0.f;
+    // (finite, for the steps of zero behind a run's end)
+    A2[s] = A2[s] < -FLT_MAX ? -FLT_MAX : A2[s];
   }
   const float bias = a.dto.bias != nullptr ? a.dto.bias[e] : 0.f;
   const float Dv = OUT && a.D != nullptr ? a.D[e] : 0.f;
@@ -203,6 +207,8 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
     for (int i = 0; i < SPL / 4; ++i) *ws_at(base, seg, i) = make_float4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
   };
 
+  // whether all of this workgroup's packs of x, dt, z and y, and of B and C, are whole
+  const bool whole_x = a.epg % PK == 0 || ch0 + kChannels <= a.epg, whole_bc = a.N % PER == 0;
   int buf = 0;
   const int wave_slot = __builtin_amdgcn_s_getreg(4 | 0 << 6 | 3 << 11);  // HW_ID: wave of its SIMD
 
@@ -224,18 +230,26 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
     auto fetch = [&](int left) {
       const int bt = btk < left ? btk : left - 1, xt = xtk < left ? xtk : left - 1;
       const int nb = bn0 < a.N ? bn0 : 0, nbn = a.N - nb;
-      auto load = [&](auto whole) {
+      auto load_x = [&](auto whole) {
         constexpr bool W = decltype(whole)::value;
         load_row<W>(dn, db, dr, __umul24(xt, ds) + (uint32_t)(xn0 * sizeof(TDT)), xnn);
         load_row<W>(xn, xb, xr, __umul24(xt, xs) + (uint32_t)(xn0 * sizeof(TIO)), xnn);
-        load_row<W>(bn, Bb, br, __umul24(bt, bs) + (uint32_t)(nb * sizeof(TIO)), nbn);
-        if constexpr (OUT) {
-          load_row<W>(cn, Cb, cr, __umul24(bt, cs) + (uint32_t)(nb * sizeof(TIO)), nbn);
-          load_row<W>(zn, zb, zr, __umul24(xt, zs) + (uint32_t)(xn0 * sizeof(TIO)), xnn);
-        }
+        if constexpr (OUT) load_row<W>(zn, zb, zr, __umul24(xt, zs) + (uint32_t)(xn0 * sizeof(TIO)), xnn);
       };
-      if (a.whole_in) load(std::true_type{});
-      else load(std::false_type{});
+      auto load_bc = [&](auto whole) {
+        constexpr bool W = decltype(whole)::value;
+        load_row<W>(bn, Bb, br, __umul24(bt, bs) + (uint32_t)(nb * sizeof(TIO)), nbn);
+        if constexpr (OUT) load_row<W>(cn, Cb, cr, __umul24(bt, cs) + (uint32_t)(nb * sizeof(TIO)), nbn);
+      };
+      if (whole_x && whole_bc) {
+        load_x(std::true_type{});
+        load_bc(std::true_type{});
+      } else {
+        if (whole_x) load_x(std::true_type{});
+        else load_x(std::false_type{});
+        if (whole_bc) load_bc(std::true_type{});
+        else load_bc(std::false_type{});
+      }
       advance(xr, TT * xs);
       advance(dr, TT * ds);
       advance(br, TT * bs);
@@ -388,8 +402,8 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
         const int yn = a.epg - ch0 - yc0;
         if (ytk < left && yn > 0) {
           RX* to = reinterpret_cast<RX*>(reinterpret_cast<char*>(yb) + yr + (ytk * ys + (uint32_t)((ch0 + yc0) * sizeof(TIO))));
-          if (a.whole_y) {
-            *reinterpret_cast<Pack<TIO, PK>*>(to) = out;
+          if (whole_x) {
+            __builtin_memcpy(to, &out, sizeof(out));
           } else {
 #pragma unroll
             for (int k = 0; k < PK; ++k)
@@ -493,19 +507,7 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
 }
 
 template <typename TIO, typename TDT, int NP>
-hipError_t launch_np(const SelectiveArgs& args, int64_t batch, hipStream_t s) {
-  SelectiveArgs a = args;
-  constexpr int TT = tile_tokens(NP), PER = TT * NP / kThreads, PK = TT * kChannels / kThreads;
-  // whole packs: widths, strides and bases in multiples of them (a pack of
-  // more than 16 bytes is aligned to 16)
-  auto whole = [](const void* p, size_t elem, int v, const Stride& st) {
-    const size_t bytes = v * elem < 16 ? v * elem : 16;
-    return reinterpret_cast<uintptr_t>(p) % bytes == 0 && st.token % v == 0 && st.batch % v == 0;
-  };
-  const bool bc = a.N % PER == 0 && whole(a.B, sizeof(TIO), PER, a.bs) && whole(a.C, sizeof(TIO), PER, a.cs);
-  a.whole_in = bc && a.epg % PK == 0 && whole(a.x, sizeof(TIO), PK, a.xs) && whole(a.dt, sizeof(TDT), PK, a.ds) &&
-              (a.z == nullptr || whole(a.z, sizeof(TIO), PK, a.zs));
-  a.whole_y = a.epg % PK == 0 && whole(a.y, sizeof(TIO), PK, Stride{a.E, a.L * a.E});
+hipError_t launch_np(const SelectiveArgs& a, int64_t batch, hipStream_t s) {
   const unsigned tiles = (unsigned)(a.tiles * (a.E / a.epg));
   const int segments = (a.cut.n + a.cut.pieces - 1) / a.cut.pieces;
   if (segments > 1) {
@@ -541,7 +543,12 @@ SelectiveCut selective_scan_cut(int64_t batch, int64_t L, int64_t E, int64_t G, 
   const int64_t full = 2048;
   const int64_t want = 2 * waves > full ? 1 : full / waves;
   int64_t len = (L + want - 1) / want;
-  if (nseq > 0 && 4 * L / nseq < len) len = 4 * L / nseq;
+  if (nseq > 0) {
+    // a run's start is waited for: about four runs to a segment, as far as
+    // eight times the segments go (they bound the workspace)
+    const int64_t runs = 4 * L / nseq, least = (len + 7) / 8;
+    if (runs < len) len = runs > least ? runs : least;
+  }
   if (len < 64) len = 64;
   if (len >= L) return SelectiveCut{1, L, 1};
   // The first walk needs half the registers of the second, so it has room for

@@ -5,7 +5,7 @@
 //
 // Streaming: the fp32 states are read once and written once, which is nearly
 // all the traffic. Four consecutive states to a lane (one 16-byte access
-// where N allows it), padded N / 4 lanes to a channel; a workgroup keeps its
+// where N is a multiple of 4), padded N / 4 lanes to a channel; a workgroup keeps its
 // channels' A for up to kRows rows of the batch, since A is as large as one
 // row's state and would otherwise double what L2 has to deliver. All rows'
 // loads are issued before the first is used. B and C in one access each took
@@ -38,7 +38,7 @@ __global__ __launch_bounds__(kThreads) void selective_step_kernel(const Selectiv
   const int nn = a.N - n0 < 0 ? 0 : a.N - n0 > 4 ? 4 : a.N - n0;  // states this lane holds
   const int nc = nn > 0 ? n0 : 0;                                 // an address inside the row for the others
 
-  Pack<float, 4> Av = load_pack<float, 4, VEC>(a.A + (int64_t)e * a.N + nc, nn);
+  Pack<float, 4> Av = load_pack<float, 4, !VEC>(a.A + (int64_t)e * a.N + nc, nn);
   const float bias = a.dto.bias != nullptr ? a.dto.bias[e] : 0.f;
   const float Dv = a.D != nullptr ? a.D[e] : 0.f;
 
@@ -57,10 +57,10 @@ __global__ __launch_bounds__(kThreads) void selective_step_kernel(const Selectiv
     if (row0 + k >= a.batch || slot[k] < 0 || slot[k] >= a.nslots) slot[k] = -1;
     const int64_t from = slot[k] < 0 ? 0 : slot[k];
     const float* hp = a.state + (from * a.E + e) * a.N + nc;
-    if (VEC && a.stream) h[k] = load_stream(reinterpret_cast<const Pack<float, 4>*>(hp));
-    else h[k] = load_pack<float, 4, VEC>(hp, nn);
-    bv[k] = load_pack<TIO, 4, VEC>(static_cast<const TIO*>(a.B) + r * a.bs + (int64_t)g * a.N + nc, nn);
-    cv[k] = load_pack<TIO, 4, VEC>(static_cast<const TIO*>(a.C) + r * a.cs + (int64_t)g * a.N + nc, nn);
+    if (VEC && a.stream) h[k] = load_stream<float, 4>(hp);
+    else h[k] = load_pack<float, 4, !VEC>(hp, nn);
+    bv[k] = load_pack<TIO, 4, !VEC>(static_cast<const TIO*>(a.B) + r * a.bs + (int64_t)g * a.N + nc, nn);
+    cv[k] = load_pack<TIO, 4, !VEC>(static_cast<const TIO*>(a.C) + r * a.cs + (int64_t)g * a.N + nc, nn);
     xv[k] = reinterpret_cast<const RX*>(a.x)[r * a.xs + e];
     dv[k] = reinterpret_cast<const typename Elem<TDT>::raw*>(a.dt)[r * a.ds + e];
     zv[k] = reinterpret_cast<const RX*>(zp)[r * zs + e];
@@ -87,8 +87,8 @@ __global__ __launch_bounds__(kThreads) void selective_step_kernel(const Selectiv
     if (slot[k] >= 0 && mine) {
       float* hp = a.state + (slot[k] * a.E + e) * a.N + n0;
       if (nn > 0) {
-        if (VEC && a.stream) store_stream(reinterpret_cast<Pack<float, 4>*>(hp), Pack<float, 4>{{hn[0], hn[1], hn[2], hn[3]}});
-        else store_pack<float, 4, VEC>(hp, hn, nn);
+        if (VEC && a.stream) store_stream<float, 4>(hp, hn);
+        else store_pack<float, 4, !VEC>(hp, hn, nn);
       }
       if (sub == 0) {
         float y = fmaf(Dv, x, p);
@@ -110,10 +110,7 @@ hipError_t launch_np(const SelectiveStepArgs& args, hipStream_t s) {
   // rows down it would cost three layers too (13.8 -> 15.7 us).
   a.stream = a.batch * a.E * a.N * (int64_t)sizeof(float) >= kMemorySideCache / 4;
   const unsigned gx = (unsigned)((a.E + kThreads / (NP / 4) - 1) / (kThreads / (NP / 4)));
-  // whole groups of four states in every row of A, B, C and of the pool
-  auto on = [](const void* p, size_t b) { return reinterpret_cast<uintptr_t>(p) % b == 0; };
-  const bool vec = a.N % 4 == 0 && on(a.A, 16) && on(a.state, 16) && on(a.B, 4 * sizeof(TIO)) &&
-                   on(a.C, 4 * sizeof(TIO)) && a.bs % 4 == 0 && a.cs % 4 == 0;
+  const bool vec = a.N % 4 == 0;  // no lane holds part of four states
   auto go = [&](auto kern, int rows) {
     kern<<<dim3(gx, (unsigned)((a.batch + rows - 1) / rows)), kThreads, 0, s>>>(a);
     return hipGetLastError();

@@ -40,10 +40,7 @@ struct SelectiveArgs {
   float* ends;       // [batch, cut.n, E, padded N]: the pieces' end states
   float* dsums;      // [batch, cut.n, E]: their sums of dt
   float* init_copy;  // as ends: initial states that the final states overwrite, else nullptr
-  // set at launch: channels per group, workgroups per group, and which rows
-  // can be taken in whole packs
-  int epg, tiles;
-  bool whole_in, whole_y;
+  int epg, tiles;    // channels per group, workgroups per group (set at launch)
 };
 // States per channel as the kernels hold them: the next of 16, 32, .. 256.
 inline int selective_padded_states(int64_t N) {
@@ -167,16 +164,18 @@ template <> struct Elem<__hip_bfloat16> {
   static __device__ __forceinline__ uint16_t bits(float v) { return bf16_bits(v); }
 };
 
-// V consecutive elements (a power of two): aligned accesses of up to 16 bytes
-// where VEC, else V of one element.
+// V consecutive elements (a power of two).
 template <typename T, int V> struct alignas(V * sizeof(T) < 16 ? V * sizeof(T) : 16) Pack {
   typename Elem<T>::raw v[V];
 };
-template <typename T, int V, bool VEC>
-__device__ __forceinline__ Pack<T, V> load_pack(const T* p, int n) {  // n: how many are there (VEC: V)
+// A pack from or to memory that is aligned to its elements only, in accesses of
+// up to 16 bytes (the hardware takes them at any address). PART: n of its V
+// elements are there; the first stands in for the others.
+template <typename T, int V, bool PART = false>
+__device__ __forceinline__ Pack<T, V> load_pack(const T* p, int n = V) {
   Pack<T, V> r;
-  if constexpr (VEC) {
-    r = *reinterpret_cast<const Pack<T, V>*>(p);
+  if (!PART || n >= V) {
+    __builtin_memcpy(&r, p, sizeof(r));
   } else {
     using R = typename Elem<T>::raw;
 #pragma unroll
@@ -184,14 +183,14 @@ __device__ __forceinline__ Pack<T, V> load_pack(const T* p, int n) {  // n: how 
   }
   return r;
 }
-template <typename T, int V, bool VEC>
-__device__ __forceinline__ void store_pack(T* p, const float (&f)[V], int n) {
+template <typename T, int V, bool PART = false>
+__device__ __forceinline__ void store_pack(T* p, const float (&f)[V], int n = V) {
   using R = typename Elem<T>::raw;
-  if constexpr (VEC) {
+  if (!PART || n >= V) {
     Pack<T, V> r;
 #pragma unroll
     for (int i = 0; i < V; ++i) r.v[i] = Elem<T>::bits(f[i]);
-    *reinterpret_cast<Pack<T, V>*>(p) = r;
+    __builtin_memcpy(p, &r, sizeof(r));
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -199,16 +198,22 @@ __device__ __forceinline__ void store_pack(T* p, const float (&f)[V], int n) {
   }
 }
 
-// 16-byte packs that are not expected to be read again soon: past the caches.
-template <typename P> __device__ __forceinline__ P load_stream(const P* p) {
-  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-  static_assert(sizeof(P) == 16, "one 16-byte access");
-  return __builtin_bit_cast(P, __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p)));
+// The same for packs that are not expected to be used again soon: past the
+// caches (non-temporal).
+typedef uint32_t u32x4_unaligned __attribute__((ext_vector_type(4), aligned(2)));
+template <typename T, int V> __device__ __forceinline__ Pack<T, V> load_stream(const T* p) {
+  static_assert(sizeof(Pack<T, V>) == 16, "one 16-byte access");
+  const u32x4_unaligned v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_unaligned*>(p));
+  return __builtin_bit_cast(Pack<T, V>, v);
 }
-template <typename P> __device__ __forceinline__ void store_stream(P* p, const P& v) {
-  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-  static_assert(sizeof(P) == 16, "one 16-byte access");
-  __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4*>(p));
+template <typename T, int V> __device__ __forceinline__ void store_stream(T* p, const float (&f)[V]) {
+  Pack<T, V> r;
+  static_assert(sizeof(r) == 16, "one 16-byte access");
+#pragma unroll
+  for (int i = 0; i < V; ++i) r.v[i] = Elem<T>::bits(f[i]);
+  u32x4_unaligned v;
+  __builtin_memcpy(&v, &r, 16);
+  __builtin_nontemporal_store(v, reinterpret_cast<u32x4_unaligned*>(p));
 }
 
 // Offset i of a packed batch, clamped into [0, T].

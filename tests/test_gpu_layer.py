@@ -31,6 +31,9 @@ SCAN = [
     (1, 70, 20, 100, 1, "fp32", "fp32", True, True, True, True, False),
     (1, 67, 12, 256, 2, "bf16", "fp32", True, True, True, True, False),
     (2, 129, 7, 200, 1, "fp32", "fp32", True, True, False, True, True),
+    (1, 100, 203, 16, 1, "bf16", "bf16", True, True, True, True, True),
+    (1, 70, 198, 14, 2, "bf16", "fp32", True, True, True, True, True),
+    (1, 45, 131, 52, 1, "fp32", "fp32", True, True, True, True, True),
 ]
 
 
@@ -224,6 +227,10 @@ def on_device(t):
     (1, 300, 24, 1, "fp32", True, True, False, False),
     (2, 77, 516, 4, "fp32", True, True, True, False),
     (1, 1000, 2048, 4, "bf16", True, True, True, False),
+    (2, 40, 1001, 4, "bf16", True, True, True, True),
+    (1, 90, 11, 3, "bf16", True, True, True, False),
+    (1, 33, 517, 2, "fp32", True, True, True, True),
+    (2, 21, 7, 4, "bf16", True, True, True, True),
 ])
 def test_conv1d_matches_the_definition(b, L, CH, K, io, act, bias, state, views):
     x, w, bv, g = conv_inputs(b, L, CH, K, io, L + CH, views)
@@ -281,7 +288,8 @@ def test_conv1d_gives_what_conv1d_split_gives():
 
 @pytest.mark.parametrize("b,CH,K,io,act,views", [(1, 1, 4, "fp32", True, False), (3, 64, 4, "bf16", True, False),
                                                  (5, 37, 3, "fp32", False, True), (300, 1028, 4, "bf16", True, False),
-                                                 (2, 516, 2, "fp32", True, False), (4, 40, 1, "bf16", True, True)])
+                                                 (2, 516, 2, "fp32", True, False), (4, 40, 1, "bf16", True, True),
+                                                 (70, 1027, 4, "bf16", True, True), (3, 6, 3, "fp32", True, True)])
 def test_conv1d_step_matches_the_definition(b, CH, K, io, act, views):
     x, w, bv, g = conv_inputs(b, 1, CH, K, io, b + CH, views)
     pool = b + 3
@@ -334,6 +342,12 @@ def test_conv1d_step_padding_and_repeated_slots():
     ((70, 24), 3, "bf16", True, False, False, True, False, False),
     ((1001, 8192), 128, "fp32", True, True, False, False, True, False),
     ((64, 96), 96, "fp32", False, True, True, False, True, False),
+    ((9, 3009), 3, "bf16", True, True, True, False, True, True),
+    ((5, 2, 1001), 1, "fp32", True, True, False, False, True, True),
+    ((6, 4999), 1, "bf16", False, True, True, False, True, True),
+    ((40, 9 * 11), 9, "bf16", True, True, False, False, True, True),
+    ((40, 12 * 3), 12, "fp32", True, False, False, True, True, True),
+    ((2, 12345), 1, "bf16", True, True, False, False, True, False),
 ])
 def test_group_norm_matches_the_definition(shape, G, io, center, gate, first, act, weights, views):
     g = torch.Generator().manual_seed(sum(shape))
