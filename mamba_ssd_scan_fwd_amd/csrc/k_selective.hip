@@ -27,8 +27,8 @@
 // a tile and written to LDS before y is stored, so that no wait for a load is
 // also a wait for a store.
 //
-// Measured (8 x 2048 tokens, 4096 channels, 16 states, bf16, gate): 274 us, the
-// vector units busy 85% of the time; 31 instructions a token and wave, of which
+// Measured (8 x 2048 tokens, 4096 channels, 16 states, bf16, gate): 264 us;
+// 31 instructions a token and wave, of which
 // the 20 above are the states' and 9 the step sizes, gates and moves. The
 // arithmetic of the 20 alone takes about 180 us, a copy of the same bytes 100.
 //
@@ -99,7 +99,11 @@ __device__ __forceinline__ void load_row(Words<T, V>& r, const T* p, uint64_t ro
   if constexpr (W::BYTES == 2) {
     r.w[0] = *reinterpret_cast<const uint16_t*>(at);
   } else if constexpr (WHOLE) {
-    __builtin_memcpy(&r, at, sizeof(r));
+    // (a vector, not memcpy: that may keep r in memory, in LDS or scratch)
+    typedef uint32_t Vec __attribute__((ext_vector_type(W::N), aligned(sizeof(T))));
+    const Vec v = *reinterpret_cast<const Vec*>(at);
+#pragma unroll
+    for (int k = 0; k < W::N; ++k) r.w[k] = v[k];
   } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int k = 0; k < V; ++k) r.w[k] = reinterpret_cast<const uint32_t*>(at)[k < n ? k : 0];
@@ -126,8 +130,11 @@ constexpr int tile_tokens(int np) { return np <= 32 ? 32 : np == 64 ? 16 : np ==
 
 // OUT: the walk that writes y and the final states; otherwise the walk that
 // leaves the segments' end states.
+// The first walk's waves: what LDS lets stand on a SIMD (16 states in 16-bit
+// types: 16384 tokens of 4096 channels 453 us in all with the four that the
+// compiler's registers would leave, 433 with five).
 template <typename TIO, typename TDT, int NP, bool OUT>
-__global__ __launch_bounds__(kThreads) void selective_scan_kernel(const SelectiveArgs a) {
+__global__ __launch_bounds__(kThreads, !OUT && NP == 16 && sizeof(TIO) + sizeof(TDT) == 4 ? 5 : 1) void selective_scan_kernel(const SelectiveArgs a) {
   constexpr int SPL = NP / 4;  // states per lane: n = 16 i + 4 q + k
   constexpr int TT = tile_tokens(NP);
   constexpr int GR = TT / 4;   // groups of four tokens per tile
@@ -145,10 +152,18 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
   const int tid = threadIdx.x;
   const int q = tid & 3;
   const int g = blockIdx.x / a.tiles;
-  const int ch0 = (blockIdx.x % a.tiles) * kChannels;
+  // The last workgroup of a group moves back to end with it, so that its packs
+  // are whole too: the channels that it shares with the one before are computed
+  // by both and written by that one alone (8 x 2048 tokens of 4095 channels:
+  // 369 us element by element, 293 moved). Where the final state lies over the
+  // initial one, the shared channels may start from what the other has already
+  // written; nothing of theirs leaves the workgroup.
+  const int ch = (blockIdx.x % a.tiles) * kChannels;
+  const int shared = a.epg >= kChannels && ch + kChannels > a.epg ? ch + kChannels - a.epg : 0;
+  const int ch0 = ch - shared;
   const int cg = ch0 + tid / 4;
-  const bool mine = cg < a.epg;
-  const int e = g * a.epg + (mine ? cg : a.epg - 1);
+  const bool mine = cg < a.epg && tid / 4 >= shared;
+  const int e = g * a.epg + (cg < a.epg ? cg : a.epg - 1);
   const int64_t b = blockIdx.z;
   // the piece of the time axis this workgroup begins with, and its tokens:
   // one piece, or with output a segment of them
@@ -208,15 +223,28 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
   };
 
   // whether all of this workgroup's packs of x, dt, z and y, and of B and C, are whole
-  const bool whole_x = a.epg % PK == 0 || ch0 + kChannels <= a.epg, whole_bc = a.N % PER == 0;
+  const bool whole = (a.epg % PK == 0 || a.epg >= kChannels) && a.N >= PER;
+  if (whole && a.N < NP) {  // what whole packs leave out stays zero
+    for (int i = tid; i < 2 * TT * ROW / 4; i += kThreads) (&bc4[0][0])[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncthreads();
+  }
   int buf = 0;
   const int wave_slot = __builtin_amdgcn_s_getreg(4 | 0 << 6 | 3 << 11);  // HW_ID: wave of its SIMD
 
-  // One run: tokens [r0, r1) of one sequence, h updated over them.
-  auto walk = [&](int64_t r0, int64_t r1) {
+  // One run: tokens [r0, r1) of one sequence, h updated over them. WHOLE: all
+  // packs are whole; MOVED: the workgroup writes its channels from `shared` on.
+  // Each is a walk of its own, not a branch inside of one: where two fetches
+  // meet, the loads are waited for, and a choice at y's store keeps it from
+  // overlapping (8 x 2048 tokens, 4096 channels: 284 us with the fetch chosen
+  // in the walk, 278 with the store, 264 with neither).
+  auto walk_as = [&](auto whole_of, auto moved_of, int64_t r0, int64_t r1) {
+    constexpr bool WHOLE = decltype(whole_of)::value, MOVED = decltype(moved_of)::value;
     // what this thread stages: states bn0.. of token btk, channels xc0.. of
-    // token xtk (the group's first where it has none there)
-    const int btk = tid * PER / NP, bn0 = tid * PER % NP;
+    // token xtk (the group's first where it has none there). WHOLE: a pack of
+    // B or C that reaches behind N moves back to end with it; what two packs
+    // share they both write, alike.
+    const int btk = tid * PER / NP, bp = tid * PER % NP;
+    const int bn0 = WHOLE && bp > a.N - PER ? a.N - PER : bp;
     const int xtk = tid * PK / kChannels, xc0 = tid * PK % kChannels;
     const int there = a.epg - ch0 - xc0;
     const int xn0 = there > 0 ? ch0 + xc0 : 0, xnn = there > 0 ? there : 1;
@@ -230,26 +258,11 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
     auto fetch = [&](int left) {
       const int bt = btk < left ? btk : left - 1, xt = xtk < left ? xtk : left - 1;
       const int nb = bn0 < a.N ? bn0 : 0, nbn = a.N - nb;
-      auto load_x = [&](auto whole) {
-        constexpr bool W = decltype(whole)::value;
-        load_row<W>(dn, db, dr, __umul24(xt, ds) + (uint32_t)(xn0 * sizeof(TDT)), xnn);
-        load_row<W>(xn, xb, xr, __umul24(xt, xs) + (uint32_t)(xn0 * sizeof(TIO)), xnn);
-        if constexpr (OUT) load_row<W>(zn, zb, zr, __umul24(xt, zs) + (uint32_t)(xn0 * sizeof(TIO)), xnn);
-      };
-      auto load_bc = [&](auto whole) {
-        constexpr bool W = decltype(whole)::value;
-        load_row<W>(bn, Bb, br, __umul24(bt, bs) + (uint32_t)(nb * sizeof(TIO)), nbn);
-        if constexpr (OUT) load_row<W>(cn, Cb, cr, __umul24(bt, cs) + (uint32_t)(nb * sizeof(TIO)), nbn);
-      };
-      if (whole_x && whole_bc) {
-        load_x(std::true_type{});
-        load_bc(std::true_type{});
-      } else {
-        if (whole_x) load_x(std::true_type{});
-        else load_x(std::false_type{});
-        if (whole_bc) load_bc(std::true_type{});
-        else load_bc(std::false_type{});
-      }
+      load_row<WHOLE>(dn, db, dr, __umul24(xt, ds) + (uint32_t)(xn0 * sizeof(TDT)), xnn);
+      load_row<WHOLE>(xn, xb, xr, __umul24(xt, xs) + (uint32_t)(xn0 * sizeof(TIO)), xnn);
+      if constexpr (OUT) load_row<WHOLE>(zn, zb, zr, __umul24(xt, zs) + (uint32_t)(xn0 * sizeof(TIO)), xnn);
+      load_row<WHOLE>(bn, Bb, br, __umul24(bt, bs) + (uint32_t)(nb * sizeof(TIO)), nbn);
+      if constexpr (OUT) load_row<WHOLE>(cn, Cb, cr, __umul24(bt, cs) + (uint32_t)(nb * sizeof(TIO)), nbn);
       advance(xr, TT * xs);
       advance(dr, TT * ds);
       advance(br, TT * bs);
@@ -264,7 +277,7 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
       float* dst = reinterpret_cast<float*>(bc4[buf]) + btk * ROW + bn0;
 #pragma unroll
       for (int k = 0; k < PER; ++k) {
-        const bool in = bn0 + k < a.N && btk < left;
+        const bool in = (WHOLE || bn0 + k < a.N) && btk < left;
         dst[k] = in ? bn.f32(k) : 0.f;
         if constexpr (OUT) dst[NP + k] = in ? cn.f32(k) : 0.f;
       }
@@ -276,9 +289,9 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
 
     // NG groups of four tokens from group i0 of the tile on. TAIL: the run may
     // end among them; behind it a step of zero leaves the state as it is.
-    auto groups = [&](auto ng, auto tail, int i0) {
+    auto groups = [&](auto ng, auto tail, auto more, int i0) {
       constexpr int NG = decltype(ng)::value;
-      constexpr bool TAIL = decltype(tail)::value;
+      constexpr bool TAIL = decltype(tail)::value, MORE = decltype(more)::value;
       const int at0 = (4 * i0 + q) * kPitch + tid / 4;
       RX* xq = xl[buf] + at0;
       const RD* dq = dl[buf] + at0;
@@ -361,7 +374,7 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
       for (int s = 0; s < SPL; ++s) asm volatile("" : "+v"(h[s]));
       // the next tile's loads are all that is in flight here; y's stores, below,
       // then have the whole of the next tile to land
-      if (NG == GR && left > TT) stage(left - TT, buf ^ 1);
+      if constexpr (MORE) stage(left - TT, buf ^ 1);
       if constexpr (OUT) {
         if (a.z != nullptr) {
           const RX* zq = zl[buf] + at0;
@@ -374,24 +387,16 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
       }
     };
 
-    fetch(left);
-    buf ^= 1;
-    stage(left, buf);
-    __syncthreads();
-    for (; left > 0; left -= TT) {
+    auto take_turns = [&] {
       // The older of two waves on a SIMD would otherwise run at its own pace
       // and leave the other to finish alone, at half of the SIMD's rate. They
       // take turns instead, by the clock: every 2^15 cycles (8 x 2048 tokens,
-      // 4096 channels: no turns 297 us, a turn a tile 283, 2^15 cycles 276, 2^19
+      // 4096 channels, when it took 276: no turns 297 us, a turn a tile 283, 2^19
       // 295; short runs want them no longer: packed 143, 143, 142, 150 us).
       if (((uint32_t)(__builtin_amdgcn_s_memtime() >> 15) ^ wave_slot) & 1) __builtin_amdgcn_s_setprio(2);
       else __builtin_amdgcn_s_setprio(0);
-      if (left > TT) fetch(left - TT);
-      if (left >= TT) {
-        groups(std::integral_constant<int, GR>{}, std::false_type{}, 0);
-      } else {
-        for (int i = 0; 4 * i < left; ++i) groups(std::integral_constant<int, 1>{}, std::true_type{}, i);
-      }
+    };
+    auto write_y = [&] {
       if constexpr (OUT) {
         // each lane writes PK channels of a token of its wave's 16
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -402,21 +407,49 @@ __global__ __launch_bounds__(kThreads) void selective_scan_kernel(const Selectiv
         const int yn = a.epg - ch0 - yc0;
         if (ytk < left && yn > 0) {
           RX* to = reinterpret_cast<RX*>(reinterpret_cast<char*>(yb) + yr + (ytk * ys + (uint32_t)((ch0 + yc0) * sizeof(TIO))));
-          if (whole_x) {
+          if (WHOLE && (!MOVED || yc0 >= shared)) {
             __builtin_memcpy(to, &out, sizeof(out));
           } else {
 #pragma unroll
             for (int k = 0; k < PK; ++k)
-              if (k < yn) to[k] = out.v[k];
+              if (k < yn && yc0 + k >= shared) to[k] = out.v[k];
           }
         }
         advance(yr, TT * ys);
       }
-      if (left > TT) {
-        __syncthreads();
-        buf ^= 1;
-      }
+    };
+
+    // (the last tile stands by itself: the others fetch and stage without asking)
+    const std::integral_constant<int, GR> tile{};
+    const std::true_type yes{};
+    const std::false_type no{};
+    fetch(left);
+    buf ^= 1;
+    stage(left, buf);
+    __syncthreads();
+    for (; left > TT; left -= TT) {
+      take_turns();
+      fetch(left - TT);
+      groups(tile, no, yes, 0);
+      write_y();
+      __syncthreads();
+      buf ^= 1;
     }
+    take_turns();
+    if (left == TT) {
+      groups(tile, no, no, 0);
+    } else {
+      for (int i = 0; 4 * i < left; ++i) groups(std::integral_constant<int, 1>{}, yes, no, i);
+    }
+    write_y();
+  };
+
+  auto walk = [&](int64_t r0, int64_t r1) {
+    const std::true_type yes{};
+    const std::false_type no{};
+    if (!whole) walk_as(no, no, r0, r1);
+    else if (OUT && shared != 0) walk_as(yes, yes, r0, r1);
+    else walk_as(yes, no, r0, r1);
   };
 
   if constexpr (!OUT) {

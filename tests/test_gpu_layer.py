@@ -113,6 +113,24 @@ def test_selective_scan_state_in_place_and_same_bits(lens):
     assert torch.equal(y, yi) and torch.equal(hT, hi)
 
 
+@pytest.mark.parametrize("E,N,G,io,lens", [
+    (99, 16, 1, "bf16", None), (130, 13, 2, "fp32", None), (127, 30, 1, "bf16", [200, 0, 3, 157]), (81, 70, 1, "fp32", None),
+    (300, 1, 3, "bf16", [1, 1, 358]), (97, 129, 1, "bf16", None)])
+def test_selective_scan_state_in_place_at_odd_channels(E, N, G, io, lens):
+    # the channels behind the last whole 64 share a workgroup with some before
+    # them, which must be written once, from the state as it was
+    s = Selective(1 if lens else 3, 360, E, N, G, io, io, True, True, True, True, True, lens=lens, seed=E)
+    kw, h0, cu = s.to(DEV)
+    note(f"[gpu] selective scan in place E={E} N={N} G={G} {io} lens={lens}")
+    if lens is None:
+        y, hT = ssd.selective_scan(init_state=h0, final_state=h0, **kw)
+    else:
+        y, hT = ssd.selective_scan_varlen(cu_seqlens=cu, init_states=h0, final_states=h0, **kw)
+    yr, yb, hr, hb = s.reference()
+    within(y, yr, yb, "y")
+    within(hT, hr, hb, "final_state")
+
+
 def test_selective_scan_time_major_and_own_workspace():
     s = Selective(3, 100, 64, 16, seed=6)
     kw, h0, _ = s.to(DEV)
