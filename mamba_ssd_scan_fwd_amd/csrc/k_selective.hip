@@ -28,7 +28,7 @@
 // also a wait for a store.
 //
 // Measured (8 x 2048 tokens, 4096 channels, 16 states, bf16, gate): 264 us;
-// 31 instructions a token and wave, of which
+// the vector units busy 86% of the time; 30 instructions a token and wave, of which
 // the 20 above are the states' and 9 the step sizes, gates and moves. The
 // arithmetic of the 20 alone takes about 180 us, a copy of the same bytes 100.
 //
@@ -585,9 +585,9 @@ SelectiveCut selective_scan_cut(int64_t batch, int64_t L, int64_t E, int64_t G, 
   if (len < 64) len = 64;
   if (len >= L) return SelectiveCut{1, L, 1};
   // The first walk needs half the registers of the second, so it has room for
-  // more waves: a quarter of a segment each (16384 tokens of 4096 channels 464
-  // -> 442 us). Packed sequences keep whole segments: every piece may end in
-  // the middle of a run (37 sequences in 8197 tokens 142 -> 154 us).
+  // more waves: a quarter of a segment each (16384 tokens of 4096 channels 462
+  // -> 434 us). Packed sequences keep whole segments: every piece may end in
+  // the middle of a run (37 sequences in 8197 tokens 139 us, in two pieces 150).
   int64_t pieces = nseq > 0 ? 1 : 4;
   int64_t unit = 32 * pieces;  // whole tiles
   len = (len + unit - 1) / unit * unit;
