@@ -152,14 +152,14 @@ __global__ __launch_bounds__(kThreads, !OUT && NP == 16 && sizeof(TIO) + sizeof(
   const int tid = threadIdx.x;
   const int q = tid & 3;
   const int g = blockIdx.x / a.tiles;
-  // The last workgroup of a group moves back to end with it, so that its packs
-  // are whole too: the channels that it shares with the one before are computed
+  // Where a group does not end with a pack, its last workgroup moves back to end
+  // with it, so that its packs are whole too: the channels that it shares with the one before are computed
   // by both and written by that one alone (8 x 2048 tokens of 4095 channels:
   // 369 us element by element, 293 moved). Where the final state lies over the
   // initial one, the shared channels may start from what the other has already
   // written; nothing of theirs leaves the workgroup.
   const int ch = (blockIdx.x % a.tiles) * kChannels;
-  const int shared = a.epg >= kChannels && ch + kChannels > a.epg ? ch + kChannels - a.epg : 0;
+  const int shared = a.epg % PK != 0 && a.epg >= kChannels && ch + kChannels > a.epg ? ch + kChannels - a.epg : 0;
   const int ch0 = ch - shared;
   const int cg = ch0 + tid / 4;
   const bool mine = cg < a.epg && tid / 4 >= shared;
