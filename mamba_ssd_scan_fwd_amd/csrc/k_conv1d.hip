@@ -172,9 +172,9 @@ __global__ __launch_bounds__(kThreads) void conv1d_kernel(const Conv1dArgs a) {
   int64_t row = seq_of(a.cu, a.nseq, a.L, t0), pos = t0;
   while (pos < t1 && row < a.nseq) {
     const int64_t first = seq_offset(a.cu, row, a.L), last = seq_offset(a.cu, row + 1, a.L);
-    if (last > pos && first <= pos) {
-      const int64_t r1 = last < t1 ? last : t1;
-      walk(row, first, pos, r1, last <= t1);
+    int64_t r0, r1;
+    if (next_run(first, last, pos, t1, r0, r1)) {
+      walk(row, first, r0, r1, last <= t1);
       pos = r1;
     }
     ++row;

@@ -461,7 +461,8 @@ __global__ __launch_bounds__(kThreads, !OUT && NP == 16 && sizeof(TIO) + sizeof(
       first = seq_offset(a.cu, row, a.L);
       last = seq_offset(a.cu, row + 1, a.L);
     }
-    if (last <= s1) return;
+    int64_t r0;
+    if (!passing_run(first, last, s0, s1, r0)) return;
     const bool starts = first >= s0;
     if (starts) {
       load_state(a.init, row);
@@ -469,7 +470,7 @@ __global__ __launch_bounds__(kThreads, !OUT && NP == 16 && sizeof(TIO) + sizeof(
     } else {
       load_state(nullptr, 0);
     }
-    walk(starts ? first : s0, s1);
+    walk(r0, s1);
     ws_store(a.ends);
     dsum += quad_xor<1>(dsum);
     dsum += quad_xor<2>(dsum);
@@ -515,10 +516,10 @@ __global__ __launch_bounds__(kThreads, !OUT && NP == 16 && sizeof(TIO) + sizeof(
     for (int64_t pos = s0; pos < s1 && row < rows; ++row) {
       const int64_t first = packed ? seq_offset(a.cu, row, a.L) : 0;
       const int64_t last = packed ? seq_offset(a.cu, row + 1, a.L) : a.L;
-      if (last <= pos || first > pos) continue;
-      const int64_t r1 = last < s1 ? last : s1;
+      int64_t r0, r1;
+      if (!next_run(first, last, pos, s1, r0, r1)) continue;
       if (first < s0) enter(first / a.cut.len); else begin(row, first / a.cut.len, last > s1);
-      walk(pos, r1);
+      walk(r0, r1);
       if (last <= s1 && a.final_state != nullptr) store_state(a.final_state, row);
       pos = r1;
     }

@@ -5,6 +5,7 @@
 
 #include <type_traits>
 
+#include "packed_runs.h"
 #include "ssd_internal.h"
 
 namespace ssd {
