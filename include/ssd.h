@@ -497,8 +497,9 @@ SSD_API ssd_status_t ssd_selective_scan(const ssd_selective_desc_t* desc, const 
 /* The scan over num_seqs packed sequences (desc->batch = 1, seqlen = T): as
  * ssd_forward_varlen, sequence s holds tokens [cu_seqlens[s],
  * cu_seqlens[s+1]), from init_states[s] to final_states[s] ([num_seqs, E, N]).
- * A sequence may be empty: its state is handed on. Tokens behind the last
- * sequence are not read, and their y is left as it was. cu_seqlens is clamped
+ * A sequence may be empty: its state is handed on. Tokens before the first
+ * sequence and behind the last are not read, and their y is left as it was, so
+ * cu_seqlens may be a part of a longer array of offsets. cu_seqlens is clamped
  * into [0, T] on the device. */
 SSD_API ssd_status_t ssd_selective_scan_varlen(const ssd_selective_desc_t* desc, const int32_t* cu_seqlens,
                                                int64_t num_seqs, const void* x, const void* dt, const float* A,
@@ -540,7 +541,7 @@ typedef struct {
 
 /* The convolution over prompts: a batch (cu_seqlens NULL, num_seqs 0), or
  * packed sequences (batch 1; cu_seqlens as for ssd_selective_scan_varlen, the
- * same rules for empty sequences and for tokens behind the last).
+ * same rules for empty sequences and for tokens of none).
  *   x               [batch, L, CH]           strided
  *   weight, bias    [CH, K], [CH]            fp32 (bias nullable)
  *   conv_state_in   [batch or num_seqs, CH, K-1] fp32, nullable: the K-1

@@ -780,7 +780,8 @@ def selective_scan_varlen(x, dt, A, B, C, D=None, z=None, *, cu_seqlens, init_st
     """``selective_scan`` over packed sequences: x, dt, z [1, T, E], B, C
     [1, T, G, N], sequence s being tokens [cu_seqlens[s], cu_seqlens[s+1])
     (int32 device tensor [S+1]). Returns (y, final_states [S, E, N] or None).
-    Where cu_seqlens ends before T, y of the tokens behind it is not written."""
+    Where cu_seqlens begins above 0 or ends before T, y of the tokens before or
+    behind it is not written."""
     return _run("selective_prompts", stream, x, dt, A, B, C, D, z, _offsets(cu_seqlens), init_states, y, final_states,
                 return_final_states, workspace, *_pre(dt_pre))[:2]
 

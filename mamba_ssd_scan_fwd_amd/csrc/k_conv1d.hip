@@ -173,6 +173,7 @@ __global__ __launch_bounds__(kThreads) void conv1d_kernel(const Conv1dArgs a) {
   while (pos < t1 && row < a.nseq) {
     const int64_t first = seq_offset(a.cu, row, a.L), last = seq_offset(a.cu, row + 1, a.L);
     int64_t r0, r1;
+    if (first >= t1) break;
     if (next_run(first, last, pos, t1, r0, r1)) {
       walk(row, first, r0, r1, last <= t1);
       pos = r1;

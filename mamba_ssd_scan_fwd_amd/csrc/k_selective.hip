@@ -517,6 +517,7 @@ __global__ __launch_bounds__(kThreads, !OUT && NP == 16 && sizeof(TIO) + sizeof(
       const int64_t first = packed ? seq_offset(a.cu, row, a.L) : 0;
       const int64_t last = packed ? seq_offset(a.cu, row + 1, a.L) : a.L;
       int64_t r0, r1;
+      if (first >= s1) break;
       if (!next_run(first, last, pos, s1, r0, r1)) continue;
       if (first < s0) enter(first / a.cut.len); else begin(row, first / a.cut.len, last > s1);
       walk(r0, r1);

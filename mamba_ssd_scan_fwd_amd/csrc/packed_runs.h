@@ -17,12 +17,12 @@ constexpr bool passing_run(int64_t first, int64_t last, int64_t s0, int64_t s1, 
   return true;
 }
 
-// The run that continues the piece at pos: tokens r0 to r1.
+// The next run of a piece whose tokens before pos are done: tokens r0 to r1.
+// (It begins behind pos where tokens before the first sequence lie between.)
 constexpr bool next_run(int64_t first, int64_t last, int64_t pos, int64_t s1, int64_t& r0, int64_t& r1) {
-  if (last <= pos || first > pos) return false;
-  r0 = pos;
+  r0 = first > pos ? first : pos;
   r1 = last < s1 ? last : s1;
-  return true;
+  return r0 < r1;
 }
 
 }  // namespace ssd

@@ -118,3 +118,25 @@ def test_right_offsets_give_every_token_its_sequence(runs):
             if begin == max(i for i in range(len(cu)) if cu[i] <= s0):
                 want = {t: r for r in range(len(cu) - 1) for t in range(cu[r], cu[r + 1]) if s0 <= t < s1}
                 assert taken == want, (cu, s0)
+
+
+def test_offsets_may_begin_behind_the_first_token(runs):
+    """A slice of a longer array of offsets: tokens before its first belong to
+    no sequence, all others to theirs."""
+    cases = [(L, n, cu) for L, n, cu in arbitrary() if cu[0] > 0 and list(cu) == sorted(cu) and cu[-1] <= L]
+    assert len(cases) > 50
+    for (L, n, cu), lines in zip(cases, runs(cases)):
+        spans = {}
+        for ln in lines:
+            if ln[0] == "B":
+                key = ln[1:]
+                spans[key] = {}
+            elif ln[0] == "O":
+                spans[key].update({t: ln[1] for t in range(ln[3], ln[4])})
+        for s0 in range(0, L, n):
+            s1 = min(s0 + n, L)
+            # the row that the search gives: the first where every offset lies behind s0
+            begin = max([i for i in range(len(cu)) if cu[i] <= s0], default=0)
+            if begin < len(cu) - 1:
+                want = {t: r for r in range(len(cu) - 1) for t in range(cu[r], cu[r + 1]) if s0 <= t < s1}
+                assert spans[(s0, s1, begin)] == want, (cu, s0)
