@@ -144,13 +144,28 @@ bool truth(PyObject* o) {
   if (v < 0) throw python_error();
   return v != 0;
 }
-void* handle(PyObject* o) { return reinterpret_cast<void*>(static_cast<uintptr_t>(PyLong_AsUnsignedLongLongMask(o))); }
+void* handle(PyObject* o) {
+  const unsigned long long v = PyLong_AsUnsignedLongLongMask(o);
+  if (v == ~0ull && PyErr_Occurred()) throw python_error();
+  return reinterpret_cast<void*>(static_cast<uintptr_t>(v));
+}
 
-// Makes the call without the interpreter's lock and raises for its status.
+// The interpreter's lock, given up while this lives.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+// Makes the call without the interpreter's lock and raises for its status. F
+// is the call of the library and nothing else: what asks Python or a tensor
+// for something (an address, a stream's handle) needs the lock and may throw,
+// so it is taken before.
 template <typename F> void call(const char* where, F&& f) {
-  PyThreadState* st = PyEval_SaveThread();
-  const ssd_status_t status = f();
-  PyEval_RestoreThread(st);
+  ssd_status_t status;
+  {
+    Unlocked unlocked;
+    status = f();
+  }
   if (status == SSD_OK) return;
   PyObject* e = PyObject_CallFunction(lib.error, "is", (int)status, where);
   if (e != nullptr) {
@@ -250,18 +265,18 @@ PyObject* selective_prompts(PyObject*, PyObject* const* a, Py_ssize_t n) {
   } else if (need > 0) {
     workspace = at::empty({(int64_t)need}, x.options().dtype(at::kByte));
   }
+  const void *xp = x.data_ptr(), *dt = data(a[1]), *B = data(a[3]), *C = data(a[4]), *z = data(a[6]);
+  void *yp = y.data_ptr(), *stream = handle(a[16]);
   void* ws = workspace.defined() ? workspace.data_ptr() : nullptr;
   const size_t ws_bytes = workspace.defined() ? workspace.nbytes() : 0;
   float* fin = final_state.defined() ? final_state.data_ptr<float>() : nullptr;
   if (S > 0)
     call("ssd_selective_scan_varlen", [&] {
-      return lib.scan_varlen(&d, cu, S, x.data_ptr(), data(a[1]), A, data(a[3]), data(a[4]), D, data(a[6]), init,
-                             y.data_ptr(), fin, ws, ws_bytes, handle(a[16]));
+      return lib.scan_varlen(&d, cu, S, xp, dt, A, B, C, D, z, init, yp, fin, ws, ws_bytes, stream);
     });
   else
     call("ssd_selective_scan", [&] {
-      return lib.scan(&d, x.data_ptr(), data(a[1]), A, data(a[3]), data(a[4]), D, data(a[6]), init, y.data_ptr(), fin,
-                      ws, ws_bytes, handle(a[16]));
+      return lib.scan(&d, xp, dt, A, B, C, D, z, init, yp, fin, ws, ws_bytes, stream);
     });
   PyObject* r = PyTuple_New(3);
   if (r == nullptr) throw python_error();
@@ -287,10 +302,9 @@ PyObject* selective_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   float* state = static_cast<float*>(dense(a[7], "state", at::kFloat, dev, {slots, d.channels, d.dstate}));
   const int32_t* map = static_cast<const int32_t*>(dense(a[8], "state_slots", at::kInt, dev, {d.batch}));
   Tensor y = output(a[9], "y", x.scalar_type(), x, x.sizes());
-  call("ssd_selective_step", [&] {
-    return lib.step(&d, x.data_ptr(), data(a[1]), A, data(a[3]), data(a[4]), D, data(a[6]), state, map, slots,
-                    y.data_ptr(), handle(a[13]));
-  });
+  const void *xp = x.data_ptr(), *dt = data(a[1]), *B = data(a[3]), *C = data(a[4]), *z = data(a[6]);
+  void *yp = y.data_ptr(), *stream = handle(a[13]);
+  call("ssd_selective_step", [&] { return lib.step(&d, xp, dt, A, B, C, D, z, state, map, slots, yp, stream); });
   return THPVariable_Wrap(y);
   END_HANDLE_TH_ERRORS
 }
@@ -303,7 +317,7 @@ struct Conv {
   const float *w, *bias;
   Tensor out[3];
   int outs;
-  void* ptr(int i) const { return i < outs ? out[i].data_ptr() : nullptr; }
+  void* ptr[3];  // their addresses, null for none
   PyObject* wrap() const {
     if (outs == 1) return THPVariable_Wrap(out[0]);
     PyObject* r = PyTuple_New(3);
@@ -331,6 +345,7 @@ Conv conv_of(const Tensor& x, PyObject* weight, PyObject* bias, PyObject* split,
     c.outs = 1;
     c.d.out_channels[0] = CH;
     c.out[0] = output(y, "y", x.scalar_type(), x, shape);
+    c.ptr[0] = c.out[0].data_ptr();
     return c;
   }
   int64_t h[4];
@@ -346,6 +361,7 @@ Conv conv_of(const Tensor& x, PyObject* weight, PyObject* bias, PyObject* split,
     s.push_back(h[i == 0 ? 1 : 3]);
     c.d.out_channels[i] = s[lead] * s[lead + 1];
     c.out[i] = at::empty(s, x.options());
+    c.ptr[i] = c.out[i].data_ptr();
   }
   return c;
 }
@@ -363,8 +379,10 @@ PyObject* conv_prompts(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t states[] = {S > 0 ? S : c.d.batch, c.d.channels, (int64_t)THPVariable_Unpack(a[1]).size(1) - 1};
   const float* in = floats(a[6], S > 0 ? "conv_states_in" : "conv_state_in", dev, states);
   float* last = const_cast<float*>(floats(a[7], S > 0 ? "conv_states_out" : "conv_state_out", dev, states));
+  const void* xp = x.data_ptr();
+  void* stream = handle(a[9]);
   call("ssd_conv1d", [&] {
-    return lib.conv(&c.d, cu, S, x.data_ptr(), c.w, c.bias, in, last, c.ptr(0), c.ptr(1), c.ptr(2), handle(a[9]));
+    return lib.conv(&c.d, cu, S, xp, c.w, c.bias, in, last, c.ptr[0], c.ptr[1], c.ptr[2], stream);
   });
   return c.wrap();
   END_HANDLE_TH_ERRORS
@@ -381,8 +399,10 @@ PyObject* conv_token(PyObject*, PyObject* const* a, Py_ssize_t n) {
   float* state = static_cast<float*>(dense(a[5], "conv_state", at::kFloat, dev,
                                            {slots, c.d.channels, (int64_t)THPVariable_Unpack(a[1]).size(1) - 1}));
   const int32_t* map = static_cast<const int32_t*>(dense(a[6], "state_slots", at::kInt, dev, {c.d.batch}));
+  const void* xp = x.data_ptr();
+  void* stream = handle(a[8]);
   call("ssd_conv1d_step", [&] {
-    return lib.conv_step(&c.d, x.data_ptr(), c.w, c.bias, state, map, slots, c.ptr(0), c.ptr(1), c.ptr(2), handle(a[8]));
+    return lib.conv_step(&c.d, xp, c.w, c.bias, state, map, slots, c.ptr[0], c.ptr[1], c.ptr[2], stream);
   });
   return c.wrap();
   END_HANDLE_TH_ERRORS
@@ -392,8 +412,8 @@ PyObject* conv_token(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* group_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   need_args(n, 11);
-  const Tensor* xp = tensor(a[0], "x");
-  if (xp != nullptr && (xp->dim() < 1 || xp->dim() > 3)) bad_value("x must have 1 to 3 dimensions");
+  const Tensor* given = tensor(a[0], "x");
+  if (given != nullptr && (given->dim() < 1 || given->dim() > 3)) bad_value("x must have 1 to 3 dimensions");
   const Tensor& x = device_tensor(a[0], "x", -1);
   const auto dev = x.device();
   const Tensor* z = tensor(a[3], "z");
@@ -416,7 +436,9 @@ PyObject* group_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const float* w = floats(a[1], "weight", dev, {d.channels});
   const float* bias = floats(a[2], "bias", dev, {d.channels});
   Tensor out = output(a[9], "out", x.scalar_type(), x, x.sizes());
-  call("ssd_group_norm", [&] { return lib.norm(&d, x.data_ptr(), w, bias, data(a[3]), out.data_ptr(), handle(a[10])); });
+  const void *xp = x.data_ptr(), *zp = data(a[3]);
+  void *op = out.data_ptr(), *stream = handle(a[10]);
+  call("ssd_group_norm", [&] { return lib.norm(&d, xp, w, bias, zp, op, stream); });
   return THPVariable_Wrap(out);
   END_HANDLE_TH_ERRORS
 }
