@@ -30,8 +30,8 @@ size_t bytes_of(int io) { return io == kBF16 ? 2 : 4; }
 bool resolve(const ssd_stride_t& s, int64_t batch, int64_t rows, int64_t width, Stride* out, int64_t* extent) {
   Stride r{s.token, s.batch};
   if (r.token == 0) r.token = width;
-  if (r.batch == 0) r.batch = rows * r.token;
   if (r.token < width || r.token > kMaxTokenStride) return false;
+  if (r.batch == 0) r.batch = rows * r.token;  // below 2^53
   if (r.batch < width || r.batch > kMaxElems) return false;
   if (rows - 1 > kMaxElems / r.token || batch - 1 > kMaxElems / r.batch) return false;
   *extent = (batch - 1) * r.batch + (rows - 1) * r.token + width;

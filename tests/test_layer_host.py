@@ -308,3 +308,15 @@ def test_structs_are_as_long_as_the_headers():
     assert ctypes.sizeof(SelectiveDesc) == 40 + 8 + 8 + 8 + 8 + 80
     assert ctypes.sizeof(Conv1dDesc) == 48 + 16 + 16
     assert ctypes.sizeof(GroupNormDesc) == 32 + 16 + 8 + 32
+
+
+@pytest.mark.parametrize("token,batch", [(1 << 62, 0), ((1 << 63) - 1, 0), (1 << 57, 0), (-(1 << 63), 0), (1 << 62, 1 << 62),
+                                         (0, (1 << 63) - 1), (0, -(1 << 63)), (64, 1 << 62)])
+def test_strides_of_any_size_are_refused_without_overflow(token, batch):
+    # (products of what is refused must not overflow either: the sanitized
+    # build of build.py ends the test there)
+    s = Stride(token, batch)
+    assert scan(sel(x_stride=s)) == SHAPE and scan(sel(B_stride=s)) == SHAPE
+    assert step(sel(seqlen=1, z_stride=s)) == SHAPE
+    assert conv_call(conv(x_stride=s)) == SHAPE and conv_step(conv(seqlen=1, x_stride=s)) == SHAPE
+    assert norm_call(norm(z_stride=s)) == SHAPE
