@@ -26,8 +26,10 @@ bool io_of(int32_t dtype, int* io) {
 size_t bytes_of(int io) { return io == kBF16 ? 2 : 4; }
 
 // Strides of [batch, rows, width]: dense where they are given as 0. False
-// where rows overlap their neighbours or the extent leaves the limits.
+// where rows overlap their neighbours, or the extent or the dense size (an
+// output's) leaves the limits.
 bool resolve(const ssd_stride_t& s, int64_t batch, int64_t rows, int64_t width, Stride* out, int64_t* extent) {
+  if (rows > kMaxElems / width || batch > kMaxElems / (rows * width)) return false;
   Stride r{s.token, s.batch};
   if (r.token == 0) r.token = width;
   if (r.token < width || r.token > kMaxTokenStride) return false;

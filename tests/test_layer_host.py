@@ -320,3 +320,15 @@ def test_strides_of_any_size_are_refused_without_overflow(token, batch):
     assert step(sel(seqlen=1, z_stride=s)) == SHAPE
     assert conv_call(conv(x_stride=s)) == SHAPE and conv_step(conv(seqlen=1, x_stride=s)) == SHAPE
     assert norm_call(norm(z_stride=s)) == SHAPE
+
+
+def test_outputs_of_any_size_are_refused_without_overflow():
+    # rows that lie over one another make a small input of any number of rows;
+    # the dense output of as many does not fit (64 x 2^16 x 2^31 and more)
+    s, n = Stride(1 << 20, 1 << 20), (1 << 31) - 1
+    assert scan(sel(batch=65535, seqlen=n, channels=1 << 20, ngroups=1, x_stride=s, dt_stride=s, z_stride=s,
+                    B_stride=Stride(16, 16), C_stride=Stride(16, 16))) == SHAPE
+    assert conv_call(conv(batch=65535, seqlen=n, channels=1 << 20, out_channels=(1 << 20, 0, 0), x_stride=s)) == SHAPE
+    few = Stride(4, 4)
+    assert norm_call(norm(batch=n, rows=n, channels=4, ngroups=1, x_stride=few, z_stride=few)) == SHAPE
+    assert norm_call(norm(batch=1 << 20, rows=1 << 20, channels=4, ngroups=1, x_stride=few, z_stride=few)) == SHAPE
