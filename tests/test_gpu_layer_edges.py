@@ -7,7 +7,8 @@ import pytest
 import torch
 
 import mamba_ssd_scan_fwd_amd as ssd
-from layer_testutil import Selective, conv_reference, within
+from layer_testutil import IO, Selective, conv_reference, norm_bound, within
+from oracle import layer_oracle as ref
 from ssd_testutil import note, np64
 
 pytestmark = pytest.mark.gpu
@@ -65,3 +66,152 @@ def test_offsets_that_begin_behind_the_first_token(cu, L, io):
     within(y[:, cu[0]:cu[-1]], want[:, cu[0]:cu[-1]], bound[:, cu[0]:cu[-1]], "conv")
     assert np.array_equal(np64(last), end)
     assert (y[:, :cu[0]] == 7.0).all() and (y[:, cu[-1]:] == 7.0).all()
+
+
+# ---- kernels that only large calls reach -------------------------------------------
+# (sizes just past the rules at the launches: several rows a workgroup, memory-side
+# cache passed by, long tiles)
+
+
+def first_rows(slots, pool):
+    """Rows that have their slot, and the others."""
+    first = {}
+    for r, k in enumerate(slots):
+        if 0 <= k < pool:
+            first.setdefault(k, r)
+    rows = sorted(first.values())
+    return rows, [r for r in range(len(slots)) if r not in set(rows)]
+
+
+def some_slots(b, pool, seed):
+    """A permutation with padding, and with slots named again in the same four
+    rows, the same two, the next ones and far behind."""
+    slots = torch.randperm(pool, generator=torch.Generator().manual_seed(seed))[:b].tolist()
+    slots[1], slots[6], slots[10], slots[11], slots[13], slots[b - 1] = slots[0], slots[4], slots[9], slots[9], slots[11], slots[2]
+    slots[17], slots[20], slots[21] = -1, pool, -1
+    return slots
+
+
+@pytest.mark.parametrize("b,E,N,io,shift", [(67, 8192, 16, "bf16", 0), (131, 8192, 16, "bf16", 0), (70, 4096, 64, "fp32", 1),
+                                            (36, 8192, 20, "bf16", 3), (401, 2050, 24, "bf16", 1)])
+def test_selective_step_of_many_rows(b, E, N, io, shift):
+    """Four rows a workgroup (from 8192 workgroups of one row on), the last
+    four incomplete; from 64 MiB of states on past the cache; the pool at any
+    element."""
+    pool = b + 9
+    slots = some_slots(b, pool, b)
+    s = Selective(b, 1, E, N, io=io, dt=io, init=False, views=True, seed=b)
+    kw, _, _ = s.to(DEV)
+    one = {k: (v[:, 0] if k in ("x", "dt", "z", "B", "C") else v) for k, v in kw.items()}
+    before = torch.randn((pool, E, N), generator=torch.Generator().manual_seed(b + 1))
+    state = torch.empty(pool * E * N + shift, device=DEV)[shift:].view(pool, E, N).copy_(before)
+    y = torch.full((b, E), 3.0, dtype=s.io, device=DEV)
+    note(f"[gpu] selective step of {b} rows, E={E} N={N} {io}")
+    ssd.selective_step(state=state, y=y, state_slots=torch.tensor(slots, dtype=torch.int32, device=DEV), **one)
+    rows, dead = first_rows(slots, pool)
+    assert len(dead) >= 8
+    s.init = torch.zeros((b, E, N))
+    s.init[rows] = before[[slots[r] for r in rows]]
+    yr, yb, hr, hb = s.reference()
+    within(y[rows], yr[rows, 0], yb[rows, 0], "y")
+    assert (y[dead] == 3.0).all()
+    within(state[[slots[r] for r in rows]], hr[rows], hb[rows], "state")
+    rest = sorted(set(range(pool)) - {slots[r] for r in rows})
+    assert torch.equal(state[rest].cpu(), before[rest])
+
+
+@pytest.mark.parametrize("b,CH,K,io,shift", [(257, 8192, 4, "bf16", 0), (411, 4100, 3, "fp32", 1), (2049, 512, 2, "bf16", 3)])
+def test_conv1d_step_of_many_rows(b, CH, K, io, shift):
+    """Two rows a workgroup, the last pair incomplete."""
+    pool = b + 9
+    slots = some_slots(b, pool, b)
+    g = torch.Generator().manual_seed(b + 2)
+    x = torch.randn((b, CH + 5), generator=g).to(IO[io])[:, 3:CH + 3]
+    w, bias = torch.randn((CH, K), generator=g) * K ** -0.5, torch.randn(CH, generator=g) * 0.3
+    before = torch.randn((pool, CH, K - 1), generator=g)
+    state = torch.empty(pool * CH * (K - 1) + shift, device=DEV)[shift:].view(pool, CH, K - 1).copy_(before)
+    y = torch.full((b, CH), 3.0, dtype=IO[io], device=DEV)
+    note(f"[gpu] conv1d step of {b} rows, CH={CH} K={K} {io}")
+    ssd.conv1d_step(x._base.to(DEV)[:, 3:CH + 3], w.to(DEV), bias.to(DEV), state, y=y,
+                    state_slots=torch.tensor(slots, dtype=torch.int32, device=DEV))
+    rows, dead = first_rows(slots, pool)
+    at = [slots[r] for r in rows]
+    want, bound, last = conv_reference(np64(x[rows])[:, None], np64(w), np64(bias), True, np64(before[at]),
+                                       [(i, 0, 1) for i in range(len(rows))], IO[io])
+    within(y[rows], want[:, 0], bound[:, 0], "y")
+    assert (y[dead] == 3.0).all()
+    expect = np64(before)
+    expect[at] = last
+    assert np.array_equal(np64(state), expect)
+
+
+@pytest.mark.parametrize("b,L,CH,K,io", [(2, 4500, 4099, 4, "bf16"), (2, 8200, 4099, 4, "bf16"), (1, 9001, 2049, 3, "fp32"),
+                                         (3, 2900, 8192, 2, "bf16"), (1, 33000, 1030, 4, "bf16")])
+def test_conv1d_of_large_inputs(b, L, CH, K, io):
+    """Outputs of 64 to 256 MiB: inputs past the cache, tiles of 32 and 64
+    tokens. Windows against the definition, everything against short calls."""
+    g = torch.Generator(device=DEV).manual_seed(L)
+    x = torch.randn((b, L, CH + 5), generator=g, device=DEV).to(IO[io])[:, :, 3:CH + 3]
+    w, bias = torch.randn((CH, K), generator=g, device=DEV) * K ** -0.5, torch.randn(CH, generator=g, device=DEV) * 0.3
+    s0 = torch.randn((b, CH, K - 1), generator=g, device=DEV)
+    size = b * L * CH * x.element_size()
+    assert 64 << 20 <= size < 256 << 20
+    note(f"[gpu] conv1d b={b} L={L} CH={CH} K={K} {io}")
+    last = torch.empty_like(s0)
+    y = ssd.conv1d(x, w, bias, conv_state_in=s0, conv_state_out=last)
+    line = torch.cat([s0.transpose(1, 2), x.float()], 1)  # token t at t + K - 1
+    assert torch.equal(last, line[:, L:].transpose(1, 2))
+    for a in list(range(0, L, 999)) + [L - 130]:
+        z = min(a + 999, L)
+        part = ssd.conv1d(x[:, a:z], w, bias, conv_state_in=line[:, a:a + K - 1].transpose(1, 2).contiguous())
+        assert torch.equal(y[:, a:z], part), a
+    for a, z in ((0, 70), (L // 2, L // 2 + 70), (L - 70, L)):
+        want, bound, _ = conv_reference(np64(x[:, a:z]), np64(w), np64(bias), True,
+                                        np64(line[:, a:a + K - 1].transpose(1, 2)), [(i, 0, z - a) for i in range(b)], IO[io])
+        within(y[:, a:z], want, bound, f"y from {a}")
+
+
+@pytest.mark.parametrize("T", [33000, 66000, 132000])
+def test_conv1d_packed_in_long_tiles(T):
+    """Tiles of 16, 32 and 64 tokens with sequences that end inside them."""
+    CH, K, S = 64, 4, 700
+    g = torch.Generator().manual_seed(T)
+    cu = torch.cat([torch.zeros(1, dtype=torch.long), torch.randint(0, T - 50, (S - 1,), generator=g).sort()[0],
+                    torch.tensor([T - 9])])
+    cu[101], cu[103], cu[301:305] = cu[100], cu[102] + 1, cu[300]
+    cu = cu.sort()[0]
+    x, w = torch.randn((1, T, CH), generator=g).to(torch.bfloat16), torch.randn((CH, K), generator=g)
+    s0 = torch.randn((S, CH, K - 1), generator=g)
+    y = torch.full((1, T, CH), 7.0, dtype=torch.bfloat16, device=DEV)
+    last = torch.empty((S, CH, K - 1), device=DEV)
+    note(f"[gpu] conv1d packed, {T} tokens")
+    ssd.conv1d_varlen(x.to(DEV), w.to(DEV), cu_seqlens=cu.int().to(DEV), conv_states_in=s0.to(DEV), conv_states_out=last, y=y)
+    spans = [(0, a, b) for a, b in zip(cu.tolist(), cu.tolist()[1:])]
+    want, bound, end = conv_reference(np64(x), np64(w), None, True, np64(s0), spans, torch.bfloat16)
+    within(y[:, :T - 9], want[:, :T - 9], bound[:, :T - 9], "y")
+    assert (y[:, T - 9:] == 7.0).all()
+    assert np.array_equal(np64(last), end)
+
+
+@pytest.mark.parametrize("R,C,G,io,gate,first,center", [
+    (6000, 4101, 3, "bf16", True, True, False), (4000, 5001, 1, "fp32", False, False, True), (3000, 9001, 1, "bf16", True, False, True),
+    (2900, 4097, 1, "fp32", True, True, True), (21000, 2050, 205, "bf16", True, False, False)])
+def test_group_norm_of_large_inputs(R, C, G, io, gate, first, center):
+    """More than 128 MiB: inputs past the cache, groups that end inside a
+    pack. Some rows against the definition, all against short calls."""
+    g = torch.Generator(device=DEV).manual_seed(R)
+    x = torch.randn((R, C + 3), generator=g, device=DEV).to(IO[io])[:, 1:C + 1]
+    z = torch.randn((R, C + 3), generator=g, device=DEV).to(IO[io])[:, 2:C + 2] if gate else None
+    w, bias = 1 + 0.3 * torch.randn(C, generator=g, device=DEV), 0.3 * torch.randn(C, generator=g, device=DEV)
+    assert R * C * x.element_size() * (3 if gate else 2) > 128 << 20
+    kw = dict(ngroups=G, center=center, gate_first=first)
+    note(f"[gpu] group norm {R} x {C} G={G} {io}")
+    o = ssd.group_norm(x, w, bias, z, **kw)
+    for a in range(0, R, 511):
+        part = ssd.group_norm(x[a:a + 511], w, bias, None if z is None else z[a:a + 511], **kw)
+        assert torch.equal(o[a:a + 511], part), a
+    rows = [0, 1, 2, R // 2, R - 3, R - 2, R - 1]
+    pick = lambda t: None if t is None else np64(t[rows])  # noqa: E731
+    want = ref.group_norm(pick(x), G, 1e-5, np64(w), np64(bias), pick(z), center, first, False)
+    bound = norm_bound(pick(x), G, 1e-5, np64(w), np64(bias), pick(z), center, first, False, IO[io], want)
+    within(o[rows], want, bound, "out")
