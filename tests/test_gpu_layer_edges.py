@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import mamba_ssd_scan_fwd_amd as ssd
-from layer_testutil import IO, Selective, conv_reference, norm_bound, within
+from layer_testutil import IO, Selective, U, conv_reference, norm_bound, within
 from oracle import layer_oracle as ref
 from ssd_testutil import note, np64
 
@@ -215,3 +215,55 @@ def test_group_norm_of_large_inputs(R, C, G, io, gate, first, center):
     want = ref.group_norm(pick(x), G, 1e-5, np64(w), np64(bias), pick(z), center, first, False)
     bound = norm_bound(pick(x), G, 1e-5, np64(w), np64(bias), pick(z), center, first, False, IO[io], want)
     within(o[rows], want, bound, "out")
+
+
+# ---- streams ------------------------------------------------------------------------
+
+
+def test_group_norm_of_a_constant_row():
+    x = torch.full((3, 256), 3.0, device=DEV)
+    x[1], x[2] = -3.0, 0.0
+    note("[gpu] group norm of constant rows")
+    o = np64(ssd.group_norm(x, center=False))
+    want = 3.0 / np.sqrt(9.0 + 1e-5)
+    assert np.abs(o[0] - want).max() <= 6 * U * want and np.abs(o[1] + want).max() <= 6 * U * want
+    assert np.all(o[2] == 0.0)
+
+
+def same_block(t):
+    """Whether the allocator gives a freed block of t's size out again at once."""
+    a = torch.empty_like(t)
+    at = a.data_ptr()
+    del a
+    return torch.empty_like(t).data_ptr() == at
+
+
+def test_memory_of_a_call_on_another_stream_is_kept_until_it_ran():
+    """The call waits behind a sleep on its stream; its inputs are dropped, and
+    blocks of their sizes overwritten on the caller's stream, before it runs.
+    Then its output is read behind a sleep on the caller's stream and dropped,
+    and blocks of its size overwritten on the other."""
+    s = Selective(1, 2000, 64, 16, seed=34)
+    kw, h0, _ = s.to(DEV)
+    want, hT = ssd.selective_scan(init_state=h0, **kw)
+    names = ("x", "dt", "z", "B", "C")
+    note("[gpu] selective scan: memory in use on two streams")
+    here, side = torch.cuda.current_stream(), torch.cuda.Stream()
+    held = torch.empty_like(kw["x"])
+    assert same_block(held)
+    mine = dict(kw, **{k: kw[k].clone() for k in names})
+    start = h0.clone()
+    side.wait_stream(here)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    y, h = ssd.selective_scan(init_state=start, stream=side, **mine)
+    del mine, start
+    junk = [torch.full_like(kw[k], float("nan")) for k in names for _ in range(2)] + [torch.full_like(h0, float("nan"))]
+    here.wait_stream(side)
+    torch.cuda._sleep(20_000_000)
+    kept, keph = y.clone(), h.clone()
+    del y, h
+    with torch.cuda.stream(side):
+        junk += [torch.full_like(want, float("nan")) for _ in range(3)] + [torch.full_like(hT, float("nan")) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert torch.equal(kept, want) and torch.equal(keph, hT)
