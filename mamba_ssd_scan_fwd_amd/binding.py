@@ -731,6 +731,8 @@ def _run(name, stream, *args):
     dev = args[0].device
     if dev.index is None:
         return fn(*args, 0)  # a host tensor: refused there
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, expected {dev}")
     if stream is None and dev.index == torch.cuda.current_device():
         return fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     with _On(dev, stream):

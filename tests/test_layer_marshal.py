@@ -83,3 +83,27 @@ print("alive", sum(range(10)))
 """)
     lines = out.splitlines()
     assert len([ln for ln in lines if ln.startswith("raised")]) == 6 and lines[-1] == "alive 45"
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    """(It would be launched on with the wrong device current.)"""
+    import torch
+
+    from mamba_ssd_scan_fwd_amd import binding
+
+    class Marshal:
+        def __getattr__(self, name):
+            return lambda *a: pytest.fail("called")
+
+    class Part:
+        def __init__(self, index):
+            self.device = torch.device("cuda", index)
+
+    monkeypatch.setattr(binding, "_marshal", Marshal)
+    monkeypatch.setattr(binding, "_On", lambda *a: pytest.fail("switched"))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    for x, stream in ((0, 1), (1, 0)):
+        with pytest.raises(ValueError, match="stream is on cuda:%d, expected cuda:%d" % (stream, x)):
+            binding.group_norm(Part(x), stream=Part(stream))
+        with pytest.raises(ValueError, match="stream"):
+            binding.selective_scan(Part(x), None, None, None, None, stream=Part(stream))
