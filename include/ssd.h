@@ -450,7 +450,8 @@ typedef struct {
  *     d_t       = pre(dt_t[e])
  *     h_t[e,n]  = exp(d_t A[e,n]) h_{t-1}[e,n] + d_t x_t[e] B_t[g,n]
  *     y_t[e]    = (sum_n h_t[e,n] C_t[g,n] + D[e] x_t[e]) * silu(z_t[e])
- * with pre() the bias, softplus and clamp of ssd_desc_t, h_{-1} the initial
+ * with pre() the bias, softplus and clamp of ssd_desc_t (except that a NaN stays
+ * NaN behind the clamp, where ssd_desc_t's gives dt_min), h_{-1} the initial
  * state (zeros when NULL), and the D and gate factors left out when D or z is
  * NULL. States, sums and decays are fp32; y is rounded once.
  *     x, z       [batch, L, E]     io dtype, strided (z nullable)

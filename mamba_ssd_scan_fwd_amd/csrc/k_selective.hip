@@ -307,7 +307,7 @@ __global__ __launch_bounds__(kThreads, !OUT && NP == 16 && sizeof(TIO) + sizeof(
       }
       if (a.dto.clamp) {
 #pragma unroll
-        for (int i = 0; i < NG; ++i) dv[i] = fminf(fmaxf(dv[i], a.dto.lo), a.dto.hi);
+        for (int i = 0; i < NG; ++i) dv[i] = clamped(dv[i], a.dto.lo, a.dto.hi);
       }
       if constexpr (TAIL) {
 #pragma unroll

@@ -140,10 +140,15 @@ __device__ __forceinline__ float softplus_f32(float v) {
   const float r = fmaf(__builtin_amdgcn_logf(w), 0.69314718055994530942f, c * __builtin_amdgcn_rcpf(w));
   return v > 20.f ? v : r;
 }
+// v within [lo, hi]; a NaN stays one (fminf and fmaxf would make it lo).
+__device__ __forceinline__ float clamped(float v, float lo, float hi) {
+  v = v < lo ? lo : v;
+  return v > hi ? hi : v;
+}
 __device__ __forceinline__ float step_size(float v, float bias, const DtOpts& o) {
   v += bias;
   if (o.softplus) v = softplus_f32(v);
-  if (o.clamp) v = fminf(fmaxf(v, o.lo), o.hi);
+  if (o.clamp) v = clamped(v, o.lo, o.hi);
   return v;
 }
 

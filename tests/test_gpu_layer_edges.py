@@ -267,3 +267,37 @@ def test_memory_of_a_call_on_another_stream_is_kept_until_it_ran():
         junk += [torch.full_like(want, float("nan")) for _ in range(3)] + [torch.full_like(hT, float("nan")) for _ in range(3)]
     torch.cuda.synchronize()
     assert torch.equal(kept, want) and torch.equal(keph, hT)
+
+
+# ---- unusual values --------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("io,L", [("fp32", 50), ("bf16", 300)])
+def test_a_step_size_of_nan_is_not_clamped_away(io, L):
+    """dt is clamped to its limits, infinities too; a NaN stays NaN and takes
+    its channel from its token on, and no other."""
+    s = Selective(1, L, 70, 16, io=io, dt=io, gate=False, seed=49)
+    kw, h0, _ = s.to(DEV)
+    want, hw = ssd.selective_scan(init_state=h0, **kw)
+    note(f"[gpu] selective scan and step: NaN step sizes, {io}")
+    t, e = L - 11, 33
+    dt = kw["dt"].clone()
+    dt[0, t, e] = float("nan")
+    y, h = ssd.selective_scan(init_state=h0, **dict(kw, dt=dt))
+    assert torch.isnan(y[0, t:, e]).all() and torch.isnan(h[0, e]).all()
+    others = torch.arange(70, device=DEV) != e
+    assert torch.equal(y[:, :, others], want[:, :, others]) and torch.equal(h[:, others], hw[:, others])
+    assert torch.equal(y[0, :t, e], want[0, :t, e])
+    state = h0.clone()
+    one = {k: (v[:, t] if k in ("x", "dt", "B", "C") else v) for k, v in dict(kw, dt=dt, z=None).items()}
+    y1 = ssd.selective_step(state=state, **one)
+    assert torch.isnan(y1[0, e]) and torch.isnan(state[0, e]).all()
+    assert torch.isfinite(y1[:, others]).all() and torch.isfinite(state[:, others]).all()
+    # beyond the limits on both sides: the same as dt at them
+    pre = dict(limit=(1e-3, 0.5))
+    near = {k: (v[:, t] if k in ("x", "B", "C") else v) for k, v in dict(kw, z=None, dt_pre=pre).items() if k != "dt"}
+    for far, at in ((float("-inf"), 1e-3), (float("inf"), 0.5)):
+        a, b = h0.clone(), h0.clone()
+        ya = ssd.selective_step(state=a, dt=torch.full((1, 70), far, device=DEV), **near)
+        yb = ssd.selective_step(state=b, dt=torch.full((1, 70), at, device=DEV), **near)
+        assert torch.equal(ya, yb) and torch.equal(a, b)
