@@ -46,8 +46,6 @@
 // beginning from its own state, so nothing of one sequence meets another.
 #include "selective.h"
 
-#include <cfloat>
-
 namespace ssd {
 namespace {
 
@@ -189,9 +187,8 @@ __global__ __launch_bounds__(kThreads, !OUT && NP == 16 && sizeof(TIO) + sizeof(
 #pragma unroll
   for (int s = 0; s < SPL; ++s) {
     const int n = (s / 4) * 16 + q * 4 + s % 4;
-    A2[s] = n < a.N ? a.A[(int64_t)e * a.N + n] * kLog2e : 0.f;
-    // (finite, for the steps of zero behind a run's end)
-    A2[s] = A2[s] < -FLT_MAX ? -FLT_MAX : A2[s];
+    // (finite, also for the steps of zero behind a run's end)
+    A2[s] = n < a.N ? log2_decay(a.A[(int64_t)e * a.N + n]) : 0.f;
   }
   const float bias = a.dto.bias != nullptr ? a.dto.bias[e] : 0.f;
   const float Dv = OUT && a.D != nullptr ? a.D[e] : 0.f;

@@ -78,7 +78,7 @@ __global__ __launch_bounds__(kThreads) void selective_step_kernel(const Selectiv
     float hn[4], p = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float dec = __builtin_amdgcn_exp2f(d * (Av.v[i] * kLog2e));
+      const float dec = __builtin_amdgcn_exp2f(d * log2_decay(Av.v[i]));
       hn[i] = fmaf(dec, h[k].v[i], u * Elem<TIO>::f32(bv[k].v[i]));
       if (i < nn) p = fmaf(hn[i], Elem<TIO>::f32(cv[k].v[i]), p);
     }

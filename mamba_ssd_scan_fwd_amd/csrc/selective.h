@@ -3,6 +3,7 @@
 // public ABI.
 #pragma once
 
+#include <cfloat>
 #include <type_traits>
 
 #include "packed_runs.h"
@@ -145,6 +146,9 @@ __device__ __forceinline__ float clamped(float v, float lo, float hi) {
   v = v < lo ? lo : v;
   return v > hi ? hi : v;
 }
+// A decay for exp2, finite (log2(e) times the lowest values is not): a step of
+// zero then leaves the state as it is.
+__device__ __forceinline__ float log2_decay(float A) { return clamped(A * kLog2e, -FLT_MAX, FLT_MAX); }
 __device__ __forceinline__ float step_size(float v, float bias, const DtOpts& o) {
   v += bias;
   if (o.softplus) v = softplus_f32(v);

@@ -301,3 +301,24 @@ def test_a_step_size_of_nan_is_not_clamped_away(io, L):
         ya = ssd.selective_step(state=a, dt=torch.full((1, 70), far, device=DEV), **near)
         yb = ssd.selective_step(state=b, dt=torch.full((1, 70), at, device=DEV), **near)
         assert torch.equal(ya, yb) and torch.equal(a, b)
+
+
+def test_decays_of_the_lowest_value():
+    """A of the type's lowest value: a step of zero keeps the state (0 times it
+    is no infinity), any other forgets it."""
+    E, N, lowest = 40, 16, torch.finfo(torch.float32).min
+    s = Selective(2, 7, E, N, gate=False, skip=False, pre=False, seed=50)
+    kw, h0, _ = s.to(DEV)
+    kw["A"][:, 3:9] = lowest
+    kw["dt"].zero_()
+    note("[gpu] selective scan and step: decays of the lowest value")
+    _, h = ssd.selective_scan(init_state=h0, **kw)
+    assert torch.equal(h, h0)
+    one = {k: (v[:, 0] if k in ("x", "dt", "B", "C") else v) for k, v in dict(kw, z=None).items()}
+    state = h0.clone()
+    ssd.selective_step(state=state, **one)
+    assert torch.equal(state, h0)
+    one["dt"] = torch.full((2, E), 0.25, device=DEV)
+    ssd.selective_step(state=state, **one)
+    u = (0.25 * one["x"])[:, :, None] * one["B"][:, :1]
+    assert torch.equal(state[:, :, 3:9], u[:, :, 3:9])
