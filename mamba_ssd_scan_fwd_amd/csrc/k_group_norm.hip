@@ -138,9 +138,13 @@ __global__ __launch_bounds__(T > 64 ? T : 256) void group_norm_kernel(const Grou
         if (counts(m, v)) sq = fmaf(x[m][v], x[m][v], sq);
       }
     const float var = team_sum(sq) * inv + a.eps;
-    // one Newton step on the hardware's reciprocal root (1 ulp)
-    float rs = __builtin_amdgcn_rsqf(var);
-    rs = var > 0.f && var < 1e38f ? rs * fmaf(-0.5f * var * rs, rs, 1.5f) : rs;
+    // one Newton step on the hardware's reciprocal root (1 ulp); it takes a
+    // subnormal for 0, so small ones go in times 2^64
+    const bool small = var < 0x1p-100f;
+    const float vs = small ? var * 0x1p64f : var;
+    float rs = __builtin_amdgcn_rsqf(vs);
+    rs = vs > 0.f && vs < 1e38f ? rs * fmaf(-0.5f * vs * rs, rs, 1.5f) : rs;
+    if (small) rs *= 0x1p32f;
 #pragma unroll
     for (int m = 0; m < M; ++m) {
       float o[V], wv[V], ov[V];

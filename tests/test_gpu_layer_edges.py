@@ -322,3 +322,22 @@ def test_decays_of_the_lowest_value():
     ssd.selective_step(state=state, **one)
     u = (0.25 * one["x"])[:, :, None] * one["B"][:, :1]
     assert torch.equal(state[:, :, 3:9], u[:, :, 3:9])
+
+
+@pytest.mark.parametrize("center", [False, True])
+@pytest.mark.parametrize("size", [3e-21, 1e-20, 1e-19, 1e18])
+def test_group_norm_of_rows_of_extreme_size(size, center):
+    """eps = 0 and squares below the smallest normal number: the statistics
+    are then as exact as subnormal sums of squares are. Of C squares and adds
+    each is off by 2^-150, as is their mean; the root halves that; 8 U for the
+    rest, and for the centre (a mean off by 66 U of mean|x|, the square of
+    which does not count here) 70 U of a deviation."""
+    C = 256
+    x = (torch.randn((5, C), generator=torch.Generator().manual_seed(51)) * size).float()
+    note(f"[gpu] group norm of rows of size {size}")
+    o = np64(ssd.group_norm(x.to(DEV), eps=0.0, center=center))
+    want = ref.group_norm(np64(x), 1, 0.0, center=center)
+    v = np64(x) - (np64(x).mean(1, keepdims=True) if center else 0.0)
+    var = (v * v).mean(1, keepdims=True)
+    rel = 0.5 * (2 * C * 2.0 ** -150 / (C * var) + 2.0 ** -150 / var) + 8 * U
+    within(o, want, np.abs(want) * rel * 1.01 + (70 * U if center else 0.0), "out")
