@@ -13,6 +13,7 @@ from .binding import (  # noqa: F401
     STATUS_WAIT_CUT_OFF_ONE_PASS,
     STATUS_WAIT_CUT_OFF_SEGMENTED,
     SSDDesc,
+    SelectiveDesc,
     SSDError,
     chunk_cumsum,
     chunk_scan,

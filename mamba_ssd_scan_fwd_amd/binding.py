@@ -17,6 +17,7 @@ import torch
 __all__ = [
     "SSDError",
     "SSDDesc",
+    "SelectiveDesc",
     "lib_path",
     "load_library",
     "make_desc",
@@ -749,6 +750,9 @@ def _pre(dt_pre):
 
 
 def selective_scan_workspace_bytes(desc: SelectiveDesc, num_seqs: int = 0) -> int:
+    """Bytes of ``workspace`` for a ``selective_scan`` (num_seqs 0) or
+    ``selective_scan_varlen`` of ``desc``'s sizes and types; strides and dt
+    preprocessing do not matter."""
     n = ctypes.c_size_t(0)
     _check(load_library().ssd_selective_scan_workspace_bytes(ctypes.byref(desc), num_seqs, ctypes.byref(n)),
            "ssd_selective_scan_workspace_bytes")

@@ -332,3 +332,14 @@ def test_outputs_of_any_size_are_refused_without_overflow():
     few = Stride(4, 4)
     assert norm_call(norm(batch=n, rows=n, channels=4, ngroups=1, x_stride=few, z_stride=few)) == SHAPE
     assert norm_call(norm(batch=1 << 20, rows=1 << 20, channels=4, ngroups=1, x_stride=few, z_stride=few)) == SHAPE
+
+
+def test_workspace_size_from_public_names():
+    lib()
+    desc = ssd.SelectiveDesc(batch=1, seqlen=8192, channels=64, dstate=16, ngroups=1, io_dtype=0, dt_dtype=0)
+    assert ssd.selective_scan_workspace_bytes(desc) > 0
+    assert ssd.selective_scan_workspace_bytes(desc, 5) > 0
+    desc.seqlen = 32
+    assert ssd.selective_scan_workspace_bytes(desc) == 0
+    with pytest.raises(ssd.SSDError):
+        ssd.selective_scan_workspace_bytes(desc, -1)
