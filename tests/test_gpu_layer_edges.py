@@ -2,6 +2,8 @@
 allows, beside those of test_gpu_layer.py: offsets, unusual values, and the
 kernels that only large calls reach. Bounds as derived in layer_testutil."""
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -341,3 +343,95 @@ def test_group_norm_of_rows_of_extreme_size(size, center):
     var = (v * v).mean(1, keepdims=True)
     rel = 0.5 * (2 * C * 2.0 ** -150 / (C * var) + 2.0 ** -150 / var) + 8 * U
     within(o, want, np.abs(want) * rel * 1.01 + (70 * U if center else 0.0), "out")
+
+
+# ---- calls at once, graphs, the C ABI ------------------------------------------------------
+
+
+def scans(seed, lens=None):
+    """A scan that is cut into segments (so it has a workspace), and its result."""
+    s = Selective(1, 900, 96, 16, io="bf16", dt="bf16", lens=lens, seed=seed)
+    kw, h0, cu = s.to(DEV)
+
+    def run():
+        u = ssd.conv1d(kw["x"], w) if cu is None else ssd.conv1d_varlen(kw["x"], w, cu_seqlens=cu)
+        a = dict(kw, x=u)
+        y, h = (ssd.selective_scan(init_state=h0, **a) if cu is None else
+                ssd.selective_scan_varlen(cu_seqlens=cu, init_states=h0, **a))
+        return [y, h, ssd.group_norm(y, ngroups=3)]
+
+    w = torch.randn((96, 4), generator=torch.Generator().manual_seed(seed)).to(DEV)
+    return run
+
+
+def test_two_streams_at_once():
+    runs = [scans(61), scans(62, [300, 0, 7, 593])]
+    wants = [r() for r in runs]
+    streams = [torch.cuda.Stream() for _ in runs]
+    note("[gpu] two streams at once")
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for r, st, g in zip(runs, streams, got):
+            with torch.cuda.stream(st):
+                g.append(r())
+    torch.cuda.synchronize()
+    for want, outs in zip(wants, got):
+        for out in outs:
+            assert all(torch.equal(a, b) for a, b in zip(want, out))
+
+
+def test_two_graphs_replayed_at_once():
+    """Each graph has its own workspace: replays on two streams, with eager
+    calls between, all give the same bits."""
+    runs = [scans(63), scans(64, [1] * 40 + [860])]
+    wants = [r() for r in runs]
+    note("[gpu] two graphs at once")
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for r in runs:
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            r()
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(r())
+    streams = [torch.cuda.Stream() for _ in runs]
+    for _ in range(4):
+        for out in outs:
+            for o in out:
+                o.zero_()
+        torch.cuda.synchronize()
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        eager = [r() for r in runs]
+        torch.cuda.synchronize()
+        for want, out, e in zip(wants, outs, eager):
+            assert all(torch.equal(a, b) for a, b in zip(want, out))
+            assert all(torch.equal(a, b) for a, b in zip(want, e))
+
+
+@pytest.mark.parametrize("own", [False, True])
+def test_workspace_of_the_c_abi(own):
+    """A null workspace is allocated and freed in stream order; one of exactly
+    the size asked for is enough, and nothing behind it is written."""
+    s = Selective(1, 1500, 64, 16, seed=65)
+    kw, h0, _ = s.to(DEV)
+    want, hw = ssd.selective_scan(init_state=h0, **kw)
+    d = ssd.SelectiveDesc(batch=1, seqlen=1500, channels=64, dstate=16, ngroups=1, io_dtype=0, dt_dtype=0,
+                          dt_bias=kw["dt_pre"]["bias"].data_ptr(), dt_softplus=1, dt_clamp=1, dt_min=1e-3, dt_max=0.5)
+    n = ssd.selective_scan_workspace_bytes(d)
+    assert n > 0
+    ws = torch.full((n + GUARD,), 255, dtype=torch.uint8, device=DEV)
+    y, h = torch.empty_like(want), torch.empty_like(hw)
+    note(f"[gpu] selective scan through the C ABI, own workspace {own}")
+    torch.cuda.synchronize()
+    p = [kw[k].data_ptr() for k in ("x", "dt", "A", "B", "C", "D", "z")] + [t.data_ptr() for t in (h0, y, h)]
+    for _ in range(3):
+        st = ssd.load_library().ssd_selective_scan(ctypes.byref(d), *p, ws.data_ptr() if own else None, n if own else 0, None)
+        assert st == 0
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.equal(h, hw)
+    assert (ws[n:] == 255).all()
