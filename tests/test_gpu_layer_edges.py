@@ -435,3 +435,35 @@ def test_workspace_of_the_c_abi(own):
     torch.cuda.synchronize()
     assert torch.equal(y, want) and torch.equal(h, hw)
     assert (ws[n:] == 255).all()
+
+
+def test_outputs_of_more_than_two_to_the_31_elements():
+    """The second of two rows lies behind 2^31 elements in part: its last
+    tokens against the definition (scan) and against a call on their own."""
+    b, L, E, N, tail = 2, 540_001, 2048, 16, 150
+    g = torch.Generator(device=DEV).manual_seed(66)
+    draw = lambda *s: torch.randn(s, generator=g, device=DEV, dtype=torch.bfloat16)  # noqa: E731
+    x, z, dt, B, C = draw(b, L, E), draw(b, L, E), draw(b, L, E), draw(b, L, 1, N), draw(b, L, 1, N)
+    A = -torch.exp(torch.rand((E, N), generator=g, device=DEV) * 2.8)
+    assert x.numel() > 1 << 31
+    note("[gpu] outputs of more than 2^31 elements")
+    # steps of 0.05 and more, so that 1280 tokens back nothing is left (e^-64)
+    pre = dict(softplus=True, limit=(0.05, 0.5))
+    y, h = ssd.selective_scan(x, dt, A, B, C, None, z, dt_pre=pre)
+    _, before = ssd.selective_scan(x[:, :-tail], dt[:, :-tail], A, B[:, :-tail], C[:, :-tail], dt_pre=pre)
+    d = np.clip(ref.softplus(np64(dt[:, -tail:])), 0.05, 0.5)
+    f = (3 * 1280 + N + 2300 + 26) * U
+    for i in range(b):
+        # (before is itself off by f of its terms' absolute values, bounded by
+        # those that 1280 steps of 0.5 of |x B| below 6 x 6 can leave)
+        yr, ya, hr, ha = ref.selective_scan(np64(x[i, -tail:]), d[i], np64(A), np64(B[i, -tail:]), np64(C[i, -tail:]), None,
+                                            np64(z[i, -tail:]), np64(before[i]))
+        left = np.exp(-np.cumsum(d[i], 0)) * 1280 * 0.5 * 36.0  # of any state, |A| being 1 at least
+        gate = np.abs(ref.silu(np64(z[i, -tail:]))) * np.abs(np64(C[i, -tail:, 0])).sum(1)[:, None]
+        within(y[i, -tail:], yr, f * (ya + left * gate) + np.abs(yr) * 2.0 ** -8, "y")
+        within(h[i], hr, f * (ha + left[-1][:, None]), "final_state")
+    w = torch.randn((E, 4), generator=g, device=DEV)
+    line = x[:, -tail - 3:]
+    assert torch.equal(ssd.conv1d(x, w)[:, -tail:], ssd.conv1d(line, w)[:, 3:])
+    assert torch.equal(ssd.group_norm(x, None, None, z, ngroups=4)[:, -tail:],
+                       ssd.group_norm(x[:, -tail:], None, None, z[:, -tail:], ngroups=4))
