@@ -467,3 +467,29 @@ def test_outputs_of_more_than_two_to_the_31_elements():
     assert torch.equal(ssd.conv1d(x, w)[:, -tail:], ssd.conv1d(line, w)[:, 3:])
     assert torch.equal(ssd.group_norm(x, None, None, z, ngroups=4)[:, -tail:],
                        ssd.group_norm(x[:, -tail:], None, None, z[:, -tail:], ngroups=4))
+
+
+def test_a_stream_given_inside_a_capture():
+    """A captured call on a second stream that forks from the capturing one
+    and joins it again."""
+    s = Selective(1, 500, 64, 16, io="bf16", dt="bf16", seed=67)
+    kw, h0, _ = s.to(DEV)
+    want, hw = ssd.selective_scan(init_state=h0, **kw)
+    note("[gpu] selective scan: stream argument inside a capture")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        y, h = ssd.selective_scan(init_state=h0, stream=side, **kw)
+        here.wait_stream(side)
+        o = ssd.group_norm(y)
+    norm = ssd.group_norm(want)
+    for _ in range(3):
+        for t in (y, h, o):
+            t.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(h, hw) and torch.equal(o, norm)
