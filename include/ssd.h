@@ -439,6 +439,7 @@ SSD_API ssd_status_t ssd_decode_step(const ssd_desc_t* desc, const void* x, cons
  *    is below 2^22). Outputs and states are dense.
  *  - Base pointers need the alignment of their elements only.
  *  - The stream's device must be the current device.
+ *  - None of them has a gradient.
  */
 typedef struct {
   int64_t token; /* elements from one token (row) to the next; 0: dense      */
@@ -453,7 +454,10 @@ typedef struct {
  * with pre() the bias, softplus and clamp of ssd_desc_t (except that a NaN stays
  * NaN behind the clamp, where ssd_desc_t's gives dt_min), h_{-1} the initial
  * state (zeros when NULL), and the D and gate factors left out when D or z is
- * NULL. States, sums and decays are fp32; y is rounded once.
+ * NULL. States, sums and decays are fp32; y is rounded once. Infinities and
+ * NaNs stay inside their channel (of x, dt, z) or group (of B, C) and sequence;
+ * behind an infinite dt x the scan may give NaN where the formula gives an
+ * infinity.
  *     x, z       [batch, L, E]     io dtype, strided (z nullable)
  *     dt         [batch, L, E]     dt dtype, strided
  *     B, C       [batch, L, G, N]  io dtype, strided ([G, N] contiguous)
@@ -508,8 +512,8 @@ SSD_API ssd_status_t ssd_selective_scan_varlen(const ssd_selective_desc_t* desc,
                                                const float* init_states, void* y, float* final_states,
                                                void* workspace, size_t workspace_bytes, void* stream);
 
-/* One token of every row (desc->seqlen = 1; the token strides are not used),
- * the states kept in a pool between calls:
+/* One token of every row (desc->seqlen = 1; the token strides are checked like
+ * the others, but not used), the states kept in a pool between calls:
  *   state        [num_slots, E, N] fp32, updated in place
  *   state_slots  [batch] int32 DEVICE pointer, nullable (row b uses slot b;
  *                num_slots >= batch then). A row whose slot is negative or

@@ -670,9 +670,12 @@ def conv1d_split(xbc, weight, bias=None, *, nheads, headdim, ngroups, dstate, si
 # ---- the layer operators around the scan -------------------------------------
 #
 # Inputs may be views of wider buffers (rows of contiguous channels, any
-# distance between tokens and batch rows). A call for one token takes a few
-# microseconds on the GPU, so its marshalling is compiled (csrc_py/marshal.cpp):
-# the checks of the tensors, the outputs and the descriptor.
+# distance between tokens and batch rows). Like all of the package they record
+# no gradient: outputs are detached from inputs that require one. ``stream`` is
+# a stream of x's device; without it the current one is used. A call for one
+# token takes a few microseconds on the GPU, so its marshalling is compiled
+# (csrc_py/marshal.cpp): the checks of the tensors, the outputs and the
+# descriptor.
 
 _native = None
 

@@ -15,7 +15,7 @@
 // workgroup, which exchanges its waves' sums through LDS.
 //
 // Bound by memory: 16384 x 4096 bf16 with gate 67 us, 6.0 TB/s; 1001 x 8192 fp32 in
-// 128 groups 17.2 us, 5.7 TB/s. Groups of 4096 channels: a workgroup of 256 lanes
+// 128 groups 18.2 us, 5.4 TB/s. Groups of 4096 channels: a workgroup of 256 lanes
 // 82 us (weights still loaded one by one), 128 lanes 96, one wave 151.
 #include "selective.h"
 

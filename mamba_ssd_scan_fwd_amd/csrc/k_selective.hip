@@ -568,7 +568,9 @@ hipError_t launch_io(const SelectiveArgs& a, int64_t batch, hipStream_t s) {
 SelectiveCut selective_scan_cut(int64_t batch, int64_t L, int64_t E, int64_t G, int64_t nseq) {
   const int64_t tiles = (E / G + kChannels - 1) / kChannels * G;
   const int64_t waves = tiles * 4 * batch;
-  // As many segments as two waves a SIMD allow: one walk takes the same time
+  // As many segments as two waves a SIMD allow (with more than 128 states the
+  // output walk's registers leave one, and its segments run in two rounds; the
+  // rule does not tell these apart): one walk takes the same time
   // for 1025 waves as for 2048, and for 1 as for 1024. 4096 tokens of 4096
   // channels, batch 2 (512 waves): 392 us in one walk, 224 in four segments;
   // batch 4: 395 and 371 in two; batch 6: 534 and, as two, 619.
@@ -587,6 +589,9 @@ SelectiveCut selective_scan_cut(int64_t batch, int64_t L, int64_t E, int64_t G, 
   // more waves: a quarter of a segment each (16384 tokens of 4096 channels 462
   // -> 434 us). Packed sequences keep whole segments: every piece may end in
   // the middle of a run (37 sequences in 8197 tokens 139 us, in two pieces 150).
+  // Narrow layers of long prompts have pieces by the hundred, and the fold over
+  // them is a load's latency each: 32768 tokens of 64 channels (1024 pieces) 309
+  // us, of 512 (256 pieces) 180.
   int64_t pieces = nseq > 0 ? 1 : 4;
   int64_t unit = 32 * pieces;  // whole tiles
   len = (len + unit - 1) / unit * unit;
