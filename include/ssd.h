@@ -595,6 +595,117 @@ typedef struct {
 SSD_API ssd_status_t ssd_group_norm(const ssd_group_norm_desc_t* desc, const void* x, const float* weight,
                                     const float* bias, const void* z, void* out, void* stream);
 
+/* ---- the gated delta rule ---------------------------------------------------
+ *
+ * A recurrence over the same P x N state per head that, before it adds a
+ * token's value, takes out what the state already answers to its key. Its
+ * arguments have the names and layouts of ssd_forward's (x the values, B the
+ * keys, C the queries), the conventions are those of the layer operators. Per
+ * head h with group g = h / (nheads / ngroups), and a_t = exp(pre(dt_t) A_h),
+ * b_t = beta_t, or sigmoid(beta_t) with beta_sigmoid:
+ *     S_t = a_t S_{t-1} + b_t (x_t - a_t S_{t-1} B_t) B_t^T        (P x N)
+ *     y_t = scale * S_t C_t
+ * with pre() as for the selective scan, S_{-1} the initial state (zeros when
+ * NULL). A = 0 gives the delta rule without a decay. Keys of length one (see
+ * ssd_head_norm) and b in [0, 2] keep it from growing; nothing is normalised
+ * here.
+ *     x          [batch, L, H, P]  io dtype, strided ([H, P] contiguous); P 1..256
+ *     B, C       [batch, L, G, N]  io dtype, strided ([G, N] contiguous); N 1..256
+ *     dt, beta   [batch, L, H]     dt dtype, strided
+ *     A          [H]               fp32 (A <= 0 expected)
+ *     y          [batch, L, H, P]  io dtype
+ *     states     [.., H, P, N]     fp32
+ * States, decays and sums are fp32; y is rounded once. Prompts may be taken in
+ * blocks of 64 tokens whose products run on the matrix cores: with bf16 io the
+ * operands of y's products (states, solutions) are rounded to bf16, those that
+ * reach a state are kept to 16 bits or more (fp32 io: all of them). An infinity
+ * or a NaN of a row of x stays in that row p of its head, one of B, C, dt or
+ * beta in its group or head, all of them in their sequence; within 64 tokens
+ * before it, though, y may be NaN too. */
+typedef struct {
+  int64_t batch;
+  int64_t seqlen;  /* L; packed sequences: the total token count T             */
+  int64_t nheads;  /* H, up to 65535; H * P and G * N up to 2^20               */
+  int64_t headdim; /* P                                                        */
+  int64_t dstate;  /* N                                                        */
+  int64_t ngroups; /* G, H % G == 0                                            */
+  int32_t io_dtype; /* ssd_dtype_t of x, B, C, y                               */
+  int32_t dt_dtype; /* ssd_dtype_t of dt and beta: fp32, or the io dtype       */
+  const float* dt_bias; /* [H] fp32 device pointer, nullable                   */
+  int32_t dt_softplus;
+  int32_t dt_clamp;     /* requires dt_min <= dt_max                           */
+  float dt_min;
+  float dt_max;
+  int32_t beta_sigmoid;
+  float scale;
+  ssd_stride_t x_stride, dt_stride, beta_stride, B_stride, C_stride;
+} ssd_delta_desc_t;
+
+/* Bytes of workspace for ssd_delta_rule (num_seqs = 0) or
+ * ssd_delta_rule_varlen. Pure host computation. */
+SSD_API ssd_status_t ssd_delta_rule_workspace_bytes(const ssd_delta_desc_t* desc, int64_t num_seqs, size_t* bytes);
+
+/* The rule over a batch of prompts: initial and final states [batch, H, P, N],
+ * both nullable. final_state may be init_state; any other overlap of an output
+ * with an argument is refused. workspace: as for ssd_selective_scan. Results
+ * are the same bits from one call to the next. */
+SSD_API ssd_status_t ssd_delta_rule(const ssd_delta_desc_t* desc, const void* x, const void* dt, const float* A,
+                                    const void* B, const void* C, const void* beta, const float* init_state,
+                                    void* y, float* final_state, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/* The rule over packed sequences (batch 1, seqlen T), states
+ * [num_seqs, H, P, N]; cu_seqlens as for ssd_selective_scan_varlen, the same
+ * rules for empty sequences and for tokens of none. */
+SSD_API ssd_status_t ssd_delta_rule_varlen(const ssd_delta_desc_t* desc, const int32_t* cu_seqlens, int64_t num_seqs,
+                                           const void* x, const void* dt, const float* A, const void* B,
+                                           const void* C, const void* beta, const float* init_states, void* y,
+                                           float* final_states, void* workspace, size_t workspace_bytes,
+                                           void* stream);
+
+/* One token of every row (desc->seqlen = 1):
+ *   state        [num_slots, H, P, N] fp32, updated in place
+ *   state_slots  as for ssd_selective_step (padding, repeated slots).
+ * state and y must not overlap each other or any input. No workspace. */
+SSD_API ssd_status_t ssd_delta_step(const ssd_delta_desc_t* desc, const void* x, const void* dt, const float* A,
+                                    const void* B, const void* C, const void* beta, float* state,
+                                    const int32_t* state_slots, int64_t num_slots, void* y, void* stream);
+
+/* ---- the norm of heads, with the rotation by position ------------------------ */
+
+/* Norm of each head of queries and keys (C and B of the scans above, or an
+ * attention layer's) over its D = headdim channels, and the rotation of the
+ * first rot = 2 * freqs of them by the token's position:
+ *     v = x / sqrt(mean(x^2) + eps) * weight,  or  x / sqrt(sum(x^2) + eps) * weight  (l2)
+ *     angle_i = position * inv_freq[i],  i < rot / 2
+ *     (v_a, v_b) <- (v_a cos - v_b sin, v_b cos + v_a sin)
+ * where (a, b) is (i, i + rot / 2), or (2 i, 2 i + 1) with pairs. Channels from
+ * rot on are only normalised. Norms and products are fp32, angles are taken in
+ * 64 bits (exact to 2^-24 of a turn for any position); outputs are rounded once.
+ *   q, k            [batch, rows, q_heads or k_heads, D]  io dtype, strided
+ *                   ([heads, D] contiguous); k_heads 0: no keys, k and k_out NULL
+ *   q_weight, k_weight  [D]                 fp32, nullable (1)
+ *   positions       [batch, rows]           int32, needed where rot > 0
+ *   inv_freq        [rot / 2]               fp32, needed where rot > 0
+ *   q_out, k_out    as q, k, dense; overlap no input and not each other */
+typedef struct {
+  int64_t batch;
+  int64_t rows;
+  int64_t q_heads;
+  int64_t k_heads;
+  int64_t headdim; /* D, 1..512 */
+  int64_t rot;     /* channels rotated: even, 0..D */
+  int32_t io_dtype;
+  int32_t l2;
+  int32_t pairs;
+  float eps; /* >= 0 */
+  ssd_stride_t q_stride, k_stride;
+} ssd_head_norm_desc_t;
+
+SSD_API ssd_status_t ssd_head_norm(const ssd_head_norm_desc_t* desc, const void* q, const void* k,
+                                   const float* q_weight, const float* k_weight, const int32_t* positions,
+                                   const float* inv_freq, void* q_out, void* k_out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

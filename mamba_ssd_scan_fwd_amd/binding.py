@@ -47,6 +47,12 @@ __all__ = [
     "conv1d_step",
     "conv1d_split_step",
     "group_norm",
+    "DeltaDesc",
+    "delta_rule",
+    "delta_rule_varlen",
+    "delta_rule_workspace_bytes",
+    "delta_step",
+    "head_norm",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -79,6 +85,11 @@ EXPORTED_SYMBOLS = (
     "ssd_conv1d",
     "ssd_conv1d_step",
     "ssd_group_norm",
+    "ssd_delta_rule_workspace_bytes",
+    "ssd_delta_rule",
+    "ssd_delta_rule_varlen",
+    "ssd_delta_step",
+    "ssd_head_norm",
 )
 
 SSD_DTYPE_F32 = 0
@@ -171,6 +182,55 @@ class GroupNormDesc(ctypes.Structure):
     ]
 
 
+class DeltaDesc(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("seqlen", ctypes.c_int64),
+        ("nheads", ctypes.c_int64),
+        ("headdim", ctypes.c_int64),
+        ("dstate", ctypes.c_int64),
+        ("ngroups", ctypes.c_int64),
+        ("io_dtype", ctypes.c_int32),
+        ("dt_dtype", ctypes.c_int32),
+        ("dt_bias", ctypes.c_void_p),
+        ("dt_softplus", ctypes.c_int32),
+        ("dt_clamp", ctypes.c_int32),
+        ("dt_min", ctypes.c_float),
+        ("dt_max", ctypes.c_float),
+        ("beta_sigmoid", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("x_token", ctypes.c_int64),
+        ("x_batch", ctypes.c_int64),
+        ("dt_token", ctypes.c_int64),
+        ("dt_batch", ctypes.c_int64),
+        ("beta_token", ctypes.c_int64),
+        ("beta_batch", ctypes.c_int64),
+        ("B_token", ctypes.c_int64),
+        ("B_batch", ctypes.c_int64),
+        ("C_token", ctypes.c_int64),
+        ("C_batch", ctypes.c_int64),
+    ]
+
+
+class HeadNormDesc(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("rows", ctypes.c_int64),
+        ("q_heads", ctypes.c_int64),
+        ("k_heads", ctypes.c_int64),
+        ("headdim", ctypes.c_int64),
+        ("rot", ctypes.c_int64),
+        ("io_dtype", ctypes.c_int32),
+        ("l2", ctypes.c_int32),
+        ("pairs", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("q_token", ctypes.c_int64),
+        ("q_batch", ctypes.c_int64),
+        ("k_token", ctypes.c_int64),
+        ("k_batch", ctypes.c_int64),
+    ]
+
+
 def lib_path() -> str:
     return os.environ.get("SSD_LIB", os.path.join(_HERE, "libssd.so"))
 
@@ -250,6 +310,17 @@ def load_library():
         lib.ssd_conv1d_step.restype = ctypes.c_int
         lib.ssd_group_norm.argtypes = [gp, vp, vp, vp, vp, vp, vp]
         lib.ssd_group_norm.restype = ctypes.c_int
+        ep, hp = ctypes.POINTER(DeltaDesc), ctypes.POINTER(HeadNormDesc)
+        lib.ssd_delta_rule_workspace_bytes.argtypes = [ep, i64, ctypes.POINTER(sz)]
+        lib.ssd_delta_rule_workspace_bytes.restype = ctypes.c_int
+        lib.ssd_delta_rule.argtypes = [ep, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        lib.ssd_delta_rule.restype = ctypes.c_int
+        lib.ssd_delta_rule_varlen.argtypes = [ep, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        lib.ssd_delta_rule_varlen.restype = ctypes.c_int
+        lib.ssd_delta_step.argtypes = [ep, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp, vp]
+        lib.ssd_delta_step.restype = ctypes.c_int
+        lib.ssd_head_norm.argtypes = [hp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        lib.ssd_head_norm.restype = ctypes.c_int
         _lib = lib
     return _lib
 
@@ -692,7 +763,8 @@ def _marshal():
                                "`python -m mamba_ssd_scan_fwd_amd.build`") from e
         at = [ctypes.cast(getattr(lib, "ssd_" + n), ctypes.c_void_p).value
               for n in ("selective_scan_workspace_bytes", "selective_scan", "selective_scan_varlen", "selective_step",
-                        "conv1d", "conv1d_step", "group_norm")]
+                        "conv1d", "conv1d_step", "group_norm", "delta_rule_workspace_bytes", "delta_rule",
+                        "delta_rule_varlen", "delta_step", "head_norm")]
         m.bind(*at, SSDError)
         _native = m
     return _native
@@ -853,3 +925,65 @@ def group_norm(x, weight=None, bias=None, z=None, *, ngroups=1, eps=1e-5, center
     before the norm with ``gate_first``, else behind it; ``silu`` applies the
     SiLU to the result instead."""
     return _run("group_norm", stream, x, weight, bias, z, ngroups, eps, center, gate_first, silu, out)
+
+
+def delta_rule_workspace_bytes(desc: DeltaDesc, num_seqs: int = 0) -> int:
+    """Bytes of ``workspace`` for a ``delta_rule`` (num_seqs 0) or
+    ``delta_rule_varlen`` of ``desc``'s sizes and types; strides, scale, beta and
+    dt preprocessing do not matter."""
+    n = ctypes.c_size_t(0)
+    _check(load_library().ssd_delta_rule_workspace_bytes(ctypes.byref(desc), num_seqs, ctypes.byref(n)),
+           "ssd_delta_rule_workspace_bytes")
+    return int(n.value)
+
+
+def delta_rule(x, dt, A, B, C, beta, init_state=None, *, scale: float = 1.0, beta_sigmoid: bool = False,
+               return_final_state: bool = True, y=None, final_state=None, workspace=None, dt_pre=None, stream=None):
+    """The gated delta rule over a batch of prompts: with a = exp(dt A),
+    S <- a S + beta (x - a S B) B^T and y = scale S C, x being the values, B the
+    keys and C the queries. Returns (y [b, L, H, P], final_state [b, H, P, N]
+    fp32 or None).
+
+    x [b, L, H, P] and B, C [b, L, G, N] in fp32 or bf16 (all the same; head h
+    reads group h // (H // G)); dt and beta [b, L, H] in fp32 or the same (both
+    alike); A [H] and init_state [b, H, P, N] (optional) in fp32; P and N up to
+    256. x, dt, beta, B and C may be views of wider buffers. ``beta_sigmoid``
+    takes sigmoid(beta), ``dt_pre`` is as for ``forward``. ``final_state`` may be
+    ``init_state``. Keys are taken as they are: ``head_norm`` with ``l2`` gives
+    them length one.
+    """
+    return _run("delta_prompts", stream, x, dt, A, B, C, beta, None, init_state, y, final_state, return_final_state,
+                workspace, scale, beta_sigmoid, *_pre(dt_pre))[:2]
+
+
+def delta_rule_varlen(x, dt, A, B, C, beta, *, cu_seqlens, init_states=None, scale: float = 1.0,
+                      beta_sigmoid: bool = False, return_final_states: bool = True, y=None, final_states=None,
+                      workspace=None, dt_pre=None, stream=None):
+    """``delta_rule`` over packed sequences: x [1, T, H, P], dt, beta [1, T, H],
+    B, C [1, T, G, N], sequence s being tokens [cu_seqlens[s], cu_seqlens[s+1])
+    (int32 device tensor [S+1]). Returns (y, final_states [S, H, P, N] or None).
+    Where cu_seqlens begins above 0 or ends before T, y of the tokens before or
+    behind it is not written."""
+    return _run("delta_prompts", stream, x, dt, A, B, C, beta, _offsets(cu_seqlens), init_states, y, final_states,
+                return_final_states, workspace, scale, beta_sigmoid, *_pre(dt_pre))[:2]
+
+
+def delta_step(x, dt, A, B, C, beta, state, *, state_slots=None, scale: float = 1.0, beta_sigmoid: bool = False,
+               y=None, dt_pre=None, stream=None):
+    """One token through the gated delta rule: x [b, H, P], dt, beta [b, H], B, C
+    [b, G, N], ``state`` [slots, H, P, N] fp32 updated in place. ``state_slots``
+    as for ``selective_step``. Returns y [b, H, P]."""
+    return _run("delta_token", stream, x, dt, A, B, C, beta, state, state_slots, y, scale, beta_sigmoid,
+                *_pre(dt_pre))
+
+
+def head_norm(q, k=None, q_weight=None, k_weight=None, *, positions=None, inv_freq=None, eps=1e-5, l2=False,
+              pairs=False, q_out=None, k_out=None, stream=None):
+    """Norm of each head of q [.., Hq, D] and k [.., Hk, D] (one or two leading
+    dimensions, views allowed, fp32 or bf16) over its channels, weights [D] fp32,
+    and the rotation of the first channels by the token's position. ``l2``
+    divides by the head's length instead of its root mean square. With
+    ``positions`` (int32, q's leading dimensions) and ``inv_freq`` (fp32 [R / 2])
+    channels i and i + R / 2, or with ``pairs`` 2 i and 2 i + 1, turn by
+    positions * inv_freq[i]. Returns q_out, or (q_out, k_out) where k is given."""
+    return _run("head_norm", stream, q, k, q_weight, k_weight, positions, inv_freq, eps, l2, pairs, q_out, k_out)

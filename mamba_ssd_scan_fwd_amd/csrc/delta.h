@@ -1,0 +1,99 @@
+// Internal declarations of the gated delta rule and of the norm of heads. Not
+// part of the public ABI.
+#pragma once
+
+#include "selective.h"
+
+namespace ssd {
+
+// ---- gated delta rule ----------------------------------------------------------
+constexpr int kDeltaMaxDim = 256;  // P, N
+
+struct DeltaArgs {
+  const void *x, *dt, *beta, *B, *C;
+  const float *A, *init;           // init nullable
+  void* y;
+  float* final_state;              // nullable
+  Stride xs, ds, es, bs, cs;       // of x, dt, beta, B, C
+  int64_t batch, L;                // packed: 1 and the tokens of the stream
+  int H, P, N, G;
+  const int32_t* cu;               // packed: sequence offsets [nseq + 1], else nullptr
+  int64_t nseq;
+  DtOpts dto;
+  int sigmoid;
+  float scale;
+  int64_t seqs() const { return nseq > 0 ? nseq : batch; }
+};
+// The recurrence token after token.
+hipError_t launch_delta_walk(const DeltaArgs& a, int io, int dt, hipStream_t s);
+
+struct DeltaStepArgs {
+  const void *x, *dt, *beta, *B, *C;  // one token per row
+  const float* A;
+  float* state;                       // [nslots, H, P, N]
+  const int32_t* slots;               // [batch], nullable: row b uses slot b
+  int64_t nslots;
+  void* y;
+  int64_t xs, ds, es, bs, cs;         // elements from one row to the next
+  int64_t batch;
+  int H, P, N, G;
+  DtOpts dto;
+  int sigmoid;
+  float scale;
+  bool stream;                        // states past the memory-side cache (set at launch)
+};
+hipError_t launch_delta_step(const DeltaStepArgs& a, int io, int dt, hipStream_t s);
+
+// ---- norm of heads -------------------------------------------------------------
+constexpr int kHeadNormMaxDim = 512;
+
+struct HeadNormArgs {
+  const void* in[2];               // q, k (nullable with no heads)
+  const float* w[2];               // [D], nullable
+  void* out[2];
+  Stride st[2];
+  int heads[2];
+  int64_t batch, rows;
+  int D, R;                        // channels of a head, of them rotated
+  const int32_t* pos;              // [batch, rows]
+  const float* freq;               // [R / 2]
+  int l2, pairs;
+  float eps;
+  int per;                         // heads a wave takes of a token (set at launch)
+};
+hipError_t launch_head_norm(const HeadNormArgs& a, int io, hipStream_t s);
+
+#ifdef __HIPCC__
+// Sum over teams of T lanes (a power of two, aligned), in all of them: DPP
+// within 16 lanes, then exchanges of rows and of halves of the wave. All lanes
+// take part.
+template <int CTRL> __device__ __forceinline__ float dpp_f32(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+template <int T> __device__ __forceinline__ float team_sum(float v) {
+  static_assert(T >= 1 && T <= 64, "lanes of a team");
+  if constexpr (T >= 2) v += dpp_f32<0xB1>(v);   // quad: lane ^ 1
+  if constexpr (T >= 4) v += dpp_f32<0x4E>(v);   // quad: lane ^ 2
+  if constexpr (T >= 8) v += dpp_f32<0x141>(v);  // mirrored in 8
+  if constexpr (T >= 16) v += dpp_f32<0x140>(v); // mirrored in 16
+  if constexpr (T >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  if constexpr (T >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  return v;
+}
+
+// log2 of a token's decay, finite (a NaN stays one), and its beta.
+__device__ __forceinline__ float delta_log2_decay(float dt, float bias, float A, const DtOpts& o) {
+  return clamped(step_size(dt, bias, o) * log2_decay(A), -FLT_MAX, FLT_MAX);
+}
+__device__ __forceinline__ float delta_beta(float v, int sigmoid) {
+  return sigmoid ? __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-v * kLog2e)) : v;
+}
+#endif
+
+}  // namespace ssd

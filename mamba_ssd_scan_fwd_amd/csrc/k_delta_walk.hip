@@ -1,0 +1,155 @@
+// The gated delta rule over prompts, token after token:
+//     a = exp(pre(dt) A);  u = beta (x - a S k);  S <- a S + u k^T;  y = scale S q
+// batched or packed. The rows of a head's state do not meet, so a team of
+// padded N / 4 lanes keeps R of them in registers, four columns to a lane, for
+// the whole sequence; S k and S q are reduced side by side (y = scale (a S q +
+// u (k q))). The next kAhead tokens' rows are loaded while the present ones are
+// worked on.
+//
+// Bound by latency: a token is two dependent reductions. It is right for every
+// size.
+#include "delta.h"
+
+namespace ssd {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kAhead = 4;
+
+template <typename TIO, typename TDT, int R> struct Token {
+  Pack<TIO, 4> k, q;
+  typename Elem<TIO>::raw x[R];
+  typename Elem<TDT>::raw dt, be;
+};
+
+template <typename TIO, typename TDT, int NP, bool VEC, int R>
+__global__ __launch_bounds__(kThreads) void delta_walk_kernel(const DeltaArgs a, int blocks_p) {
+  constexpr int LPR = NP / 4;
+  constexpr int TEAMS = kThreads / LPR;
+  using RX = typename Elem<TIO>::raw;
+  using RD = typename Elem<TDT>::raw;
+  const int tid = threadIdx.x, sub = tid % LPR, team = tid / LPR;
+  const int pb = blockIdx.x % blocks_p;
+  const int64_t sh = blockIdx.x / blocks_p;
+  const int h = (int)(sh % a.H);
+  const int64_t seq = sh / a.H;
+  const int g = h / (a.H / a.G);
+  const int n0 = 4 * sub;
+  const int nn = a.N - n0 < 0 ? 0 : a.N - n0 > 4 ? 4 : a.N - n0;
+  const int nc = nn > 0 ? n0 : 0;
+
+  const int64_t row = a.cu != nullptr ? 0 : seq;  // batch row
+  int64_t first = 0, last = a.L;
+  if (a.cu != nullptr) first = seq_offset(a.cu, seq, a.L), last = seq_offset(a.cu, seq + 1, a.L);
+  const TIO* xp = static_cast<const TIO*>(a.x) + row * a.xs.batch;
+  const TIO* Bp = static_cast<const TIO*>(a.B) + row * a.bs.batch + (int64_t)g * a.N + nc;
+  const TIO* Cp = static_cast<const TIO*>(a.C) + row * a.cs.batch + (int64_t)g * a.N + nc;
+  const RD* dp = static_cast<const RD*>(a.dt) + row * a.ds.batch + h;
+  const RD* ep = static_cast<const RD*>(a.beta) + row * a.es.batch + h;
+  RX* yp = static_cast<RX*>(a.y) + (row * a.L * a.H + h) * a.P;
+  const float bias = a.dto.bias != nullptr ? a.dto.bias[h] : 0.f, Ah = a.A[h];
+
+  int p[R];
+  bool mine[R];
+  float S[R][4];
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    const int pr = (pb * R + k) * TEAMS + team;
+    mine[k] = pr < a.P;
+    p[k] = mine[k] ? pr : a.P - 1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) S[k][i] = 0.f;
+    if (a.init != nullptr) {
+      const Pack<float, 4> v = load_pack<float, 4, !VEC>(a.init + ((seq * a.H + h) * a.P + p[k]) * a.N + nc, nn);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S[k][i] = i < nn ? v.v[i] : 0.f;
+    }
+  }
+  auto load = [&](Token<TIO, TDT, R>(&v)[kAhead], int64_t t0) {
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int64_t t = t0 + j < last ? t0 + j : last - 1;
+      v[j].k = load_pack<TIO, 4, !VEC>(Bp + t * a.bs.token, nn);
+      v[j].q = load_pack<TIO, 4, !VEC>(Cp + t * a.cs.token, nn);
+      v[j].dt = dp[t * a.ds.token];
+      v[j].be = ep[t * a.es.token];
+#pragma unroll
+      for (int k = 0; k < R; ++k) v[j].x[k] = reinterpret_cast<const RX*>(xp)[t * a.xs.token + (int64_t)h * a.P + p[k]];
+    }
+  };
+  Token<TIO, TDT, R> next[kAhead];
+  if (first < last) load(next, first);
+  for (int64_t t0 = first; t0 < last; t0 += kAhead) {
+    Token<TIO, TDT, R> cur[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) cur[j] = next[j];
+    if (t0 + kAhead < last) load(next, t0 + kAhead);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (t0 + j >= last) break;
+      const float dec = __builtin_amdgcn_exp2f(delta_log2_decay(Elem<TDT>::f32(cur[j].dt), bias, Ah, a.dto));
+      const float beta = delta_beta(Elem<TDT>::f32(cur[j].be), a.sigmoid);
+      float kf[4], qf[4], kq = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        kf[i] = i < nn ? Elem<TIO>::f32(cur[j].k.v[i]) : 0.f;
+        qf[i] = i < nn ? Elem<TIO>::f32(cur[j].q.v[i]) : 0.f;
+        kq = fmaf(kf[i], qf[i], kq);
+      }
+      kq = team_sum<LPR>(kq);
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        float sk = 0.f, sq = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          S[k][i] *= dec;
+          sk = fmaf(S[k][i], kf[i], sk);
+          sq = fmaf(S[k][i], qf[i], sq);
+        }
+        sk = team_sum<LPR>(sk);
+        sq = team_sum<LPR>(sq);
+        const float u = beta * (Elem<TIO>::f32(cur[j].x[k]) - sk);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) S[k][i] = fmaf(u, kf[i], S[k][i]);
+        if (sub == 0 && mine[k])
+          yp[(t0 + j) * a.H * a.P + p[k]] = Elem<TIO>::bits(a.scale * fmaf(u, kq, sq));
+      }
+    }
+  }
+  if (a.final_state != nullptr && nn > 0) {
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      if (mine[k]) store_pack<float, 4, !VEC>(a.final_state + ((seq * a.H + h) * a.P + p[k]) * a.N + n0, S[k], nn);
+  }
+}
+
+template <typename TIO, typename TDT, int NP>
+hipError_t launch_np(const DeltaArgs& a, hipStream_t s) {
+  constexpr int R = 2, TEAMS = kThreads / (NP / 4);
+  const int blocks_p = (a.P + TEAMS * R - 1) / (TEAMS * R);
+  const dim3 grid((unsigned)(a.seqs() * a.H * blocks_p));
+  if (a.N % 4 == 0) delta_walk_kernel<TIO, TDT, NP, true, R><<<grid, kThreads, 0, s>>>(a, blocks_p);
+  else delta_walk_kernel<TIO, TDT, NP, false, R><<<grid, kThreads, 0, s>>>(a, blocks_p);
+  return hipGetLastError();
+}
+
+template <typename TIO, typename TDT>
+hipError_t launch_io(const DeltaArgs& a, hipStream_t s) {
+  switch (selective_padded_states(a.N)) {
+    case 16: return launch_np<TIO, TDT, 16>(a, s);
+    case 32: return launch_np<TIO, TDT, 32>(a, s);
+    case 64: return launch_np<TIO, TDT, 64>(a, s);
+    case 128: return launch_np<TIO, TDT, 128>(a, s);
+    default: return launch_np<TIO, TDT, 256>(a, s);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_delta_walk(const DeltaArgs& a, int io, int dt, hipStream_t s) {
+  if (io == kF32) return launch_io<float, float>(a, s);
+  if (dt == kF32) return launch_io<__hip_bfloat16, float>(a, s);
+  return launch_io<__hip_bfloat16, __hip_bfloat16>(a, s);
+}
+
+}  // namespace ssd

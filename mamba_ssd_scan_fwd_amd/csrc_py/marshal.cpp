@@ -31,6 +31,11 @@ struct Library {
   decltype(&ssd_conv1d) conv;
   decltype(&ssd_conv1d_step) conv_step;
   decltype(&ssd_group_norm) norm;
+  decltype(&ssd_delta_rule_workspace_bytes) delta_bytes;
+  decltype(&ssd_delta_rule) delta;
+  decltype(&ssd_delta_rule_varlen) delta_varlen;
+  decltype(&ssd_delta_step) delta_step;
+  decltype(&ssd_head_norm) head_norm;
   PyObject* error;  // SSDError
 };
 Library lib{};
@@ -179,7 +184,26 @@ void need_args(Py_ssize_t n, Py_ssize_t want) {
   if (n != want) bad_type("expected " + std::to_string(want) + " arguments, got " + std::to_string(n));
 }
 
-// (x, dt, A, B, C, z) and the dt preprocessing (bias, softplus, limit).
+// The dt preprocessing (bias, softplus, limit) of a descriptor.
+template <typename Desc>
+void preprocessing(Desc& d, PyObject* bias, PyObject* softplus, PyObject* limit, c10::Device dev, int64_t width) {
+  d.dt_bias = floats(bias, "dt bias", dev, {width});
+  d.dt_softplus = truth(softplus);
+  if (limit != Py_None) {
+    PyObject* lo = PySequence_GetItem(limit, 0);
+    PyObject* hi = lo == nullptr ? nullptr : PySequence_GetItem(limit, 1);
+    if (hi != nullptr) {
+      d.dt_clamp = 1;
+      d.dt_min = (float)PyFloat_AsDouble(lo);
+      d.dt_max = (float)PyFloat_AsDouble(hi);
+    }
+    Py_XDECREF(lo);
+    Py_XDECREF(hi);
+    if (PyErr_Occurred()) throw python_error();
+  }
+}
+
+// (x, dt, A, B, C, z) and the dt preprocessing.
 ssd_selective_desc_t selective_desc(const Tensor& x, PyObject* const* a, PyObject* pre_bias, PyObject* pre_softplus,
                                     PyObject* pre_limit, int64_t lead) {
   const Tensor& dt = device_tensor(a[1], "dt", lead + 1);
@@ -200,20 +224,7 @@ ssd_selective_desc_t selective_desc(const Tensor& x, PyObject* const* a, PyObjec
   if (dt.scalar_type() != at::kFloat && dt.scalar_type() != io)
     bad_type("dt must be torch.float32 or " + text(io) + ", got " + text(dt.scalar_type()));
   d.dt_dtype = io_code(dt, "dt");
-  d.dt_bias = floats(pre_bias, "dt bias", dev, {d.channels});
-  d.dt_softplus = truth(pre_softplus);
-  if (pre_limit != Py_None) {
-    PyObject* lo = PySequence_GetItem(pre_limit, 0);
-    PyObject* hi = lo == nullptr ? nullptr : PySequence_GetItem(pre_limit, 1);
-    if (hi != nullptr) {
-      d.dt_clamp = 1;
-      d.dt_min = (float)PyFloat_AsDouble(lo);
-      d.dt_max = (float)PyFloat_AsDouble(hi);
-    }
-    Py_XDECREF(lo);
-    Py_XDECREF(hi);
-    if (PyErr_Occurred()) throw python_error();
-  }
+  preprocessing(d, pre_bias, pre_softplus, pre_limit, dev, d.channels);
   Dims bc(shape.begin(), shape.begin() + lead);
   bc.push_back(d.ngroups);
   bc.push_back(d.dstate);
@@ -237,6 +248,28 @@ const int32_t* offsets(PyObject* o, c10::Device device, int64_t* num_seqs) {
   return static_cast<const int32_t*>(dense(o, "cu_seqlens", at::kInt, device, t->sizes()));
 }
 
+// The workspace given, or a new one of the bytes needed (none for 0).
+Tensor workspace_of(PyObject* o, size_t need, const Tensor& x) {
+  const Tensor* given = tensor(o, "workspace");
+  if (given != nullptr) {
+    if (!given->is_contiguous() || given->device() != x.device() || given->nbytes() < need)
+      bad_value("workspace needs " + std::to_string(need) + " contiguous bytes on " + x.device().str());
+    return *given;
+  }
+  return need > 0 ? at::empty({(int64_t)need}, x.options().dtype(at::kByte)) : Tensor();
+}
+// (y, final or None, workspace or None)
+PyObject* results(const Tensor& y, const Tensor& final_state, const Tensor& workspace) {
+  PyObject* r = PyTuple_New(3);
+  if (r == nullptr) throw python_error();
+  PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(y));
+  if (!final_state.defined()) Py_INCREF(Py_None);
+  PyTuple_SET_ITEM(r, 1, final_state.defined() ? THPVariable_Wrap(final_state) : Py_None);
+  if (!workspace.defined()) Py_INCREF(Py_None);
+  PyTuple_SET_ITEM(r, 2, workspace.defined() ? THPVariable_Wrap(workspace) : Py_None);
+  return r;
+}
+
 // x dt A B C D z cu_seqlens init y final want_final workspace bias softplus limit stream -> (y, final, workspace)
 PyObject* selective_prompts(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -252,19 +285,12 @@ PyObject* selective_prompts(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const float* D = floats(a[5], "D", dev, {d.channels});
   const float* init = floats(a[8], S > 0 ? "init_states" : "init_state", dev, states);
   Tensor y = output(a[9], "y", x.scalar_type(), x, x.sizes());
-  Tensor final_state, workspace;
+  Tensor final_state;
   if (a[10] != Py_None || truth(a[11]))
     final_state = output(a[10], S > 0 ? "final_states" : "final_state", at::kFloat, x, states);
   size_t need = 0;
   call("ssd_selective_scan_workspace_bytes", [&] { return lib.workspace_bytes(&d, S, &need); });
-  const Tensor* given = tensor(a[12], "workspace");
-  if (given != nullptr) {
-    if (!given->is_contiguous() || given->device() != dev || given->nbytes() < need)
-      bad_value("workspace needs " + std::to_string(need) + " contiguous bytes on " + dev.str());
-    workspace = *given;
-  } else if (need > 0) {
-    workspace = at::empty({(int64_t)need}, x.options().dtype(at::kByte));
-  }
+  const Tensor workspace = workspace_of(a[12], need, x);
   const void *xp = x.data_ptr(), *dt = data(a[1]), *B = data(a[3]), *C = data(a[4]), *z = data(a[6]);
   void *yp = y.data_ptr(), *stream = handle(a[16]);
   void* ws = workspace.defined() ? workspace.data_ptr() : nullptr;
@@ -278,14 +304,7 @@ PyObject* selective_prompts(PyObject*, PyObject* const* a, Py_ssize_t n) {
     call("ssd_selective_scan", [&] {
       return lib.scan(&d, xp, dt, A, B, C, D, z, init, yp, fin, ws, ws_bytes, stream);
     });
-  PyObject* r = PyTuple_New(3);
-  if (r == nullptr) throw python_error();
-  PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(y));
-  if (!final_state.defined()) Py_INCREF(Py_None);
-  PyTuple_SET_ITEM(r, 1, final_state.defined() ? THPVariable_Wrap(final_state) : Py_None);
-  if (!workspace.defined()) Py_INCREF(Py_None);
-  PyTuple_SET_ITEM(r, 2, workspace.defined() ? THPVariable_Wrap(workspace) : Py_None);
-  return r;
+  return results(y, final_state, workspace);
   END_HANDLE_TH_ERRORS
 }
 
@@ -443,6 +462,155 @@ PyObject* group_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// (x, dt, A, B, C, beta) from a[0], a[1], .., and (scale, beta_sigmoid, bias,
+// softplus, limit) from o[0], o[1], ..
+ssd_delta_desc_t delta_desc(const Tensor& x, PyObject* const* a, PyObject* const* o, int64_t lead) {
+  const Tensor& dt = device_tensor(a[1], "dt", lead + 1);
+  const Tensor& B = device_tensor(a[3], "B", lead + 2);
+  const Tensor& C = device_tensor(a[4], "C", lead + 2);
+  const Tensor& beta = device_tensor(a[5], "beta", lead + 1);
+  const auto dev = x.device();
+  const auto io = x.scalar_type();
+  const IntArrayRef shape = x.sizes();
+  ssd_delta_desc_t d{};
+  d.batch = shape[0];
+  d.seqlen = lead == 2 ? shape[1] : 1;
+  d.nheads = shape[lead];
+  d.headdim = shape[lead + 1];
+  d.ngroups = B.size(lead);
+  d.dstate = B.size(lead + 1);
+  d.io_dtype = io_code(x, "x");
+  if (dt.scalar_type() != at::kFloat && dt.scalar_type() != io)
+    bad_type("dt must be torch.float32 or " + text(io) + ", got " + text(dt.scalar_type()));
+  d.dt_dtype = io_code(dt, "dt");
+  d.scale = (float)number(o[0]);
+  d.beta_sigmoid = truth(o[1]);
+  preprocessing(d, o[2], o[3], o[4], dev, d.nheads);
+  Dims steps(shape.begin(), shape.begin() + lead + 1), bc(shape.begin(), shape.begin() + lead);
+  bc.push_back(d.ngroups);
+  bc.push_back(d.dstate);
+  d.x_stride = strides(x, "x", lead);
+  d.dt_stride = strided(dt, "dt", dt.scalar_type(), dev, steps, lead);
+  d.beta_stride = strided(beta, "beta", dt.scalar_type(), dev, steps, lead);
+  d.B_stride = strided(B, "B", io, dev, bc, lead);
+  d.C_stride = strided(C, "C", io, dev, bc, lead);
+  return d;
+}
+
+// x dt A B C beta cu_seqlens init y final want_final workspace scale beta_sigmoid bias softplus limit stream
+// -> (y, final, workspace)
+PyObject* delta_prompts(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  need_args(n, 18);
+  const Tensor& x = device_tensor(a[0], "x", 4);
+  const auto dev = x.device();
+  const ssd_delta_desc_t d = delta_desc(x, a, a + 12, 2);
+  int64_t S;
+  const int32_t* cu = offsets(a[6], dev, &S);
+  if (S > 0 && d.batch != 1) bad_value("packed sequences: x must be [1, T, H, P]");
+  const int64_t states[] = {S > 0 ? S : d.batch, d.nheads, d.headdim, d.dstate};
+  const float* A = floats(a[2], "A", dev, {d.nheads});
+  if (A == nullptr) bad_value("A is required");
+  const float* init = floats(a[7], S > 0 ? "init_states" : "init_state", dev, states);
+  Tensor y = output(a[8], "y", x.scalar_type(), x, x.sizes());
+  Tensor final_state;
+  if (a[9] != Py_None || truth(a[10]))
+    final_state = output(a[9], S > 0 ? "final_states" : "final_state", at::kFloat, x, states);
+  size_t need = 0;
+  call("ssd_delta_rule_workspace_bytes", [&] { return lib.delta_bytes(&d, S, &need); });
+  const Tensor workspace = workspace_of(a[11], need, x);
+  const void *xp = x.data_ptr(), *dt = data(a[1]), *B = data(a[3]), *C = data(a[4]), *beta = data(a[5]);
+  void *yp = y.data_ptr(), *stream = handle(a[17]);
+  void* ws = workspace.defined() ? workspace.data_ptr() : nullptr;
+  const size_t ws_bytes = workspace.defined() ? workspace.nbytes() : 0;
+  float* fin = final_state.defined() ? final_state.data_ptr<float>() : nullptr;
+  if (S > 0)
+    call("ssd_delta_rule_varlen", [&] {
+      return lib.delta_varlen(&d, cu, S, xp, dt, A, B, C, beta, init, yp, fin, ws, ws_bytes, stream);
+    });
+  else
+    call("ssd_delta_rule", [&] { return lib.delta(&d, xp, dt, A, B, C, beta, init, yp, fin, ws, ws_bytes, stream); });
+  return results(y, final_state, workspace);
+  END_HANDLE_TH_ERRORS
+}
+
+// x dt A B C beta state slots y scale beta_sigmoid bias softplus limit stream -> y
+PyObject* delta_token(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  need_args(n, 15);
+  const Tensor& x = device_tensor(a[0], "x", 3);
+  const auto dev = x.device();
+  const ssd_delta_desc_t d = delta_desc(x, a, a + 9, 1);
+  const int64_t slots = device_tensor(a[6], "state", 4).size(0);
+  const float* A = floats(a[2], "A", dev, {d.nheads});
+  if (A == nullptr) bad_value("A is required");
+  float* state = static_cast<float*>(dense(a[6], "state", at::kFloat, dev, {slots, d.nheads, d.headdim, d.dstate}));
+  const int32_t* map = static_cast<const int32_t*>(dense(a[7], "state_slots", at::kInt, dev, {d.batch}));
+  Tensor y = output(a[8], "y", x.scalar_type(), x, x.sizes());
+  const void *xp = x.data_ptr(), *dt = data(a[1]), *B = data(a[3]), *C = data(a[4]), *beta = data(a[5]);
+  void *yp = y.data_ptr(), *stream = handle(a[14]);
+  call("ssd_delta_step", [&] { return lib.delta_step(&d, xp, dt, A, B, C, beta, state, map, slots, yp, stream); });
+  return THPVariable_Wrap(y);
+  END_HANDLE_TH_ERRORS
+}
+
+// q k q_weight k_weight positions inv_freq eps l2 pairs q_out k_out stream -> q_out or (q_out, k_out)
+PyObject* head_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  need_args(n, 12);
+  const Tensor* given = tensor(a[0], "q");
+  if (given != nullptr && given->dim() != 3 && given->dim() != 4) bad_value("q must have 3 or 4 dimensions");
+  const Tensor& q = device_tensor(a[0], "q", -1);
+  const Tensor* k = tensor(a[1], "k");
+  const auto dev = q.device();
+  const int64_t dims = q.dim(), D = q.size(dims - 1);
+  auto in4 = [](const Tensor& t) { return t.dim() == 4 ? t : t.unsqueeze(0); };
+  const Tensor q4 = in4(q);
+  ssd_head_norm_desc_t d{};
+  d.batch = q4.size(0);
+  d.rows = q4.size(1);
+  d.q_heads = q4.size(2);
+  d.headdim = D;
+  d.io_dtype = io_code(q, "q");
+  d.eps = (float)number(a[6]);
+  d.l2 = truth(a[7]);
+  d.pairs = truth(a[8]);
+  d.q_stride = strides(q4, "q", 2);
+  if (k != nullptr) {
+    if (k->dim() != dims) bad_value("k must have " + std::to_string(dims) + " dimensions, got " + std::to_string(k->dim()));
+    Dims shape(q.sizes().begin(), q.sizes().end());
+    shape[dims - 2] = k->size(dims - 2);
+    check(*k, "k", q.scalar_type(), dev, shape);
+    d.k_heads = shape[dims - 2];
+    if (d.k_heads < 1) bad_value("k must have a head at least");
+    d.k_stride = strides(in4(*k), "k", 2);
+  } else if (a[3] != Py_None || a[10] != Py_None) {
+    bad_value("k_weight and k_out need k");
+  }
+  const Tensor* freq = tensor(a[5], "inv_freq");
+  if ((freq == nullptr) != (a[4] == Py_None)) bad_value("positions and inv_freq go together");
+  if (freq != nullptr) {
+    if (freq->dim() != 1) bad_value("inv_freq must have 1 dimension, got " + std::to_string(freq->dim()));
+    d.rot = 2 * freq->numel();
+  }
+  const float* fp = floats(a[5], "inv_freq", dev, {d.rot / 2});
+  const Dims tokens(q.sizes().begin(), q.sizes().end() - 2);
+  const int32_t* pos = static_cast<const int32_t*>(dense(a[4], "positions", at::kInt, dev, tokens));
+  const float *wq = floats(a[2], "q_weight", dev, {D}), *wk = floats(a[3], "k_weight", dev, {D});
+  Tensor qo = output(a[9], "q_out", q.scalar_type(), q, q.sizes()), ko;
+  if (k != nullptr) ko = output(a[10], "k_out", q.scalar_type(), q, k->sizes());
+  const void *qp = q.data_ptr(), *kp = data(a[1]);
+  void *qop = qo.data_ptr(), *kop = ko.defined() ? ko.data_ptr() : nullptr, *stream = handle(a[11]);
+  call("ssd_head_norm", [&] { return lib.head_norm(&d, qp, kp, wq, wk, pos, fp, qop, kop, stream); });
+  if (k == nullptr) return THPVariable_Wrap(qo);
+  PyObject* r = PyTuple_New(2);
+  if (r == nullptr) throw python_error();
+  PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(qo));
+  PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(ko));
+  return r;
+  END_HANDLE_TH_ERRORS
+}
+
 // strides(t, lead) -> (token, batch), 0 for dense
 PyObject* strides_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -457,7 +625,7 @@ PyObject* strides_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // bind(addresses in the order of Library, error class)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  need_args(n, 8);
+  need_args(n, 13);
   int i = 0;
   auto take = [&](auto& f) {
     f = reinterpret_cast<std::remove_reference_t<decltype(f)>>(handle(a[i++]));
@@ -470,6 +638,11 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   take(lib.conv);
   take(lib.conv_step);
   take(lib.norm);
+  take(lib.delta_bytes);
+  take(lib.delta);
+  take(lib.delta_varlen);
+  take(lib.delta_step);
+  take(lib.head_norm);
   Py_INCREF(a[i]);
   Py_XDECREF(lib.error);
   lib.error = a[i];
@@ -485,6 +658,9 @@ PyMethodDef methods[] = {FAST("bind", bind),
                          FAST("conv_prompts", conv_prompts),
                          FAST("conv_token", conv_token),
                          FAST("group_norm", group_norm),
+                         FAST("delta_prompts", delta_prompts),
+                         FAST("delta_token", delta_token),
+                         FAST("head_norm", head_norm),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
