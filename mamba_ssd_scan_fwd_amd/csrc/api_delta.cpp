@@ -12,6 +12,7 @@ struct DeltaPlan {
   DeltaArgs a;
   int io, dt;
   int64_t x_ext, dt_ext, e_ext, b_ext, c_ext;  // extents in elements
+  bool blocks;                                 // in blocks, or token after token
   size_t total;                                // workspace
 };
 
@@ -46,7 +47,18 @@ ssd_status_t plan_delta(const ssd_delta_desc_t* d, int64_t nseq, DeltaPlan* p) {
   a.dto = DtOpts{d->dt_bias, d->dt_softplus != 0, d->dt_clamp != 0, d->dt_min, d->dt_max};
   a.sigmoid = d->beta_sigmoid != 0;
   a.scale = d->scale;
+  return SSD_OK;
+}
+
+// The prompt form: the way it is walked, and the workspace that needs.
+ssd_status_t plan_rule(const ssd_delta_desc_t* d, int64_t nseq, DeltaPlan* p) {
+  const ssd_status_t st = plan_delta(d, nseq, p);
+  if (st != SSD_OK) return st;
+  p->blocks = delta_blocks_apply(p->a, p->io);
   p->total = 0;
+  if (!p->blocks) return SSD_OK;
+  if (delta_slots(p->a) > (kMaxRows - 1) / p->a.H) return SSD_ERR_BAD_SHAPE;  // waves of the first kernel
+  p->total = delta_blocks_workspace(p->a, p->io);
   return SSD_OK;
 }
 
@@ -75,7 +87,16 @@ ssd_status_t run_rule(DeltaPlan& p, const int32_t* cu, const void* x, const void
   if (overlap(rf, ri) && rf.lo != ri.lo) return SSD_ERR_ALIAS;  // the same array or none of it
   a.x = x, a.dt = dt, a.A = A, a.B = B, a.C = C, a.beta = beta, a.init = init, a.y = y, a.final_state = final_state;
   a.cu = cu;
-  return from_hip(launch_delta_walk(a, p.io, p.dt, s));
+  if (!p.blocks) return from_hip(launch_delta_walk(a, p.io, p.dt, s));
+  void* w = workspace;
+  if (w == nullptr && hipMallocAsync(&w, p.total, s) != hipSuccess) return SSD_ERR_HIP;
+  a.ws = static_cast<char*>(w);
+  hipError_t e = launch_delta_blocks(a, p.io, p.dt, s);
+  if (workspace == nullptr) {
+    const hipError_t fe = hipFreeAsync(w, s);
+    if (e == hipSuccess) e = fe;
+  }
+  return from_hip(e);
 }
 
 }  // namespace
@@ -87,7 +108,7 @@ ssd_status_t ssd_delta_rule_workspace_bytes(const ssd_delta_desc_t* desc, int64_
   if (bytes == nullptr) return SSD_ERR_NULL_POINTER;
   if (num_seqs < 0) return SSD_ERR_BAD_SHAPE;
   ssd::DeltaPlan p;
-  const ssd_status_t st = ssd::plan_delta(desc, num_seqs, &p);
+  const ssd_status_t st = ssd::plan_rule(desc, num_seqs, &p);
   if (st != SSD_OK) return st;
   if (num_seqs > 0 && desc->batch != 1) return SSD_ERR_BAD_SHAPE;
   *bytes = p.total;
@@ -98,7 +119,7 @@ ssd_status_t ssd_delta_rule(const ssd_delta_desc_t* desc, const void* x, const v
                             const void* C, const void* beta, const float* init_state, void* y, float* final_state,
                             void* workspace, size_t workspace_bytes, void* stream) {
   ssd::DeltaPlan p;
-  const ssd_status_t st = ssd::plan_delta(desc, 0, &p);
+  const ssd_status_t st = ssd::plan_rule(desc, 0, &p);
   if (st != SSD_OK) return st;
   return ssd::run_rule(p, nullptr, x, dt, A, B, C, beta, init_state, y, final_state, workspace, workspace_bytes,
                        static_cast<hipStream_t>(stream));
@@ -110,7 +131,7 @@ ssd_status_t ssd_delta_rule_varlen(const ssd_delta_desc_t* desc, const int32_t* 
                                    void* workspace, size_t workspace_bytes, void* stream) {
   ssd::DeltaPlan p;
   if (num_seqs < 1) return desc == nullptr ? SSD_ERR_NULL_POINTER : SSD_ERR_BAD_SHAPE;
-  const ssd_status_t st = ssd::plan_delta(desc, num_seqs, &p);
+  const ssd_status_t st = ssd::plan_rule(desc, num_seqs, &p);
   if (st != SSD_OK) return st;
   if (desc->batch != 1) return SSD_ERR_BAD_SHAPE;
   if (cu_seqlens == nullptr) return SSD_ERR_NULL_POINTER;

@@ -22,10 +22,24 @@ struct DeltaArgs {
   DtOpts dto;
   int sigmoid;
   float scale;
+  char* ws;                        // the workspace where the blocks take it
   int64_t seqs() const { return nseq > 0 ? nseq : batch; }
 };
 // The recurrence token after token.
 hipError_t launch_delta_walk(const DeltaArgs& a, int io, int dt, hipStream_t s);
+
+// In blocks of kDeltaBlock tokens. A sequence's blocks begin with it; the blocks
+// of all sequences lie behind one another in slots, sequence s of a packed
+// stream from slot offset / kDeltaBlock + s on (so that nobody has to sum the
+// sequences' block counts; a few slots stay empty).
+constexpr int kDeltaBlock = 64;
+inline int64_t delta_slots(const DeltaArgs& a) {
+  return a.nseq > 0 ? a.L / kDeltaBlock + a.nseq : a.batch * ((a.L + kDeltaBlock - 1) / kDeltaBlock);
+}
+bool delta_blocks_apply(const DeltaArgs& a, int io);
+size_t delta_blocks_workspace(const DeltaArgs& a, int io);
+hipError_t launch_delta_blocks(const DeltaArgs& a, int io, int dt, hipStream_t s);
+hipError_t launch_delta_solve(const DeltaArgs& a, int io, int dt, hipStream_t s);
 
 struct DeltaStepArgs {
   const void *x, *dt, *beta, *B, *C;  // one token per row

@@ -1,0 +1,282 @@
+// The gated delta rule in blocks, first kernel: for every block of 64 tokens
+// and head, the solution T = (1 + A)^-1 beta of its triangular system and its
+// scores M (delta_blocks.h), as operands for the second kernel.
+//
+// One wave to a block and head; nothing is shared, so there is no barrier.
+// K K^T and Q K^T run on the matrix cores (only the tiles on and below the
+// diagonal), operands straight from memory. The decays' exponents g_i - g_j are
+// differences of sums in 64 bits: in 32, one token that decays by e^-300 would cost
+// the tokens behind it five digits. The inverse is taken in fp32 in three
+// steps: the four 16 x 16 blocks of the diagonal by substitution, a column to a
+// lane; then T10 = -T11 A10 T00 for the two pairs of them, and once more for the
+// two halves, as products of fp32 matrix instructions, whose result in
+// registers is the right operand of the next as it stands.
+#include "delta_blocks.h"
+
+namespace ssd {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kPitch = 68;  // floats from one row of the matrix to the next
+// a token's log2 decay: exp2 of either end is 0 or infinity by far, and a sum of 64 keeps its digits
+constexpr float kMostDecay = 1024.f;
+
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+__device__ __forceinline__ f32x4_t ld4(const float* p) { return *reinterpret_cast<const f32x4_t*>(p); }
+// D += A B of 16 x 16 each: a = A[r][4 g ..], b = B[4 g ..][r]
+__device__ __forceinline__ f32x4_t mul16(const f32x4_t& a, const f32x4_t& b, f32x4_t d) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], d, 0, 0, 0);
+  return d;
+}
+
+template <typename TIO, typename TDT, int NP>
+__global__ __launch_bounds__(64 * kWaves) void delta_solve_kernel(const DeltaArgs a, int64_t tasks) {
+  constexpr int TERMS = sizeof(TIO) == 4 ? 2 : 1;
+  constexpr int KS = NP / 32;
+  using Rec = DeltaRecord<TERMS>;
+  using RD = typename Elem<TDT>::raw;
+  struct Shared {
+    float m[64 * kPitch];
+    double g[64];
+    float beta[64];
+  };
+  __shared__ __align__(16) Shared shared[kWaves];
+  const int wave = threadIdx.x / 64, lane = threadIdx.x % 64, g = lane / 16, r = lane % 16;
+  const int64_t task = (int64_t)blockIdx.x * kWaves + wave;
+  if (task >= tasks) return;
+  const int64_t slot = task / a.H;
+  const int h = (int)(task - slot * a.H);
+  const DeltaSlot at = delta_slot(a, slot);
+  if (at.n < 1) return;
+  Shared& sh = shared[wave];
+  float* m = sh.m;
+  char* rec = a.ws + task * Rec::bytes;
+
+  // keys: row 16 i + r, columns 32 ks + 8 g ..
+  const int grp = h / (a.H / a.G);
+  const TIO* Bp = static_cast<const TIO*>(a.B) + at.row * a.bs.batch + at.t0 * a.bs.token + (int64_t)grp * a.N;
+  const TIO* Cp = static_cast<const TIO*>(a.C) + at.row * a.cs.batch + at.t0 * a.cs.token + (int64_t)grp * a.N;
+  bf16x8_t k[4][KS], kl[TERMS == 2 ? 4 : 1][TERMS == 2 ? KS : 1];
+  auto rows = [&](const TIO* p, int64_t token, int i, int ks, bf16x8_t& hi, bf16x8_t& lo) {
+    const int t = 16 * i + r;
+    const bool there = t < at.n;
+    const Raw8<TIO> v = load8<TIO>(p + (there ? t : 0) * token, 32 * ks + 8 * g, a.N, there);
+    if constexpr (TERMS == 2) {
+      uint4 vh, vl;
+      split_raw(v, vh, vl);
+      hi = as_bf16x8(vh), lo = as_bf16x8(vl);
+    } else {
+      hi = as_bf16x8(v.v);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) rows(Bp, a.bs.token, i, ks, k[i][ks], kl[TERMS == 2 ? i : 0][TERMS == 2 ? ks : 0]);
+
+  // a lane to a token: beta, and the sum of the log2 decays
+  {
+    const bool there = lane < at.n;
+    const int64_t t = at.t0 + (there ? lane : 0);
+    const float dt = Elem<TDT>::f32(static_cast<const RD*>(a.dt)[at.row * a.ds.batch + t * a.ds.token + h]);
+    const float be = Elem<TDT>::f32(static_cast<const RD*>(a.beta)[at.row * a.es.batch + t * a.es.token + h]);
+    const float bias = a.dto.bias != nullptr ? a.dto.bias[h] : 0.f;
+    const float l = clamped(delta_log2_decay(dt, bias, a.A[h], a.dto), -kMostDecay, kMostDecay);
+    double sum = there ? (double)l : 0.0;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const double below = __shfl_up(sum, off, 64);
+      if (lane >= off) sum += below;
+    }
+    const double end = __shfl(sum, 63, 64);
+    sh.g[lane] = sum;
+    sh.beta[lane] = there ? delta_beta(be, a.sigmoid) : 0.f;
+    float* dec = reinterpret_cast<float*>(rec + Rec::decays);
+    dec[lane] = __builtin_amdgcn_exp2f((float)sum);
+    dec[64 + lane] = __builtin_amdgcn_exp2f((float)(end - sum));
+  }
+  wave_sync();
+
+  // A into LDS, M in registers: tile (i, j), rows 16 i + 4 g .., column 16 j + r
+  f32x4_t sc[10];
+  double gc[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) gc[j] = sh.g[16 * j + r];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    bf16x8_t q[KS], ql[TERMS == 2 ? KS : 1];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) rows(Cp, a.cs.token, i, ks, q[ks], ql[TERMS == 2 ? ks : 0]);
+    const f32x4_t beta = ld4(sh.beta + 16 * i + 4 * g);
+    double gr[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) gr[e] = sh.g[16 * i + 4 * g + e];
+#pragma unroll
+    for (int j = 0; j <= i; ++j) {
+      f32x4_t kk = {0.f, 0.f, 0.f, 0.f}, qk = kk;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        kk = mfma_16x16x32(k[i][ks], k[j][ks], kk);
+        qk = mfma_16x16x32(q[ks], k[j][ks], qk);
+        if constexpr (TERMS == 2) {
+          kk = mfma_16x16x32(k[i][ks], kl[j][ks], kk);
+          kk = mfma_16x16x32(kl[i][ks], k[j][ks], kk);
+          qk = mfma_16x16x32(q[ks], kl[j][ks], qk);
+          qk = mfma_16x16x32(ql[ks], k[j][ks], qk);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float dec = __builtin_amdgcn_exp2f((float)(gr[e] - gc[j]));
+        const int row = 4 * g + e;
+        m[(16 * i + row) * kPitch + 16 * j + r] = j < i || r < row ? beta[e] * dec * kk[e] : 0.f;
+        sc[i * (i + 1) / 2 + j][e] = j < i || r <= row ? a.scale * dec * qk[e] : 0.f;
+      }
+    }
+  }
+  wave_sync();
+
+  // the blocks of the diagonal: column r of block g
+  float x[16];
+  {
+    const float* d = m + 16 * g * kPitch + 16 * g;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float v = i == r ? 1.f : 0.f;
+#pragma unroll
+      for (int j = 0; j < i; j += 4) {
+        const f32x4_t row = ld4(d + i * kPitch + j);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (j + e < i) v = fmaf(-row[e], x[j + e], v);
+      }
+      x[i] = v;
+    }
+  }
+  wave_sync();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m[(16 * g + i) * kPitch + 16 * g + r] = x[i];
+  // zeros right of blocks 0 and 2 in the diagonal
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    m[(4 * g + e) * kPitch + 16 + r] = 0.f;
+    m[(32 + 4 * g + e) * kPitch + 48 + r] = 0.f;
+  }
+  wave_sync();
+
+  const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+  auto left = [&](int i, int j) { return ld4(m + (16 * i + r) * kPitch + 16 * j + 4 * g); };
+  auto right = [&](int i, int j) {
+    f32x4_t v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = m[(16 * i + 4 * g + e) * kPitch + 16 * j + r];
+    return v;
+  };
+  auto put = [&](int i, int j, const f32x4_t& v) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m[(16 * i + 4 * g + e) * kPitch + 16 * j + r] = -v[e];
+  };
+  {
+    const f32x4_t y0 = mul16(left(1, 0), right(0, 0), zero), y1 = mul16(left(3, 2), right(2, 2), zero);
+    const f32x4_t t0 = mul16(left(1, 1), y0, zero), t1 = mul16(left(3, 3), y1, zero);
+    wave_sync();
+    put(1, 0, t0);
+    put(3, 2, t1);
+    wave_sync();
+  }
+  {
+    f32x4_t y[2][2];
+    const f32x4_t b00 = right(0, 0), b10 = right(1, 0), b11 = right(1, 1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const f32x4_t l0 = left(2 + i, 0), l1 = left(2 + i, 1);
+      y[i][0] = mul16(l1, b10, mul16(l0, b00, zero));
+      y[i][1] = mul16(l1, b11, zero);
+    }
+    const f32x4_t a22 = left(2, 2), a32 = left(3, 2), a33 = left(3, 3);
+    f32x4_t t[2][2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      t[0][j] = mul16(a22, y[0][j], zero);
+      t[1][j] = mul16(a33, y[1][j], mul16(a32, y[0][j], zero));
+    }
+    wave_sync();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) put(2 + i, j, t[i][j]);
+    wave_sync();
+  }
+
+  // T beta: the operands' rows are 32 kk + 8 (r / 4) + 4 h + r % 4
+  auto eight = [&](int row, int col, float (&f)[8]) {
+    const f32x4_t lo = ld4(m + row * kPitch + col), hi = ld4(m + row * kPitch + col + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = lo[e], f[4 + e] = hi[e];
+  };
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+      for (int ks = 0; ks <= kk; ++ks) {
+        float f[8];
+        eight(32 * kk + 8 * (r / 4) + 4 * hh + r % 4, 32 * ks + 8 * g, f);
+        const f32x4_t b0 = ld4(sh.beta + 32 * ks + 8 * g), b1 = ld4(sh.beta + 32 * ks + 8 * g + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] *= b0[e], f[4 + e] *= b1[e];
+        uint4 hi, lo;
+        split8(f, hi, lo);
+        st16(rec + Rec::T_hi + tri_frag(kk, hh, ks) * kFragBytes + 16 * lane, hi);
+        st16(rec + Rec::T_lo + tri_frag(kk, hh, ks) * kFragBytes + 16 * lane, lo);
+      }
+  wave_sync();
+
+  // scale M: the operands' rows are 32 kk + 16 h + r
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j <= i; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m[(16 * i + 4 * g + e) * kPitch + 16 * j + r] = sc[i * (i + 1) / 2 + j][e];
+  wave_sync();
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+      for (int ks = 0; ks <= kk; ++ks) {
+        float f[8];
+        eight(32 * kk + 16 * hh + r, 32 * ks + 8 * g, f);
+        uint4 hi, lo;
+        split8(f, hi, lo);
+        st16(rec + Rec::M + tri_frag(kk, hh, ks) * kFragBytes + 16 * lane, hi);
+        if constexpr (TERMS == 2) st16(rec + Rec::M + (kTriFrags + tri_frag(kk, hh, ks)) * kFragBytes + 16 * lane, lo);
+      }
+}
+
+template <typename TIO, typename TDT>
+hipError_t launch_io(const DeltaArgs& a, hipStream_t s) {
+  const int64_t tasks = delta_slots(a) * a.H;
+  const dim3 grid((unsigned)((tasks + kWaves - 1) / kWaves));
+  if (a.N <= 32) delta_solve_kernel<TIO, TDT, 32><<<grid, 64 * kWaves, 0, s>>>(a, tasks);
+  else if (a.N <= 64) delta_solve_kernel<TIO, TDT, 64><<<grid, 64 * kWaves, 0, s>>>(a, tasks);
+  else if (a.N <= 128) delta_solve_kernel<TIO, TDT, 128><<<grid, 64 * kWaves, 0, s>>>(a, tasks);
+  else if constexpr (sizeof(TIO) == 2) delta_solve_kernel<TIO, TDT, 256><<<grid, 64 * kWaves, 0, s>>>(a, tasks);
+  else return hipErrorInvalidValue;
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_delta_solve(const DeltaArgs& a, int io, int dt, hipStream_t s) {
+  if (io == kF32) return launch_io<float, float>(a, s);
+  if (dt == kF32) return launch_io<__hip_bfloat16, float>(a, s);
+  return launch_io<__hip_bfloat16, __hip_bfloat16>(a, s);
+}
+
+}  // namespace ssd

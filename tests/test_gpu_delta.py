@@ -177,7 +177,8 @@ def test_without_decay_and_with_whole_ones(io):
     # in the state and of the difference to it: each one operand's rounding, 2^-8 of
     # up to 2 max|x| and 1 max|x| in y (two terms with fp32 io), 2^-16 in the state
     top = float(kw["x"].float().abs().max())
-    assert torch.equal(y[:, :N], kw["x"][:, :N])
+    if io == "bf16":  # (of fp32, two terms keep 16 bits)
+        assert torch.equal(y[:, :N], kw["x"][:, :N])
     assert (y.float() - kw["x"].float()).abs().max() <= (3 * 2.0 ** -16 if io == "fp32" else 4 * 2.0 ** -8) * top
     last = torch.stack([kw["x"][0, max(i for i in range(L) if i % N == n), 0] for n in range(N)], 1)
     assert (hT[0, 0] - last.float()).abs().max() <= 9 * 2.0 ** -16 * top
