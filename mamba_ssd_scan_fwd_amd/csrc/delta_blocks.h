@@ -67,32 +67,62 @@ __device__ __forceinline__ DeltaSlot delta_slot(const DeltaArgs& a, int64_t slot
   return r;
 }
 
-// Eight consecutive elements from column n on of a row of N (zeros behind it,
-// or all zeros), as they lie in memory.
-template <typename TIO> struct Raw8;
-template <> struct Raw8<__hip_bfloat16> { uint4 v; };
-template <> struct Raw8<float> { uint4 v, w; };
+// Rows of a block's tokens through a buffer descriptor: what lies behind the
+// block's last row reads as zeros, and so does an offset of kNowhere. Pieces of
+// eight elements; where N is no multiple of eight (WHOLE false) the last piece of
+// a row ends with it and is moved into place after the load.
+constexpr uint32_t kNowhere = 0x7ffffff0u;
+template <typename TIO> struct Piece;
+template <> struct Piece<__hip_bfloat16> { uint4 v; };
+template <> struct Piece<float> { uint4 v, w; };
 template <typename TIO>
-__device__ __forceinline__ Raw8<TIO> load8(const TIO* row, int n, int N, bool there) {
-  Raw8<TIO> r;
-  if (N % 8 == 0) {
-    const bool in = there && n < N;
-    const TIO* p = row + (in ? n : 0);
-    __builtin_memcpy(&r, p, sizeof(r));
-    r.v = in ? r.v : make_uint4(0, 0, 0, 0);
-    if constexpr (sizeof(TIO) == 4) r.w = in ? r.w : make_uint4(0, 0, 0, 0);
-  } else {
-    const int nn = !there || n >= N ? 0 : N - n < 8 ? N - n : 8;
-    if (nn == 8) {
-      __builtin_memcpy(&r, row + n, sizeof(r));
-    } else {
-      Pack<TIO, 8> p;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) p.v[i] = i < nn ? reinterpret_cast<const typename Elem<TIO>::raw*>(row)[n + i] : 0;
-      __builtin_memcpy(&r, &p, sizeof(r));
-    }
-  }
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t block_rows(const TIO* first, int64_t token, int n, int N) {
+  return buffer_range(const_cast<TIO*>(first), (uint32_t)((n - 1) * token + N) * (uint32_t)sizeof(TIO));
+}
+__device__ __forceinline__ uint4 buffer_ld16(__amdgpu_buffer_rsrc_t rows, uint32_t off) {
+  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rows, (int)off, 0, 0));
+}
+// Byte offset of the piece from column c on within its row, and how many
+// elements it is moved by.
+template <typename TIO, bool WHOLE>
+__device__ __forceinline__ uint32_t piece_at(int c, int N, int& moved, int len = 8) {
+  moved = 0;
+  if (c >= N) return kNowhere;
+  if (!WHOLE && c + len > N) moved = c + len - N;
+  return (uint32_t)(c - moved) * (uint32_t)sizeof(TIO);
+}
+// row: its byte offset
+template <typename TIO> __device__ __forceinline__ Piece<TIO> load_piece(__amdgpu_buffer_rsrc_t rows, uint32_t row, uint32_t at) {
+  const uint32_t off = at == kNowhere ? kNowhere : row + at;
+  Piece<TIO> r;
+  r.v = buffer_ld16(rows, off);
+  if constexpr (sizeof(TIO) == 4) r.w = buffer_ld16(rows, off + 16);
   return r;
+}
+// W words down by `moved` elements (fewer than W words'), zeros behind.
+template <typename TIO, int W> __device__ __forceinline__ void move_down(uint32_t (&w)[W], int moved) {
+  int words = moved;
+  if constexpr (sizeof(TIO) == 2) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const uint32_t above = i + 1 < W ? w[i + 1] : 0u;
+      w[i] = moved & 1 ? (w[i] >> 16) | (above << 16) : w[i];
+    }
+    words = moved / 2;
+  }
+#pragma unroll
+  for (int s = 1; s < W; s *= 2)
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = words & s ? (i + s < W ? w[i + s] : 0u) : w[i];
+}
+template <typename TIO, bool WHOLE> __device__ __forceinline__ void move_piece(Piece<TIO>& p, int moved) {
+  if constexpr (!WHOLE) {
+    constexpr int W = sizeof(Piece<TIO>) / 4;
+    uint32_t w[W];
+    __builtin_memcpy(w, &p, sizeof(p));
+    move_down<TIO, W>(w, moved);
+    __builtin_memcpy(&p, w, sizeof(p));
+  }
 }
 
 // fp32 values as a bf16 and the bf16 of what it leaves. (An infinity leaves a NaN.)
@@ -106,7 +136,7 @@ __device__ __forceinline__ void split8(const float (&f)[8], uint4& hi, uint4& lo
   split2(f[4], f[5], hi.z, lo.z);
   split2(f[6], f[7], hi.w, lo.w);
 }
-__device__ __forceinline__ void split_raw(const Raw8<float>& r, uint4& hi, uint4& lo) {
+__device__ __forceinline__ void split_piece(const Piece<float>& r, uint4& hi, uint4& lo) {
   const float f[8] = {__uint_as_float(r.v.x), __uint_as_float(r.v.y), __uint_as_float(r.v.z), __uint_as_float(r.v.w),
                       __uint_as_float(r.w.x), __uint_as_float(r.w.y), __uint_as_float(r.w.z), __uint_as_float(r.w.w)};
   split8(f, hi, lo);

@@ -41,8 +41,11 @@ template <int NP> __device__ __forceinline__ int q_swz(int t) {
 }
 __device__ __forceinline__ int x_swz(int t) { return (t & 2) | ((t >> 1) & 4); }
 
-template <typename TIO, int NP, int TERMS = BlockLds<TIO, NP>::TERMS>
-__global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs a, int blocks_p) {
+// Nothing but ordinary arithmetic is moved across.
+__device__ __forceinline__ void hold() { __builtin_amdgcn_sched_barrier(0x6); }
+
+template <typename TIO, int NP, bool WHOLE, int TERMS = BlockLds<TIO, NP>::TERMS>
+__global__ __launch_bounds__(kThreads, NP <= 128 && TERMS == 1 ? 2 : 1) void delta_blocks_kernel(const DeltaArgs a, int blocks_p) {
   using L = BlockLds<TIO, NP>;
   using Rec = DeltaRecord<TERMS>;
   constexpr int KN = NP / 32;          // 32-column groups of N
@@ -87,52 +90,46 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
     }
 
   // the next block on its way
-  Raw8<TIO> kq[2][CK];
+  Piece<TIO> kq[2][CK];
   uint4 rc[CR], xv[CX];
+  int kmoved, xmoved;
+  const int kc = tid % PACKS, xc = tid % (kCols / XP);  // this thread's piece of a row
+  const uint32_t kcol = piece_at<TIO, WHOLE>(8 * kc, a.N, kmoved);
+  const uint32_t xcol = piece_at<TIO, WHOLE>(p0 + XP * xc, a.P, xmoved, XP);
   auto fetch = [&](int64_t t0, int64_t sl) {
     const int n = (int)(last - t0 < 64 ? last - t0 : 64);
-    const char* rec = a.ws + (sl * a.H + h) * Rec::bytes;
+    const __amdgpu_buffer_rsrc_t Br = block_rows(Bp + t0 * a.bs.token, a.bs.token, n, a.N),
+                                 Cr = block_rows(Cp + t0 * a.cs.token, a.cs.token, n, a.N),
+                                 Xr = block_rows(Xp + t0 * a.xs.token, a.xs.token, n, a.P),
+                                 Rr = buffer_range(a.ws + (sl * a.H + h) * Rec::bytes, Rec::bytes);
 #pragma unroll
     for (int j = 0; j < CK; ++j) {
-      const int q = j * kThreads + tid, t = q / PACKS, c = q % PACKS;
-      const int64_t tt = t0 + (t < n ? t : 0);
-      kq[0][j] = load8<TIO>(Bp + tt * a.bs.token, 8 * c, a.N, t < n);
-      kq[1][j] = load8<TIO>(Cp + tt * a.cs.token, 8 * c, a.N, t < n);
+      const int t = (j * kThreads + tid) / PACKS;
+      kq[0][j] = load_piece<TIO>(Br, (uint32_t)(t * (int)a.bs.token) * (uint32_t)sizeof(TIO), kcol);
+      kq[1][j] = load_piece<TIO>(Cr, (uint32_t)(t * (int)a.cs.token) * (uint32_t)sizeof(TIO), kcol);
     }
 #pragma unroll
-    for (int j = 0; j < CR; ++j) {
-      const int q = j * kThreads + tid;
-      rc[j] = ld16(rec + 16 * (q < Rec::bytes / 16 ? q : 0));
-    }
+    for (int j = 0; j < CR; ++j) rc[j] = buffer_ld16(Rr, 16 * (j * kThreads + tid));
 #pragma unroll
     for (int j = 0; j < CX; ++j) {
-      const int q = j * kThreads + tid, t = q / (kCols / XP), c = q % (kCols / XP);
-      const int64_t tt = t0 + (t < n ? t : 0);
-      const int pc = p0 + c * XP;
-      const TIO* src = Xp + tt * a.xs.token;
-      const int nn = t >= n || pc >= a.P ? 0 : a.P - pc < XP ? a.P - pc : XP;
-      if (a.P % XP == 0) {
-        __builtin_memcpy(&xv[j], src + (nn > 0 ? pc : 0), 16);
-        xv[j] = nn > 0 ? xv[j] : make_uint4(0, 0, 0, 0);
-      } else {
-        Pack<TIO, XP> v;
-#pragma unroll
-        for (int i = 0; i < XP; ++i) v.v[i] = i < nn ? reinterpret_cast<const typename Elem<TIO>::raw*>(src)[pc + i] : 0;
-        __builtin_memcpy(&xv[j], &v, 16);
-      }
+      const int t = (j * kThreads + tid) / (kCols / XP);
+      const uint32_t off = (uint32_t)(t * (int)a.xs.token) * (uint32_t)sizeof(TIO) + xcol;
+      xv[j] = buffer_ld16(Xr, xcol == kNowhere ? kNowhere : off);
     }
   };
   auto stage = [&] {
 #pragma unroll
     for (int j = 0; j < CK; ++j) {
-      const int q = j * kThreads + tid, t = q / PACKS, c = q % PACKS;
+      const int t = (j * kThreads + tid) / PACKS, c = kc;
+      move_piece<TIO, WHOLE>(kq[0][j], kmoved);
+      move_piece<TIO, WHOLE>(kq[1][j], kmoved);
       unsigned char* kd = lds + L::K + t * (NP * 2) + 16 * (c ^ k_swz<NP>(t));
       unsigned char* qd = lds + L::Q + t * (NP * 2) + 16 * (c ^ q_swz<NP>(t));
       if constexpr (TERMS == 2) {
         uint4 hi, lo;
-        split_raw(kq[0][j], hi, lo);
+        split_piece(kq[0][j], hi, lo);
         st16(kd, hi), st16(kd + L::tile, lo);
-        split_raw(kq[1][j], hi, lo);
+        split_piece(kq[1][j], hi, lo);
         st16(qd, hi), st16(qd + L::tile, lo);
       } else {
         st16(kd, kq[0][j].v), st16(qd, kq[1][j].v);
@@ -145,7 +142,12 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
     }
 #pragma unroll
     for (int j = 0; j < CX; ++j) {
-      const int q = j * kThreads + tid, t = q / (kCols / XP), c = q % (kCols / XP);
+      const int t = (j * kThreads + tid) / (kCols / XP), c = xc;
+      if constexpr (!WHOLE) {
+        uint32_t w[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
+        move_down<TIO, 4>(w, xmoved);
+        xv[j] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
       if constexpr (TERMS == 2) st16(lds + L::X + t * 256 + ((16 * c + 64 * ((t >> 3) & 3)) & 255), xv[j]);
       else st16(lds + L::X + t * 128 + 16 * (c ^ x_swz(t)), xv[j]);
     }
@@ -172,7 +174,7 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
     const uint2 lo = lds_tr8(s), hi = lds_tr8(s + 4 * (NP * 2));
     return as_bf16x8(make_uint4(lo.x, lo.y, hi.x, hi.y));
   };
-  auto tri = [&](int at, int kk, int hh, int ks) { return as_bf16x8(ld16(rec + at + tri_frag(kk, hh, ks) * kFragBytes)); };
+  auto frag = [&](int at, int i) { return as_bf16x8(ld16(rec + at + i * kFragBytes)); };
   auto split_tiles = [&](const f32x4_t& t0, const f32x4_t& t1, bf16x8_t& hi, bf16x8_t& lo) {
     const float f[8] = {t0[0], t0[1], t0[2], t0[3], t1[0], t1[1], t1[2], t1[3]};
     uint4 vh, vl;
@@ -194,73 +196,141 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
     if (!live) continue;
     const int n = (int)(last - t0 < 64 ? last - t0 : 64);
 
+    // Operands are read a group ahead of the products that use them, and the
+    // order is held (hold()): the compiler by itself reads each right before its
+    // use and waits for it.
+    bf16x8_t f[2][4][TERMS];
+    auto k_group = [&](bf16x8_t (&v)[4][TERMS], int kn) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < TERMS; ++e) v[i][e] = kfrag(i / 2, i % 2, kn, e);
+    };
+    auto q_group = [&](bf16x8_t (&v)[4][TERMS], int kn) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < TERMS; ++e) v[i][e] = qfrag(i, kn, e);
+    };
+    auto kt_group = [&](bf16x8_t (&v)[4][TERMS], int kn) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < TERMS; ++e) v[i][e] = ktfrag(kn, i % 2, i / 2, e);
+    };
+    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+
     // K S0^T (rows t, column p) and S0 Q^T (rows p, column t)
-    f32x4_t R[2][2], O[4];
+    f32x4_t R[2][2] = {{zero, zero}, {zero, zero}}, O[4] = {zero, zero, zero, zero}, e[2][2];
+    float x[2][2][4];
+    uint2 xr[2][2];
+    k_group(f[0], 0);
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk)
+    for (int kn = 0; kn < KN; ++kn) {
+      if (kn + 1 < KN) k_group(f[(kn + 1) % 2], kn + 1);
+      else q_group(f[(kn + 1) % 2], 0);
+      hold();
+      auto& k = f[kn % 2];
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        R[kk][hh] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < 4; ++i) R[i / 2][i % 2] = mfma_16x16x32(k[i][0], Sh[kn], R[i / 2][i % 2]);
 #pragma unroll
-        for (int kn = 0; kn < KN; ++kn) {
-          const bf16x8_t k = kfrag(kk, hh, kn, 0);
-          R[kk][hh] = mfma_16x16x32(k, Sh[kn], R[kk][hh]);
-          R[kk][hh] = mfma_16x16x32(k, Sl[kn], R[kk][hh]);
-          if constexpr (TERMS == 2) R[kk][hh] = mfma_16x16x32(kfrag(kk, hh, kn, 1), Sh[kn], R[kk][hh]);
-        }
+      for (int i = 0; i < 4; ++i) R[i / 2][i % 2] = mfma_16x16x32(k[i][0], Sl[kn], R[i / 2][i % 2]);
+      if constexpr (TERMS == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) R[i / 2][i % 2] = mfma_16x16x32(k[i][1], Sh[kn], R[i / 2][i % 2]);
       }
+      hold();
+    }
 #pragma unroll
-    for (int tt = 0; tt < 4; ++tt) {
-      O[tt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int kn = 0; kn < KN; ++kn) {
+      if (kn + 1 < KN) {
+        q_group(f[(KN + kn + 1) % 2], kn + 1);
+      } else {
+        // X by columns, and the decays
 #pragma unroll
-      for (int kn = 0; kn < KN; ++kn) {
-        const bf16x8_t q = qfrag(tt, kn, 0);
-        O[tt] = mfma_16x16x32(Sh[kn], q, O[tt]);
-        if constexpr (TERMS == 2) {
-          O[tt] = mfma_16x16x32(Sl[kn], q, O[tt]);
-          O[tt] = mfma_16x16x32(Sh[kn], qfrag(tt, kn, 1), O[tt]);
-        }
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            e[kk][hh] = *reinterpret_cast<const f32x4_t*>(eg + 32 * kk + 8 * g + 4 * hh);
+            if constexpr (TERMS == 2) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                x[kk][hh][i] = *reinterpret_cast<const float*>(lds + L::X + (32 * kk + 8 * g + 4 * hh + i) * 256 +
+                                                               ((4 * (16 * wave + r) + 64 * g) & 255));
+            } else {
+              const int t = 32 * kk + 8 * g + 4 * hh + ta;
+              xr[kk][hh] = lds_tr8(lds + L::X + t * 128 + 16 * ((2 * wave + tb / 2) ^ x_swz(t)) + 8 * (tb & 1));
+            }
+          }
       }
+      hold();
+      auto& q = f[(KN + kn) % 2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) O[i] = mfma_16x16x32(Sh[kn], q[i][0], O[i]);
+      if constexpr (TERMS == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) O[i] = mfma_16x16x32(Sl[kn], q[i][0], O[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) O[i] = mfma_16x16x32(Sh[kn], q[i][1], O[i]);
+      }
+      hold();
     }
     // R = X - e^g K S0^T
+    bf16x8_t th[kTriFrags], tl[kTriFrags];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) th[i] = frag(Rec::T_hi, i), tl[i] = frag(Rec::T_lo, i);
+    hold();
     bf16x8_t Rh[2], Rl[2];
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
-        const f32x4_t e = *reinterpret_cast<const f32x4_t*>(eg + 32 * kk + 8 * g + 4 * hh);
-        float x[4];
-        if constexpr (TERMS == 2) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            x[i] = *reinterpret_cast<const float*>(lds + L::X + (32 * kk + 8 * g + 4 * hh + i) * 256 +
-                                                   ((4 * (16 * wave + r) + 64 * g) & 255));
-        } else {
-          const int t = 32 * kk + 8 * g + 4 * hh + ta;
-          const uint2 v = lds_tr8(lds + L::X + t * 128 + 16 * ((2 * wave + tb / 2) ^ x_swz(t)) + 8 * (tb & 1));
-          x[0] = bf16_lo(v.x), x[1] = bf16_hi(v.x), x[2] = bf16_lo(v.y), x[3] = bf16_hi(v.y);
+        if constexpr (TERMS == 1) {
+          const uint2 v = xr[kk][hh];
+          x[kk][hh][0] = bf16_lo(v.x), x[kk][hh][1] = bf16_hi(v.x), x[kk][hh][2] = bf16_lo(v.y), x[kk][hh][3] = bf16_hi(v.y);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) R[kk][hh][i] = fmaf(-e[i], R[kk][hh][i], x[i]);
+        for (int i = 0; i < 4; ++i) R[kk][hh][i] = fmaf(-e[kk][hh][i], R[kk][hh][i], x[kk][hh][i]);
       }
       split_tiles(R[kk][0], R[kk][1], Rh[kk], Rl[kk]);
     }
     // U = T R
-    f32x4_t U[2][2];
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk)
+    for (int i = 2; i < kTriFrags; ++i) th[i] = frag(Rec::T_hi, i), tl[i] = frag(Rec::T_lo, i);
+    hold();
+    f32x4_t U[2][2] = {{zero, zero}, {zero, zero}};
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        U[kk][hh] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int hh = 0; hh < 2; ++hh) U[0][hh] = mfma_16x16x32(th[hh], Rh[0], U[0][hh]);
 #pragma unroll
-        for (int ks = 0; ks <= kk; ++ks) {
-          const bf16x8_t th = tri(Rec::T_hi, kk, hh, ks);
-          U[kk][hh] = mfma_16x16x32(th, Rh[ks], U[kk][hh]);
-          U[kk][hh] = mfma_16x16x32(th, Rl[ks], U[kk][hh]);
-          U[kk][hh] = mfma_16x16x32(tri(Rec::T_lo, kk, hh, ks), Rh[ks], U[kk][hh]);
-        }
-      }
-    // Y^T = scale e^g S0 Q^T + U^T (scale M)^T
+    for (int hh = 0; hh < 2; ++hh) U[0][hh] = mfma_16x16x32(th[hh], Rl[0], U[0][hh]);
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) U[0][hh] = mfma_16x16x32(tl[hh], Rh[0], U[0][hh]);
+    hold();
+    bf16x8_t mf[kTriFrags][TERMS];
+    f32x4_t d[2][2];
+    float er[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      d[i / 2][i % 2] = *reinterpret_cast<const f32x4_t*>(ed + 32 * (i / 2) + 8 * g + 4 * (i % 2));
+      er[i] = eg[16 * i + r];
+    }
+    const float end = eg[63];
+    hold();
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) U[1][hh] = mfma_16x16x32(th[tri_frag(1, hh, ks)], Rh[ks], U[1][hh]);
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) U[1][hh] = mfma_16x16x32(th[tri_frag(1, hh, ks)], Rl[ks], U[1][hh]);
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) U[1][hh] = mfma_16x16x32(tl[tri_frag(1, hh, ks)], Rh[ks], U[1][hh]);
+    }
+#pragma unroll
+    for (int i = 0; i < kTriFrags; ++i)
+#pragma unroll
+      for (int k = 0; k < TERMS; ++k) mf[i][k] = frag(Rec::M, i + k * kTriFrags);
+    hold();
+    // Y^T = scale e^g S0 Q^T + U^T (scale M)^T, and U' = e^(g_end - g) U
     bf16x8_t Uh[2], Ul[2];
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
@@ -270,50 +340,56 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
         Uh[kk] = as_bf16x8(make_uint4(pack_bf16x2(U[kk][0][0], U[kk][0][1]), pack_bf16x2(U[kk][0][2], U[kk][0][3]),
                                       pack_bf16x2(U[kk][1][0], U[kk][1][1]), pack_bf16x2(U[kk][1][2], U[kk][1][3])));
       }
-    }
 #pragma unroll
-    for (int tt = 0; tt < 4; ++tt) {
-      const float e = a.scale * eg[16 * tt + r];
+      for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) O[tt][i] *= e;
-#pragma unroll
-      for (int ks = 0; ks <= tt / 2; ++ks) {
-        const bf16x8_t mh = tri(Rec::M, tt / 2, tt % 2, ks);
-        O[tt] = mfma_16x16x32(Uh[ks], mh, O[tt]);
-        if constexpr (TERMS == 2) {
-          O[tt] = mfma_16x16x32(Ul[ks], mh, O[tt]);
-          O[tt] = mfma_16x16x32(Uh[ks], tri(Rec::M + kTriFrags * kFragBytes, tt / 2, tt % 2, ks), O[tt]);
-        }
-      }
-    }
-    // S^T <- e^g_end S^T + K^T U'
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const f32x4_t d = *reinterpret_cast<const f32x4_t*>(ed + 32 * kk + 8 * g + 4 * hh);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) U[kk][hh][i] *= d[i];
-      }
+        for (int i = 0; i < 4; ++i) U[kk][hh][i] *= d[kk][hh][i];
       split_tiles(U[kk][0], U[kk][1], Rh[kk], Rl[kk]);
     }
-    const float end = eg[63];
+    kt_group(f[0], 0);
+    hold();
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) O[tt][i] *= a.scale * er[tt];
+    }
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int tt = 2 * ks; tt < 4; ++tt) {
+        const auto& mm = mf[tri_frag(tt / 2, tt % 2, ks)];
+        O[tt] = mfma_16x16x32(Uh[ks], mm[0], O[tt]);
+        if constexpr (TERMS == 2) {
+          O[tt] = mfma_16x16x32(Ul[ks], mm[0], O[tt]);
+          O[tt] = mfma_16x16x32(Uh[ks], mm[1], O[tt]);
+        }
+      }
+    hold();
+    // S^T <- e^g_end S^T + K^T U'
 #pragma unroll
     for (int kn = 0; kn < KN; ++kn) {
+      if (kn + 1 < KN) kt_group(f[(kn + 1) % 2], kn + 1);
+      hold();
+      auto& k = f[kn % 2];
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
+      for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
         for (int i = 0; i < 4; ++i) S[kn][hh][i] *= end;
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-          const bf16x8_t k = ktfrag(kn, hh, kk, 0);
-          S[kn][hh] = mfma_16x16x32(k, Rh[kk], S[kn][hh]);
-          S[kn][hh] = mfma_16x16x32(k, Rl[kk], S[kn][hh]);
-          if constexpr (TERMS == 2) S[kn][hh] = mfma_16x16x32(ktfrag(kn, hh, kk, 1), Rh[kk], S[kn][hh]);
+      for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) S[kn][hh] = mfma_16x16x32(k[2 * kk + hh][0], Rh[kk], S[kn][hh]);
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) S[kn][hh] = mfma_16x16x32(k[2 * kk + hh][0], Rl[kk], S[kn][hh]);
+        if constexpr (TERMS == 2) {
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) S[kn][hh] = mfma_16x16x32(k[2 * kk + hh][1], Rh[kk], S[kn][hh]);
         }
       }
-      split_tiles(S[kn][0], S[kn][1], Sh[kn], Sl[kn]);
+      hold();
     }
+#pragma unroll
+    for (int kn = 0; kn < KN; ++kn) split_tiles(S[kn][0], S[kn][1], Sh[kn], Sl[kn]);
     // rows pw + 4 g .., column t = 16 tt + r
     const int pr = pw + 4 * g, pn = a.P - pr;
 #pragma unroll
@@ -342,7 +418,9 @@ hipError_t launch_np(const DeltaArgs& a, hipStream_t s) {
   using L = BlockLds<TIO, NP>;
   static_assert(L::bytes <= 160 * 1024, "LDS of a compute unit");
   const int blocks_p = (a.P + kCols - 1) / kCols;
-  delta_blocks_kernel<TIO, NP><<<dim3((unsigned)(a.seqs() * a.H * blocks_p)), kThreads, 0, s>>>(a, blocks_p);
+  const dim3 grid((unsigned)(a.seqs() * a.H * blocks_p));
+  if (a.N % 8 == 0 && a.P % (16 / sizeof(TIO)) == 0) delta_blocks_kernel<TIO, NP, true><<<grid, kThreads, 0, s>>>(a, blocks_p);
+  else delta_blocks_kernel<TIO, NP, false><<<grid, kThreads, 0, s>>>(a, blocks_p);
   return hipGetLastError();
 }
 
@@ -358,7 +436,7 @@ hipError_t launch_io(const DeltaArgs& a, hipStream_t s) {
 }  // namespace
 
 bool delta_blocks_apply(const DeltaArgs& a, int io) {
-  return (io == kBF16 || a.N <= 128) && a.L >= 16;
+  return (io == kBF16 || a.N <= 128) && a.L >= 16 && a.N >= 8 && a.P >= 8;
 }
 size_t delta_blocks_workspace(const DeltaArgs& a, int io) {
   return size_t(delta_slots(a)) * a.H * (io == kBF16 ? DeltaRecord<1>::bytes : DeltaRecord<2>::bytes);

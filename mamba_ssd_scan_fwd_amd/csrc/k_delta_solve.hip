@@ -33,7 +33,7 @@ __device__ __forceinline__ f32x4_t mul16(const f32x4_t& a, const f32x4_t& b, f32
   return d;
 }
 
-template <typename TIO, typename TDT, int NP>
+template <typename TIO, typename TDT, int NP, bool WHOLE>
 __global__ __launch_bounds__(64 * kWaves) void delta_solve_kernel(const DeltaArgs a, int64_t tasks) {
   constexpr int TERMS = sizeof(TIO) == 4 ? 2 : 1;
   constexpr int KS = NP / 32;
@@ -61,22 +61,30 @@ __global__ __launch_bounds__(64 * kWaves) void delta_solve_kernel(const DeltaArg
   const TIO* Bp = static_cast<const TIO*>(a.B) + at.row * a.bs.batch + at.t0 * a.bs.token + (int64_t)grp * a.N;
   const TIO* Cp = static_cast<const TIO*>(a.C) + at.row * a.cs.batch + at.t0 * a.cs.token + (int64_t)grp * a.N;
   bf16x8_t k[4][KS], kl[TERMS == 2 ? 4 : 1][TERMS == 2 ? KS : 1];
-  auto rows = [&](const TIO* p, int64_t token, int i, int ks, bf16x8_t& hi, bf16x8_t& lo) {
-    const int t = 16 * i + r;
-    const bool there = t < at.n;
-    const Raw8<TIO> v = load8<TIO>(p + (there ? t : 0) * token, 32 * ks + 8 * g, a.N, there);
+  uint32_t col[KS];
+  int moved[KS];
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) col[ks] = piece_at<TIO, WHOLE>(32 * ks + 8 * g, a.N, moved[ks]);
+  auto rows = [&](__amdgpu_buffer_rsrc_t from, int64_t token, int i, Piece<TIO>(&v)[KS]) {
+    const uint32_t row = (uint32_t)((16 * i + r) * token) * (uint32_t)sizeof(TIO);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) v[ks] = load_piece<TIO>(from, row, col[ks]);
+  };
+  auto operand = [&](Piece<TIO> v, int ks, bf16x8_t& hi, bf16x8_t& lo) {
+    move_piece<TIO, WHOLE>(v, moved[ks]);
     if constexpr (TERMS == 2) {
       uint4 vh, vl;
-      split_raw(v, vh, vl);
+      split_piece(v, vh, vl);
       hi = as_bf16x8(vh), lo = as_bf16x8(vl);
     } else {
       hi = as_bf16x8(v.v);
     }
   };
+  const __amdgpu_buffer_rsrc_t Br = block_rows(Bp, a.bs.token, at.n, a.N), Cr = block_rows(Cp, a.cs.token, at.n, a.N);
+  Piece<TIO> kraw[4][KS], qraw[KS];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) rows(Bp, a.bs.token, i, ks, k[i][ks], kl[TERMS == 2 ? i : 0][TERMS == 2 ? ks : 0]);
+  for (int i = 0; i < 4; ++i) rows(Br, a.bs.token, i, kraw[i]);
+  rows(Cr, a.cs.token, 0, qraw);
 
   // a lane to a token: beta, and the sum of the log2 decays
   {
@@ -110,7 +118,11 @@ __global__ __launch_bounds__(64 * kWaves) void delta_solve_kernel(const DeltaArg
   for (int i = 0; i < 4; ++i) {
     bf16x8_t q[KS], ql[TERMS == 2 ? KS : 1];
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) rows(Cp, a.cs.token, i, ks, q[ks], ql[TERMS == 2 ? ks : 0]);
+    for (int ks = 0; ks < KS; ++ks) {
+      operand(kraw[i][ks], ks, k[i][ks], kl[TERMS == 2 ? i : 0][TERMS == 2 ? ks : 0]);
+      operand(qraw[ks], ks, q[ks], ql[TERMS == 2 ? ks : 0]);
+    }
+    if (i < 3) rows(Cr, a.cs.token, i + 1, qraw);
     const f32x4_t beta = ld4(sh.beta + 16 * i + 4 * g);
     double gr[4];
 #pragma unroll
@@ -263,10 +275,14 @@ template <typename TIO, typename TDT>
 hipError_t launch_io(const DeltaArgs& a, hipStream_t s) {
   const int64_t tasks = delta_slots(a) * a.H;
   const dim3 grid((unsigned)((tasks + kWaves - 1) / kWaves));
-  if (a.N <= 32) delta_solve_kernel<TIO, TDT, 32><<<grid, 64 * kWaves, 0, s>>>(a, tasks);
-  else if (a.N <= 64) delta_solve_kernel<TIO, TDT, 64><<<grid, 64 * kWaves, 0, s>>>(a, tasks);
-  else if (a.N <= 128) delta_solve_kernel<TIO, TDT, 128><<<grid, 64 * kWaves, 0, s>>>(a, tasks);
-  else if constexpr (sizeof(TIO) == 2) delta_solve_kernel<TIO, TDT, 256><<<grid, 64 * kWaves, 0, s>>>(a, tasks);
+  auto go = [&](auto whole, auto other) {
+    if (a.N % 8 == 0) whole<<<grid, 64 * kWaves, 0, s>>>(a, tasks);
+    else other<<<grid, 64 * kWaves, 0, s>>>(a, tasks);
+  };
+  if (a.N <= 32) go(delta_solve_kernel<TIO, TDT, 32, true>, delta_solve_kernel<TIO, TDT, 32, false>);
+  else if (a.N <= 64) go(delta_solve_kernel<TIO, TDT, 64, true>, delta_solve_kernel<TIO, TDT, 64, false>);
+  else if (a.N <= 128) go(delta_solve_kernel<TIO, TDT, 128, true>, delta_solve_kernel<TIO, TDT, 128, false>);
+  else if constexpr (sizeof(TIO) == 2) go(delta_solve_kernel<TIO, TDT, 256, true>, delta_solve_kernel<TIO, TDT, 256, false>);
   else return hipErrorInvalidValue;
   return hipGetLastError();
 }
