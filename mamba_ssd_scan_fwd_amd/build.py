@@ -50,6 +50,11 @@ COMMON = [
     "-Wno-unused-function",
 ]
 
+# per source: matrix results in ordinary registers. The compiler otherwise puts
+# accumulators of a kernel that may use more than 256 registers into the other
+# half of the file, from where every scaling and rounding has to fetch them.
+EXTRA = {name: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for name in ("k_delta_blocks.hip", "k_delta_solve.hip")}
+
 
 def hipcc() -> str:
     for cand in (shutil.which("hipcc"), "/opt/rocm/bin/hipcc"):
@@ -75,7 +80,7 @@ SAN_LIB = os.path.join(BUILD, "libssd_host_san.so")
 
 def _compile(src: str, verbose: bool, sanitize: bool = False) -> str:
     obj = os.path.join(SAN_BUILD if sanitize else BUILD, os.path.basename(src) + ".o")
-    cmd = [hipcc(), *COMMON, *(HOST_SAN if sanitize else []), "-c", src, "-o", obj]
+    cmd = [hipcc(), *COMMON, *EXTRA.get(os.path.basename(src), []), *(HOST_SAN if sanitize else []), "-c", src, "-o", obj]
     if src.endswith(".cpp"):
         cmd[1:1] = ["-x", "hip"]
     if verbose:

@@ -7,8 +7,14 @@
 //     Y = scale (e^g Q S0^T + M U),       M_ij = e^(g_i - g_j) q_i k_j     (j <= i)
 //     S = e^g_end S0 + U^T e^(g_end - g) K
 // A record holds, for one block and head, T = (1 + A)^-1 beta and scale M as
-// matrix-core operands, and the decays. T is 16 bits or more (two bf16 terms);
-// M one bf16, or two for fp32 io.
+// matrix-core operands, and the decays.
+//
+// Operands of the matrix cores are bf16, so an fp32 value enters a product as a sum
+// of terms: itself rounded, what that leaves rounded, and so on. Terms:
+//   io     B and C: 1 with bf16 io (exact), 3 with fp32 io
+//   state  S, R, T, U' (all that reaches a state): 2 with bf16 io (off by 2^-16),
+//          3 with fp32 io (off by 2^-24)
+//   y      S, U, M in y's own products: 1 with bf16 io, beside y's rounding; 3
 #pragma once
 
 #include "delta.h"
@@ -16,16 +22,60 @@
 
 namespace ssd {
 
+template <typename TIO> struct DeltaTerms {
+  static constexpr bool wide = sizeof(TIO) == 4;
+  static constexpr int io = wide ? 3 : 1, state = wide ? 3 : 2, y = wide ? 3 : 1;
+};
+
 constexpr int kTriFrags = 6;  // 16 x 32 operands of a lower triangle of 64 x 64: those of its 32 x 32 blocks
 constexpr int kFragBytes = 1024;
 // Operand of rows 32 kk + .. (half h of them) and columns 32 ks + .., ks <= kk.
 constexpr int tri_frag(int kk, int h, int ks) { return kk == 0 ? h : 2 + 2 * h + ks; }
 
-template <int TERMS> struct DeltaRecord {  // TERMS: of the io type's operands
-  static constexpr int T_hi = 0, T_lo = kTriFrags * kFragBytes, M = 2 * kTriFrags * kFragBytes,
-                       decays = M + TERMS * kTriFrags * kFragBytes,  // e^g [64], e^(g_end - g) [64]
+template <typename TIO> struct DeltaRecord {
+  static constexpr int T = 0, M = T + DeltaTerms<TIO>::state * kTriFrags * kFragBytes,
+                       decays = M + DeltaTerms<TIO>::y * kTriFrags * kFragBytes,  // e^g [64], e^(g_end - g) [64]
                        bytes = decays + 512;
 };
+
+// fp32 values as terms, packed in pairs.
+template <int T> __device__ __forceinline__ void split2(float a, float b, uint32_t (&w)[T]) {
+#pragma unroll
+  for (int i = 0; i < T; ++i) {
+    w[i] = pack_bf16x2(a, b);
+    if (i + 1 < T) a -= bf16_lo(w[i]), b -= bf16_hi(w[i]);
+  }
+}
+// Operand of T terms.
+template <int T> struct Terms { bf16x8_t v[T]; };
+template <int T> __device__ __forceinline__ Terms<T> split8(const float (&f)[8]) {
+  uint32_t w[4][T];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split2<T>(f[2 * i], f[2 * i + 1], w[i]);
+  Terms<T> r;
+#pragma unroll
+  for (int i = 0; i < T; ++i) r.v[i] = as_bf16x8(make_uint4(w[0][i], w[1][i], w[2][i], w[3][i]));
+  return r;
+}
+// acc += A B, one of its pairs of terms (all that are as large as the longer
+// operand's last): a caller spreads them over accumulators.
+constexpr int term_pairs(int ta, int tb) {
+  int n = 0;
+  for (int i = 0; i < ta; ++i)
+    for (int j = 0; j < tb; ++j) n += i + j < (ta > tb ? ta : tb);
+  return n;
+}
+template <int TA, int TB> __device__ __forceinline__ void mul_pair(f32x4_t& acc, const Terms<TA>& a, const Terms<TB>& b, int pair) {
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < TA; ++i)
+#pragma unroll
+    for (int j = 0; j < TB; ++j)
+      if (i + j < (TA > TB ? TA : TB)) {
+        if (n == pair) acc = mfma_16x16x32(a.v[i], b.v[j], acc);
+        ++n;
+      }
+}
 
 // Tokens of a slot: n (0: the slot is empty) from token t0 of batch row `row`.
 struct DeltaSlot {
@@ -125,21 +175,13 @@ template <typename TIO, bool WHOLE> __device__ __forceinline__ void move_piece(P
   }
 }
 
-// fp32 values as a bf16 and the bf16 of what it leaves. (An infinity leaves a NaN.)
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  hi = pack_bf16x2(a, b);
-  lo = pack_bf16x2(a - bf16_lo(hi), b - bf16_hi(hi));
-}
-__device__ __forceinline__ void split8(const float (&f)[8], uint4& hi, uint4& lo) {
-  split2(f[0], f[1], hi.x, lo.x);
-  split2(f[2], f[3], hi.y, lo.y);
-  split2(f[4], f[5], hi.z, lo.z);
-  split2(f[6], f[7], hi.w, lo.w);
-}
-__device__ __forceinline__ void split_piece(const Piece<float>& r, uint4& hi, uint4& lo) {
+template <int T> __device__ __forceinline__ Terms<T> split_piece(const Piece<float>& r) {
   const float f[8] = {__uint_as_float(r.v.x), __uint_as_float(r.v.y), __uint_as_float(r.v.z), __uint_as_float(r.v.w),
                       __uint_as_float(r.w.x), __uint_as_float(r.w.y), __uint_as_float(r.w.z), __uint_as_float(r.w.w)};
-  split8(f, hi, lo);
+  return split8<T>(f);
 }
+
+// Nothing is moved across by the compiler.
+__device__ __forceinline__ void hold() { __builtin_amdgcn_sched_barrier(0); }
 
 }  // namespace ssd

@@ -2,7 +2,7 @@
 // blocks of 64 tokens (delta_blocks.h has the formulas and what the first
 // kernel left), batched or packed.
 //
-// The state's rows p do not meet, so a wave keeps 16 of them, transposed
+// The state's rows p do not meet, so a wave keeps 16 PT of them, transposed
 // (S^T [N, 16] in accumulators), for the whole sequence, and nothing of the chain
 //     R = X - e^g K S0^T;  U = T R;  S^T <- e^g_end S^T + K^T (e^(g_end - g) U)
 // leaves its registers: a product's result, four consecutive rows of a column to a
@@ -10,48 +10,62 @@
 // pair of result tiles are numbered 8 (r / 4) + 4 h + r % 4 (r the row, h the tile).
 // The left operands (K by rows and by columns, Q, T, M) are shared by the
 // workgroup's four waves through LDS, its 16-byte pieces permuted so that the
-// reads by rows and the transposing ones meet few bank conflicts; the next
-// block's are loaded into registers while a block is worked on.
+// reads by rows and the transposing ones meet few bank conflicts.
 //
-// Roundings. S, R and U' = e^(g_end - g) U are held in fp32 and enter the
-// products as two bf16 terms (2^-16; K is exact with bf16 io and two terms with
-// fp32 io), so that states keep fp32's use over thousands of tokens. y's own
-// products take one bf16 term of S, U and M with bf16 io, beside y's rounding.
+// Aligned bf16 rows go from memory to the other half of the LDS while a block is
+// worked on (DMA); others through registers, where odd rows are put in order and
+// fp32 is split into terms.
+//
+// S, R and U' = e^(g_end - g) U are held in fp32. As operands they are terms
+// (delta_blocks.h).
+#include <type_traits>
+
 #include "delta_blocks.h"
 
 namespace ssd {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kCols = 64;  // rows p of a workgroup
 
-template <typename TIO, int NP> struct BlockLds {
-  static constexpr int TERMS = sizeof(TIO) == 4 ? 2 : 1;
+template <typename TIO, int NP, int PT, bool DMA> struct Layout {
+  static constexpr int IO = DeltaTerms<TIO>::io;
+  static constexpr int cols = 64 * PT;      // rows p of a workgroup
   static constexpr int tile = 64 * NP * 2;  // K or Q, one term
-  static constexpr int K = 0, Q = TERMS * tile, rec = 2 * TERMS * tile, X = rec + DeltaRecord<TERMS>::bytes,
-                       bytes = X + 64 * kCols * (int)sizeof(TIO);
+  static constexpr int xrow = cols * (int)sizeof(TIO);
+  static constexpr int K = 0, Q = IO * tile, rec = 2 * IO * tile, X = rec + (DeltaRecord<TIO>::bytes + 1023) / 1024 * 1024,
+                       half = X + 64 * xrow, bytes = DMA ? 2 * half : half;
 };
 
-// Where the 16-byte piece c of row t lies in K's and in Q's tile.
+// Where the 16-byte piece c of row t lies in K's, Q's and (bf16) X's tile: c
+// with these bits flipped.
 template <int NP> __device__ __forceinline__ int k_swz(int t) {
   return NP >= 128 ? ((t & 3) << 2) | ((t >> 3) & 3) : NP == 64 ? ((t & 2) << 1) | ((t >> 3) & 3) : (t >> 3) & 3;
 }
 template <int NP> __device__ __forceinline__ int q_swz(int t) {
   return NP >= 128 ? ((t & 3) << 2) | ((t >> 2) & 3) : NP == 64 ? ((t & 2) << 1) | ((t >> 2) & 3) : (t >> 2) & 3;
 }
-__device__ __forceinline__ int x_swz(int t) { return (t & 2) | ((t >> 1) & 4); }
+template <int PT> __device__ __forceinline__ int x_swz(int t) { return PT == 2 ? (t & 3) << 2 : (t & 2) | ((t >> 1) & 4); }
 
-// Nothing but ordinary arithmetic is moved across.
-__device__ __forceinline__ void hold() { __builtin_amdgcn_sched_barrier(0x6); }
+// One matrix product, then V ordinary instructions, M times: what runs beside what.
+template <int M, int V> __device__ __forceinline__ void spread() {
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x2, V, 0);
+  }
+}
 
-template <typename TIO, int NP, bool WHOLE, int TERMS = BlockLds<TIO, NP>::TERMS>
-__global__ __launch_bounds__(kThreads, NP <= 128 && TERMS == 1 ? 2 : 1) void delta_blocks_kernel(const DeltaArgs a, int blocks_p) {
-  using L = BlockLds<TIO, NP>;
-  using Rec = DeltaRecord<TERMS>;
+template <typename TIO, int NP, int PT, bool DMA, bool WHOLE>
+__global__ __launch_bounds__(kThreads, DMA && PT == 2 ? 2 : 1) void delta_blocks_kernel(const DeltaArgs a, int blocks_p) {
+  using L = Layout<TIO, NP, PT, DMA>;
+  using Rec = DeltaRecord<TIO>;
+  constexpr int IO = DeltaTerms<TIO>::io, ST = DeltaTerms<TIO>::state, YT = DeltaTerms<TIO>::y;
   constexpr int KN = NP / 32;          // 32-column groups of N
-  constexpr int PACKS = NP / 8;        // 16-byte pieces to a row
-  constexpr int CK = 64 * PACKS / kThreads, CR = (Rec::bytes / 16 + kThreads - 1) / kThreads,
-                CX = 64 * kCols * (int)sizeof(TIO) / 16 / kThreads, XP = 16 / (int)sizeof(TIO);
+  constexpr int PACKS = NP / 8;        // 16-byte pieces to a row of K
+  constexpr int XP = 16 / (int)sizeof(TIO), XPACKS = L::cols / XP;
+  constexpr int CK = 64 * PACKS / kThreads, CR = (Rec::bytes / 16 + kThreads - 1) / kThreads, CX = 64 * XPACKS / kThreads;
+  constexpr int SZ = (int)sizeof(TIO);
+  static_assert(!DMA || (IO == 1 && WHOLE), "rows as they lie");
   __shared__ __align__(16) unsigned char lds[L::bytes];
   const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64, g = lane / 16, r = lane % 16;
 
@@ -60,7 +74,9 @@ __global__ __launch_bounds__(kThreads, NP <= 128 && TERMS == 1 ? 2 : 1) void del
   const int64_t sh = bid / blocks_p;
   const int h = (int)(sh % a.H);
   const int64_t seq = sh / a.H;
-  const int p0 = pb * kCols, pw = p0 + 16 * wave, p = pw + r;
+  const int p0 = pb * L::cols, pw = p0 + 16 * PT * wave;
+  // column r of tile pt
+  auto column = [&](int pt) { return PT == 2 ? pw + 8 * (r / 4) + 4 * pt + r % 4 : pw + r; };
 
   int64_t row = seq, first = 0, last = a.L, slot = seq * ((a.L + kDeltaBlock - 1) / kDeltaBlock);
   if (a.cu != nullptr) {
@@ -72,356 +88,475 @@ __global__ __launch_bounds__(kThreads, NP <= 128 && TERMS == 1 ? 2 : 1) void del
   const TIO* Bp = static_cast<const TIO*>(a.B) + row * a.bs.batch + grp * a.N;
   const TIO* Cp = static_cast<const TIO*>(a.C) + row * a.cs.batch + grp * a.N;
   TIO* Yp = static_cast<TIO*>(a.y) + (row * a.L * a.H + h) * a.P;
+  const int HP = a.H * a.P;
 
-  // S^T: tile (kn, hh) rows 32 kn + 8 g + 4 hh .., column p
-  f32x4_t S[KN][2];
-  const int64_t state = (seq * a.H + h) * (int64_t)a.P + (p < a.P ? p : 0);
+  // S^T: tile (pt, kn, hh) rows 32 kn + 8 g + 4 hh .., column `column(pt)`
+  f32x4_t S[PT][KN][2];
+  Terms<ST> Sv[PT][KN];
+  auto state_at = [&](int pt) { return (seq * a.H + h) * (int64_t)a.P + (column(pt) < a.P ? column(pt) : 0); };
+  auto split_tiles = [&](auto terms, const f32x4_t& t0, const f32x4_t& t1) {
+    const float f[8] = {t0[0], t0[1], t0[2], t0[3], t1[0], t1[1], t1[2], t1[3]};
+    return split8<decltype(terms)::value>(f);
+  };
+  constexpr std::integral_constant<int, ST> st_terms{};
+  constexpr std::integral_constant<int, YT> y_terms{};
 #pragma unroll
-  for (int kn = 0; kn < KN; ++kn)
+  for (int pt = 0; pt < PT; ++pt)
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      S[kn][hh] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      const int n = 32 * kn + 8 * g + 4 * hh;
-      if (a.init != nullptr && p < a.P && n < a.N) {
-        const Pack<float, 4> v = load_pack<float, 4, true>(a.init + state * a.N + n, a.N - n);
+    for (int kn = 0; kn < KN; ++kn) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) S[kn][hh][i] = n + i < a.N ? v.v[i] : 0.f;
+      for (int hh = 0; hh < 2; ++hh) {
+        S[pt][kn][hh] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        const int n = 32 * kn + 8 * g + 4 * hh;
+        if (a.init != nullptr && column(pt) < a.P && n < a.N) {
+          const Pack<float, 4> v = load_pack<float, 4, true>(a.init + state_at(pt) * a.N + n, a.N - n);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) S[pt][kn][hh][i] = n + i < a.N ? v.v[i] : 0.f;
+        }
       }
+      Sv[pt][kn] = split_tiles(st_terms, S[pt][kn][0], S[pt][kn][1]);
     }
 
-  // the next block on its way
-  Piece<TIO> kq[2][CK];
-  uint4 rc[CR], xv[CX];
+  // ---- rows into LDS
+  struct Rows {
+    __amdgpu_buffer_rsrc_t B, C, X, R;
+  };
+  auto rows_of = [&](int64_t t0, int64_t sl) {
+    const int n = (int)(last - t0 < 64 ? last - t0 : 64);
+    return Rows{block_rows(Bp + t0 * a.bs.token, a.bs.token, n, a.N), block_rows(Cp + t0 * a.cs.token, a.cs.token, n, a.N),
+                block_rows(Xp + t0 * a.xs.token, a.xs.token, n, a.P), buffer_range(a.ws + (sl * a.H + h) * Rec::bytes, Rec::bytes)};
+  };
+  // by DMA: piece c of the LDS holds the row's piece c with the tile's bits
+  // flipped. The block to come is sent in parts, spread over the present one's work:
+  // all at once they would fill the queue and hold the wave up.
+  v4i32_t Br, Cr, Xr, Rr;
+  uint32_t dst = 0;
+  bool more = false;
+  auto aim = [&](int64_t t0, int64_t sl, int buf) {
+    const int n = (int)(last - t0 < 64 ? last - t0 : 64);
+    Br = buffer_words(Bp + t0 * a.bs.token, (uint32_t)((n - 1) * a.bs.token + a.N) * SZ);
+    Cr = buffer_words(Cp + t0 * a.cs.token, (uint32_t)((n - 1) * a.cs.token + a.N) * SZ);
+    Xr = buffer_words(Xp + t0 * a.xs.token, (uint32_t)((n - 1) * a.xs.token + a.P) * SZ);
+    Rr = buffer_words(a.ws + (sl * a.H + h) * Rec::bytes, Rec::bytes);
+    dst = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)lds + buf * L::half + wave * 1024;
+  };
+  constexpr int PARTS = 2 * CK + CX + CR;
+  auto send = [&](int i) {
+    if constexpr (DMA) {
+      if (!more) return;
+      if (i < 2 * CK) {
+        const int j = i / 2, t = (j * kThreads + tid) / PACKS, c = tid % PACKS;
+        const int n = 8 * (c ^ (i % 2 == 0 ? k_swz<NP>(t) : q_swz<NP>(t)));
+        const int token = (int)(i % 2 == 0 ? a.bs.token : a.cs.token);
+        dma16(i % 2 == 0 ? Br : Cr, dst + (i % 2 == 0 ? L::K : L::Q) + j * kThreads * 16,
+              n < a.N ? (uint32_t)(t * token + n) * SZ : kNowhere);
+      } else if (i < 2 * CK + CX) {
+        const int j = i - 2 * CK, t = (j * kThreads + tid) / XPACKS, c = p0 + 8 * ((tid % XPACKS) ^ x_swz<PT>(t));
+        dma16(Xr, dst + L::X + j * kThreads * 16, c < a.P ? (uint32_t)(t * (int)a.xs.token + c) * SZ : kNowhere);
+      } else if (i < PARTS) {
+        const int j = i - 2 * CK - CX;
+        if (j * 4 + wave < (Rec::bytes + 1023) / 1024) dma16(Rr, dst + L::rec + j * kThreads * 16, 16 * (j * kThreads + tid));
+      }
+    }
+  };
+  // part of the parts: step s of S
+  auto send_step = [&](int s, int steps) {
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i)
+      if (i * steps / PARTS == s) send(i);
+  };
+  // through registers
+  Piece<TIO> kq[2][DMA ? 1 : CK];
+  uint4 rc[DMA ? 1 : CR], xv[DMA ? 1 : CX];
   int kmoved, xmoved;
-  const int kc = tid % PACKS, xc = tid % (kCols / XP);  // this thread's piece of a row
+  const int kc = tid % PACKS, xc = tid % XPACKS;  // this thread's piece of a row
   const uint32_t kcol = piece_at<TIO, WHOLE>(8 * kc, a.N, kmoved);
   const uint32_t xcol = piece_at<TIO, WHOLE>(p0 + XP * xc, a.P, xmoved, XP);
   auto fetch = [&](int64_t t0, int64_t sl) {
-    const int n = (int)(last - t0 < 64 ? last - t0 : 64);
-    const __amdgpu_buffer_rsrc_t Br = block_rows(Bp + t0 * a.bs.token, a.bs.token, n, a.N),
-                                 Cr = block_rows(Cp + t0 * a.cs.token, a.cs.token, n, a.N),
-                                 Xr = block_rows(Xp + t0 * a.xs.token, a.xs.token, n, a.P),
-                                 Rr = buffer_range(a.ws + (sl * a.H + h) * Rec::bytes, Rec::bytes);
+    if constexpr (!DMA) {
+      const Rows from = rows_of(t0, sl);
 #pragma unroll
-    for (int j = 0; j < CK; ++j) {
-      const int t = (j * kThreads + tid) / PACKS;
-      kq[0][j] = load_piece<TIO>(Br, (uint32_t)(t * (int)a.bs.token) * (uint32_t)sizeof(TIO), kcol);
-      kq[1][j] = load_piece<TIO>(Cr, (uint32_t)(t * (int)a.cs.token) * (uint32_t)sizeof(TIO), kcol);
-    }
+      for (int j = 0; j < CK; ++j) {
+        const int t = (j * kThreads + tid) / PACKS;
+        kq[0][j] = load_piece<TIO>(from.B, (uint32_t)(t * (int)a.bs.token) * SZ, kcol);
+        kq[1][j] = load_piece<TIO>(from.C, (uint32_t)(t * (int)a.cs.token) * SZ, kcol);
+      }
 #pragma unroll
-    for (int j = 0; j < CR; ++j) rc[j] = buffer_ld16(Rr, 16 * (j * kThreads + tid));
+      for (int j = 0; j < CR; ++j) rc[j] = buffer_ld16(from.R, 16 * (j * kThreads + tid));
 #pragma unroll
-    for (int j = 0; j < CX; ++j) {
-      const int t = (j * kThreads + tid) / (kCols / XP);
-      const uint32_t off = (uint32_t)(t * (int)a.xs.token) * (uint32_t)sizeof(TIO) + xcol;
-      xv[j] = buffer_ld16(Xr, xcol == kNowhere ? kNowhere : off);
+      for (int j = 0; j < CX; ++j) {
+        const int t = (j * kThreads + tid) / XPACKS;
+        xv[j] = buffer_ld16(from.X, xcol == kNowhere ? kNowhere : (uint32_t)(t * (int)a.xs.token) * SZ + xcol);
+      }
     }
   };
   auto stage = [&] {
+    if constexpr (!DMA) {
 #pragma unroll
-    for (int j = 0; j < CK; ++j) {
-      const int t = (j * kThreads + tid) / PACKS, c = kc;
-      move_piece<TIO, WHOLE>(kq[0][j], kmoved);
-      move_piece<TIO, WHOLE>(kq[1][j], kmoved);
-      unsigned char* kd = lds + L::K + t * (NP * 2) + 16 * (c ^ k_swz<NP>(t));
-      unsigned char* qd = lds + L::Q + t * (NP * 2) + 16 * (c ^ q_swz<NP>(t));
-      if constexpr (TERMS == 2) {
-        uint4 hi, lo;
-        split_piece(kq[0][j], hi, lo);
-        st16(kd, hi), st16(kd + L::tile, lo);
-        split_piece(kq[1][j], hi, lo);
-        st16(qd, hi), st16(qd + L::tile, lo);
-      } else {
-        st16(kd, kq[0][j].v), st16(qd, kq[1][j].v);
+      for (int j = 0; j < CK; ++j) {
+        const int t = (j * kThreads + tid) / PACKS;
+        unsigned char* kd = lds + L::K + t * (NP * 2) + 16 * (kc ^ k_swz<NP>(t));
+        unsigned char* qd = lds + L::Q + t * (NP * 2) + 16 * (kc ^ q_swz<NP>(t));
+        move_piece<TIO, WHOLE>(kq[0][j], kmoved);
+        move_piece<TIO, WHOLE>(kq[1][j], kmoved);
+        if constexpr (IO > 1) {
+          const Terms<IO> k = split_piece<IO>(kq[0][j]), q = split_piece<IO>(kq[1][j]);
+#pragma unroll
+          for (int i = 0; i < IO; ++i) {
+            st16(kd + i * L::tile, __builtin_bit_cast(uint4, k.v[i]));
+            st16(qd + i * L::tile, __builtin_bit_cast(uint4, q.v[i]));
+          }
+        } else {
+          st16(kd, kq[0][j].v), st16(qd, kq[1][j].v);
+        }
       }
-    }
 #pragma unroll
-    for (int j = 0; j < CR; ++j) {
-      const int q = j * kThreads + tid;
-      if (q < Rec::bytes / 16) st16(lds + L::rec + 16 * q, rc[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < CX; ++j) {
-      const int t = (j * kThreads + tid) / (kCols / XP), c = xc;
-      if constexpr (!WHOLE) {
-        uint32_t w[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
-        move_down<TIO, 4>(w, xmoved);
-        xv[j] = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int j = 0; j < CR; ++j) {
+        const int q = j * kThreads + tid;
+        if (q < Rec::bytes / 16) st16(lds + L::rec + 16 * q, rc[j]);
       }
-      if constexpr (TERMS == 2) st16(lds + L::X + t * 256 + ((16 * c + 64 * ((t >> 3) & 3)) & 255), xv[j]);
-      else st16(lds + L::X + t * 128 + 16 * (c ^ x_swz(t)), xv[j]);
+#pragma unroll
+      for (int j = 0; j < CX; ++j) {
+        const int t = (j * kThreads + tid) / XPACKS;
+        if constexpr (!WHOLE) {
+          uint32_t w[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
+          move_down<TIO, 4>(w, xmoved);
+          xv[j] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if constexpr (SZ == 4) st16(lds + L::X + t * L::xrow + ((16 * xc + 64 * ((t >> 3) & 3)) & 255), xv[j]);
+        else st16(lds + L::X + t * L::xrow + 16 * (xc ^ x_swz<PT>(t)), xv[j]);
+      }
     }
   };
 
-  // this lane's operands in LDS
+  // ---- this lane's operands in LDS
   const int rt = 8 * (r / 4) + r % 4;  // its row of a pair of tiles
   const int ta = r / 4, tb = r % 4;    // its row and piece of a transposing read
-  const unsigned char* kbase = lds + L::K + rt * (NP * 2);
-  const unsigned char* qbase = lds + L::Q + r * (NP * 2);
-  const unsigned char* tbase = lds + L::K + (8 * g + ta) * (NP * 2);
+  const int kat = L::K + rt * (NP * 2), qat = L::Q + r * (NP * 2), tat = L::K + (8 * g + ta) * (NP * 2);
   const int kf = k_swz<NP>(rt), qf = q_swz<NP>(r), tf = k_swz<NP>(8 * g + ta);
-  const unsigned char* rec = lds + L::rec + 16 * lane;
-  const float* eg = reinterpret_cast<const float*>(lds + L::rec + Rec::decays);
-  const float* ed = eg + 64;
-  auto kfrag = [&](int kk, int hh, int kn, int term) {
-    return as_bf16x8(ld16(kbase + term * L::tile + (32 * kk + 4 * hh) * (NP * 2) + 16 * ((4 * kn + g) ^ kf)));
-  };
-  auto qfrag = [&](int tt, int kn, int term) {
-    return as_bf16x8(ld16(qbase + term * L::tile + 16 * tt * (NP * 2) + 16 * ((4 * kn + g) ^ qf)));
-  };
-  auto ktfrag = [&](int kn, int hh, int kk, int term) {
-    const unsigned char* s = tbase + term * L::tile + 32 * kk * (NP * 2) + 16 * ((4 * kn + tb) ^ tf) + 8 * hh;
-    const uint2 lo = lds_tr8(s), hi = lds_tr8(s + 4 * (NP * 2));
-    return as_bf16x8(make_uint4(lo.x, lo.y, hi.x, hi.y));
-  };
-  auto frag = [&](int at, int i) { return as_bf16x8(ld16(rec + at + i * kFragBytes)); };
-  auto split_tiles = [&](const f32x4_t& t0, const f32x4_t& t1, bf16x8_t& hi, bf16x8_t& lo) {
-    const float f[8] = {t0[0], t0[1], t0[2], t0[3], t1[0], t1[1], t1[2], t1[3]};
-    uint4 vh, vl;
-    split8(f, vh, vl);
-    hi = as_bf16x8(vh), lo = as_bf16x8(vl);
-  };
-
-  bf16x8_t Sh[KN], Sl[KN];
-#pragma unroll
-  for (int kn = 0; kn < KN; ++kn) split_tiles(S[kn][0], S[kn][1], Sh[kn], Sl[kn]);
 
   const bool live = pw < a.P;
-  if (first < last) fetch(first, slot);
+  int buf = 0;
+  if (first < last) {
+    if constexpr (DMA) {
+      more = true;
+      aim(first, slot, 0);
+      send_step(0, 1);
+    } else {
+      fetch(first, slot);
+    }
+  }
   for (int64_t t0 = first; t0 < last; t0 += 64, ++slot) {
-    __syncthreads();  // the last block's operands have been read
-    stage();
-    __syncthreads();
-    if (t0 + 64 < last) fetch(t0 + 64, slot + 1);
+    if constexpr (DMA) {
+      // this block's rows are there (the last block's four stores are younger)
+      if (live && t0 != first) vm_wait<4>();
+      else vm_wait<0>();
+      __syncthreads();
+      more = t0 + 64 < last;
+      if (more) aim(t0 + 64, slot + 1, buf ^ 1);
+      if (!live) send_step(0, 1);
+    } else {
+      __syncthreads();  // the last block's operands have been read
+      stage();
+      __syncthreads();
+      if (t0 + 64 < last) fetch(t0 + 64, slot + 1);
+    }
+    const unsigned char* at = lds + buf * L::half;
+    if constexpr (DMA) buf ^= 1;
     if (!live) continue;
     const int n = (int)(last - t0 < 64 ? last - t0 : 64);
 
-    // Operands are read a group ahead of the products that use them, and the
-    // order is held (hold()): the compiler by itself reads each right before its
-    // use and waits for it.
-    bf16x8_t f[2][4][TERMS];
-    auto k_group = [&](bf16x8_t (&v)[4][TERMS], int kn) {
+    const float* eg = reinterpret_cast<const float*>(at + L::rec + Rec::decays);
+    const float* ed = eg + 64;
+    auto kfrag = [&](int i, int kn) {  // rows of tile i, columns 32 kn ..
+      Terms<IO> v;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < TERMS; ++e) v[i][e] = kfrag(i / 2, i % 2, kn, e);
+      for (int e = 0; e < IO; ++e)
+        v.v[e] = as_bf16x8(ld16(at + kat + e * L::tile + (32 * (i / 2) + 4 * (i % 2)) * (NP * 2) + 16 * ((4 * kn + g) ^ kf)));
+      return v;
     };
-    auto q_group = [&](bf16x8_t (&v)[4][TERMS], int kn) {
+    auto qfrag = [&](int i, int kn) {
+      Terms<IO> v;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < TERMS; ++e) v[i][e] = qfrag(i, kn, e);
+      for (int e = 0; e < IO; ++e) v.v[e] = as_bf16x8(ld16(at + qat + e * L::tile + 16 * i * (NP * 2) + 16 * ((4 * kn + g) ^ qf)));
+      return v;
     };
-    auto kt_group = [&](bf16x8_t (&v)[4][TERMS], int kn) {
+    auto ktfrag = [&](int hh, int kk, int kn) {  // tile hh of columns 32 kn .., rows 32 kk ..
+      Terms<IO> v;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < TERMS; ++e) v[i][e] = ktfrag(kn, i % 2, i / 2, e);
-    };
-    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-
-    // K S0^T (rows t, column p) and S0 Q^T (rows p, column t)
-    f32x4_t R[2][2] = {{zero, zero}, {zero, zero}}, O[4] = {zero, zero, zero, zero}, e[2][2];
-    float x[2][2][4];
-    uint2 xr[2][2];
-    k_group(f[0], 0);
-#pragma unroll
-    for (int kn = 0; kn < KN; ++kn) {
-      if (kn + 1 < KN) k_group(f[(kn + 1) % 2], kn + 1);
-      else q_group(f[(kn + 1) % 2], 0);
-      hold();
-      auto& k = f[kn % 2];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) R[i / 2][i % 2] = mfma_16x16x32(k[i][0], Sh[kn], R[i / 2][i % 2]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) R[i / 2][i % 2] = mfma_16x16x32(k[i][0], Sl[kn], R[i / 2][i % 2]);
-      if constexpr (TERMS == 2) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) R[i / 2][i % 2] = mfma_16x16x32(k[i][1], Sh[kn], R[i / 2][i % 2]);
+      for (int e = 0; e < IO; ++e) {
+        const unsigned char* s = at + tat + e * L::tile + 32 * kk * (NP * 2) + 16 * ((4 * kn + tb) ^ tf) + 8 * hh;
+        const uint2 lo = lds_tr8(s), hi = lds_tr8(s + 4 * (NP * 2));
+        v.v[e] = as_bf16x8(make_uint4(lo.x, lo.y, hi.x, hi.y));
       }
-      hold();
-    }
+      return v;
+    };
+    auto tri = [&](auto terms, int from, int i) {
+      Terms<decltype(terms)::value> v;
+#pragma unroll
+      for (int e = 0; e < decltype(terms)::value; ++e)
+        v.v[e] = as_bf16x8(ld16(at + L::rec + 16 * lane + from + (e * kTriFrags + i) * kFragBytes));
+      return v;
+    };
+    auto of_y = [&](const Terms<ST>& s) {
+      Terms<YT> v;
+#pragma unroll
+      for (int e = 0; e < YT; ++e) v.v[e] = s.v[e];
+      return v;
+    };
+
+    // Operands are read a group ahead of the products that use them, and the
+    // order is held: the compiler by itself reads each right before its use and
+    // waits for it.
+    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+    constexpr int STEPS = 2 * KN + PT;
+    const float end = eg[63];
+    f32x4_t R[PT][4], O[PT][4], e[4];
+    float xw[PT][4][4];
+    uint2 xr[PT][4];
+#pragma unroll
+    for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) R[pt][i] = O[pt][i] = zero;
+    Terms<IO> f[2][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[0][i] = kfrag(i, 0);
+
+    // K S0^T (rows t, column p); beside it S^T e^g_end
 #pragma unroll
     for (int kn = 0; kn < KN; ++kn) {
       if (kn + 1 < KN) {
-        q_group(f[(KN + kn + 1) % 2], kn + 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[(kn + 1) % 2][i] = kfrag(i, kn + 1);
       } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[(kn + 1) % 2][i] = qfrag(i, 0);
         // X by columns, and the decays
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
+        for (int i = 0; i < 4; ++i) {
+          const int tr = 32 * (i / 2) + 8 * g + 4 * (i % 2);
+          e[i] = *reinterpret_cast<const f32x4_t*>(eg + tr);
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            e[kk][hh] = *reinterpret_cast<const f32x4_t*>(eg + 32 * kk + 8 * g + 4 * hh);
-            if constexpr (TERMS == 2) {
+          for (int pt = 0; pt < PT; ++pt) {
+            if constexpr (SZ == 4) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                x[kk][hh][i] = *reinterpret_cast<const float*>(lds + L::X + (32 * kk + 8 * g + 4 * hh + i) * 256 +
-                                                               ((4 * (16 * wave + r) + 64 * g) & 255));
+              for (int k = 0; k < 4; ++k)
+                xw[pt][i][k] = *reinterpret_cast<const float*>(at + L::X + (tr + k) * L::xrow + ((4 * (16 * wave + r) + 64 * g) & 255));
             } else {
-              const int t = 32 * kk + 8 * g + 4 * hh + ta;
-              xr[kk][hh] = lds_tr8(lds + L::X + t * 128 + 16 * ((2 * wave + tb / 2) ^ x_swz(t)) + 8 * (tb & 1));
+              const int t = tr + ta, c = PT == 2 ? 4 * wave + tb : 2 * wave + tb / 2, half = PT == 2 ? pt : tb & 1;
+              xr[pt][i] = lds_tr8(at + L::X + t * L::xrow + 16 * (c ^ x_swz<PT>(t)) + 8 * half);
             }
           }
-      }
-      hold();
-      auto& q = f[(KN + kn) % 2];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) O[i] = mfma_16x16x32(Sh[kn], q[i][0], O[i]);
-      if constexpr (TERMS == 2) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) O[i] = mfma_16x16x32(Sl[kn], q[i][0], O[i]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) O[i] = mfma_16x16x32(Sh[kn], q[i][1], O[i]);
-      }
-      hold();
-    }
-    // R = X - e^g K S0^T
-    bf16x8_t th[kTriFrags], tl[kTriFrags];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) th[i] = frag(Rec::T_hi, i), tl[i] = frag(Rec::T_lo, i);
-    hold();
-    bf16x8_t Rh[2], Rl[2];
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        if constexpr (TERMS == 1) {
-          const uint2 v = xr[kk][hh];
-          x[kk][hh][0] = bf16_lo(v.x), x[kk][hh][1] = bf16_hi(v.x), x[kk][hh][2] = bf16_lo(v.y), x[kk][hh][3] = bf16_hi(v.y);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) R[kk][hh][i] = fmaf(-e[kk][hh][i], R[kk][hh][i], x[kk][hh][i]);
-      }
-      split_tiles(R[kk][0], R[kk][1], Rh[kk], Rl[kk]);
-    }
-    // U = T R
-#pragma unroll
-    for (int i = 2; i < kTriFrags; ++i) th[i] = frag(Rec::T_hi, i), tl[i] = frag(Rec::T_lo, i);
-    hold();
-    f32x4_t U[2][2] = {{zero, zero}, {zero, zero}};
-#pragma unroll
-    for (int hh = 0; hh < 2; ++hh) U[0][hh] = mfma_16x16x32(th[hh], Rh[0], U[0][hh]);
-#pragma unroll
-    for (int hh = 0; hh < 2; ++hh) U[0][hh] = mfma_16x16x32(th[hh], Rl[0], U[0][hh]);
-#pragma unroll
-    for (int hh = 0; hh < 2; ++hh) U[0][hh] = mfma_16x16x32(tl[hh], Rh[0], U[0][hh]);
-    hold();
-    bf16x8_t mf[kTriFrags][TERMS];
-    f32x4_t d[2][2];
-    float er[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      d[i / 2][i % 2] = *reinterpret_cast<const f32x4_t*>(ed + 32 * (i / 2) + 8 * g + 4 * (i % 2));
-      er[i] = eg[16 * i + r];
-    }
-    const float end = eg[63];
-    hold();
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) U[1][hh] = mfma_16x16x32(th[tri_frag(1, hh, ks)], Rh[ks], U[1][hh]);
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) U[1][hh] = mfma_16x16x32(th[tri_frag(1, hh, ks)], Rl[ks], U[1][hh]);
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) U[1][hh] = mfma_16x16x32(tl[tri_frag(1, hh, ks)], Rh[ks], U[1][hh]);
-    }
-#pragma unroll
-    for (int i = 0; i < kTriFrags; ++i)
-#pragma unroll
-      for (int k = 0; k < TERMS; ++k) mf[i][k] = frag(Rec::M, i + k * kTriFrags);
-    hold();
-    // Y^T = scale e^g S0 Q^T + U^T (scale M)^T, and U' = e^(g_end - g) U
-    bf16x8_t Uh[2], Ul[2];
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      if constexpr (TERMS == 2) {
-        split_tiles(U[kk][0], U[kk][1], Uh[kk], Ul[kk]);
-      } else {
-        Uh[kk] = as_bf16x8(make_uint4(pack_bf16x2(U[kk][0][0], U[kk][0][1]), pack_bf16x2(U[kk][0][2], U[kk][0][3]),
-                                      pack_bf16x2(U[kk][1][0], U[kk][1][1]), pack_bf16x2(U[kk][1][2], U[kk][1][3])));
-      }
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) U[kk][hh][i] *= d[kk][hh][i];
-      split_tiles(U[kk][0], U[kk][1], Rh[kk], Rl[kk]);
-    }
-    kt_group(f[0], 0);
-    hold();
-#pragma unroll
-    for (int tt = 0; tt < 4; ++tt) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) O[tt][i] *= a.scale * er[tt];
-    }
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-      for (int tt = 2 * ks; tt < 4; ++tt) {
-        const auto& mm = mf[tri_frag(tt / 2, tt % 2, ks)];
-        O[tt] = mfma_16x16x32(Uh[ks], mm[0], O[tt]);
-        if constexpr (TERMS == 2) {
-          O[tt] = mfma_16x16x32(Ul[ks], mm[0], O[tt]);
-          O[tt] = mfma_16x16x32(Uh[ks], mm[1], O[tt]);
         }
       }
-    hold();
-    // S^T <- e^g_end S^T + K^T U'
+      hold();
+#pragma unroll
+      for (int pair = 0; pair < term_pairs(IO, ST); ++pair)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int pt = 0; pt < PT; ++pt) mul_pair(R[pt][i], f[kn % 2][i], Sv[pt][kn], pair);
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) S[pt][kn][i / 4][i % 4] *= end;
+      spread<4 * PT * term_pairs(IO, ST), 1>();
+      hold();
+      send_step(kn, STEPS);
+    }
+    // S0 Q^T (rows p, column t); beside it R = X - e^g K S0^T
+    Terms<ST> Rv[PT][2];
+    Terms<ST> tf_[kTriFrags];
 #pragma unroll
     for (int kn = 0; kn < KN; ++kn) {
-      if (kn + 1 < KN) kt_group(f[(kn + 1) % 2], kn + 1);
+      if (kn + 1 < KN) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[(KN + kn + 1) % 2][i] = qfrag(i, kn + 1);
+      }
+#pragma unroll
+      for (int i = 0; i < kTriFrags; ++i)
+        if (i * KN / kTriFrags == kn) tf_[i] = tri(st_terms, Rec::T, i);
       hold();
-      auto& k = f[kn % 2];
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh)
+      for (int pair = 0; pair < term_pairs(YT, IO); ++pair)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) S[kn][hh][i] *= end;
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int pt = 0; pt < PT; ++pt) mul_pair(O[pt][i], of_y(Sv[pt][kn]), f[(KN + kn) % 2][i], pair);
+#pragma unroll
+      for (int u = 0; u < 2 * PT; ++u) {
+        if (u * KN / (2 * PT) != kn) continue;
+        const int pt = u / 2, kk = u % 2;
+#pragma unroll
+        for (int i = 2 * kk; i < 2 * kk + 2; ++i) {
+          if constexpr (SZ == 2) {
+            xw[pt][i][0] = bf16_lo(xr[pt][i].x), xw[pt][i][1] = bf16_hi(xr[pt][i].x);
+            xw[pt][i][2] = bf16_lo(xr[pt][i].y), xw[pt][i][3] = bf16_hi(xr[pt][i].y);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) R[pt][i][k] = fmaf(-e[i][k], R[pt][i][k], xw[pt][i][k]);
+        }
+        Rv[pt][kk] = split_tiles(st_terms, R[pt][2 * kk], R[pt][2 * kk + 1]);
+      }
+      spread<4 * PT * term_pairs(YT, IO), 3>();
+      hold();
+      send_step(KN + kn, STEPS);
+    }
+    // U = T R, one 16 columns after the other; beside the first O e^g, beside the
+    // others, and beside U^T (scale M)^T, what becomes of the one before
+    f32x4_t U[PT][4], d[4];
+    float er[4];
+    Terms<YT> mf[kTriFrags], Uy[PT][2];
+    auto turn_u = [&](int pt) {  // operands of y, and U' = e^(g_end - g) U
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
+        Uy[pt][kk] = split_tiles(y_terms, U[pt][2 * kk], U[pt][2 * kk + 1]);
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) S[kn][hh] = mfma_16x16x32(k[2 * kk + hh][0], Rh[kk], S[kn][hh]);
+        for (int i = 2 * kk; i < 2 * kk + 2; ++i)
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) S[kn][hh] = mfma_16x16x32(k[2 * kk + hh][0], Rl[kk], S[kn][hh]);
-        if constexpr (TERMS == 2) {
+          for (int k = 0; k < 4; ++k) U[pt][i][k] *= d[i][k];
+        Rv[pt][kk] = split_tiles(st_terms, U[pt][2 * kk], U[pt][2 * kk + 1]);
+      }
+    };
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) S[kn][hh] = mfma_16x16x32(k[2 * kk + hh][1], Rh[kk], S[kn][hh]);
+    for (int i = 0; i < 4; ++i) er[i] = eg[16 * i + r];
+    hold();
+#pragma unroll
+    for (int pt = 0; pt < PT; ++pt) {
+      if (pt == PT - 1) {
+#pragma unroll
+        for (int i = 0; i < kTriFrags; ++i) mf[i] = tri(y_terms, Rec::M, i);
+        hold();
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) U[pt][i] = zero;
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int pair = 0; pair < term_pairs(ST, ST); ++pair)
+#pragma unroll
+          for (int i = 2 * ks; i < 4; ++i) mul_pair(U[pt][i], tf_[tri_frag(i / 2, i % 2, ks)], Rv[pt][ks], pair);
+      if (pt == 0) {
+#pragma unroll
+        for (int q = 0; q < PT; ++q)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) O[q][i][k] *= a.scale * er[i];
+      } else {
+        turn_u(pt - 1);
+      }
+      spread<6 * term_pairs(ST, ST), 4>();
+      hold();
+      send_step(2 * KN + pt, STEPS);
+      if (pt == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = *reinterpret_cast<const f32x4_t*>(ed + 32 * (i / 2) + 8 * g + 4 * (i % 2));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[0][i] = ktfrag(i % 2, i / 2, 0);
+    hold();
+    auto times_m = [&](int pt) {
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int pair = 0; pair < term_pairs(YT, YT); ++pair)
+#pragma unroll
+          for (int i = 2 * ks; i < 4; ++i) mul_pair(O[pt][i], Uy[pt][ks], mf[tri_frag(i / 2, i % 2, ks)], pair);
+    };
+    if constexpr (PT == 2) times_m(0);
+    turn_u(PT - 1);
+    hold();
+    times_m(PT - 1);
+    // y: rows p of a lane (4, or 8 of two tiles) at token 16 i + r
+    auto put_y = [&] {
+      const __amdgpu_buffer_rsrc_t Yr = buffer_range(Yp + t0 * HP, (uint32_t)((n - 1) * HP + a.P) * SZ);
+      const int pr = pw + 4 * PT * g;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t off = (uint32_t)((16 * i + r) * HP + pr) * SZ;
+        if constexpr (WHOLE) {
+          const uint32_t to = pr < a.P ? off : kNowhere;
+          if constexpr (SZ == 4) {
+            buffer_st16(__builtin_bit_cast(uint4, O[0][i]), Yr, to);
+          } else {
+            const uint2 lo = make_uint2(pack_bf16x2(O[0][i][0], O[0][i][1]), pack_bf16x2(O[0][i][2], O[0][i][3]));
+            if constexpr (PT == 2)
+              buffer_st16(make_uint4(lo.x, lo.y, pack_bf16x2(O[1][i][0], O[1][i][1]), pack_bf16x2(O[1][i][2], O[1][i][3])), Yr, to);
+            else
+              buffer_st8(lo, Yr, to);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4 * PT; ++k) {
+            const uint32_t to = pr + k < a.P ? off + k * SZ : kNowhere;
+            const float v = O[k / 4][i][k % 4];
+            if constexpr (SZ == 4) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), Yr, (int)to, 0, 0);
+            else __builtin_amdgcn_raw_buffer_store_b16(bf16_bits(v), Yr, (int)to, 0, 0);
+          }
         }
       }
-      hold();
-    }
+    };
+    // S^T += K^T U'; beside it the terms of the group before, and y
 #pragma unroll
-    for (int kn = 0; kn < KN; ++kn) split_tiles(S[kn][0], S[kn][1], Sh[kn], Sl[kn]);
-    // rows pw + 4 g .., column t = 16 tt + r
-    const int pr = pw + 4 * g, pn = a.P - pr;
+    for (int kn = 0; kn < KN; ++kn) {
+      if (kn + 1 < KN) {
 #pragma unroll
-    for (int tt = 0; tt < 4; ++tt) {
-      const int t = 16 * tt + r;
-      if (t < n && pn > 0) {
-        const float f[4] = {O[tt][0], O[tt][1], O[tt][2], O[tt][3]};
-        store_pack<TIO, 4, true>(Yp + (t0 + t) * a.H * a.P + pr, f, pn);
+        for (int i = 0; i < 4; ++i) f[(kn + 1) % 2][i] = ktfrag(i % 2, i / 2, kn + 1);
       }
+      hold();
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int pair = 0; pair < term_pairs(IO, ST); ++pair)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt) mul_pair(S[pt][kn][hh], f[kn % 2][2 * kk + hh], Rv[pt][kk], pair);
+      if (kn > 0) {
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) Sv[pt][kn - 1] = split_tiles(st_terms, S[pt][kn - 1][0], S[pt][kn - 1][1]);
+      }
+      spread<4 * PT * term_pairs(IO, ST), 3>();
+      hold();
+      if (kn == 0) put_y();
     }
+#pragma unroll
+    for (int pt = 0; pt < PT; ++pt) Sv[pt][KN - 1] = split_tiles(st_terms, S[pt][KN - 1][0], S[pt][KN - 1][1]);
   }
 
-  if (a.final_state == nullptr || p >= a.P) return;
+  if (a.final_state == nullptr) return;
 #pragma unroll
-  for (int kn = 0; kn < KN; ++kn)
+  for (int pt = 0; pt < PT; ++pt)
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      const int n = 32 * kn + 8 * g + 4 * hh;
-      const float f[4] = {S[kn][hh][0], S[kn][hh][1], S[kn][hh][2], S[kn][hh][3]};
-      if (n < a.N) store_pack<float, 4, true>(a.final_state + state * a.N + n, f, a.N - n);
-    }
+    for (int kn = 0; kn < KN; ++kn)
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const int n = 32 * kn + 8 * g + 4 * hh;
+        const float v[4] = {S[pt][kn][hh][0], S[pt][kn][hh][1], S[pt][kn][hh][2], S[pt][kn][hh][3]};
+        if (column(pt) < a.P && n < a.N) store_pack<float, 4, true>(a.final_state + state_at(pt) * a.N + n, v, a.N - n);
+      }
 }
 
 template <typename TIO, int NP>
 hipError_t launch_np(const DeltaArgs& a, hipStream_t s) {
-  using L = BlockLds<TIO, NP>;
-  static_assert(L::bytes <= 160 * 1024, "LDS of a compute unit");
-  const int blocks_p = (a.P + kCols - 1) / kCols;
-  const dim3 grid((unsigned)(a.seqs() * a.H * blocks_p));
-  if (a.N % 8 == 0 && a.P % (16 / sizeof(TIO)) == 0) delta_blocks_kernel<TIO, NP, true><<<grid, kThreads, 0, s>>>(a, blocks_p);
-  else delta_blocks_kernel<TIO, NP, false><<<grid, kThreads, 0, s>>>(a, blocks_p);
-  return hipGetLastError();
+  auto go = [&](auto kern, int cols) {
+    const int blocks_p = (a.P + cols - 1) / cols;
+    kern<<<dim3((unsigned)(a.seqs() * a.H * blocks_p)), kThreads, 0, s>>>(a, blocks_p);
+    return hipGetLastError();
+  };
+  constexpr int XP = 16 / (int)sizeof(TIO);
+  const bool whole = a.N % 8 == 0 && a.P % XP == 0;
+  if constexpr (sizeof(TIO) == 2 && NP <= 128) {
+    auto lies = [](const void* p, const Stride& st) {
+      return (reinterpret_cast<uintptr_t>(p) | (uintptr_t)(st.token * 2) | (uintptr_t)(st.batch * 2)) % 16 == 0;
+    };
+    if (whole && lies(a.x, a.xs) && lies(a.B, a.bs) && lies(a.C, a.cs))
+      return a.P > 64 ? go(delta_blocks_kernel<TIO, NP, 2, true, true>, 128) : go(delta_blocks_kernel<TIO, NP, 1, true, true>, 64);
+    return go(delta_blocks_kernel<TIO, NP, 1, false, false>, 64);
+  }
+  return whole ? go(delta_blocks_kernel<TIO, NP, 1, false, true>, 64) : go(delta_blocks_kernel<TIO, NP, 1, false, false>, 64);
 }
 
 template <typename TIO>
@@ -439,7 +574,7 @@ bool delta_blocks_apply(const DeltaArgs& a, int io) {
   return (io == kBF16 || a.N <= 128) && a.L >= 16 && a.N >= 8 && a.P >= 8;
 }
 size_t delta_blocks_workspace(const DeltaArgs& a, int io) {
-  return size_t(delta_slots(a)) * a.H * (io == kBF16 ? DeltaRecord<1>::bytes : DeltaRecord<2>::bytes);
+  return size_t(delta_slots(a)) * a.H * (io == kBF16 ? DeltaRecord<__hip_bfloat16>::bytes : DeltaRecord<float>::bytes);
 }
 
 hipError_t launch_delta_blocks(const DeltaArgs& a, int io, int dt, hipStream_t s) {

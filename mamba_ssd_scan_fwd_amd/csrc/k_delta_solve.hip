@@ -33,11 +33,21 @@ __device__ __forceinline__ f32x4_t mul16(const f32x4_t& a, const f32x4_t& b, f32
   return d;
 }
 
+// The same of 16 x 32 and 32 x 16: fp32 io by fp32 instructions, one of every
+// piece's elements each.
+__device__ __forceinline__ f32x4_t product(const Piece<__hip_bfloat16>& a, const Piece<__hip_bfloat16>& b, const f32x4_t& d) {
+  return mfma_16x16x32(as_bf16x8(a.v), as_bf16x8(b.v), d);
+}
+__device__ __forceinline__ f32x4_t product(const Piece<float>& a, const Piece<float>& b, f32x4_t d) {
+  d = mul16(__builtin_bit_cast(f32x4_t, a.v), __builtin_bit_cast(f32x4_t, b.v), d);
+  return mul16(__builtin_bit_cast(f32x4_t, a.w), __builtin_bit_cast(f32x4_t, b.w), d);
+}
+
 template <typename TIO, typename TDT, int NP, bool WHOLE>
 __global__ __launch_bounds__(64 * kWaves) void delta_solve_kernel(const DeltaArgs a, int64_t tasks) {
-  constexpr int TERMS = sizeof(TIO) == 4 ? 2 : 1;
   constexpr int KS = NP / 32;
-  using Rec = DeltaRecord<TERMS>;
+  constexpr int TT = DeltaTerms<TIO>::state, MT = DeltaTerms<TIO>::y;
+  using Rec = DeltaRecord<TIO>;
   using RD = typename Elem<TDT>::raw;
   struct Shared {
     float m[64 * kPitch];
@@ -60,7 +70,6 @@ __global__ __launch_bounds__(64 * kWaves) void delta_solve_kernel(const DeltaArg
   const int grp = h / (a.H / a.G);
   const TIO* Bp = static_cast<const TIO*>(a.B) + at.row * a.bs.batch + at.t0 * a.bs.token + (int64_t)grp * a.N;
   const TIO* Cp = static_cast<const TIO*>(a.C) + at.row * a.cs.batch + at.t0 * a.cs.token + (int64_t)grp * a.N;
-  bf16x8_t k[4][KS], kl[TERMS == 2 ? 4 : 1][TERMS == 2 ? KS : 1];
   uint32_t col[KS];
   int moved[KS];
 #pragma unroll
@@ -70,21 +79,11 @@ __global__ __launch_bounds__(64 * kWaves) void delta_solve_kernel(const DeltaArg
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) v[ks] = load_piece<TIO>(from, row, col[ks]);
   };
-  auto operand = [&](Piece<TIO> v, int ks, bf16x8_t& hi, bf16x8_t& lo) {
-    move_piece<TIO, WHOLE>(v, moved[ks]);
-    if constexpr (TERMS == 2) {
-      uint4 vh, vl;
-      split_piece(v, vh, vl);
-      hi = as_bf16x8(vh), lo = as_bf16x8(vl);
-    } else {
-      hi = as_bf16x8(v.v);
-    }
-  };
   const __amdgpu_buffer_rsrc_t Br = block_rows(Bp, a.bs.token, at.n, a.N), Cr = block_rows(Cp, a.cs.token, at.n, a.N);
-  Piece<TIO> kraw[4][KS], qraw[KS];
+  Piece<TIO> k[4][KS], q[2][KS];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) rows(Br, a.bs.token, i, kraw[i]);
-  rows(Cr, a.cs.token, 0, qraw);
+  for (int i = 0; i < 4; ++i) rows(Br, a.bs.token, i, k[i]);
+  rows(Cr, a.cs.token, 0, q[0]);
 
   // a lane to a token: beta, and the sum of the log2 decays
   {
@@ -116,13 +115,13 @@ __global__ __launch_bounds__(64 * kWaves) void delta_solve_kernel(const DeltaArg
   for (int j = 0; j < 4; ++j) gc[j] = sh.g[16 * j + r];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    bf16x8_t q[KS], ql[TERMS == 2 ? KS : 1];
+    if (i < 3) rows(Cr, a.cs.token, i + 1, q[(i + 1) % 2]);
+    hold();
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      operand(kraw[i][ks], ks, k[i][ks], kl[TERMS == 2 ? i : 0][TERMS == 2 ? ks : 0]);
-      operand(qraw[ks], ks, q[ks], ql[TERMS == 2 ? ks : 0]);
+      move_piece<TIO, WHOLE>(k[i][ks], moved[ks]);
+      move_piece<TIO, WHOLE>(q[i % 2][ks], moved[ks]);
     }
-    if (i < 3) rows(Cr, a.cs.token, i + 1, qraw);
     const f32x4_t beta = ld4(sh.beta + 16 * i + 4 * g);
     double gr[4];
 #pragma unroll
@@ -132,14 +131,8 @@ __global__ __launch_bounds__(64 * kWaves) void delta_solve_kernel(const DeltaArg
       f32x4_t kk = {0.f, 0.f, 0.f, 0.f}, qk = kk;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        kk = mfma_16x16x32(k[i][ks], k[j][ks], kk);
-        qk = mfma_16x16x32(q[ks], k[j][ks], qk);
-        if constexpr (TERMS == 2) {
-          kk = mfma_16x16x32(k[i][ks], kl[j][ks], kk);
-          kk = mfma_16x16x32(kl[i][ks], k[j][ks], kk);
-          qk = mfma_16x16x32(q[ks], kl[j][ks], qk);
-          qk = mfma_16x16x32(ql[ks], k[j][ks], qk);
-        }
+        kk = product(k[i][ks], k[j][ks], kk);
+        qk = product(q[i % 2][ks], k[j][ks], qk);
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -156,18 +149,26 @@ __global__ __launch_bounds__(64 * kWaves) void delta_solve_kernel(const DeltaArg
   float x[16];
   {
     const float* d = m + 16 * g * kPitch + 16 * g;
+    // (rows are read ahead, in two parts)
+    auto part = [&](auto first, auto last) {
+      constexpr int F = first, L = last;
+      f32x4_t row[L - F][(L + 2) / 4];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float v = i == r ? 1.f : 0.f;
+      for (int i = F; i < L; ++i)
 #pragma unroll
-      for (int j = 0; j < i; j += 4) {
-        const f32x4_t row = ld4(d + i * kPitch + j);
+        for (int j = 0; j < i; j += 4) row[i - F][j / 4] = ld4(d + i * kPitch + j);
+      hold();
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (j + e < i) v = fmaf(-row[e], x[j + e], v);
+      for (int i = F; i < L; ++i) {
+        float v = i == r ? 1.f : 0.f;
+#pragma unroll
+        for (int j = 0; j < i; ++j) v = fmaf(-row[i - F][j / 4][j % 4], x[j], v);
+        x[i] = v;
       }
-      x[i] = v;
-    }
+      hold();
+    };
+    part(std::integral_constant<int, 0>{}, std::integral_constant<int, 9>{});
+    part(std::integral_constant<int, 9>{}, std::integral_constant<int, 16>{});
   }
   wave_sync();
 #pragma unroll
@@ -241,10 +242,10 @@ __global__ __launch_bounds__(64 * kWaves) void delta_solve_kernel(const DeltaArg
         const f32x4_t b0 = ld4(sh.beta + 32 * ks + 8 * g), b1 = ld4(sh.beta + 32 * ks + 8 * g + 4);
 #pragma unroll
         for (int e = 0; e < 4; ++e) f[e] *= b0[e], f[4 + e] *= b1[e];
-        uint4 hi, lo;
-        split8(f, hi, lo);
-        st16(rec + Rec::T_hi + tri_frag(kk, hh, ks) * kFragBytes + 16 * lane, hi);
-        st16(rec + Rec::T_lo + tri_frag(kk, hh, ks) * kFragBytes + 16 * lane, lo);
+        const Terms<TT> v = split8<TT>(f);
+#pragma unroll
+        for (int e = 0; e < TT; ++e)
+          st16(rec + Rec::T + (e * kTriFrags + tri_frag(kk, hh, ks)) * kFragBytes + 16 * lane, __builtin_bit_cast(uint4, v.v[e]));
       }
   wave_sync();
 
@@ -264,10 +265,10 @@ __global__ __launch_bounds__(64 * kWaves) void delta_solve_kernel(const DeltaArg
       for (int ks = 0; ks <= kk; ++ks) {
         float f[8];
         eight(32 * kk + 16 * hh + r, 32 * ks + 8 * g, f);
-        uint4 hi, lo;
-        split8(f, hi, lo);
-        st16(rec + Rec::M + tri_frag(kk, hh, ks) * kFragBytes + 16 * lane, hi);
-        if constexpr (TERMS == 2) st16(rec + Rec::M + (kTriFrags + tri_frag(kk, hh, ks)) * kFragBytes + 16 * lane, lo);
+        const Terms<MT> v = split8<MT>(f);
+#pragma unroll
+        for (int e = 0; e < MT; ++e)
+          st16(rec + Rec::M + (e * kTriFrags + tri_frag(kk, hh, ks)) * kFragBytes + 16 * lane, __builtin_bit_cast(uint4, v.v[e]));
       }
 }
 
