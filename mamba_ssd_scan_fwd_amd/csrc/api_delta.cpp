@@ -39,7 +39,7 @@ ssd_status_t plan_delta(const ssd_delta_desc_t* d, int64_t nseq, DeltaPlan* p) {
     return SSD_ERR_BAD_SHAPE;
   const int64_t rows = nseq > d->batch ? nseq : d->batch;
   if (rows > kMaxElems / (HP * d->dstate)) return SSD_ERR_BAD_SHAPE;
-  // one workgroup per row, head and (at the finest) value row: a grid's limit
+  // a workgroup per row, head and, at the finest, row of the state: a grid's limit
   if (rows > (kMaxRows - 1) / HP) return SSD_ERR_BAD_SHAPE;
   a.batch = d->batch, a.L = d->seqlen;
   a.H = (int)H, a.P = (int)d->headdim, a.N = (int)d->dstate, a.G = (int)d->ngroups;
@@ -47,6 +47,7 @@ ssd_status_t plan_delta(const ssd_delta_desc_t* d, int64_t nseq, DeltaPlan* p) {
   a.dto = DtOpts{d->dt_bias, d->dt_softplus != 0, d->dt_clamp != 0, d->dt_min, d->dt_max};
   a.sigmoid = d->beta_sigmoid != 0;
   a.scale = d->scale;
+  a.seg = 0;
   return SSD_OK;
 }
 
@@ -58,7 +59,9 @@ ssd_status_t plan_rule(const ssd_delta_desc_t* d, int64_t nseq, DeltaPlan* p) {
   p->total = 0;
   if (!p->blocks) return SSD_OK;
   if (delta_slots(p->a) > (kMaxRows - 1) / p->a.H) return SSD_ERR_BAD_SHAPE;  // waves of the first kernel
-  p->total = delta_blocks_workspace(p->a, p->io);
+  const int64_t bytes = delta_blocks_workspace(p->a, p->io);
+  if (bytes > kMaxElems) return SSD_ERR_BAD_SHAPE;
+  p->total = size_t(bytes);
   return SSD_OK;
 }
 

@@ -22,7 +22,10 @@ struct DeltaArgs {
   DtOpts dto;
   int sigmoid;
   float scale;
-  char* ws;                        // the workspace where the blocks take it
+  // in blocks (set at launch)
+  char* ws;                        // workspace: the blocks' records
+  int64_t seg;                     // tokens of a segment; 0: sequences in one piece
+  float *ends, *enter;             // workspace: segments' ends and entering states
   int64_t seqs() const { return nseq > 0 ? nseq : batch; }
 };
 // The recurrence token after token.
@@ -33,13 +36,15 @@ hipError_t launch_delta_walk(const DeltaArgs& a, int io, int dt, hipStream_t s);
 // stream from slot offset / kDeltaBlock + s on (so that nobody has to sum the
 // sequences' block counts; a few slots stay empty).
 constexpr int kDeltaBlock = 64;
-inline int64_t delta_slots(const DeltaArgs& a) {
-  return a.nseq > 0 ? a.L / kDeltaBlock + a.nseq : a.batch * ((a.L + kDeltaBlock - 1) / kDeltaBlock);
+// (Segments, of several blocks, have slots of the same kind.)
+inline int64_t delta_slots(const DeltaArgs& a, int64_t unit = kDeltaBlock) {
+  return a.nseq > 0 ? a.L / unit + a.nseq : a.batch * ((a.L + unit - 1) / unit);
 }
 bool delta_blocks_apply(const DeltaArgs& a, int io);
-size_t delta_blocks_workspace(const DeltaArgs& a, int io);
+int64_t delta_blocks_workspace(DeltaArgs& a, int io);  // in bytes; sets a.seg
 hipError_t launch_delta_blocks(const DeltaArgs& a, int io, int dt, hipStream_t s);
 hipError_t launch_delta_solve(const DeltaArgs& a, int io, int dt, hipStream_t s);
+hipError_t launch_delta_join(const DeltaArgs& a, hipStream_t s);
 
 struct DeltaStepArgs {
   const void *x, *dt, *beta, *B, *C;  // one token per row

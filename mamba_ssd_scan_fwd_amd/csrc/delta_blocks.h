@@ -77,43 +77,43 @@ template <int TA, int TB> __device__ __forceinline__ void mul_pair(f32x4_t& acc,
       }
 }
 
-// Tokens of a slot: n (0: the slot is empty) from token t0 of batch row `row`.
+// A slot of `unit` tokens: its sequence, which of the sequence's it is, the
+// sequence's tokens [first, last), of batch row `row`, and the slot's own:
+// from t0 up to t1 (t1 <= t0: the slot is empty).
 struct DeltaSlot {
-  int64_t row, t0;
-  int n;
+  int64_t seq, part, row, first, last, t0, t1;
 };
-__device__ __forceinline__ int64_t delta_first_slot(const DeltaArgs& a, int64_t s) {
-  return seq_offset(a.cu, s, a.L) / kDeltaBlock + s;
+__device__ __forceinline__ int64_t delta_first_slot(const DeltaArgs& a, int64_t s, int64_t unit) {
+  return a.cu != nullptr ? seq_offset(a.cu, s, a.L) / unit + s : s * ((a.L + unit - 1) / unit);
 }
 // (by a whole wave)
-__device__ __forceinline__ DeltaSlot delta_slot(const DeltaArgs& a, int64_t slot) {
+__device__ __forceinline__ DeltaSlot delta_slot(const DeltaArgs& a, int64_t slot, int64_t unit) {
   DeltaSlot r;
   if (a.cu == nullptr) {
-    const int64_t nc = (a.L + kDeltaBlock - 1) / kDeltaBlock;
-    r.row = slot / nc;
-    r.t0 = (slot - r.row * nc) * kDeltaBlock;
-    r.n = (int)(a.L - r.t0 < kDeltaBlock ? a.L - r.t0 : kDeltaBlock);
-    return r;
+    const int64_t nc = (a.L + unit - 1) / unit;
+    r.seq = r.row = slot / nc;
+    r.first = 0, r.last = a.L;
+  } else {
+    // the last sequence whose slots begin at or before this one
+    const int lane = threadIdx.x & 63;
+    int64_t lo = 0, n = a.nseq;
+    while (n > 1) {
+      const int64_t step = (n + 63) / 64;
+      const int64_t i = lo + lane * step;
+      const bool le = lane * step < n && delta_first_slot(a, i, unit) <= slot;
+      const uint64_t m = __ballot(le);
+      const int k = m == 0 ? 0 : 63 - __builtin_clzll(m);
+      const int64_t left = n - k * step;
+      lo += k * step;
+      n = left < step ? left : step;
+    }
+    r.seq = lo, r.row = 0;
+    r.first = seq_offset(a.cu, lo, a.L), r.last = seq_offset(a.cu, lo + 1, a.L);
   }
-  // the last sequence whose slots begin at or before this one
-  const int lane = threadIdx.x & 63;
-  int64_t lo = 0, n = a.nseq;
-  while (n > 1) {
-    const int64_t step = (n + 63) / 64;
-    const int64_t i = lo + lane * step;
-    const bool le = lane * step < n && delta_first_slot(a, i) <= slot;
-    const uint64_t m = __ballot(le);
-    const int k = m == 0 ? 0 : 63 - __builtin_clzll(m);
-    const int64_t left = n - k * step;
-    lo += k * step;
-    n = left < step ? left : step;
-  }
-  const int64_t first = seq_offset(a.cu, lo, a.L), last = seq_offset(a.cu, lo + 1, a.L);
-  const int64_t c = slot - delta_first_slot(a, lo);
-  r.row = 0;
-  r.t0 = first + c * kDeltaBlock;
-  const int64_t left = last - r.t0;
-  r.n = c < 0 || left < 1 ? 0 : (int)(left < kDeltaBlock ? left : kDeltaBlock);
+  r.part = slot - delta_first_slot(a, r.seq, unit);
+  r.t0 = r.first + r.part * unit;
+  r.t1 = r.t0 + unit < r.last ? r.t0 + unit : r.last;
+  if (r.part < 0) r.t1 = r.t0;  // (before the first sequence)
   return r;
 }
 

@@ -55,8 +55,11 @@ template <int M, int V> __device__ __forceinline__ void spread() {
   }
 }
 
-template <typename TIO, int NP, int PT, bool DMA, bool WHOLE>
-__global__ __launch_bounds__(kThreads, DMA && PT == 2 ? 2 : 1) void delta_blocks_kernel(const DeltaArgs a, int blocks_p) {
+// PASS 0: over sequences, or over their segments from the states that enter
+// them. PASS 1: over segments, what becomes of a state of zeros (rows p) and, with
+// values of zero, of the unit states (rows P + n): see delta_join.
+template <typename TIO, int NP, int PT, bool DMA, bool WHOLE, int PASS>
+__global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs a, int blocks_p) {
   using L = Layout<TIO, NP, PT, DMA>;
   using Rec = DeltaRecord<TIO>;
   constexpr int IO = DeltaTerms<TIO>::io, ST = DeltaTerms<TIO>::state, YT = DeltaTerms<TIO>::y;
@@ -73,16 +76,26 @@ __global__ __launch_bounds__(kThreads, DMA && PT == 2 ? 2 : 1) void delta_blocks
   const int pb = (int)(bid % blocks_p);
   const int64_t sh = bid / blocks_p;
   const int h = (int)(sh % a.H);
-  const int64_t seq = sh / a.H;
+  const int64_t piece = sh / a.H;
   const int p0 = pb * L::cols, pw = p0 + 16 * PT * wave;
   // column r of tile pt
   auto column = [&](int pt) { return PT == 2 ? pw + 8 * (r / 4) + 4 * pt + r % 4 : pw + r; };
 
-  int64_t row = seq, first = 0, last = a.L, slot = seq * ((a.L + kDeltaBlock - 1) / kDeltaBlock);
-  if (a.cu != nullptr) {
-    row = 0, first = seq_offset(a.cu, seq, a.L), last = seq_offset(a.cu, seq + 1, a.L);
-    slot = delta_first_slot(a, seq);
+  // the tokens: of a sequence, or of one of its segments
+  DeltaSlot sl;
+  if (a.seg != 0) {
+    sl = delta_slot(a, piece, a.seg);
+    if (sl.part < 0 || (sl.part > 0 && sl.t1 <= sl.t0)) return;
+    if (PASS == 1 && sl.t1 >= sl.last) return;  // nothing begins behind the last one
+  } else {
+    sl.seq = piece, sl.row = a.cu != nullptr ? 0 : piece;
+    sl.t0 = a.cu != nullptr ? seq_offset(a.cu, piece, a.L) : 0;
+    sl.t1 = sl.last = a.cu != nullptr ? seq_offset(a.cu, piece + 1, a.L) : a.L;
+    sl.first = sl.t0;
   }
+  const int64_t row = sl.row, first = sl.t0, last = sl.t1;
+  int64_t slot = delta_first_slot(a, sl.seq, kDeltaBlock) + (first - sl.first) / kDeltaBlock;
+  const int rows_p = PASS == 1 ? a.P + a.N : a.P;  // rows in all
   const int64_t grp = h / (a.H / a.G);
   const TIO* Xp = static_cast<const TIO*>(a.x) + row * a.xs.batch + (int64_t)h * a.P;
   const TIO* Bp = static_cast<const TIO*>(a.B) + row * a.bs.batch + grp * a.N;
@@ -93,7 +106,9 @@ __global__ __launch_bounds__(kThreads, DMA && PT == 2 ? 2 : 1) void delta_blocks
   // S^T: tile (pt, kn, hh) rows 32 kn + 8 g + 4 hh .., column `column(pt)`
   f32x4_t S[PT][KN][2];
   Terms<ST> Sv[PT][KN];
-  auto state_at = [&](int pt) { return (seq * a.H + h) * (int64_t)a.P + (column(pt) < a.P ? column(pt) : 0); };
+  const int64_t states = (a.seg != 0 ? piece : sl.seq) * a.H + h;
+  const float* init = PASS == 1 ? nullptr : a.seg != 0 ? a.enter : a.init;
+  auto state_at = [&](int pt, int64_t of) { return (of * rows_p + (column(pt) < rows_p ? column(pt) : 0)) * a.N; };
   auto split_tiles = [&](auto terms, const f32x4_t& t0, const f32x4_t& t1) {
     const float f[8] = {t0[0], t0[1], t0[2], t0[3], t1[0], t1[1], t1[2], t1[3]};
     return split8<decltype(terms)::value>(f);
@@ -108,10 +123,14 @@ __global__ __launch_bounds__(kThreads, DMA && PT == 2 ? 2 : 1) void delta_blocks
       for (int hh = 0; hh < 2; ++hh) {
         S[pt][kn][hh] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         const int n = 32 * kn + 8 * g + 4 * hh;
-        if (a.init != nullptr && column(pt) < a.P && n < a.N) {
-          const Pack<float, 4> v = load_pack<float, 4, true>(a.init + state_at(pt) * a.N + n, a.N - n);
+        if (init != nullptr && column(pt) < a.P && n < a.N) {
+          const Pack<float, 4> v = load_pack<float, 4, true>(init + state_at(pt, states) + n, a.N - n);
 #pragma unroll
           for (int i = 0; i < 4; ++i) S[pt][kn][hh][i] = n + i < a.N ? v.v[i] : 0.f;
+        }
+        if constexpr (PASS == 1) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) S[pt][kn][hh][i] = column(pt) - a.P == n + i ? 1.f : 0.f;
         }
       }
       Sv[pt][kn] = split_tiles(st_terms, S[pt][kn][0], S[pt][kn][1]);
@@ -143,7 +162,7 @@ __global__ __launch_bounds__(kThreads, DMA && PT == 2 ? 2 : 1) void delta_blocks
   constexpr int PARTS = 2 * CK + CX + CR;
   auto send = [&](int i) {
     if constexpr (DMA) {
-      if (!more) return;
+      if (!more || (PASS == 1 && i < 2 * CK && i % 2 == 1)) return;
       if (i < 2 * CK) {
         const int j = i / 2, t = (j * kThreads + tid) / PACKS, c = tid % PACKS;
         const int n = 8 * (c ^ (i % 2 == 0 ? k_swz<NP>(t) : q_swz<NP>(t)));
@@ -235,7 +254,7 @@ __global__ __launch_bounds__(kThreads, DMA && PT == 2 ? 2 : 1) void delta_blocks
   const int kat = L::K + rt * (NP * 2), qat = L::Q + r * (NP * 2), tat = L::K + (8 * g + ta) * (NP * 2);
   const int kf = k_swz<NP>(rt), qf = q_swz<NP>(r), tf = k_swz<NP>(8 * g + ta);
 
-  const bool live = pw < a.P;
+  const bool live = pw < rows_p;
   int buf = 0;
   if (first < last) {
     if constexpr (DMA) {
@@ -249,7 +268,7 @@ __global__ __launch_bounds__(kThreads, DMA && PT == 2 ? 2 : 1) void delta_blocks
   for (int64_t t0 = first; t0 < last; t0 += 64, ++slot) {
     if constexpr (DMA) {
       // this block's rows are there (the last block's four stores are younger)
-      if (live && t0 != first) vm_wait<4>();
+      if (PASS == 0 && live && t0 != first) vm_wait<4>();
       else vm_wait<0>();
       __syncthreads();
       more = t0 + 64 < last;
@@ -330,7 +349,7 @@ __global__ __launch_bounds__(kThreads, DMA && PT == 2 ? 2 : 1) void delta_blocks
         for (int i = 0; i < 4; ++i) f[(kn + 1) % 2][i] = kfrag(i, kn + 1);
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[(kn + 1) % 2][i] = qfrag(i, 0);
+        for (int i = 0; i < 4 && PASS == 0; ++i) f[(kn + 1) % 2][i] = qfrag(i, 0);
         // X by columns, and the decays
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -369,7 +388,7 @@ __global__ __launch_bounds__(kThreads, DMA && PT == 2 ? 2 : 1) void delta_blocks
     Terms<ST> tf_[kTriFrags];
 #pragma unroll
     for (int kn = 0; kn < KN; ++kn) {
-      if (kn + 1 < KN) {
+      if (PASS == 0 && kn + 1 < KN) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[(KN + kn + 1) % 2][i] = qfrag(i, kn + 1);
       }
@@ -378,7 +397,7 @@ __global__ __launch_bounds__(kThreads, DMA && PT == 2 ? 2 : 1) void delta_blocks
         if (i * KN / kTriFrags == kn) tf_[i] = tri(st_terms, Rec::T, i);
       hold();
 #pragma unroll
-      for (int pair = 0; pair < term_pairs(YT, IO); ++pair)
+      for (int pair = 0; pair < term_pairs(YT, IO) && PASS == 0; ++pair)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -410,7 +429,7 @@ __global__ __launch_bounds__(kThreads, DMA && PT == 2 ? 2 : 1) void delta_blocks
     auto turn_u = [&](int pt) {  // operands of y, and U' = e^(g_end - g) U
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
-        Uy[pt][kk] = split_tiles(y_terms, U[pt][2 * kk], U[pt][2 * kk + 1]);
+        if constexpr (PASS == 0) Uy[pt][kk] = split_tiles(y_terms, U[pt][2 * kk], U[pt][2 * kk + 1]);
 #pragma unroll
         for (int i = 2 * kk; i < 2 * kk + 2; ++i)
 #pragma unroll
@@ -419,11 +438,11 @@ __global__ __launch_bounds__(kThreads, DMA && PT == 2 ? 2 : 1) void delta_blocks
       }
     };
 #pragma unroll
-    for (int i = 0; i < 4; ++i) er[i] = eg[16 * i + r];
+    for (int i = 0; i < 4 && PASS == 0; ++i) er[i] = eg[16 * i + r];
     hold();
 #pragma unroll
     for (int pt = 0; pt < PT; ++pt) {
-      if (pt == PT - 1) {
+      if (PASS == 0 && pt == PT - 1) {
 #pragma unroll
         for (int i = 0; i < kTriFrags; ++i) mf[i] = tri(y_terms, Rec::M, i);
         hold();
@@ -438,7 +457,7 @@ __global__ __launch_bounds__(kThreads, DMA && PT == 2 ? 2 : 1) void delta_blocks
           for (int i = 2 * ks; i < 4; ++i) mul_pair(U[pt][i], tf_[tri_frag(i / 2, i % 2, ks)], Rv[pt][ks], pair);
       if (pt == 0) {
 #pragma unroll
-        for (int q = 0; q < PT; ++q)
+        for (int q = 0; q < PT && PASS == 0; ++q)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -465,10 +484,10 @@ __global__ __launch_bounds__(kThreads, DMA && PT == 2 ? 2 : 1) void delta_blocks
 #pragma unroll
           for (int i = 2 * ks; i < 4; ++i) mul_pair(O[pt][i], Uy[pt][ks], mf[tri_frag(i / 2, i % 2, ks)], pair);
     };
-    if constexpr (PT == 2) times_m(0);
+    if constexpr (PT == 2 && PASS == 0) times_m(0);
     turn_u(PT - 1);
     hold();
-    times_m(PT - 1);
+    if constexpr (PASS == 0) times_m(PT - 1);
     // y: rows p of a lane (4, or 8 of two tiles) at token 16 i + r
     auto put_y = [&] {
       const __amdgpu_buffer_rsrc_t Yr = buffer_range(Yp + t0 * HP, (uint32_t)((n - 1) * HP + a.P) * SZ);
@@ -520,13 +539,14 @@ __global__ __launch_bounds__(kThreads, DMA && PT == 2 ? 2 : 1) void delta_blocks
       }
       spread<4 * PT * term_pairs(IO, ST), 3>();
       hold();
-      if (kn == 0) put_y();
+      if (PASS == 0 && kn == 0) put_y();
     }
 #pragma unroll
     for (int pt = 0; pt < PT; ++pt) Sv[pt][KN - 1] = split_tiles(st_terms, S[pt][KN - 1][0], S[pt][KN - 1][1]);
   }
 
-  if (a.final_state == nullptr) return;
+  float* out = PASS == 1 ? a.ends : sl.t1 >= sl.last ? a.final_state : nullptr;
+  if (out == nullptr) return;
 #pragma unroll
   for (int pt = 0; pt < PT; ++pt)
 #pragma unroll
@@ -535,15 +555,18 @@ __global__ __launch_bounds__(kThreads, DMA && PT == 2 ? 2 : 1) void delta_blocks
       for (int hh = 0; hh < 2; ++hh) {
         const int n = 32 * kn + 8 * g + 4 * hh;
         const float v[4] = {S[pt][kn][hh][0], S[pt][kn][hh][1], S[pt][kn][hh][2], S[pt][kn][hh][3]};
-        if (column(pt) < a.P && n < a.N) store_pack<float, 4, true>(a.final_state + state_at(pt) * a.N + n, v, a.N - n);
+        if (column(pt) < rows_p && n < a.N)
+          store_pack<float, 4, true>(out + state_at(pt, PASS == 1 ? states : sl.seq * a.H + h) + n, v, a.N - n);
       }
 }
 
-template <typename TIO, int NP>
-hipError_t launch_np(const DeltaArgs& a, hipStream_t s) {
+template <typename TIO, int NP, int PASS>
+hipError_t launch_pass(const DeltaArgs& a, hipStream_t s) {
+  const int rows_p = PASS == 1 ? a.P + a.N : a.P;
   auto go = [&](auto kern, int cols) {
-    const int blocks_p = (a.P + cols - 1) / cols;
-    kern<<<dim3((unsigned)(a.seqs() * a.H * blocks_p)), kThreads, 0, s>>>(a, blocks_p);
+    const int blocks_p = (rows_p + cols - 1) / cols;
+    const int64_t pieces = a.seg != 0 ? delta_slots(a, a.seg) : a.seqs();
+    kern<<<dim3((unsigned)(pieces * a.H * blocks_p)), kThreads, 0, s>>>(a, blocks_p);
     return hipGetLastError();
   };
   constexpr int XP = 16 / (int)sizeof(TIO);
@@ -553,10 +576,22 @@ hipError_t launch_np(const DeltaArgs& a, hipStream_t s) {
       return (reinterpret_cast<uintptr_t>(p) | (uintptr_t)(st.token * 2) | (uintptr_t)(st.batch * 2)) % 16 == 0;
     };
     if (whole && lies(a.x, a.xs) && lies(a.B, a.bs) && lies(a.C, a.cs))
-      return a.P > 64 ? go(delta_blocks_kernel<TIO, NP, 2, true, true>, 128) : go(delta_blocks_kernel<TIO, NP, 1, true, true>, 64);
-    return go(delta_blocks_kernel<TIO, NP, 1, false, false>, 64);
+      return rows_p > 64 ? go(delta_blocks_kernel<TIO, NP, 2, true, true, PASS>, 128)
+                         : go(delta_blocks_kernel<TIO, NP, 1, true, true, PASS>, 64);
+    return go(delta_blocks_kernel<TIO, NP, 1, false, false, PASS>, 64);
   }
-  return whole ? go(delta_blocks_kernel<TIO, NP, 1, false, true>, 64) : go(delta_blocks_kernel<TIO, NP, 1, false, false>, 64);
+  return whole ? go(delta_blocks_kernel<TIO, NP, 1, false, true, PASS>, 64)
+               : go(delta_blocks_kernel<TIO, NP, 1, false, false, PASS>, 64);
+}
+
+template <typename TIO, int NP>
+hipError_t launch_np(const DeltaArgs& a, hipStream_t s) {
+  if (a.seg != 0) {
+    hipError_t e = launch_pass<TIO, NP, 1>(a, s);
+    if (e == hipSuccess) e = launch_delta_join(a, s);
+    if (e != hipSuccess) return e;
+  }
+  return launch_pass<TIO, NP, 0>(a, s);
 }
 
 template <typename TIO>
@@ -568,16 +603,53 @@ hipError_t launch_io(const DeltaArgs& a, hipStream_t s) {
   return hipErrorInvalidValue;
 }
 
+// Tokens of a segment, 0 where sequences are walked in one piece. A sequence's
+// blocks depend on one another; where all rows, heads and columns give fewer workgroups
+// than the card has compute units, the time axis is cut: a first walk gives what each segment
+// makes of any state (P + N rows instead of P, without y, about 3/4 of a block's time
+// a row), the states are joined in turn, and the segments are walked side by side.
+// In quarters of a block's time on a compute unit; a join takes about a block's.
+// Of packed sequences only the number is known here: the stream is taken for so many
+// of four times their mean length.
+int64_t delta_segment(const DeltaArgs& a, int io) {
+  const int64_t cols = io == kBF16 && a.N <= 128 && a.P > 64 ? 128 : 64, cols1 = io == kBF16 && a.N <= 128 ? 128 : 64;
+  int64_t tokens = a.L, seqs = a.batch;
+  if (a.nseq > 0) tokens = 4 * ((a.L + a.nseq - 1) / a.nseq) < a.L ? 4 * ((a.L + a.nseq - 1) / a.nseq) : a.L, seqs = (a.L + tokens - 1) / tokens;
+  const int64_t wgs = seqs * a.H * ((a.P + cols - 1) / cols), first = seqs * a.H * ((a.P + a.N + cols1 - 1) / cols1);
+  const int64_t blocks = (tokens + kDeltaBlock - 1) / kDeltaBlock, cus = 256;
+  auto turns = [&](int64_t w) { return (w + cus - 1) / cus; };
+  int64_t best = turns(wgs) * blocks * 4, cut = 0;
+  for (int64_t n = 2; n <= 64 && n * 4 <= blocks; ++n) {
+    const int64_t len = (blocks + n - 1) / n;
+    const int64_t t = turns(wgs * n) * len * 4 + turns(first * (n - 1)) * len * 3 + n * 4 + 12;
+    if (t < best) best = t, cut = len;
+  }
+  return cut * kDeltaBlock;
+}
+
+size_t record_bytes(int io) { return io == kBF16 ? DeltaRecord<__hip_bfloat16>::bytes : DeltaRecord<float>::bytes; }
+
 }  // namespace
 
 bool delta_blocks_apply(const DeltaArgs& a, int io) {
   return (io == kBF16 || a.N <= 128) && a.L >= 16 && a.N >= 8 && a.P >= 8;
 }
-size_t delta_blocks_workspace(const DeltaArgs& a, int io) {
-  return size_t(delta_slots(a)) * a.H * (io == kBF16 ? DeltaRecord<__hip_bfloat16>::bytes : DeltaRecord<float>::bytes);
+
+int64_t delta_blocks_workspace(DeltaArgs& a, int io) {
+  const int64_t records = delta_slots(a) * a.H * (int64_t)record_bytes(io);
+  a.seg = delta_segment(a, io);
+  if (a.seg == 0) return records;
+  const int64_t states = delta_slots(a, a.seg) * a.H;
+  return records + states * (2 * a.P + a.N) * a.N * (int64_t)sizeof(float);
 }
 
-hipError_t launch_delta_blocks(const DeltaArgs& a, int io, int dt, hipStream_t s) {
+hipError_t launch_delta_blocks(const DeltaArgs& args, int io, int dt, hipStream_t s) {
+  DeltaArgs a = args;
+  if (a.seg != 0) {
+    const int64_t states = delta_slots(a, a.seg) * a.H;
+    a.ends = reinterpret_cast<float*>(a.ws + delta_slots(a) * a.H * (int64_t)record_bytes(io));
+    a.enter = a.ends + states * (a.P + a.N) * a.N;
+  }
   const hipError_t e = launch_delta_solve(a, io, dt, s);
   if (e != hipSuccess) return e;
   return io == kBF16 ? launch_io<__hip_bfloat16>(a, s) : launch_io<float>(a, s);

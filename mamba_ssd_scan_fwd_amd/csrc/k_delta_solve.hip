@@ -60,8 +60,9 @@ __global__ __launch_bounds__(64 * kWaves) void delta_solve_kernel(const DeltaArg
   if (task >= tasks) return;
   const int64_t slot = task / a.H;
   const int h = (int)(task - slot * a.H);
-  const DeltaSlot at = delta_slot(a, slot);
-  if (at.n < 1) return;
+  const DeltaSlot at = delta_slot(a, slot, kDeltaBlock);
+  if (at.t1 <= at.t0) return;
+  const int n = (int)(at.t1 - at.t0);
   Shared& sh = shared[wave];
   float* m = sh.m;
   char* rec = a.ws + task * Rec::bytes;
@@ -79,7 +80,7 @@ __global__ __launch_bounds__(64 * kWaves) void delta_solve_kernel(const DeltaArg
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) v[ks] = load_piece<TIO>(from, row, col[ks]);
   };
-  const __amdgpu_buffer_rsrc_t Br = block_rows(Bp, a.bs.token, at.n, a.N), Cr = block_rows(Cp, a.cs.token, at.n, a.N);
+  const __amdgpu_buffer_rsrc_t Br = block_rows(Bp, a.bs.token, n, a.N), Cr = block_rows(Cp, a.cs.token, n, a.N);
   Piece<TIO> k[4][KS], q[2][KS];
 #pragma unroll
   for (int i = 0; i < 4; ++i) rows(Br, a.bs.token, i, k[i]);
@@ -87,7 +88,7 @@ __global__ __launch_bounds__(64 * kWaves) void delta_solve_kernel(const DeltaArg
 
   // a lane to a token: beta, and the sum of the log2 decays
   {
-    const bool there = lane < at.n;
+    const bool there = lane < n;
     const int64_t t = at.t0 + (there ? lane : 0);
     const float dt = Elem<TDT>::f32(static_cast<const RD*>(a.dt)[at.row * a.ds.batch + t * a.ds.token + h]);
     const float be = Elem<TDT>::f32(static_cast<const RD*>(a.beta)[at.row * a.es.batch + t * a.es.token + h]);

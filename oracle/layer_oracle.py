@@ -90,7 +90,7 @@ def delta_rule(x, a, beta, k, q, scale=1.0, S0=None):
     return y, S
 
 
-def delta_magnitudes(x, a, beta, k, q, scale=1.0, S0=None, block=64):
+def delta_magnitudes(x, a, beta, k, q, scale=1.0, S0=None, block=64, cut=False):
     """What rounding errors of ``delta_rule`` are multiples of, for keys and
     betas whose transitions do not grow (beta |k|^2 <= 2): an error of a row of
     the state, in the 2-norm, is then passed on with the decay and no more.
@@ -99,6 +99,9 @@ def delta_magnitudes(x, a, beta, k, q, scale=1.0, S0=None, block=64):
     In blocks, whose solution is U = T R with R = beta (x - e^g S0 k) and
     T = (1 + A)^-1: |U| <= K = |T| |1 + A| |T| beta (|x| + e^g |S0| |k|), and
     E <- e^g E + e^g |S0| + sum_j e^(g - g_j) |k_j| K_j.
+    With ``cut`` for states that are joined from what a segment makes of the state
+    that enters it, S0 M, and of none, B: |S0 M| <= |S0| and |B| <= |S| + |S0|, so
+    both have 3 max|S| in |S0|'s place.
     Returns (token [P], block [P], y's token and block form [L, P], y's block
     terms themselves [L, P]): the latter what roundings of the operands of y's
     products alone are multiples of."""
@@ -109,6 +112,13 @@ def delta_magnitudes(x, a, beta, k, q, scale=1.0, S0=None, block=64):
     et, eb = np.zeros(P), np.zeros(P)
     yt, yb, yo = np.zeros((L, P)), np.zeros((L, P)), np.zeros((L, P))
     norm = lambda m: np.linalg.norm(m, axis=1)  # noqa: E731
+    top = norm(S)
+    if cut:
+        for t in range(L):
+            S = a[t] * S
+            S = S + np.outer(beta[t] * (x[t] - S @ k[t]), k[t])
+            top = np.maximum(top, norm(S))
+        S = np.zeros((P, k.shape[1])) if S0 is None else S0.astype(np.float64).copy()
     for t0 in range(0, L, block):
         t1 = min(L, t0 + block)
         n, kk, qq, xx, bb = t1 - t0, k[t0:t1], q[t0:t1], x[t0:t1], beta[t0:t1]
@@ -118,7 +128,7 @@ def delta_magnitudes(x, a, beta, k, q, scale=1.0, S0=None, block=64):
         dec = np.where(i >= j, np.exp(np.where(i >= j, g[:, None] - g[None, :], 0.0)), 0.0)
         IA = np.eye(n) + np.where(i > j, bb[:, None] * dec * (kk @ kk.T), 0.0)
         T = np.abs(np.linalg.inv(IA))
-        s0 = norm(S)
+        s0 = 3 * top if cut else norm(S)
         K = T @ np.abs(IA) @ T @ (bb[:, None] * (np.abs(xx) + np.exp(g)[:, None] * s0 * kn[t0:t1, None]))
         att = dec * np.abs(qq @ kk.T)
         for r in range(n):

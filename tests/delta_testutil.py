@@ -92,7 +92,7 @@ class Delta:
         return dict(x=move(self.x), dt=move(self.dt), A=self.A.to(dev), B=move(self.B), C=move(self.C),
                     beta=move(self.beta), dt_pre=pre, scale=self.scale, beta_sigmoid=self.sigmoid), move(self.init), move(self.cu)
 
-    def reference(self):
+    def reference(self, cut=False):
         """(y, bound of y, states, bound of states), rows or sequences in turn."""
         x, B, C, A = np64(self.x), np64(self.B), np64(self.C), np64(self.A)
         dt, beta = np64(self.dt), np64(self.beta)
@@ -118,7 +118,7 @@ class Delta:
                 args = (x[i, f:e, h], a[i, f:e, h], beta[i, f:e, h], B[i, f:e, g], C[i, f:e, g], scale,
                         None if self.init is None else np64(self.init[s, h]))
                 y[i, f:e, h], S[s, h] = ref.delta_rule(*args)
-                et, eb, yt, ybl, yo = ref.delta_magnitudes(*args)
+                et, eb, yt, ybl, yo = ref.delta_magnitudes(*args, cut=cut)
                 Sb[s, h, :, 0] = ct * et + cb * eb
                 yb[i, f:e, h] = ct * yt + cb * ybl + cy * yo + HALF[self.io] * np.abs(y[i, f:e, h])
         return y, yb, S, Sb

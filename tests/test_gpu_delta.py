@@ -155,6 +155,67 @@ def test_rule_carries_over_calls(io):
     within(h, hr, 2 * hb, "final_state")
 
 
+# ---- long sequences of few heads: the time axis in segments -------------------------
+
+
+def is_cut(s, S=0):
+    """Whether the call's workspace holds more than the blocks' records."""
+    d = ssd.DeltaDesc(batch=s.b, seqlen=s.L, nheads=s.H, headdim=s.P, dstate=s.N, ngroups=s.G, io_dtype=int(s.io == torch.bfloat16),
+                      scale=1.0)
+    slots = s.L // 64 + S if S else s.b * -(-s.L // 64)
+    return ssd.delta_rule_workspace_bytes(d, S) > slots * s.H * (18944 if s.io == torch.bfloat16 else 37376)
+
+
+@pytest.mark.parametrize("L,H,P,N,io,views", [(1100, 2, 64, 64, "bf16", False), (1025, 1, 128, 128, "bf16", False),
+                                              (1300, 1, 40, 77, "bf16", True), (1100, 1, 20, 64, "fp32", False),
+                                              (1088, 1, 33, 100, "fp32", True), (1100, 1, 16, 256, "bf16", False),
+                                              (2200, 1, 16, 32, "bf16", False)])
+def test_long_rule_in_segments(L, H, P, N, io, views):
+    s = Delta(1, L, H, P, N, 1, io, "fp32", views=views, seed=L)
+    assert is_cut(s)
+    kw, h0, _ = s.to(DEV)
+    note(f"[gpu] delta rule in segments L={L} H={H} P={P} N={N} {io}")
+    y, hT = ssd.delta_rule(init_state=h0, **kw)
+    yr, yb, hr, hb = s.reference(cut=True)
+    within(y, yr, yb, "y")
+    within(hT, hr, hb, "final_state")
+    near(hT, hr, "final_state")
+    again = ssd.delta_rule(init_state=h0, final_state=h0, **kw)
+    assert torch.equal(y, again[0]) and torch.equal(hT, h0)
+
+
+@pytest.mark.parametrize("lens", [[1500, 0, 700], [3, 2000], [0, 0, 1600, 0], [640, 640, 641]])
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+def test_long_packed_rule_in_segments(lens, io):
+    s = Delta(1, sum(lens), 1, 24, 64, 1, io, "fp32", lens=lens, seed=len(lens))
+    assert is_cut(s, len(lens))
+    kw, h0, cu = s.to(DEV)
+    note(f"[gpu] delta rule packed in segments {lens} {io}")
+    y, hT = ssd.delta_rule_varlen(cu_seqlens=cu, init_states=h0, **kw)
+    yr, yb, hr, hb = s.reference(cut=True)
+    within(y, yr, yb, "y")
+    within(hT, hr, hb, "final_states")
+    again = ssd.delta_rule_varlen(cu_seqlens=cu, init_states=h0, final_states=h0, **kw)
+    assert torch.equal(y, again[0]) and torch.equal(hT, h0)
+
+
+@pytest.mark.parametrize("cu", [[0, 50, 30, 1000], [0, 1 << 30, 100], [-5, 400, 1000], [20, 600, 800], [0, 0, 0], [1000, 0, 1000],
+                                [990, 64, 1000, 3]])
+@pytest.mark.parametrize("H", [1, 64])
+def test_bad_offsets_stay_inside(cu, H):
+    """Whatever the offsets hold, nothing outside the arrays is touched; sequences
+    of offsets in order are right."""
+    T, P, N = 1000, 16, 32
+    s = Delta(1, T, H, P, N, 1, "bf16", "fp32", init=False, seed=12)
+    kw, _, _ = s.to(DEV)
+    S = len(cu) - 1
+    y = torch.full((1, T + 64, H, P), 7.0, device=DEV, dtype=torch.bfloat16)
+    h = torch.full((S + 2, H, P, N), 5.0, device=DEV)
+    note(f"[gpu] delta rule: offsets {cu} H={H}")
+    ssd.delta_rule_varlen(cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=DEV), y=y[:, :T], final_states=h[1:S + 1], **kw)
+    assert (y[:, T:] == 7.0).all() and (h[0] == 5.0).all() and (h[S + 1] == 5.0).all()
+
+
 # ---- decays and betas at their borders ---------------------------------------------
 
 
