@@ -36,13 +36,10 @@ template <typename TIO, int NP, int PT, bool DMA> struct Layout {
                        half = X + 64 * xrow, bytes = DMA ? 2 * half : half;
 };
 
-// Where the 16-byte piece c of row t lies in K's, Q's and (bf16) X's tile: c
+// Where the 16-byte piece c of row t lies in K's and Q's and in (bf16) X's tile: c
 // with these bits flipped.
 template <int NP> __device__ __forceinline__ int k_swz(int t) {
   return NP >= 128 ? ((t & 3) << 2) | ((t >> 3) & 3) : NP == 64 ? ((t & 2) << 1) | ((t >> 3) & 3) : (t >> 3) & 3;
-}
-template <int NP> __device__ __forceinline__ int q_swz(int t) {
-  return NP >= 128 ? ((t & 3) << 2) | ((t >> 2) & 3) : NP == 64 ? ((t & 2) << 1) | ((t >> 2) & 3) : (t >> 2) & 3;
 }
 template <int PT> __device__ __forceinline__ int x_swz(int t) { return PT == 2 ? (t & 3) << 2 : (t & 2) | ((t >> 1) & 4); }
 
@@ -165,7 +162,7 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
       if (!more || (PASS == 1 && i < 2 * CK && i % 2 == 1)) return;
       if (i < 2 * CK) {
         const int j = i / 2, t = (j * kThreads + tid) / PACKS, c = tid % PACKS;
-        const int n = 8 * (c ^ (i % 2 == 0 ? k_swz<NP>(t) : q_swz<NP>(t)));
+        const int n = 8 * (c ^ k_swz<NP>(t));
         const int token = (int)(i % 2 == 0 ? a.bs.token : a.cs.token);
         dma16(i % 2 == 0 ? Br : Cr, dst + (i % 2 == 0 ? L::K : L::Q) + j * kThreads * 16,
               n < a.N ? (uint32_t)(t * token + n) * SZ : kNowhere);
@@ -215,7 +212,7 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
       for (int j = 0; j < CK; ++j) {
         const int t = (j * kThreads + tid) / PACKS;
         unsigned char* kd = lds + L::K + t * (NP * 2) + 16 * (kc ^ k_swz<NP>(t));
-        unsigned char* qd = lds + L::Q + t * (NP * 2) + 16 * (kc ^ q_swz<NP>(t));
+        unsigned char* qd = lds + L::Q + t * (NP * 2) + 16 * (kc ^ k_swz<NP>(t));
         move_piece<TIO, WHOLE>(kq[0][j], kmoved);
         move_piece<TIO, WHOLE>(kq[1][j], kmoved);
         if constexpr (IO > 1) {
@@ -251,8 +248,8 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
   // ---- this lane's operands in LDS
   const int rt = 8 * (r / 4) + r % 4;  // its row of a pair of tiles
   const int ta = r / 4, tb = r % 4;    // its row and piece of a transposing read
-  const int kat = L::K + rt * (NP * 2), qat = L::Q + r * (NP * 2), tat = L::K + (8 * g + ta) * (NP * 2);
-  const int kf = k_swz<NP>(rt), qf = q_swz<NP>(r), tf = k_swz<NP>(8 * g + ta);
+  const int kat = rt * (NP * 2), tat = L::K + (8 * g + ta) * (NP * 2);
+  const int kf = k_swz<NP>(rt), tf = k_swz<NP>(8 * g + ta);
 
   const bool live = pw < rows_p;
   int buf = 0;
@@ -287,19 +284,15 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
 
     const float* eg = reinterpret_cast<const float*>(at + L::rec + Rec::decays);
     const float* ed = eg + 64;
-    auto kfrag = [&](int i, int kn) {  // rows of tile i, columns 32 kn ..
+    auto by_rows = [&](int from, int i, int kn) {  // rows of tile i, columns 32 kn ..
       Terms<IO> v;
 #pragma unroll
       for (int e = 0; e < IO; ++e)
-        v.v[e] = as_bf16x8(ld16(at + kat + e * L::tile + (32 * (i / 2) + 4 * (i % 2)) * (NP * 2) + 16 * ((4 * kn + g) ^ kf)));
+        v.v[e] = as_bf16x8(ld16(at + from + kat + e * L::tile + (32 * (i / 2) + 4 * (i % 2)) * (NP * 2) + 16 * ((4 * kn + g) ^ kf)));
       return v;
     };
-    auto qfrag = [&](int i, int kn) {
-      Terms<IO> v;
-#pragma unroll
-      for (int e = 0; e < IO; ++e) v.v[e] = as_bf16x8(ld16(at + qat + e * L::tile + 16 * i * (NP * 2) + 16 * ((4 * kn + g) ^ qf)));
-      return v;
-    };
+    auto kfrag = [&](int i, int kn) { return by_rows(L::K, i, kn); };
+    auto qfrag = [&](int i, int kn) { return by_rows(L::Q, i, kn); };
     auto ktfrag = [&](int hh, int kk, int kn) {  // tile hh of columns 32 kn .., rows 32 kk ..
       Terms<IO> v;
 #pragma unroll
@@ -438,7 +431,7 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
       }
     };
 #pragma unroll
-    for (int i = 0; i < 4 && PASS == 0; ++i) er[i] = eg[16 * i + r];
+    for (int i = 0; i < 4 && PASS == 0; ++i) er[i] = eg[32 * (i / 2) + 4 * (i % 2) + rt];
     hold();
 #pragma unroll
     for (int pt = 0; pt < PT; ++pt) {
@@ -488,13 +481,13 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
     turn_u(PT - 1);
     hold();
     if constexpr (PASS == 0) times_m(PT - 1);
-    // y: rows p of a lane (4, or 8 of two tiles) at token 16 i + r
+    // y: rows p of a lane (4, or 8 of two tiles) at token 32 (i / 2) + 4 (i % 2) + rt
     auto put_y = [&] {
       const __amdgpu_buffer_rsrc_t Yr = buffer_range(Yp + t0 * HP, (uint32_t)((n - 1) * HP + a.P) * SZ);
       const int pr = pw + 4 * PT * g;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t off = (uint32_t)((16 * i + r) * HP + pr) * SZ;
+        const uint32_t off = (uint32_t)((32 * (i / 2) + 4 * (i % 2) + rt) * HP + pr) * SZ;
         if constexpr (WHOLE) {
           const uint32_t to = pr < a.P ? off : kNowhere;
           if constexpr (SZ == 4) {
