@@ -5,12 +5,17 @@
 // (a, b) = (i, i + R / 2) or (2 i, 2 i + 1).
 //
 // One pass over memory: a team of T lanes holds a head in registers, M packs of
-// V consecutive channels to a lane, sums its squares by DPP, and exchanges the
-// halves of the pairs through LDS, where the wave's lanes need no barrier. A
+// V consecutive channels to a lane, and sums its squares by DPP. A
 // wave takes one token: its 64 lanes compute one angle each (product and
 // reduction to a turn in 64 bits, so that positions in the millions keep the
-// angle's digits; sine and cosine of the reduced angle in fp32), and all heads of the token use
-// them. Queries and keys are one launch.
+// angle's digits; sine and cosine of the reduced angle in fp32), each lane takes
+// those of its channels into registers, and all heads of the token are turned by them. Queries
+// and keys are one launch.
+//
+// The other half of a pair lies in the same lane (neighbouring channels), in lane
+// ^ T / 2 where all channels of a head that fills the team are turned (DPP or one
+// exchange of rows), or anywhere: through LDS, where the wave's lanes need no
+// barrier.
 #include "delta.h"
 
 namespace ssd {
@@ -18,11 +23,26 @@ namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 
-template <typename TIO, int T, int M, bool WHOLE>
+enum Exchange { kNone, kSameLane, kHalfTeam, kAnywhere };
+
+// The value of lane ^ T / 2.
+template <int T> __device__ __forceinline__ float half_team(float v) {
+  if constexpr (T == 8) return dpp_f32<0x141>(dpp_f32<0x1B>(v));  // mirrored in 4, then in 8
+  if constexpr (T == 16) return dpp_f32<0x128>(v);                // turned by 8 in 16
+  const uint32_t u = __float_as_uint(v);
+  if constexpr (T == 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return __uint_as_float(threadIdx.x & 16 ? r[0] : r[1]);
+  }
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __uint_as_float(threadIdx.x & 32 ? r[0] : r[1]);
+}
+
+template <typename TIO, int T, int M, bool WHOLE, Exchange X>
 __global__ __launch_bounds__(kThreads) void head_norm_kernel(const HeadNormArgs a) {
   constexpr int V = 16 / sizeof(TIO), TEAMS = 64 / T, DP = T * M * V;  // DP: channels that a team has room for
-  __shared__ float2 turns[kWaves][kHeadNormMaxDim / 2];  // cos, sin of this wave's token
-  __shared__ __align__(16) float swap[kWaves][TEAMS][DP];
+  __shared__ float2 turns[X != kNone ? kWaves : 1][X != kNone ? kHeadNormMaxDim / 2 : 1];  // cos, sin of this wave's token
+  __shared__ __align__(16) float line_[X == kAnywhere ? kWaves : 1][X == kAnywhere ? TEAMS : 1][X == kAnywhere ? DP : 1];
   const int wave = threadIdx.x / 64, lane = threadIdx.x % 64, team = lane / T, sub = lane % T;
   const int heads = a.heads[0] + a.heads[1];
   const int parts = (heads + a.per - 1) / a.per;  // waves to a token
@@ -41,41 +61,72 @@ __global__ __launch_bounds__(kThreads) void head_norm_kernel(const HeadNormArgs 
     skip[m] = c - from;
     at[m] = nn[m] > 0 ? from : 0;
   }
+  float w[2][M][V];
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int i = 0; i < V; ++i) w[x][m][i] = a.w[x] != nullptr ? a.w[x][at[m] + (i < nn[m] ? i : 0)] : 1.f;
 
   const int64_t tasks = a.batch * a.rows * parts;
   for (int64_t task = (int64_t)blockIdx.x * kWaves + wave; task < tasks; task += (int64_t)gridDim.x * kWaves) {
-    const int64_t token = task / parts;
-    const int h0 = (int)(task % parts) * a.per;
+    const int64_t token = parts == 1 ? task : task / parts;
+    const int h0 = (int)(task - token * parts) * a.per;
     const int h1 = h0 + a.per < heads ? h0 + a.per : heads;
-    const int64_t b = token / a.rows, t = token - b * a.rows;
-    if (half > 0) {
+    const int64_t b = a.batch == 1 ? 0 : token / a.rows, t = token - b * a.rows;
+    auto load = [&](int hb, Pack<TIO, V>(&x)[M]) {
+      const int hh = hb + team < h1 ? hb + team : h1 - 1;
+      const int which = hh >= a.heads[0];
+      const TIO* xp = static_cast<const TIO*>(a.in[which]) + b * a.st[which].batch + t * a.st[which].token +
+                      (int64_t)(which ? hh - a.heads[0] : hh) * a.D;
+#pragma unroll
+      for (int m = 0; m < M; ++m) x[m] = load_pack<TIO, V, !WHOLE>(xp + at[m], nn[m]);
+    };
+    Pack<TIO, V> next[M];
+    load(h0, next);
+    // what this lane's channels are multiplied with, and the others of their pairs
+    float cs[X != kNone ? M : 1][V], sn[X != kNone ? M : 1][V];
+    if constexpr (X != kNone) {
       const double pos = (double)a.pos[token];
       for (int i = lane; i < half; i += 64) {
         const double rev = pos * ((double)a.freq[i] * 0.15915494309189533577);  // turns
-        float sn, cs;
-        sincospif(2.f * (float)(rev - rint(rev)), &sn, &cs);
-        turns[wave][i] = make_float2(cs, sn);
+        float s, c;
+        sincospif(2.f * (float)(rev - rint(rev)), &s, &c);
+        turns[wave][i] = make_float2(c, s);
       }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int c = at[m] + i;
+          const bool second = a.pairs ? c & 1 : c >= half;
+          const bool turned = i < nn[m] && c < a.R;
+          const float2 f = turns[wave][!turned ? 0 : a.pairs ? c / 2 : second ? c - half : c];
+          cs[m][i] = f.x;
+          sn[m][i] = second ? f.y : -f.y;
+        }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
     }
     for (int hb = h0; hb < h1; hb += TEAMS) {
       const bool live = hb + team < h1;
       const int hh = live ? hb + team : h1 - 1;
       const int which = hh >= a.heads[0];
-      const int h = which ? hh - a.heads[0] : hh;
-      const TIO* xp = static_cast<const TIO*>(a.in[which]) + b * a.st[which].batch + t * a.st[which].token + (int64_t)h * a.D;
-      const float* w = a.w[which];
+      Pack<TIO, V> x[M];
+#pragma unroll
+      for (int m = 0; m < M; ++m) x[m] = next[m];
+      if (hb + TEAMS < h1) load(hb + TEAMS, next);
       float v[M][V], sq = 0.f;
 #pragma unroll
-      for (int m = 0; m < M; ++m) {
-        const Pack<TIO, V> x = load_pack<TIO, V, !WHOLE>(xp + at[m], nn[m]);
+      for (int m = 0; m < M; ++m)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          v[m][i] = Elem<TIO>::f32(x.v[i]);
+          v[m][i] = Elem<TIO>::f32(x[m].v[i]);
           if (i < nn[m] && i >= skip[m]) sq = fmaf(v[m][i], v[m][i], sq);
         }
-      }
       const float var = team_sum<T>(sq) * inv + a.eps;
       // one Newton step on the hardware's reciprocal root (1 ulp); it takes a
       // subnormal for 0, so small ones go in times 2^64
@@ -87,35 +138,47 @@ __global__ __launch_bounds__(kThreads) void head_norm_kernel(const HeadNormArgs 
 #pragma unroll
       for (int m = 0; m < M; ++m)
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          v[m][i] *= rs;
-          if (w != nullptr) v[m][i] *= w[at[m] + (i < nn[m] ? i : 0)];
+        for (int i = 0; i < V; ++i) v[m][i] = v[m][i] * rs * (which ? w[1][m][i] : w[0][m][i]);
+      if constexpr (X != kNone) {
+        float other[M][V];
+        if constexpr (X == kSameLane) {
+#pragma unroll
+          for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int i = 0; i < V; ++i) other[m][i] = v[m][i ^ 1];
+        } else if constexpr (X == kHalfTeam) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) other[0][i] = half_team<T>(v[0][i]);
+        } else {
+          float* line = line_[wave][team];
+#pragma unroll
+          for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+              if (i < nn[m]) line[at[m] + i] = v[m][i];
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          __builtin_amdgcn_wave_barrier();
+#pragma unroll
+          for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              const int c = at[m] + i;
+              const bool turned = i < nn[m] && c < a.R;
+              other[m][i] = line[!turned ? 0 : a.pairs ? c ^ 1 : c >= half ? c - half : c + half];
+            }
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          __builtin_amdgcn_wave_barrier();
         }
-      if (half > 0) {
-        float* line = swap[wave][team];
-#pragma unroll
-        for (int m = 0; m < M; ++m)
-#pragma unroll
-          for (int i = 0; i < V; ++i)
-            if (i < nn[m]) line[at[m] + i] = v[m][i];
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int m = 0; m < M; ++m)
 #pragma unroll
           for (int i = 0; i < V; ++i) {
-            const int c = at[m] + i;
-            if (i < nn[m] && c < a.R) {
-              const bool second = a.pairs ? c & 1 : c >= half;
-              const float2 cs = turns[wave][a.pairs ? c / 2 : second ? c - half : c];
-              const float other = line[a.pairs ? c ^ 1 : second ? c - half : c + half];
-              v[m][i] = second ? fmaf(v[m][i], cs.x, other * cs.y) : fmaf(v[m][i], cs.x, -other * cs.y);
-            }
+            const float turned = fmaf(v[m][i], cs[m][i], other[m][i] * sn[m][i]);
+            // (half a team: every channel is turned)
+            v[m][i] = X == kHalfTeam || at[m] + i < a.R ? turned : v[m][i];
           }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
       }
-      TIO* op = static_cast<TIO*>(a.out[which]) + (token * a.heads[which] + h) * a.D;
+      TIO* op = static_cast<TIO*>(a.out[which]) + (token * a.heads[which] + (which ? hh - a.heads[0] : hh)) * a.D;
 #pragma unroll
       for (int m = 0; m < M; ++m)
         if (live && nn[m] > 0) store_pack<TIO, V, !WHOLE>(op + at[m], v[m], nn[m]);
@@ -144,12 +207,25 @@ hipError_t launch_io(const HeadNormArgs& args, hipStream_t s) {
     kern<<<dim3((unsigned)blocks), kThreads, 0, s>>>(a);
     return hipGetLastError();
   };
-  if (a.D < V) return go(head_norm_kernel<TIO, 8, 1, false>, 8);
-  if (packs <= 8) return go(head_norm_kernel<TIO, 8, 1, true>, 8);
-  if (packs <= 16) return go(head_norm_kernel<TIO, 16, 1, true>, 16);
-  if (packs <= 32) return go(head_norm_kernel<TIO, 32, 1, true>, 32);
-  if (packs <= 64) return go(head_norm_kernel<TIO, 64, 1, true>, 64);
-  if constexpr (V == 4) return go(head_norm_kernel<TIO, 64, 2, true>, 64);
+  auto team = [&](auto lanes, auto packs_each, auto whole) {
+    constexpr int T = decltype(lanes)::value, M = decltype(packs_each)::value;
+    constexpr bool W = decltype(whole)::value;
+    if (a.R == 0) return go(head_norm_kernel<TIO, T, M, W, kNone>, T);
+    if constexpr (W) {
+      if (a.pairs && a.D % 2 == 0) return go(head_norm_kernel<TIO, T, M, W, kSameLane>, T);
+      if constexpr (M == 1)
+        if (!a.pairs && a.R == a.D && a.D == T * V) return go(head_norm_kernel<TIO, T, M, W, kHalfTeam>, T);
+    }
+    return go(head_norm_kernel<TIO, T, M, W, kAnywhere>, T);
+  };
+  using std::integral_constant;
+  constexpr integral_constant<int, 1> one{};
+  if (a.D < V) return team(integral_constant<int, 8>{}, one, std::false_type{});
+  if (packs <= 8) return team(integral_constant<int, 8>{}, one, std::true_type{});
+  if (packs <= 16) return team(integral_constant<int, 16>{}, one, std::true_type{});
+  if (packs <= 32) return team(integral_constant<int, 32>{}, one, std::true_type{});
+  if (packs <= 64) return team(integral_constant<int, 64>{}, one, std::true_type{});
+  if constexpr (V == 4) return team(integral_constant<int, 64>{}, integral_constant<int, 2>{}, std::true_type{});
   return hipErrorInvalidValue;
 }
 
