@@ -79,6 +79,7 @@ struct HeadNormArgs {
   int l2, pairs;
   float eps;
   int per;                         // heads a wave takes of a token (set at launch)
+  bool stream;                     // read past the memory-side cache (set at launch)
 };
 hipError_t launch_head_norm(const HeadNormArgs& a, int io, hipStream_t s);
 

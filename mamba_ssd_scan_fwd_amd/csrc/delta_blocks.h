@@ -83,14 +83,15 @@ template <int TA, int TB> __device__ __forceinline__ void mul_pair(f32x4_t& acc,
 struct DeltaSlot {
   int64_t seq, part, row, first, last, t0, t1;
 };
-__device__ __forceinline__ int64_t delta_first_slot(const DeltaArgs& a, int64_t s, int64_t unit) {
-  return a.cu != nullptr ? seq_offset(a.cu, s, a.L) / unit + s : s * ((a.L + unit - 1) / unit);
+// (Tokens, slots and units are below 2^31: their quotients are taken in 32 bits.)
+__device__ __forceinline__ int64_t delta_first_slot(const DeltaArgs& a, int64_t s, uint32_t unit) {
+  return a.cu != nullptr ? (uint32_t)seq_offset(a.cu, s, a.L) / unit + s : s * (((uint32_t)a.L + unit - 1) / unit);
 }
 // (by a whole wave)
-__device__ __forceinline__ DeltaSlot delta_slot(const DeltaArgs& a, int64_t slot, int64_t unit) {
+__device__ __forceinline__ DeltaSlot delta_slot(const DeltaArgs& a, uint32_t slot, uint32_t unit) {
   DeltaSlot r;
   if (a.cu == nullptr) {
-    const int64_t nc = (a.L + unit - 1) / unit;
+    const uint32_t nc = ((uint32_t)a.L + unit - 1) / unit;
     r.seq = r.row = slot / nc;
     r.first = 0, r.last = a.L;
   } else {
@@ -100,7 +101,7 @@ __device__ __forceinline__ DeltaSlot delta_slot(const DeltaArgs& a, int64_t slot
     while (n > 1) {
       const int64_t step = (n + 63) / 64;
       const int64_t i = lo + lane * step;
-      const bool le = lane * step < n && delta_first_slot(a, i, unit) <= slot;
+      const bool le = lane * step < n && delta_first_slot(a, i, unit) <= (int64_t)slot;
       const uint64_t m = __ballot(le);
       const int k = m == 0 ? 0 : 63 - __builtin_clzll(m);
       const int64_t left = n - k * step;
@@ -110,7 +111,7 @@ __device__ __forceinline__ DeltaSlot delta_slot(const DeltaArgs& a, int64_t slot
     r.seq = lo, r.row = 0;
     r.first = seq_offset(a.cu, lo, a.L), r.last = seq_offset(a.cu, lo + 1, a.L);
   }
-  r.part = slot - delta_first_slot(a, r.seq, unit);
+  r.part = (int64_t)slot - delta_first_slot(a, r.seq, unit);
   r.t0 = r.first + r.part * unit;
   r.t1 = r.t0 + unit < r.last ? r.t0 + unit : r.last;
   if (r.part < 0) r.t1 = r.t0;  // (before the first sequence)

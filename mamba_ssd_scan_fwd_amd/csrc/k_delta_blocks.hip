@@ -56,7 +56,7 @@ template <int M, int V> __device__ __forceinline__ void spread() {
 // them. PASS 1: over segments, what becomes of a state of zeros (rows p) and, with
 // values of zero, of the unit states (rows P + n): see delta_join.
 template <typename TIO, int NP, int PT, bool DMA, bool WHOLE, int PASS>
-__global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs a, int blocks_p) {
+__global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs a, uint32_t blocks_p) {
   using L = Layout<TIO, NP, PT, DMA>;
   using Rec = DeltaRecord<TIO>;
   constexpr int IO = DeltaTerms<TIO>::io, ST = DeltaTerms<TIO>::state, YT = DeltaTerms<TIO>::y;
@@ -69,11 +69,12 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
   __shared__ __align__(16) unsigned char lds[L::bytes];
   const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64, g = lane / 16, r = lane % 16;
 
-  const int64_t bid = xcd_local_order(blockIdx.x, gridDim.x);
-  const int pb = (int)(bid % blocks_p);
-  const int64_t sh = bid / blocks_p;
-  const int h = (int)(sh % a.H);
-  const int64_t piece = sh / a.H;
+  // (32-bit divisions: those of 64 bits took a microsecond each)
+  const uint32_t bid = (uint32_t)xcd_local_order(blockIdx.x, gridDim.x);
+  const uint32_t sh = bid / blocks_p;
+  const int pb = (int)(bid - sh * blocks_p);
+  const int64_t piece = sh / (uint32_t)a.H;
+  const int h = (int)(sh - (uint32_t)piece * a.H);
   const int p0 = pb * L::cols, pw = p0 + 16 * PT * wave;
   // column r of tile pt
   auto column = [&](int pt) { return PT == 2 ? pw + 8 * (r / 4) + 4 * pt + r % 4 : pw + r; };
@@ -81,7 +82,7 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
   // the tokens: of a sequence, or of one of its segments
   DeltaSlot sl;
   if (a.seg != 0) {
-    sl = delta_slot(a, piece, a.seg);
+    sl = delta_slot(a, (uint32_t)piece, (uint32_t)a.seg);
     if (sl.part < 0 || (sl.part > 0 && sl.t1 <= sl.t0)) return;
     if (PASS == 1 && sl.t1 >= sl.last) return;  // nothing begins behind the last one
   } else {
@@ -93,7 +94,7 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
   const int64_t row = sl.row, first = sl.t0, last = sl.t1;
   int64_t slot = delta_first_slot(a, sl.seq, kDeltaBlock) + (first - sl.first) / kDeltaBlock;
   const int rows_p = PASS == 1 ? a.P + a.N : a.P;  // rows in all
-  const int64_t grp = h / (a.H / a.G);
+  const int64_t grp = (uint32_t)h / ((uint32_t)a.H / (uint32_t)a.G);
   const TIO* Xp = static_cast<const TIO*>(a.x) + row * a.xs.batch + (int64_t)h * a.P;
   const TIO* Bp = static_cast<const TIO*>(a.B) + row * a.bs.batch + grp * a.N;
   const TIO* Cp = static_cast<const TIO*>(a.C) + row * a.cs.batch + grp * a.N;
@@ -557,7 +558,7 @@ template <typename TIO, int NP, int PASS>
 hipError_t launch_pass(const DeltaArgs& a, hipStream_t s) {
   const int rows_p = PASS == 1 ? a.P + a.N : a.P;
   auto go = [&](auto kern, int cols) {
-    const int blocks_p = (rows_p + cols - 1) / cols;
+    const uint32_t blocks_p = (rows_p + cols - 1) / cols;
     const int64_t pieces = a.seg != 0 ? delta_slots(a, a.seg) : a.seqs();
     kern<<<dim3((unsigned)(pieces * a.H * blocks_p)), kThreads, 0, s>>>(a, blocks_p);
     return hipGetLastError();

@@ -16,15 +16,15 @@ namespace {
 constexpr int kThreads = 256, kRows = 16;
 
 template <int NP>
-__global__ __launch_bounds__(kThreads) void delta_join_kernel(const DeltaArgs a, int blocks_p) {
+__global__ __launch_bounds__(kThreads) void delta_join_kernel(const DeltaArgs a, uint32_t blocks_p) {
   constexpr int PITCH = NP + 4;
   constexpr int CT = (NP / 16 + 3) / 4;  // 16-column tiles of a wave
   __shared__ __align__(16) float s[kRows * PITCH];
   const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64, g = lane / 16, r = lane % 16;
-  const int pb = blockIdx.x % blocks_p;
-  const int64_t sh = blockIdx.x / blocks_p;
-  const int h = (int)(sh % a.H);
-  const int64_t seq = sh / a.H;
+  const uint32_t sh = blockIdx.x / blocks_p;
+  const int pb = (int)(blockIdx.x - sh * blocks_p);
+  const int64_t seq = sh / (uint32_t)a.H;
+  const int h = (int)(sh - (uint32_t)seq * a.H);
   const int p0 = pb * kRows;
   const int64_t base = delta_first_slot(a, seq, a.seg);
   const int64_t first = a.cu != nullptr ? seq_offset(a.cu, seq, a.L) : 0, last = a.cu != nullptr ? seq_offset(a.cu, seq + 1, a.L) : a.L;
@@ -98,7 +98,7 @@ __global__ __launch_bounds__(kThreads) void delta_join_kernel(const DeltaArgs a,
 }  // namespace
 
 hipError_t launch_delta_join(const DeltaArgs& a, hipStream_t s) {
-  const int blocks_p = (a.P + kRows - 1) / kRows;
+  const uint32_t blocks_p = (a.P + kRows - 1) / kRows;
   const dim3 grid((unsigned)(a.seqs() * a.H * blocks_p));
   if (a.N <= 32) delta_join_kernel<32><<<grid, kThreads, 0, s>>>(a, blocks_p);
   else if (a.N <= 64) delta_join_kernel<64><<<grid, kThreads, 0, s>>>(a, blocks_p);

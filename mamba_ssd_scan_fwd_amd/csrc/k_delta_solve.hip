@@ -80,7 +80,7 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TIO) == 2 && NP <= 128 ? 2 : 1)
   char* rec = a.ws + (int64_t)task * Rec::bytes;
 
   // columns 32 ks + 8 g .. of a row
-  const int grp = h / (a.H / a.G);
+  const int grp = (int)((uint32_t)h / ((uint32_t)a.H / (uint32_t)a.G));
   const TIO* Bp = static_cast<const TIO*>(a.B) + at.row * a.bs.batch + at.t0 * a.bs.token + (int64_t)grp * a.N;
   const TIO* Cp = static_cast<const TIO*>(a.C) + at.row * a.cs.batch + at.t0 * a.cs.token + (int64_t)grp * a.N;
   uint32_t col[KS];

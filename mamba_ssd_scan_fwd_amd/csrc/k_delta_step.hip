@@ -21,14 +21,14 @@ namespace {
 constexpr int kThreads = 256;
 
 template <typename TIO, typename TDT, int NP, bool VEC, int R>
-__global__ __launch_bounds__(kThreads) void delta_step_kernel(const DeltaStepArgs a, int blocks_p) {
+__global__ __launch_bounds__(kThreads) void delta_step_kernel(const DeltaStepArgs a, uint32_t blocks_p) {
   constexpr int LPR = NP / 4;             // lanes per row of the state
   constexpr int TEAMS = kThreads / LPR;
   const int tid = threadIdx.x, sub = tid % LPR, team = tid / LPR;
-  const int pb = blockIdx.x % blocks_p;
-  const int64_t rh = blockIdx.x / blocks_p;
-  const int h = (int)(rh % a.H);
-  const int64_t r = rh / a.H;
+  const uint32_t rh = blockIdx.x / blocks_p;
+  const int pb = (int)(blockIdx.x - rh * blocks_p);
+  const int64_t r = rh / (uint32_t)a.H;
+  const int h = (int)(rh - (uint32_t)r * a.H);
   const int g = h / (a.H / a.G);
   const int n0 = 4 * sub;
   const int nn = a.N - n0 < 0 ? 0 : a.N - n0 > 4 ? 4 : a.N - n0;  // columns this lane holds
@@ -105,7 +105,7 @@ hipError_t launch_np(const DeltaStepArgs& args, hipStream_t s) {
   a.stream = a.batch * a.H * a.P * a.N * (int64_t)sizeof(float) >= kMemorySideCache / 4;
   constexpr int TEAMS = kThreads / (NP / 4);
   auto go = [&](auto kern, int rows) {
-    const int blocks_p = (a.P + TEAMS * rows - 1) / (TEAMS * rows);
+    const uint32_t blocks_p = (a.P + TEAMS * rows - 1) / (TEAMS * rows);
     kern<<<dim3((unsigned)(a.batch * a.H * blocks_p)), kThreads, 0, s>>>(a, blocks_p);
     return hipGetLastError();
   };

@@ -23,16 +23,16 @@ template <typename TIO, typename TDT, int R> struct Token {
 };
 
 template <typename TIO, typename TDT, int NP, bool VEC, int R>
-__global__ __launch_bounds__(kThreads) void delta_walk_kernel(const DeltaArgs a, int blocks_p) {
+__global__ __launch_bounds__(kThreads) void delta_walk_kernel(const DeltaArgs a, uint32_t blocks_p) {
   constexpr int LPR = NP / 4;
   constexpr int TEAMS = kThreads / LPR;
   using RX = typename Elem<TIO>::raw;
   using RD = typename Elem<TDT>::raw;
   const int tid = threadIdx.x, sub = tid % LPR, team = tid / LPR;
-  const int pb = blockIdx.x % blocks_p;
-  const int64_t sh = blockIdx.x / blocks_p;
-  const int h = (int)(sh % a.H);
-  const int64_t seq = sh / a.H;
+  const uint32_t sh = blockIdx.x / blocks_p;
+  const int pb = (int)(blockIdx.x - sh * blocks_p);
+  const int64_t seq = sh / (uint32_t)a.H;
+  const int h = (int)(sh - (uint32_t)seq * a.H);
   const int g = h / (a.H / a.G);
   const int n0 = 4 * sub;
   const int nn = a.N - n0 < 0 ? 0 : a.N - n0 > 4 ? 4 : a.N - n0;
@@ -126,7 +126,7 @@ __global__ __launch_bounds__(kThreads) void delta_walk_kernel(const DeltaArgs a,
 template <typename TIO, typename TDT, int NP>
 hipError_t launch_np(const DeltaArgs& a, hipStream_t s) {
   constexpr int R = 2, TEAMS = kThreads / (NP / 4);
-  const int blocks_p = (a.P + TEAMS * R - 1) / (TEAMS * R);
+  const uint32_t blocks_p = (a.P + TEAMS * R - 1) / (TEAMS * R);
   const dim3 grid((unsigned)(a.seqs() * a.H * blocks_p));
   if (a.N % 4 == 0) delta_walk_kernel<TIO, TDT, NP, true, R><<<grid, kThreads, 0, s>>>(a, blocks_p);
   else delta_walk_kernel<TIO, TDT, NP, false, R><<<grid, kThreads, 0, s>>>(a, blocks_p);
