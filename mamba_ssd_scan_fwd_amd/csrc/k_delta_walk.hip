@@ -4,10 +4,12 @@
 // padded N / 4 lanes keeps R of them in registers, four columns to a lane, for
 // the whole sequence; S k and S q are reduced side by side (y = scale (a S q +
 // u (k q))). The next kAhead tokens' rows are loaded while the present ones are
-// worked on.
+// worked on. Decays and betas are taken by a lane for a token, 64 tokens at once: by
+// every lane for every token they were half of all instructions.
 //
-// Bound by latency: a token is two dependent reductions. It is right for every
-// size.
+// Bound by a wave's instructions and their latency, some 450 cycles a token.
+// For prompts of a few tokens, which the blocks' two kernels do not repay, and
+// for sizes that have no blocks.
 #include "delta.h"
 
 namespace ssd {
@@ -16,10 +18,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kAhead = 4;
 
-template <typename TIO, typename TDT, int R> struct Token {
+template <typename TIO, int R> struct Token {
   Pack<TIO, 4> k, q;
   typename Elem<TIO>::raw x[R];
-  typename Elem<TDT>::raw dt, be;
 };
 
 template <typename TIO, typename TDT, int NP, bool VEC, int R>
@@ -65,30 +66,37 @@ __global__ __launch_bounds__(kThreads) void delta_walk_kernel(const DeltaArgs a,
       for (int i = 0; i < 4; ++i) S[k][i] = i < nn ? v.v[i] : 0.f;
     }
   }
-  auto load = [&](Token<TIO, TDT, R>(&v)[kAhead], int64_t t0) {
+  auto load = [&](Token<TIO, R>(&v)[kAhead], int64_t t0) {
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const int64_t t = t0 + j < last ? t0 + j : last - 1;
       v[j].k = load_pack<TIO, 4, !VEC>(Bp + t * a.bs.token, nn);
       v[j].q = load_pack<TIO, 4, !VEC>(Cp + t * a.cs.token, nn);
-      v[j].dt = dp[t * a.ds.token];
-      v[j].be = ep[t * a.es.token];
 #pragma unroll
       for (int k = 0; k < R; ++k) v[j].x[k] = reinterpret_cast<const RX*>(xp)[t * a.xs.token + (int64_t)h * a.P + p[k]];
     }
   };
-  Token<TIO, TDT, R> next[kAhead];
+  Token<TIO, R> next[kAhead];
   if (first < last) load(next, first);
+  // decay and beta of token `from` + lane
+  float decays = 0.f, betas = 0.f;
+  auto gates = [&](int64_t from) {
+    const int64_t t = from + (tid & 63) < last ? from + (tid & 63) : last - 1;
+    decays = __builtin_amdgcn_exp2f(delta_log2_decay(Elem<TDT>::f32(dp[t * a.ds.token]), bias, Ah, a.dto));
+    betas = delta_beta(Elem<TDT>::f32(ep[t * a.es.token]), a.sigmoid);
+  };
+  auto of_lane = [](float v, int lane) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane)); };
   for (int64_t t0 = first; t0 < last; t0 += kAhead) {
-    Token<TIO, TDT, R> cur[kAhead];
+    const int at = (int)(t0 - first) & 63;  // (kAhead divides 64)
+    if (at == 0) gates(t0);
+    Token<TIO, R> cur[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) cur[j] = next[j];
     if (t0 + kAhead < last) load(next, t0 + kAhead);
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       if (t0 + j >= last) break;
-      const float dec = __builtin_amdgcn_exp2f(delta_log2_decay(Elem<TDT>::f32(cur[j].dt), bias, Ah, a.dto));
-      const float beta = delta_beta(Elem<TDT>::f32(cur[j].be), a.sigmoid);
+      const float dec = of_lane(decays, at + j), beta = of_lane(betas, at + j);
       float kf[4], qf[4], kq = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
