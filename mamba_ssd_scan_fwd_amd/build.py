@@ -53,7 +53,8 @@ COMMON = [
 # per source: matrix results in ordinary registers. The compiler otherwise puts
 # accumulators of a kernel that may use more than 256 registers into the other
 # half of the file, from where every scaling and rounding has to fetch them.
-EXTRA = {name: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for name in ("k_delta_blocks.hip", "k_delta_solve.hip")}
+EXTRA = {name: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for name in ("k_delta_blocks.hip", "k_delta_chain.hip", "k_delta_join.hip",
+                                                                      "k_delta_solve.hip")}
 
 
 def hipcc() -> str:

@@ -44,6 +44,8 @@ bool delta_blocks_apply(const DeltaArgs& a, int io);
 int64_t delta_blocks_workspace(DeltaArgs& a, int io);  // in bytes; sets a.seg
 hipError_t launch_delta_blocks(const DeltaArgs& a, int io, int dt, hipStream_t s);
 hipError_t launch_delta_solve(const DeltaArgs& a, int io, int dt, hipStream_t s);
+bool delta_chain_applies(const DeltaArgs& a, int io);
+hipError_t launch_delta_chain(const DeltaArgs& a, int pass, hipStream_t s);
 hipError_t launch_delta_join(const DeltaArgs& a, hipStream_t s);
 
 struct DeltaStepArgs {

@@ -118,6 +118,37 @@ __device__ __forceinline__ DeltaSlot delta_slot(const DeltaArgs& a, uint32_t slo
   return r;
 }
 
+// What a workgroup walks: a sequence, or (a.seg != 0) one of the sequences' segments.
+// PASS 0: from the states that enter them. PASS 1: over segments, what becomes of a
+// state of zeros (rows p) and, with values of zero, of the unit states (rows P + n),
+// see delta_join. False: nothing to walk.
+template <int PASS> __device__ __forceinline__ bool delta_piece(const DeltaArgs& a, int64_t piece, DeltaSlot& sl) {
+  if (a.seg != 0) {
+    sl = delta_slot(a, (uint32_t)piece, (uint32_t)a.seg);
+    if (sl.part < 0 || (sl.part > 0 && sl.t1 <= sl.t0)) return false;
+    return PASS == 0 || sl.t1 < sl.last;  // nothing begins behind the last one
+  }
+  sl.seq = piece, sl.part = 0, sl.row = a.cu != nullptr ? 0 : piece;
+  sl.t0 = sl.first = a.cu != nullptr ? seq_offset(a.cu, piece, a.L) : 0;
+  sl.t1 = sl.last = a.cu != nullptr ? seq_offset(a.cu, piece + 1, a.L) : a.L;
+  return true;
+}
+
+// Where the 16-byte piece c of row t lies in K's and Q's tile in LDS: c with these
+// bits flipped.
+template <int NP> __device__ __forceinline__ int k_swz(int t) {
+  return NP >= 128 ? ((t & 3) << 2) | ((t >> 3) & 3) : NP == 64 ? ((t & 2) << 1) | ((t >> 3) & 3) : (t >> 3) & 3;
+}
+
+// One matrix product, then V ordinary instructions, M times: what runs beside what.
+template <int M, int V> __device__ __forceinline__ void spread() {
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x2, V, 0);
+  }
+}
+
 // Rows of a block's tokens through a buffer descriptor: what lies behind the
 // block's last row reads as zeros, and so does an offset of kNowhere. Pieces of
 // eight elements; where N is no multiple of eight (WHOLE false) the last piece of

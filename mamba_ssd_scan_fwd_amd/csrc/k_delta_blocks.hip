@@ -1,25 +1,11 @@
-// The gated delta rule in blocks, second kernel: the walk over a sequence's
-// blocks of 64 tokens (delta_blocks.h has the formulas and what the first
-// kernel left), batched or packed.
+// The gated delta rule in blocks, the walk over a sequence's blocks for rows that
+// k_delta_chain.hip does not take: fp32, states of more than 128 columns, odd sizes
+// and rows that are not aligned. (And the choice between them.)
 //
-// The state's rows p do not meet, so a wave keeps 16 of them, transposed
-// (S^T [N, 16] in accumulators), for the whole sequence, and nothing of the chain
-//     R = X - e^g K S0^T;  U = T R;  S^T <- e^g_end S^T + K^T (e^(g_end - g) U)
-// leaves its registers: a product's result, four consecutive rows of a column to a
-// lane, is the next product's right operand as it stands once the rows of a
-// pair of result tiles are numbered 8 (r / 4) + 4 h + r % 4 (r the row, h the tile).
-// The left operands (K by rows and by columns, Q, T, M) are shared by the
-// workgroup's four waves through LDS, its 16-byte pieces permuted so that the
-// reads by rows and the transposing ones meet few bank conflicts.
-//
-// Aligned bf16 rows go from memory straight to the LDS (DMA), the next block's while a
-// block is worked on: K, which a block needs first and last, into a second tile, what
-// else into its own place once it has been read. So two workgroups fit a compute
-// unit, and one's products run beside the other's roundings and waits: with 32 rows a
-// wave and one workgroup a block of 128 rows took 8600 cycles (each wave's
-// instructions one after the other), with all of the LDS once and the whole load waited
-// for 8400, of which 3900 were that wait. Other rows go through registers, where odd ones are put
-// in order and fp32 is split into terms.
+// The same products in the same layouts, by one kind of waves: each keeps 16 rows of the state
+// and makes their y too. The next block's rows are loaded into registers while
+// a block is worked on; on the way from there to the LDS odd rows are put in order and
+// fp32 is split into terms.
 //
 // S, R and U' = e^(g_end - g) U are held in fp32. As operands they are terms
 // (delta_blocks.h).
@@ -33,36 +19,21 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kCols = 64;  // rows p of a workgroup
 
-template <typename TIO, int NP, bool DMA> struct Layout {
+template <typename TIO, int NP> struct Layout {
   static constexpr int IO = DeltaTerms<TIO>::io;
   static constexpr int tile = 64 * NP * 2;  // K or Q, one term
   static constexpr int xrow = kCols * (int)sizeof(TIO);
-  static constexpr int K = 0, Q = (DMA ? 2 : IO) * tile, rec = Q + IO * tile,
+  static constexpr int K = 0, Q = IO * tile, rec = Q + IO * tile,
                        X = rec + (DeltaRecord<TIO>::bytes + 1023) / 1024 * 1024, bytes = X + 64 * xrow;
 };
 
-// Where the 16-byte piece c of row t lies in K's and Q's and in (bf16) X's tile: c
-// with these bits flipped.
-template <int NP> __device__ __forceinline__ int k_swz(int t) {
-  return NP >= 128 ? ((t & 3) << 2) | ((t >> 3) & 3) : NP == 64 ? ((t & 2) << 1) | ((t >> 3) & 3) : (t >> 3) & 3;
-}
+// Likewise in (bf16) X's tile.
 __device__ __forceinline__ int x_swz(int t) { return (t & 2) | ((t >> 1) & 4); }
 
-// One matrix product, then V ordinary instructions, M times: what runs beside what.
-template <int M, int V> __device__ __forceinline__ void spread() {
-#pragma unroll
-  for (int i = 0; i < M; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x2, V, 0);
-  }
-}
-
-// PASS 0: over sequences, or over their segments from the states that enter
-// them. PASS 1: over segments, what becomes of a state of zeros (rows p) and, with
-// values of zero, of the unit states (rows P + n): see delta_join.
-template <typename TIO, int NP, bool DMA, bool WHOLE, int PASS>
-__global__ __launch_bounds__(kThreads, DMA && NP <= 128 ? 2 : 1) void delta_blocks_kernel(const DeltaArgs a, uint32_t blocks_p) {
-  using L = Layout<TIO, NP, DMA>;
+// PASS: see delta_piece.
+template <typename TIO, int NP, bool WHOLE, int PASS>
+__global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs a, uint32_t blocks_p) {
+  using L = Layout<TIO, NP>;
   using Rec = DeltaRecord<TIO>;
   constexpr int IO = DeltaTerms<TIO>::io, ST = DeltaTerms<TIO>::state, YT = DeltaTerms<TIO>::y;
   constexpr int KN = NP / 32;          // 32-column groups of N
@@ -70,10 +41,9 @@ __global__ __launch_bounds__(kThreads, DMA && NP <= 128 ? 2 : 1) void delta_bloc
   constexpr int XP = 16 / (int)sizeof(TIO), XPACKS = kCols / XP;
   constexpr int CK = 64 * PACKS / kThreads, CR = (Rec::bytes / 16 + kThreads - 1) / kThreads, CX = 64 * XPACKS / kThreads;
   constexpr int SZ = (int)sizeof(TIO);
-  static_assert(!DMA || (IO == 1 && WHOLE), "rows as they lie");
   static_assert(L::bytes <= 160 * 1024, "LDS of a compute unit");
   __shared__ __align__(16) unsigned char lds[L::bytes];
-  const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64, g = lane / 16, r = lane % 16;
+  const int tid = threadIdx.x, wave = (int)__builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64, g = lane / 16, r = lane % 16;
 
   // (32-bit divisions: those of 64 bits took a microsecond each)
   const uint32_t bid = (uint32_t)xcd_local_order(blockIdx.x, gridDim.x);
@@ -83,18 +53,8 @@ __global__ __launch_bounds__(kThreads, DMA && NP <= 128 ? 2 : 1) void delta_bloc
   const int h = (int)(sh - (uint32_t)piece * a.H);
   const int p0 = pb * kCols, pw = p0 + 16 * wave, p = pw + r;  // this wave's rows, this lane's
 
-  // the tokens: of a sequence, or of one of its segments
   DeltaSlot sl;
-  if (a.seg != 0) {
-    sl = delta_slot(a, (uint32_t)piece, (uint32_t)a.seg);
-    if (sl.part < 0 || (sl.part > 0 && sl.t1 <= sl.t0)) return;
-    if (PASS == 1 && sl.t1 >= sl.last) return;  // nothing begins behind the last one
-  } else {
-    sl.seq = piece, sl.row = a.cu != nullptr ? 0 : piece;
-    sl.t0 = a.cu != nullptr ? seq_offset(a.cu, piece, a.L) : 0;
-    sl.t1 = sl.last = a.cu != nullptr ? seq_offset(a.cu, piece + 1, a.L) : a.L;
-    sl.first = sl.t0;
-  }
+  if (!delta_piece<PASS>(a, piece, sl)) return;
   const int64_t row = sl.row, first = sl.t0, last = sl.t1;
   int64_t slot = delta_first_slot(a, sl.seq, kDeltaBlock) + (first - sl.first) / kDeltaBlock;
   const int rows_p = PASS == 1 ? a.P + a.N : a.P;  // rows in all
@@ -114,103 +74,62 @@ __global__ __launch_bounds__(kThreads, DMA && NP <= 128 ? 2 : 1) void delta_bloc
     return Rows{block_rows(Bp + t0 * a.bs.token, a.bs.token, n, a.N), block_rows(Cp + t0 * a.cs.token, a.cs.token, n, a.N),
                 block_rows(Xp + t0 * a.xs.token, a.xs.token, n, a.P), buffer_range(a.ws + (sl * a.H + h) * Rec::bytes, Rec::bytes)};
   };
-  // by DMA: piece c of the LDS holds the row's piece c with the tile's bits flipped
-  struct Words {
-    v4i32_t B, C, X, R;
-    int ktile;
-  } to;
-  bool more = false;
-  auto aim = [&](int64_t t0, int64_t sl, int ktile) {
-    const int n = (int)(last - t0 < 64 ? last - t0 : 64);
-    to.B = buffer_words(Bp + t0 * a.bs.token, (uint32_t)((n - 1) * a.bs.token + a.N) * SZ);
-    to.C = buffer_words(Cp + t0 * a.cs.token, (uint32_t)((n - 1) * a.cs.token + a.N) * SZ);
-    to.X = buffer_words(Xp + t0 * a.xs.token, (uint32_t)((n - 1) * a.xs.token + a.P) * SZ);
-    to.R = buffer_words(a.ws + (sl * a.H + h) * Rec::bytes, Rec::bytes);
-    to.ktile = ktile;
-  };
-  const uint32_t here = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)lds + wave * 1024;
-  auto send_rows = [&](const v4i32_t& words, int64_t token, uint32_t at, int j) {
-    const int t = (j * kThreads + tid) / PACKS, n = 8 * ((tid % PACKS) ^ k_swz<NP>(t));
-    dma16(words, here + at + j * kThreads * 16, n < a.N ? (uint32_t)(t * (int)token + n) * SZ : kNowhere);
-  };
-  auto send_k = [&](int j) { send_rows(to.B, a.bs.token, L::K + to.ktile * L::tile, j); };
-  auto send_q_x = [&] {
-    if constexpr (PASS == 0) {
-#pragma unroll
-      for (int j = 0; j < CK; ++j) send_rows(to.C, a.cs.token, L::Q, j);
-    }
-#pragma unroll
-    for (int j = 0; j < CX; ++j) {
-      const int t = (j * kThreads + tid) / XPACKS, c = p0 + 8 * ((tid % XPACKS) ^ x_swz(t));
-      dma16(to.X, here + L::X + j * kThreads * 16, c < a.P ? (uint32_t)(t * (int)a.xs.token + c) * SZ : kNowhere);
-    }
-  };
-  auto send_record = [&] {
-#pragma unroll
-    for (int j = 0; j < CR; ++j)
-      if (j * 4 + wave < (Rec::bytes + 1023) / 1024) dma16(to.R, here + L::rec + j * kThreads * 16, 16 * (j * kThreads + tid));
-  };
-  // through registers
-  Piece<TIO> kq[2][DMA ? 1 : CK];
-  uint4 rc[DMA ? 1 : CR], xv[DMA ? 1 : CX];
+  Piece<TIO> kq[2][CK];
+  uint4 rc[CR], xv[CX];
   int kmoved, xmoved;
   const int kc = tid % PACKS, xc = tid % XPACKS;  // this thread's piece of a row
   const uint32_t kcol = piece_at<TIO, WHOLE>(8 * kc, a.N, kmoved);
   const uint32_t xcol = piece_at<TIO, WHOLE>(p0 + XP * xc, a.P, xmoved, XP);
   auto fetch = [&](int64_t t0, int64_t sl) {
-    if constexpr (!DMA) {
-      const Rows from = rows_of(t0, sl);
+    const Rows from = rows_of(t0, sl);
 #pragma unroll
-      for (int j = 0; j < CK; ++j) {
-        const int t = (j * kThreads + tid) / PACKS;
-        kq[0][j] = load_piece<TIO>(from.B, (uint32_t)(t * (int)a.bs.token) * SZ, kcol);
-        kq[1][j] = load_piece<TIO>(from.C, (uint32_t)(t * (int)a.cs.token) * SZ, kcol);
-      }
+    for (int j = 0; j < CK; ++j) {
+      const int t = (j * kThreads + tid) / PACKS;
+      kq[0][j] = load_piece<TIO>(from.B, (uint32_t)(t * (int)a.bs.token) * SZ, kcol);
+      kq[1][j] = load_piece<TIO>(from.C, (uint32_t)(t * (int)a.cs.token) * SZ, kcol);
+    }
 #pragma unroll
-      for (int j = 0; j < CR; ++j) rc[j] = buffer_ld16(from.R, 16 * (j * kThreads + tid));
+    for (int j = 0; j < CR; ++j) rc[j] = buffer_ld16(from.R, 16 * (j * kThreads + tid));
 #pragma unroll
-      for (int j = 0; j < CX; ++j) {
-        const int t = (j * kThreads + tid) / XPACKS;
-        xv[j] = buffer_ld16(from.X, xcol == kNowhere ? kNowhere : (uint32_t)(t * (int)a.xs.token) * SZ + xcol);
-      }
+    for (int j = 0; j < CX; ++j) {
+      const int t = (j * kThreads + tid) / XPACKS;
+      xv[j] = buffer_ld16(from.X, xcol == kNowhere ? kNowhere : (uint32_t)(t * (int)a.xs.token) * SZ + xcol);
     }
   };
   auto stage = [&] {
-    if constexpr (!DMA) {
 #pragma unroll
-      for (int j = 0; j < CK; ++j) {
-        const int t = (j * kThreads + tid) / PACKS;
-        unsigned char* kd = lds + L::K + t * (NP * 2) + 16 * (kc ^ k_swz<NP>(t));
-        unsigned char* qd = lds + L::Q + t * (NP * 2) + 16 * (kc ^ k_swz<NP>(t));
-        move_piece<TIO, WHOLE>(kq[0][j], kmoved);
-        move_piece<TIO, WHOLE>(kq[1][j], kmoved);
-        if constexpr (IO > 1) {
-          const Terms<IO> k = split_piece<IO>(kq[0][j]), q = split_piece<IO>(kq[1][j]);
+    for (int j = 0; j < CK; ++j) {
+      const int t = (j * kThreads + tid) / PACKS;
+      unsigned char* kd = lds + L::K + t * (NP * 2) + 16 * (kc ^ k_swz<NP>(t));
+      unsigned char* qd = lds + L::Q + t * (NP * 2) + 16 * (kc ^ k_swz<NP>(t));
+      move_piece<TIO, WHOLE>(kq[0][j], kmoved);
+      move_piece<TIO, WHOLE>(kq[1][j], kmoved);
+      if constexpr (IO > 1) {
+        const Terms<IO> k = split_piece<IO>(kq[0][j]), q = split_piece<IO>(kq[1][j]);
 #pragma unroll
-          for (int i = 0; i < IO; ++i) {
-            st16(kd + i * L::tile, __builtin_bit_cast(uint4, k.v[i]));
-            st16(qd + i * L::tile, __builtin_bit_cast(uint4, q.v[i]));
-          }
-        } else {
-          st16(kd, kq[0][j].v), st16(qd, kq[1][j].v);
+        for (int i = 0; i < IO; ++i) {
+          st16(kd + i * L::tile, __builtin_bit_cast(uint4, k.v[i]));
+          st16(qd + i * L::tile, __builtin_bit_cast(uint4, q.v[i]));
         }
+      } else {
+        st16(kd, kq[0][j].v), st16(qd, kq[1][j].v);
       }
+    }
 #pragma unroll
-      for (int j = 0; j < CR; ++j) {
-        const int q = j * kThreads + tid;
-        if (q < Rec::bytes / 16) st16(lds + L::rec + 16 * q, rc[j]);
-      }
+    for (int j = 0; j < CR; ++j) {
+      const int q = j * kThreads + tid;
+      if (q < Rec::bytes / 16) st16(lds + L::rec + 16 * q, rc[j]);
+    }
 #pragma unroll
-      for (int j = 0; j < CX; ++j) {
-        const int t = (j * kThreads + tid) / XPACKS;
-        if constexpr (!WHOLE) {
-          uint32_t w[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
-          move_down<TIO, 4>(w, xmoved);
-          xv[j] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        if constexpr (SZ == 4) st16(lds + L::X + t * L::xrow + ((16 * xc + 64 * ((t >> 3) & 3)) & 255), xv[j]);
-        else st16(lds + L::X + t * L::xrow + 16 * (xc ^ x_swz(t)), xv[j]);
+    for (int j = 0; j < CX; ++j) {
+      const int t = (j * kThreads + tid) / XPACKS;
+      if constexpr (!WHOLE) {
+        uint32_t w[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
+        move_down<TIO, 4>(w, xmoved);
+        xv[j] = make_uint4(w[0], w[1], w[2], w[3]);
       }
+      if constexpr (SZ == 4) st16(lds + L::X + t * L::xrow + ((16 * xc + 64 * ((t >> 3) & 3)) & 255), xv[j]);
+      else st16(lds + L::X + t * L::xrow + 16 * (xc ^ x_swz(t)), xv[j]);
     }
   };
 
@@ -220,17 +139,7 @@ __global__ __launch_bounds__(kThreads, DMA && NP <= 128 ? 2 : 1) void delta_bloc
   const int kat = rt * (NP * 2), tat = L::K + (8 * g + ta) * (NP * 2);
   const int kf = k_swz<NP>(rt), tf = k_swz<NP>(8 * g + ta);
 
-  if (first < last) {
-    if constexpr (DMA) {
-      aim(first, slot, 0);
-#pragma unroll
-      for (int j = 0; j < CK; ++j) send_k(j);
-      send_q_x();
-      send_record();
-    } else {
-      fetch(first, slot);
-    }
-  }
+  if (first < last) fetch(first, slot);
 
   // S^T: tile (kn, hh) rows 32 kn + 8 g + 4 hh .., column p
   f32x4_t S[KN][2];
@@ -264,52 +173,15 @@ __global__ __launch_bounds__(kThreads, DMA && NP <= 128 ? 2 : 1) void delta_bloc
   }
 
   const bool live = pw < rows_p;
-  int ktile = 0;
   for (int64_t t0 = first; t0 < last; t0 += 64, ++slot) {
-    more = t0 + 64 < last;
-    if constexpr (DMA) {
-      // this block's rows are there (the last block's four stores are younger)
-      if (PASS == 0 && live && t0 != first) vm_wait<4>();
-      else vm_wait<0>();
-      __syncthreads();
-      if (more) aim(t0 + 64, slot + 1, ktile ^ 1);
-    } else {
-      __syncthreads();  // the last block's operands have been read
-      stage();
-      __syncthreads();
-      if (more) fetch(t0 + 64, slot + 1);
-    }
-    // The places of Q and X, and later of the record, are free for the next block's.
-    auto free_q_x = [&] {
-      if constexpr (DMA) {
-        __syncthreads();
-        if (more) send_q_x();
-      }
-    };
-    auto free_record = [&] {
-      if constexpr (DMA) {
-        __syncthreads();
-        if (more) send_record();
-      }
-    };
-    if (!live) {
-      if constexpr (DMA) {
-        if (more) {
-#pragma unroll
-          for (int j = 0; j < CK; ++j) send_k(j);
-        }
-        ktile ^= 1;
-      }
-      free_q_x();
-      free_record();
-      continue;
-    }
-    const unsigned char* at = lds;
-    const unsigned char* ktiles = lds + L::K + (DMA ? ktile * L::tile : 0);
-    if constexpr (DMA) ktile ^= 1;
+    __syncthreads();  // the last block's operands have been read
+    stage();
+    __syncthreads();
+    if (t0 + 64 < last) fetch(t0 + 64, slot + 1);
+    if (!live) continue;
     const int n = (int)(last - t0 < 64 ? last - t0 : 64);
 
-    const float* eg = reinterpret_cast<const float*>(at + L::rec + Rec::decays);
+    const float* eg = reinterpret_cast<const float*>(lds + L::rec + Rec::decays);
     const float* ed = eg + 64;
     auto by_rows = [&](const unsigned char* from, int i, int kn) {  // rows of tile i, columns 32 kn ..
       Terms<IO> v;
@@ -318,13 +190,13 @@ __global__ __launch_bounds__(kThreads, DMA && NP <= 128 ? 2 : 1) void delta_bloc
         v.v[e] = as_bf16x8(ld16(from + kat + e * L::tile + (32 * (i / 2) + 4 * (i % 2)) * (NP * 2) + 16 * ((4 * kn + g) ^ kf)));
       return v;
     };
-    auto kfrag = [&](int i, int kn) { return by_rows(ktiles, i, kn); };
-    auto qfrag = [&](int i, int kn) { return by_rows(at + L::Q, i, kn); };
+    auto kfrag = [&](int i, int kn) { return by_rows(lds + L::K, i, kn); };
+    auto qfrag = [&](int i, int kn) { return by_rows(lds + L::Q, i, kn); };
     auto ktfrag = [&](int hh, int kk, int kn) {  // tile hh of columns 32 kn .., rows 32 kk ..
       Terms<IO> v;
 #pragma unroll
       for (int e = 0; e < IO; ++e) {
-        const unsigned char* s = ktiles + tat + e * L::tile + 32 * kk * (NP * 2) + 16 * ((4 * kn + tb) ^ tf) + 8 * hh;
+        const unsigned char* s = lds + L::K + tat + e * L::tile + 32 * kk * (NP * 2) + 16 * ((4 * kn + tb) ^ tf) + 8 * hh;
         const uint2 lo = lds_tr8(s), hi = lds_tr8(s + 4 * (NP * 2));
         v.v[e] = as_bf16x8(make_uint4(lo.x, lo.y, hi.x, hi.y));
       }
@@ -334,7 +206,7 @@ __global__ __launch_bounds__(kThreads, DMA && NP <= 128 ? 2 : 1) void delta_bloc
       Terms<decltype(terms)::value> v;
 #pragma unroll
       for (int e = 0; e < decltype(terms)::value; ++e)
-        v.v[e] = as_bf16x8(ld16(at + L::rec + 16 * lane + from + (e * kTriFrags + i) * kFragBytes));
+        v.v[e] = as_bf16x8(ld16(lds + L::rec + 16 * lane + from + (e * kTriFrags + i) * kFragBytes));
       return v;
     };
     auto of_y = [&](const Terms<ST>& s) {
@@ -375,10 +247,10 @@ __global__ __launch_bounds__(kThreads, DMA && NP <= 128 ? 2 : 1) void delta_bloc
           if constexpr (SZ == 4) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              xw[i][k] = *reinterpret_cast<const float*>(at + L::X + (tr + k) * L::xrow + ((4 * (16 * wave + r) + 64 * g) & 255));
+              xw[i][k] = *reinterpret_cast<const float*>(lds + L::X + (tr + k) * L::xrow + ((4 * (16 * wave + r) + 64 * g) & 255));
           } else {
             const int t = tr + ta;
-            xr[i] = lds_tr8(at + L::X + t * L::xrow + 16 * ((2 * wave + tb / 2) ^ x_swz(t)) + 8 * (tb & 1));
+            xr[i] = lds_tr8(lds + L::X + t * L::xrow + 16 * ((2 * wave + tb / 2) ^ x_swz(t)) + 8 * (tb & 1));
           }
         }
       }
@@ -391,13 +263,6 @@ __global__ __launch_bounds__(kThreads, DMA && NP <= 128 ? 2 : 1) void delta_bloc
       for (int i = 0; i < 8; ++i) S[kn][i / 4][i % 4] *= end;
       spread<4 * term_pairs(IO, ST), 1>();
       hold();
-      if constexpr (DMA) {
-        if (more) {
-#pragma unroll
-          for (int j = 0; j < CK; ++j)
-            if (j * KN / CK == kn) send_k(j);
-        }
-      }
     }
     // S0 Q^T (rows p, column t); beside it R = X - e^g K S0^T
     Terms<ST> Rv[2];
@@ -433,7 +298,6 @@ __global__ __launch_bounds__(kThreads, DMA && NP <= 128 ? 2 : 1) void delta_bloc
       spread<4 * term_pairs(YT, IO), 2>();
       hold();
     }
-    free_q_x();
     // U = T R; beside it O e^g
     f32x4_t U[4], d[4];
     float er[4];
@@ -481,7 +345,6 @@ __global__ __launch_bounds__(kThreads, DMA && NP <= 128 ? 2 : 1) void delta_bloc
 #pragma unroll
         for (int i = 2 * ks; i < 4; ++i) mul_pair(O[i], Uy[ks], mf[tri_frag(i / 2, i % 2, ks)], pair);
     hold();
-    free_record();
     // y: rows pw + 4 g .. of a lane at token 32 (i / 2) + 4 (i % 2) + rt
     auto put_y = [&] {
       const __amdgpu_buffer_rsrc_t Yr = buffer_range(Yp + t0 * HP, (uint32_t)((n - 1) * HP + a.P) * SZ);
@@ -547,34 +410,21 @@ hipError_t launch_pass(const DeltaArgs& a, hipStream_t s) {
     return hipGetLastError();
   };
   const bool whole = a.N % 8 == 0 && a.P % (16 / sizeof(TIO)) == 0;
-  if constexpr (sizeof(TIO) == 2) {
-    auto lies = [](const void* p, const Stride& st) {
-      return (reinterpret_cast<uintptr_t>(p) | (uintptr_t)(st.token * 2) | (uintptr_t)(st.batch * 2)) % 16 == 0;
-    };
-    if (whole && lies(a.x, a.xs) && lies(a.B, a.bs) && lies(a.C, a.cs)) return go(delta_blocks_kernel<TIO, NP, true, true, PASS>);
-    return go(delta_blocks_kernel<TIO, NP, false, false, PASS>);
-  } else {
-    return whole ? go(delta_blocks_kernel<TIO, NP, false, true, PASS>) : go(delta_blocks_kernel<TIO, NP, false, false, PASS>);
-  }
+  return whole ? go(delta_blocks_kernel<TIO, NP, true, PASS>) : go(delta_blocks_kernel<TIO, NP, false, PASS>);
 }
 
-template <typename TIO, int NP>
-hipError_t launch_np(const DeltaArgs& a, hipStream_t s) {
-  if (a.seg != 0) {
-    hipError_t e = launch_pass<TIO, NP, 1>(a, s);
-    if (e == hipSuccess) e = launch_delta_join(a, s);
-    if (e != hipSuccess) return e;
-  }
-  return launch_pass<TIO, NP, 0>(a, s);
-}
-
-template <typename TIO>
+template <typename TIO, int PASS>
 hipError_t launch_io(const DeltaArgs& a, hipStream_t s) {
-  if (a.N <= 32) return launch_np<TIO, 32>(a, s);
-  if (a.N <= 64) return launch_np<TIO, 64>(a, s);
-  if (a.N <= 128) return launch_np<TIO, 128>(a, s);
-  if constexpr (sizeof(TIO) == 2) return launch_np<TIO, 256>(a, s);
+  if (a.N <= 32) return launch_pass<TIO, 32, PASS>(a, s);
+  if (a.N <= 64) return launch_pass<TIO, 64, PASS>(a, s);
+  if (a.N <= 128) return launch_pass<TIO, 128, PASS>(a, s);
+  if constexpr (sizeof(TIO) == 2) return launch_pass<TIO, 256, PASS>(a, s);
   return hipErrorInvalidValue;
+}
+
+template <int PASS> hipError_t launch_walk(const DeltaArgs& a, int io, hipStream_t s) {
+  if (delta_chain_applies(a, io)) return launch_delta_chain(a, PASS, s);
+  return io == kBF16 ? launch_io<__hip_bfloat16, PASS>(a, s) : launch_io<float, PASS>(a, s);
 }
 
 // Tokens of a segment, 0 where sequences are walked in one piece. A sequence's
@@ -588,8 +438,10 @@ hipError_t launch_io(const DeltaArgs& a, hipStream_t s) {
 int64_t delta_segment(const DeltaArgs& a, int io) {
   int64_t tokens = a.L, seqs = a.batch;
   if (a.nseq > 0) tokens = 4 * ((a.L + a.nseq - 1) / a.nseq) < a.L ? 4 * ((a.L + a.nseq - 1) / a.nseq) : a.L, seqs = (a.L + tokens - 1) / tokens;
-  const int64_t wgs = seqs * a.H * ((a.P + kCols - 1) / kCols), first = seqs * a.H * ((a.P + a.N + kCols - 1) / kCols);
-  const int64_t blocks = (tokens + kDeltaBlock - 1) / kDeltaBlock, cus = io == kBF16 && a.N <= 128 ? 512 : 256;  // workgroups at once
+  const bool pairs = io == kBF16 && a.N <= 128;  // of 64 columns, in the walk for aligned rows
+  const int64_t cols = pairs && a.P > 64 ? 128 : 64, cols1 = pairs ? 128 : 64;
+  const int64_t wgs = seqs * a.H * ((a.P + cols - 1) / cols), first = seqs * a.H * ((a.P + a.N + cols1 - 1) / cols1);
+  const int64_t blocks = (tokens + kDeltaBlock - 1) / kDeltaBlock, cus = 256;
   auto turns = [&](int64_t w) { return (w + cus - 1) / cus; };
   int64_t best = turns(wgs) * blocks * 4, cut = 0;
   for (int64_t n = 2; n <= 64 && n * 4 <= blocks; ++n) {
@@ -623,9 +475,12 @@ hipError_t launch_delta_blocks(const DeltaArgs& args, int io, int dt, hipStream_
     a.ends = reinterpret_cast<float*>(a.ws + delta_slots(a) * a.H * (int64_t)record_bytes(io));
     a.enter = a.ends + states * (a.P + a.N) * a.N;
   }
-  const hipError_t e = launch_delta_solve(a, io, dt, s);
-  if (e != hipSuccess) return e;
-  return io == kBF16 ? launch_io<__hip_bfloat16>(a, s) : launch_io<float>(a, s);
+  hipError_t e = launch_delta_solve(a, io, dt, s);
+  if (e == hipSuccess && a.seg != 0) {
+    e = launch_walk<1>(a, io, s);
+    if (e == hipSuccess) e = launch_delta_join(a, s);
+  }
+  return e == hipSuccess ? launch_walk<0>(a, io, s) : e;
 }
 
 }  // namespace ssd
