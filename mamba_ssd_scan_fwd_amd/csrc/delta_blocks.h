@@ -213,7 +213,11 @@ template <int T> __device__ __forceinline__ Terms<T> split_piece(const Piece<flo
   return split8<T>(f);
 }
 
-// Nothing is moved across by the compiler.
-__device__ __forceinline__ void hold() { __builtin_amdgcn_sched_barrier(0); }
+// Nothing is moved across by the compiler: no memory access by any of its passes,
+// nothing at all by the scheduler.
+__device__ __forceinline__ void hold() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
 
 }  // namespace ssd

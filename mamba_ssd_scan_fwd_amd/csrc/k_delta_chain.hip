@@ -127,8 +127,6 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(const DeltaArgs a
         send_record(Rec::M, L::M + half * L::mbytes, L::mbytes);
       }
     };
-    constexpr int TN = Rec::M / 4096;  // instructions of a wave for T
-    static_assert(Rec::M % 4096 == 0, "every wave sends as many");
     auto send_t = [&] { send_record(Rec::T, L::T, Rec::M); };
     int half = 0;
     if (first < last) {
@@ -138,14 +136,10 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(const DeltaArgs a
     }
     for (int64_t t0 = first; t0 < last; t0 += 64, ++slot, half ^= 1) {
       const bool more = t0 + 64 < last;
-      // This block's rows are there, then its T: behind the rest lie T's instructions
-      // and the last block's four stores, behind T the stores.
-      const bool stores = PASS == 0 && live && t0 != first;
-      if (stores) vm_wait<TN + 4>();
-      else vm_wait<TN>();
-      __syncthreads();
-      if (stores) vm_wait<4>();
+      // this block's rows are there (the last block's four stores are younger)
+      if (PASS == 0 && live && t0 != first) vm_wait<4>();
       else vm_wait<0>();
+      __syncthreads();
       if (more) {
         aim(t0 + 64, slot + 1);
         send_rest(half ^ 1);
@@ -187,7 +181,6 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(const DeltaArgs a
           }
         }
       }
-      __syncthreads();  // T is there
       __syncthreads();  // T has been read, U is there
       if (more) send_t();
       if constexpr (PASS == 0) {
@@ -220,6 +213,14 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(const DeltaArgs a
             buffer_st8(lo, Yr, to);
         }
       }
+    }
+    return;
+  }
+
+  if (!live) {
+    for (int64_t t0 = first; t0 < last; t0 += 64) {
+      __syncthreads();
+      __syncthreads();
     }
     return;
   }
@@ -270,11 +271,6 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(const DeltaArgs a
   int half = 0;
   for (int64_t t0 = first; t0 < last; t0 += 64, half ^= 1) {
     __syncthreads();
-    if (!live) {
-      __syncthreads();
-      __syncthreads();
-      continue;
-    }
     const float* eg = reinterpret_cast<const float*>(lds + L::decays + half * 1024);
     const int k_at = L::K + half * L::tile;
     auto ktfrag = [&](int hh, int kk, int kn) {  // tile hh of columns 32 kn .., rows 32 kk ..
@@ -329,7 +325,6 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(const DeltaArgs a
       spread<4 * PT * ST, 1>();
       hold();
     }
-    __syncthreads();  // T is there
     // R = X - e^g K S0^T
 #pragma unroll
     for (int i = 0; i < kTriFrags; ++i)
