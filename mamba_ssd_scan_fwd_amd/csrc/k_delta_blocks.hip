@@ -456,8 +456,27 @@ size_t record_bytes(int io) { return io == kBF16 ? DeltaRecord<__hip_bfloat16>::
 
 }  // namespace
 
+// Blocks or token after token, by the times that either was measured to take, in
+// microseconds. The walk: 6, and 0.37 a token of the longest sequence, or, where the card is full,
+// 0.36 a token and million of the state's elements (packed sequences are uneven: half as much
+// again). Blocks: two launches and a block's latency, 16 for aligned rows of
+// N = 128 and 27 for others, and 4 a block; or, where the card is full, what a
+// record and a block's products cost for each head.
+// Measured (blocks / walk): one sequence of 32 heads, P = N = 128, bf16: 16 tokens 19 / 11, 48 tokens 19 / 24;
+// 64 of them: 4 tokens 99 / 95, 8 tokens 101 / 139. 8 sequences of 32 heads, P = N = 64, fp32: 48 tokens 32 / 25,
+// 96 tokens 39 / 46. Packed, bf16: 64 sequences of one token 92 / 66, of 16 tokens 104 / 246.
 bool delta_blocks_apply(const DeltaArgs& a, int io) {
-  return (io == kBF16 || a.N <= 128) && a.L >= 16 && a.N >= 8 && a.P >= 8;
+  if ((io != kBF16 && a.N > 128) || a.N < 8 || a.P < 8) return false;
+  const bool packed = a.nseq > 0;
+  const double state = (double)a.P * a.N;
+  const double tokens = (double)a.batch * a.L, longest = packed ? 2. * a.L / a.nseq : (double)a.L;
+  const double full = tokens * a.H * state * (packed ? 5.4e-7 : 3.6e-7), alone = 0.37 * longest;
+  const double walk = 6 + (full > alone ? full : alone);
+  const double records = packed ? (double)(a.L / kDeltaBlock + a.nseq) : (double)a.batch * ((a.L + kDeltaBlock - 1) / kDeltaBlock);
+  const bool chain = io == kBF16 && a.N <= 128;
+  const double latency = (chain ? 8 + a.N / 16. : 27) + 4 * longest / kDeltaBlock;
+  const double work = 10 + records * a.H * (chain ? state * 2.6e-6 : state * 6e-6 + 0.03);
+  return (latency > work ? latency : work) < walk;
 }
 
 int64_t delta_blocks_workspace(DeltaArgs& a, int io) {

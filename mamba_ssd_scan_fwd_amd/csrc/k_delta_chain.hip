@@ -16,8 +16,12 @@
 // workgroup through LDS, its 16-byte pieces permuted so that the reads by rows and
 // the transposing ones meet few bank conflicts. All but T have two places, so that
 // the next block's have a block's time to arrive; U takes the place of the X that it came from,
-// and T, which a block needs last, is refilled once it has been read. (With Q, X and T refilled in
-// place, each block waited for them: 435 instead of XXX us for 8 x 2048 tokens.)
+// and T, which a block needs last, is refilled once it has been read.
+//
+// Measured: 8 sequences of 2048 tokens, 32 heads, P = N = 128: 118 us, 3.4 us a block
+// (8400 cycles). Bound by the chain's instructions: 164 matrix and some 560 others a wave
+// and block, which alone take 6600 cycles; the rest is the partner's share of the
+// SIMD and of the LDS. The register-staged walk of one kind of waves took 158 us.
 #include <type_traits>
 
 #include "delta_blocks.h"

@@ -32,6 +32,10 @@ RULE = [
     (2, 300, 2, 48, 24, 1, "bf16", "fp32", False, True, True, True),
     (1, 300, 1, 131, 77, 1, "fp32", "fp32", True, True, True, True),
     (1, 520, 2, 64, 128, 1, "bf16", "bf16", True, True, True, False),
+    # blocks that end early, of many heads
+    (8, 13, 32, 128, 128, 4, "bf16", "bf16", True, True, True, False),
+    (2, 20, 200, 128, 100, 1, "bf16", "fp32", True, True, True, True),
+    (1, 50, 300, 64, 64, 300, "fp32", "fp32", False, True, True, False),
 ]
 
 
@@ -47,7 +51,8 @@ def test_rule_matches_the_recurrence(b, L, H, P, N, G, io, dt, init, pre, sigmoi
     near(hT, hr, "final_state")
 
 
-PACKED = [[5, 0, 1, 64, 33, 0, 0, 150, 2, 1, 1, 31, 0], [200], [64, 64, 128], [1] * 40]
+PACKED = [[5, 0, 1, 64, 33, 0, 0, 150, 2, 1, 1, 31, 0], [200], [64, 64, 128], [1] * 40,
+          [64, 0, 1, 300, 33, 0, 0, 150, 63, 65, 0]]
 
 
 @pytest.mark.parametrize("lens", PACKED)
