@@ -509,8 +509,8 @@ PyObject* delta_prompts(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int32_t* cu = offsets(a[6], dev, &S);
   if (S > 0 && d.batch != 1) bad_value("packed sequences: x must be [1, T, H, P]");
   const int64_t states[] = {S > 0 ? S : d.batch, d.nheads, d.headdim, d.dstate};
+  if (a[2] == Py_None) bad_value("A is required");
   const float* A = floats(a[2], "A", dev, {d.nheads});
-  if (A == nullptr) bad_value("A is required");
   const float* init = floats(a[7], S > 0 ? "init_states" : "init_state", dev, states);
   Tensor y = output(a[8], "y", x.scalar_type(), x, x.sizes());
   Tensor final_state;
@@ -542,8 +542,8 @@ PyObject* delta_token(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const auto dev = x.device();
   const ssd_delta_desc_t d = delta_desc(x, a, a + 9, 1);
   const int64_t slots = device_tensor(a[6], "state", 4).size(0);
+  if (a[2] == Py_None) bad_value("A is required");
   const float* A = floats(a[2], "A", dev, {d.nheads});
-  if (A == nullptr) bad_value("A is required");
   float* state = static_cast<float*>(dense(a[6], "state", at::kFloat, dev, {slots, d.nheads, d.headdim, d.dstate}));
   const int32_t* map = static_cast<const int32_t*>(dense(a[7], "state_slots", at::kInt, dev, {d.batch}));
   Tensor y = output(a[8], "y", x.scalar_type(), x, x.sizes());
