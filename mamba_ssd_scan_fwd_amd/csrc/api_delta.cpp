@@ -51,6 +51,9 @@ ssd_status_t plan_delta(const ssd_delta_desc_t* d, int64_t nseq, DeltaPlan* p) {
   return SSD_OK;
 }
 
+// (A launch of too many threads is one of too many rows.)
+ssd_status_t from_launch(hipError_t e) { return e == hipErrorInvalidConfiguration ? SSD_ERR_BAD_SHAPE : from_hip(e); }
+
 // The prompt form: the way it is walked, and the workspace that needs.
 ssd_status_t plan_rule(const ssd_delta_desc_t* d, int64_t nseq, DeltaPlan* p) {
   const ssd_status_t st = plan_delta(d, nseq, p);
@@ -90,7 +93,7 @@ ssd_status_t run_rule(DeltaPlan& p, const int32_t* cu, const void* x, const void
   if (overlap(rf, ri) && rf.lo != ri.lo) return SSD_ERR_ALIAS;  // the same array or none of it
   a.x = x, a.dt = dt, a.A = A, a.B = B, a.C = C, a.beta = beta, a.init = init, a.y = y, a.final_state = final_state;
   a.cu = cu;
-  if (!p.blocks) return from_hip(launch_delta_walk(a, p.io, p.dt, s));
+  if (!p.blocks) return from_launch(launch_delta_walk(a, p.io, p.dt, s));
   void* w = workspace;
   if (w == nullptr && hipMallocAsync(&w, p.total, s) != hipSuccess) return SSD_ERR_HIP;
   a.ws = static_cast<char*>(w);
@@ -99,7 +102,7 @@ ssd_status_t run_rule(DeltaPlan& p, const int32_t* cu, const void* x, const void
     const hipError_t fe = hipFreeAsync(w, s);
     if (e == hipSuccess) e = fe;
   }
-  return from_hip(e);
+  return from_launch(e);
 }
 
 }  // namespace
@@ -176,7 +179,7 @@ ssd_status_t ssd_delta_step(const ssd_delta_desc_t* desc, const void* x, const v
   r.dto = a.dto;
   r.sigmoid = a.sigmoid;
   r.scale = a.scale;
-  return from_hip(launch_delta_step(r, p.io, p.dt, static_cast<hipStream_t>(stream)));
+  return from_launch(launch_delta_step(r, p.io, p.dt, static_cast<hipStream_t>(stream)));
 }
 
 ssd_status_t ssd_head_norm(const ssd_head_norm_desc_t* desc, const void* q, const void* k, const float* q_weight,

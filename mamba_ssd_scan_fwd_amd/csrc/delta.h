@@ -85,6 +85,10 @@ struct HeadNormArgs {
 };
 hipError_t launch_head_norm(const HeadNormArgs& a, int io, hipStream_t s);
 
+// Whether a launch's threads can be counted (in 32 bits). What launches more answers
+// hipErrorInvalidConfiguration, here before any launch.
+inline bool grid_fits(int64_t groups, int threads) { return groups < (int64_t(1) << 32) / threads; }
+
 #ifdef __HIPCC__
 // Sum over teams of T lanes (a power of two, aligned), in all of them: DPP
 // within 16 lanes, then exchanges of rows and of halves of the wave. All lanes

@@ -406,6 +406,7 @@ hipError_t launch_pass(const DeltaArgs& a, hipStream_t s) {
   const uint32_t blocks_p = (rows_p + kCols - 1) / kCols;
   const int64_t pieces = a.seg != 0 ? delta_slots(a, a.seg) : a.seqs();
   auto go = [&](auto kern) {
+    if (!grid_fits(pieces * a.H * blocks_p, kThreads)) return hipErrorInvalidConfiguration;
     kern<<<dim3((unsigned)(pieces * a.H * blocks_p)), kThreads, 0, s>>>(a, blocks_p);
     return hipGetLastError();
   };

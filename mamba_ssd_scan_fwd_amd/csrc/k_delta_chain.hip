@@ -442,6 +442,7 @@ template <int NP, int PASS> hipError_t launch_np(const DeltaArgs& a, hipStream_t
   const int64_t pieces = a.seg != 0 ? delta_slots(a, a.seg) : a.seqs();
   auto go = [&](auto kern, int cols) {
     const uint32_t blocks_p = (rows_p + cols - 1) / cols;
+    if (!grid_fits(pieces * a.H * blocks_p, kThreads)) return hipErrorInvalidConfiguration;
     kern<<<dim3((unsigned)(pieces * a.H * blocks_p)), kThreads, 0, s>>>(a, blocks_p);
     return hipGetLastError();
   };

@@ -285,6 +285,7 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TIO) == 2 && NP <= 128 ? 2 : 1)
 template <typename TIO, typename TDT>
 hipError_t launch_io(const DeltaArgs& a, hipStream_t s) {
   const uint32_t tasks = (uint32_t)(delta_slots(a) * a.H);  // below 2^31 (api)
+  if (!grid_fits((tasks + kWaves - 1) / kWaves, 64 * kWaves)) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)((tasks + kWaves - 1) / kWaves));
   auto go = [&](auto whole, auto other) {
     if (a.N % 8 == 0) whole<<<grid, 64 * kWaves, 0, s>>>(a, tasks);

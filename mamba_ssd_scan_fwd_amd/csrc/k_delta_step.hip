@@ -106,6 +106,7 @@ hipError_t launch_np(const DeltaStepArgs& args, hipStream_t s) {
   constexpr int TEAMS = kThreads / (NP / 4);
   auto go = [&](auto kern, int rows) {
     const uint32_t blocks_p = (a.P + TEAMS * rows - 1) / (TEAMS * rows);
+    if (!grid_fits(a.batch * a.H * blocks_p, kThreads)) return hipErrorInvalidConfiguration;
     kern<<<dim3((unsigned)(a.batch * a.H * blocks_p)), kThreads, 0, s>>>(a, blocks_p);
     return hipGetLastError();
   };

@@ -135,6 +135,7 @@ template <typename TIO, typename TDT, int NP>
 hipError_t launch_np(const DeltaArgs& a, hipStream_t s) {
   constexpr int R = 2, TEAMS = kThreads / (NP / 4);
   const uint32_t blocks_p = (a.P + TEAMS * R - 1) / (TEAMS * R);
+  if (!grid_fits(a.seqs() * a.H * blocks_p, kThreads)) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)(a.seqs() * a.H * blocks_p));
   if (a.N % 4 == 0) delta_walk_kernel<TIO, TDT, NP, true, R><<<grid, kThreads, 0, s>>>(a, blocks_p);
   else delta_walk_kernel<TIO, TDT, NP, false, R><<<grid, kThreads, 0, s>>>(a, blocks_p);

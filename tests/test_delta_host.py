@@ -179,6 +179,15 @@ def test_sizes_of_any_kind_are_refused_without_overflow():
     assert norm(heads(batch=n, rows=n, q_heads=1, k_heads=0, headdim=1, rot=0, q_stride=one)) == SHAPE
 
 
+def test_launches_of_too_many_threads_are_refused():
+    """2^26 rows and heads of 256 threads each and more: refused before a launch."""
+    many = dict(batch=1 << 20, seqlen=1, nheads=64, ngroups=1, headdim=5, dstate=5)
+    far = {n: BASE + (i << 40) for i, n in enumerate(NAMES)}
+    assert call(rule(**many), **far) == SHAPE
+    assert call(rule(**dict(many, batch=1, seqlen=10)), S=1 << 20, **far) == SHAPE
+    assert step(rule(**many), n=1 << 20, **far) == SHAPE
+
+
 def test_workspace_follows_the_way_that_is_taken():
     # token after token needs none, blocks a record for each block and head, and
     # whether a type, an alignment or a stride is one or another does not matter

@@ -206,15 +206,14 @@ def test_long_packed_rule_in_segments(lens, io):
 
 @pytest.mark.parametrize("cu", [[0, 50, 30, 1000], [0, 1 << 30, 100], [-5, 400, 1000], [20, 600, 800], [0, 0, 0], [1000, 0, 1000],
                                 [990, 64, 1000, 3]])
-@pytest.mark.parametrize("H", [1, 64])
-def test_bad_offsets_stay_inside(cu, H):
-    """Whatever the offsets hold, nothing outside the arrays is touched; sequences
-    of offsets in order are right."""
-    T, P, N = 1000, 16, 32
-    s = Delta(1, T, H, P, N, 1, "bf16", "fp32", init=False, seed=12)
+@pytest.mark.parametrize("H,P,io", [(1, 16, "bf16"), (64, 16, "bf16"), (1, 16, "fp32"), (64, 16, "fp32"), (2, 5, "bf16")])
+def test_bad_offsets_stay_inside(cu, H, P, io):
+    """Whatever the offsets hold, nothing outside the arrays is touched."""
+    T, N = 1000, 32
+    s = Delta(1, T, H, P, N, 1, io, "fp32", init=False, seed=12)
     kw, _, _ = s.to(DEV)
     S = len(cu) - 1
-    y = torch.full((1, T + 64, H, P), 7.0, device=DEV, dtype=torch.bfloat16)
+    y = torch.full((1, T + 64, H, P), 7.0, device=DEV, dtype=s.io)
     h = torch.full((S + 2, H, P, N), 5.0, device=DEV)
     note(f"[gpu] delta rule: offsets {cu} H={H}")
     ssd.delta_rule_varlen(cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=DEV), y=y[:, :T], final_states=h[1:S + 1], **kw)
