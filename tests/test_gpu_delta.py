@@ -289,7 +289,9 @@ def test_steps_of_zero_keep_the_state():
 
 STEP = [(1, 1, 1, 1, 1, "fp32", "fp32"), (3, 2, 20, 16, 1, "bf16", "bf16"), (5, 4, 64, 5, 2, "fp32", "fp32"),
         (2, 6, 33, 100, 3, "bf16", "fp32"), (4, 2, 128, 128, 1, "bf16", "bf16"), (2, 2, 256, 256, 2, "fp32", "fp32"),
-        (2, 1, 255, 253, 1, "bf16", "bf16"), (70, 32, 128, 128, 16, "bf16", "bf16"), (67, 32, 128, 60, 32, "fp32", "fp32")]
+        (2, 1, 255, 253, 1, "bf16", "bf16"), (70, 32, 128, 128, 16, "bf16", "bf16"), (67, 32, 128, 60, 32, "fp32", "fp32"),
+        # two and four rows of the state to a team, the last of them short
+        (33, 32, 50, 64, 8, "fp32", "fp32"), (130, 32, 70, 61, 4, "bf16", "bf16"), (300, 32, 36, 64, 1, "bf16", "fp32")]
 
 
 @pytest.mark.parametrize("b,H,P,N,G,io,dt", STEP)
