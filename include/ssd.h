@@ -617,8 +617,8 @@ SSD_API ssd_status_t ssd_group_norm(const ssd_group_norm_desc_t* desc, const voi
  *     states     [.., H, P, N]     fp32
  * States, decays and sums are fp32; y is rounded once. Prompts may be taken in
  * blocks of 64 tokens whose products run on the matrix cores: with bf16 io the
- * operands of y's products (states, solutions) are rounded to bf16, those that
- * reach a state are kept to 16 bits or more (fp32 io: all of them). An infinity
+ * operands of y's products (states, scores, solutions) are rounded to bf16, those
+ * that reach a state are kept to 16 bits (fp32 io: all of them to 24). An infinity
  * or a NaN of a row of x stays in that row p of its head, one of B, C, dt or
  * beta in its group or head, all of them in their sequence; within 64 tokens
  * before it, though, y may be NaN too. */

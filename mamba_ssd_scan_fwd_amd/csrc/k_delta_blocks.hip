@@ -9,6 +9,10 @@
 //
 // S, R and U' = e^(g_end - g) U are held in fp32. As operands they are terms
 // (delta_blocks.h).
+//
+// Measured: 3 sequences of 1001 tokens, 32 heads, P = N = 64, fp32: 85 us, 5.3 us a block (12 700
+// cycles), of which 216 matrix instructions take 3500; bound by one wave a SIMD's
+// instructions and LDS latency, in turn (96 workgroups on 256 compute units).
 #include <type_traits>
 
 #include "delta_blocks.h"

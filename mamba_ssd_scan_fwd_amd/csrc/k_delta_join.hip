@@ -7,7 +7,8 @@
 // wave a quarter of the columns; fp32 matrix instructions, since nothing may be
 // lost that the walks keep. Bound by the latency of M and B (64 KB and more a
 // segment, from the caches), so the next segment's are on their way, all at
-// once, while a segment is joined.
+// once, while a segment is joined: 8 segments of 32 heads, P = N = 128 32 us, where loads
+// at their use took 195.
 #include "delta_blocks.h"
 
 namespace ssd {

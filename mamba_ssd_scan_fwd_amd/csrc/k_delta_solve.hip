@@ -14,6 +14,10 @@
 // lane; then T10 = -T11 A10 T00 for the two pairs of them, and once more for the
 // two halves, as products of fp32 matrix instructions, whose result in
 // registers is the right operand of the next as it stands.
+//
+// Bound by memory, two waves a SIMD covering it poorly: 8192 blocks of N = 128, bf16 (74 MB in
+// from memory, 152 MB of records out) 65 us; without the stores 45, without the
+// loads 42, without both 33. Three waves a SIMD spill and took 67.
 #include "delta_blocks.h"
 
 namespace ssd {

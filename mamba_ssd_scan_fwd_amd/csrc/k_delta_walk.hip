@@ -7,7 +7,8 @@
 // worked on. Decays and betas are taken by a lane for a token, 64 tokens at once: by
 // every lane for every token they were half of all instructions.
 //
-// Bound by a wave's instructions and their latency, some 450 cycles a token.
+// Bound by a wave's instructions and their latency, some 800 cycles a token of one
+// sequence of 32 heads, P = N = 128 (0.38 us), 1.6 us a token of eight of them (two waves a SIMD).
 // For prompts of a few tokens, which the blocks' two kernels do not repay, and
 // for sizes that have no blocks.
 #include "delta.h"

@@ -2,7 +2,8 @@
 rule and of the norm of heads.
 
 Bounds. u = 2^-24. A two-term operand (a bf16 and the bf16 of what it leaves) is
-off by at most 2^-8 * 2^-8 = 2^-16.
+off by at most 2^-8 * 2^-8 = 2^-16; with fp32 io there are three terms, 2^-24, and the
+bounds for two below are wider than they need be.
 
 - decay exp2(d A log2 e): its argument r is off by (32 + 3) u r (layer_testutil's
   softplus, A's and d's products), exp2 by 2 u, and e^-r r < 0.37; summed over

@@ -240,9 +240,9 @@ def test_without_decay_and_with_whole_ones(io):
     y, hT = ssd.delta_rule(**kw)
     # products with 0 and 1 of values of x as they came; later ones of what is left
     # in the state and of the difference to it: each one operand's rounding, 2^-8 of
-    # up to 2 max|x| and 1 max|x| in y (two terms with fp32 io), 2^-16 in the state
+    # up to 2 max|x| and 1 max|x| in y, 2^-16 in the state (2^-24 with fp32 io)
     top = float(kw["x"].float().abs().max())
-    if io == "bf16":  # (of fp32, two terms keep 16 bits)
+    if io == "bf16":  # (of fp32, the terms are products and sums of their own)
         assert torch.equal(y[:, :N], kw["x"][:, :N])
     assert (y.float() - kw["x"].float()).abs().max() <= (3 * 2.0 ** -16 if io == "fp32" else 4 * 2.0 ** -8) * top
     last = torch.stack([kw["x"][0, max(i for i in range(L) if i % N == n), 0] for n in range(N)], 1)
