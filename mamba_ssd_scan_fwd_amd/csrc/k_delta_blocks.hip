@@ -2,17 +2,23 @@
 // k_delta_chain.hip does not take: fp32, states of more than 128 columns, odd sizes
 // and rows that are not aligned. (And the choice between them.)
 //
-// The same products in the same layouts, by one kind of waves: each keeps 16 rows of the state
-// and makes their y too. The next block's rows are loaded into registers while
-// a block is worked on; on the way from there to the LDS odd rows are put in order and
-// fp32 is split into terms.
+// The same products in the same layouts. Each of four waves keeps 16 rows of the state.
+// The next block's rows are loaded into registers while a block is worked on; on the way
+// from there to the LDS odd rows are put in order and fp32 is split into terms.
+//
+// Where a workgroup has a compute unit to itself by its LDS (fp32 of N <= 64, bf16 of
+// N > 128) each wave has a partner, which brings the rows and makes y, as in
+// k_delta_chain.hip: handed S0's terms and U in fp32. Elsewhere (two workgroups to a compute unit,
+// or, fp32 of N > 64, no LDS left for S0 and U) the wave does it all. Measured without / with
+// partners, both kernels: 3 sequences of 1001 tokens, 32 heads, P = N = 64, fp32 118 / 102 us (the walk 85 /
+// 69), of N = 32 87 / 74; 16384 tokens of 16 heads, P = 128, N = 256, bf16 716 / 617.
 //
 // S, R and U' = e^(g_end - g) U are held in fp32. As operands they are terms
 // (delta_blocks.h).
 //
-// Measured: 3 sequences of 1001 tokens, 32 heads, P = N = 64, fp32: 85 us, 5.3 us a block (12 700
-// cycles), of which 216 matrix instructions take 3500; bound by one wave a SIMD's
-// instructions and LDS latency, in turn (96 workgroups on 256 compute units).
+// Of the 69 us, 4.3 a block (10 000 cycles): rows to LDS 2400, K S0^T, R and U 3200 beside the
+// partner's 4400 (half of them the issue of its loads), U' and the state 2800. Later or
+// split issue of the loads, and terms made ahead of the LDS's turn, took 71 to 79.
 #include <type_traits>
 
 #include "delta_blocks.h"
@@ -20,7 +26,7 @@
 namespace ssd {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // of the waves of either kind
 constexpr int kCols = 64;  // rows p of a workgroup
 
 template <typename TIO, int NP> struct Layout {
@@ -29,14 +35,16 @@ template <typename TIO, int NP> struct Layout {
   static constexpr int xrow = kCols * (int)sizeof(TIO);
   static constexpr int K = 0, Q = IO * tile, rec = Q + IO * tile,
                        X = rec + (DeltaRecord<TIO>::bytes + 1023) / 1024 * 1024, bytes = X + 64 * xrow;
+  // handed to the partners
+  static constexpr int S0 = bytes, U = S0 + DeltaTerms<TIO>::y * kCols * NP * 2, two = U + 64 * kCols * 4;
 };
 
 // Likewise in (bf16) X's tile.
 __device__ __forceinline__ int x_swz(int t) { return (t & 2) | ((t >> 1) & 4); }
 
 // PASS: see delta_piece.
-template <typename TIO, int NP, bool WHOLE, int PASS>
-__global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs a, uint32_t blocks_p) {
+template <typename TIO, int NP, bool WHOLE, int PASS, bool TWO>
+__global__ __launch_bounds__(TWO ? 2 * kThreads : kThreads) void delta_blocks_kernel(const DeltaArgs a, uint32_t blocks_p) {
   using L = Layout<TIO, NP>;
   using Rec = DeltaRecord<TIO>;
   constexpr int IO = DeltaTerms<TIO>::io, ST = DeltaTerms<TIO>::state, YT = DeltaTerms<TIO>::y;
@@ -45,9 +53,14 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
   constexpr int XP = 16 / (int)sizeof(TIO), XPACKS = kCols / XP;
   constexpr int CK = 64 * PACKS / kThreads, CR = (Rec::bytes / 16 + kThreads - 1) / kThreads, CX = 64 * XPACKS / kThreads;
   constexpr int SZ = (int)sizeof(TIO);
-  static_assert(L::bytes <= 160 * 1024, "LDS of a compute unit");
-  __shared__ __align__(16) unsigned char lds[L::bytes];
-  const int tid = threadIdx.x, wave = (int)__builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64, g = lane / 16, r = lane % 16;
+  constexpr bool Y = PASS == 0 && !TWO;  // whether the chain's waves make y
+  constexpr int BYTES = TWO && PASS == 0 ? L::two : L::bytes;
+  static_assert(BYTES <= 160 * 1024, "LDS of a compute unit");
+  __shared__ __align__(16) unsigned char lds[BYTES];
+  // (known to be the same in all lanes: the two kinds' barriers are then behind branches of the whole wave)
+  const int any_wave = (int)__builtin_amdgcn_readfirstlane(threadIdx.x / 64), wave = any_wave % 4;
+  const bool chain = !TWO || any_wave < 4;
+  const int tid = threadIdx.x % kThreads, lane = tid % 64, g = lane / 16, r = lane % 16;
 
   // (32-bit divisions: those of 64 bits took a microsecond each)
   const uint32_t bid = (uint32_t)xcd_local_order(blockIdx.x, gridDim.x);
@@ -143,7 +156,142 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
   const int kat = rt * (NP * 2), tat = L::K + (8 * g + ta) * (NP * 2);
   const int kf = k_swz<NP>(rt), tf = k_swz<NP>(8 * g + ta);
 
-  if (first < last) fetch(first, slot);
+  const bool live = pw < rows_p;
+  const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+  auto split_tiles = [&](auto terms, const f32x4_t& t0, const f32x4_t& t1) {
+    const float f[8] = {t0[0], t0[1], t0[2], t0[3], t1[0], t1[1], t1[2], t1[3]};
+    return split8<decltype(terms)::value>(f);
+  };
+  constexpr std::integral_constant<int, ST> st_terms{};
+  constexpr std::integral_constant<int, YT> y_terms{};
+  const float* eg = reinterpret_cast<const float*>(lds + L::rec + Rec::decays);
+  const float* ed = eg + 64;
+  auto by_rows = [&](const unsigned char* from, int i, int kn) {  // rows of tile i, columns 32 kn ..
+    Terms<IO> v;
+#pragma unroll
+    for (int e = 0; e < IO; ++e)
+      v.v[e] = as_bf16x8(ld16(from + kat + e * L::tile + (32 * (i / 2) + 4 * (i % 2)) * (NP * 2) + 16 * ((4 * kn + g) ^ kf)));
+    return v;
+  };
+  auto kfrag = [&](int i, int kn) { return by_rows(lds + L::K, i, kn); };
+  auto qfrag = [&](int i, int kn) { return by_rows(lds + L::Q, i, kn); };
+  auto ktfrag = [&](int hh, int kk, int kn) {  // tile hh of columns 32 kn .., rows 32 kk ..
+    Terms<IO> v;
+#pragma unroll
+    for (int e = 0; e < IO; ++e) {
+      const unsigned char* s = lds + L::K + tat + e * L::tile + 32 * kk * (NP * 2) + 16 * ((4 * kn + tb) ^ tf) + 8 * hh;
+      const uint2 lo = lds_tr8(s), hi = lds_tr8(s + 4 * (NP * 2));
+      v.v[e] = as_bf16x8(make_uint4(lo.x, lo.y, hi.x, hi.y));
+    }
+    return v;
+  };
+  auto tri = [&](auto terms, int from, int i) {
+    Terms<decltype(terms)::value> v;
+#pragma unroll
+    for (int e = 0; e < decltype(terms)::value; ++e)
+      v.v[e] = as_bf16x8(ld16(lds + L::rec + 16 * lane + from + (e * kTriFrags + i) * kFragBytes));
+    return v;
+  };
+  // y of the block from t0 on: rows pw + 4 g .. of a lane at token 32 (i / 2) + 4 (i % 2) + rt
+  auto put_y = [&](const f32x4_t (&O)[4], int64_t t0) {
+    const int n = (int)(last - t0 < 64 ? last - t0 : 64);
+    const __amdgpu_buffer_rsrc_t Yr = buffer_range(Yp + t0 * HP, (uint32_t)((n - 1) * HP + a.P) * SZ);
+    const int pr = pw + 4 * g;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t off = (uint32_t)((32 * (i / 2) + 4 * (i % 2) + rt) * HP + pr) * SZ;
+      if constexpr (WHOLE) {
+        const uint32_t where = pr < a.P ? off : kNowhere;
+        if constexpr (SZ == 4) buffer_st16(__builtin_bit_cast(uint4, O[i]), Yr, where);
+        else buffer_st8(make_uint2(pack_bf16x2(O[i][0], O[i][1]), pack_bf16x2(O[i][2], O[i][3])), Yr, where);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t where = pr + k < a.P ? off + k * SZ : kNowhere;
+          if constexpr (SZ == 4) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(O[i][k]), Yr, (int)where, 0, 0);
+          else __builtin_amdgcn_raw_buffer_store_b16(bf16_bits(O[i][k]), Yr, (int)where, 0, 0);
+        }
+      }
+    }
+  };
+  unsigned char* const s_place = lds + L::S0 + wave * KN * YT * kFragBytes + 16 * lane;
+  unsigned char* const u_place = lds + L::U + wave * 4096 + 16 * lane;
+
+  if constexpr (TWO) {
+    if (!chain) {
+      // ---- the partners: rows to LDS, and y
+      if (first < last) fetch(first, slot);
+      for (int64_t t0 = first; t0 < last; t0 += 64, ++slot) {
+        __syncthreads();  // the last block's operands have been read
+        stage();
+        __syncthreads();
+        if (t0 + 64 < last) fetch(t0 + 64, slot + 1);
+        f32x4_t O[4];
+        if constexpr (PASS == 0) {
+          // S0 Q^T (rows p, column t) scale e^g
+          Terms<IO> q[2][4];
+          Terms<YT> s[2];
+          auto group = [&](int b, int kn) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q[b][i] = qfrag(i, kn);
+#pragma unroll
+            for (int e = 0; e < YT; ++e) s[b].v[e] = as_bf16x8(ld16(s_place + (kn * YT + e) * kFragBytes));
+          };
+#pragma unroll
+          for (int i = 0; i < 4; ++i) O[i] = zero;
+          group(0, 0);
+#pragma unroll
+          for (int kn = 0; kn < KN; ++kn) {
+            if (kn + 1 < KN) group((kn + 1) % 2, kn + 1);
+            hold();
+#pragma unroll
+            for (int pair = 0; pair < term_pairs(YT, IO); ++pair)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) mul_pair(O[i], s[kn % 2], q[kn % 2][i], pair);
+            hold();
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float e = a.scale * eg[32 * (i / 2) + 4 * (i % 2) + rt];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) O[i][k] *= e;
+          }
+        }
+        __syncthreads();  // U is there
+        if constexpr (PASS == 0) {
+          // + U^T (scale M)^T
+          Terms<YT> mf[kTriFrags], Uy[2];
+          f32x4_t U[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) U[i] = *reinterpret_cast<const f32x4_t*>(u_place + i * 1024);
+#pragma unroll
+          for (int i = 0; i < kTriFrags; ++i) mf[i] = tri(y_terms, Rec::M, i);
+          hold();
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk) Uy[kk] = split_tiles(y_terms, U[2 * kk], U[2 * kk + 1]);
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int pair = 0; pair < term_pairs(YT, YT); ++pair)
+#pragma unroll
+              for (int i = 2 * ks; i < 4; ++i) mul_pair(O[i], Uy[ks], mf[tri_frag(i / 2, i % 2, ks)], pair);
+          // (a wave without rows reads what no wave wrote and stores nothing)
+          put_y(O, t0);
+        }
+      }
+      return;
+    }
+    if (!live) {
+      for (int64_t t0 = first; t0 < last; t0 += 64) {
+        __syncthreads();
+        __syncthreads();
+        __syncthreads();
+      }
+      return;
+    }
+  } else {
+    if (first < last) fetch(first, slot);
+  }
 
   // S^T: tile (kn, hh) rows 32 kn + 8 g + 4 hh .., column p
   f32x4_t S[KN][2];
@@ -151,17 +299,11 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
   const int64_t states = (a.seg != 0 ? piece : sl.seq) * a.H + h;
   const float* init = PASS == 1 ? nullptr : a.seg != 0 ? a.enter : a.init;
   auto state_at = [&](int64_t of) { return (of * rows_p + (p < rows_p ? p : 0)) * a.N; };
-  auto split_tiles = [&](auto terms, const f32x4_t& t0, const f32x4_t& t1) {
-    const float f[8] = {t0[0], t0[1], t0[2], t0[3], t1[0], t1[1], t1[2], t1[3]};
-    return split8<decltype(terms)::value>(f);
-  };
-  constexpr std::integral_constant<int, ST> st_terms{};
-  constexpr std::integral_constant<int, YT> y_terms{};
 #pragma unroll
   for (int kn = 0; kn < KN; ++kn) {
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
-      S[kn][hh] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      S[kn][hh] = zero;
       const int n = 32 * kn + 8 * g + 4 * hh;
       if (init != nullptr && p < a.P && n < a.N) {
         const Pack<float, 4> v = load_pack<float, 4, true>(init + state_at(states) + n, a.N - n);
@@ -175,44 +317,23 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
     }
     Sv[kn] = split_tiles(st_terms, S[kn][0], S[kn][1]);
   }
+  auto hand_over_s = [&] {
+#pragma unroll
+    for (int kn = 0; kn < KN && TWO && PASS == 0; ++kn)
+#pragma unroll
+      for (int e = 0; e < YT; ++e) st16(s_place + (kn * YT + e) * kFragBytes, __builtin_bit_cast(uint4, Sv[kn].v[e]));
+  };
+  hand_over_s();
 
-  const bool live = pw < rows_p;
   for (int64_t t0 = first; t0 < last; t0 += 64, ++slot) {
     __syncthreads();  // the last block's operands have been read
-    stage();
+    if constexpr (!TWO) stage();
     __syncthreads();
-    if (t0 + 64 < last) fetch(t0 + 64, slot + 1);
-    if (!live) continue;
-    const int n = (int)(last - t0 < 64 ? last - t0 : 64);
+    if constexpr (!TWO) {
+      if (t0 + 64 < last) fetch(t0 + 64, slot + 1);
+      if (!live) continue;
+    }
 
-    const float* eg = reinterpret_cast<const float*>(lds + L::rec + Rec::decays);
-    const float* ed = eg + 64;
-    auto by_rows = [&](const unsigned char* from, int i, int kn) {  // rows of tile i, columns 32 kn ..
-      Terms<IO> v;
-#pragma unroll
-      for (int e = 0; e < IO; ++e)
-        v.v[e] = as_bf16x8(ld16(from + kat + e * L::tile + (32 * (i / 2) + 4 * (i % 2)) * (NP * 2) + 16 * ((4 * kn + g) ^ kf)));
-      return v;
-    };
-    auto kfrag = [&](int i, int kn) { return by_rows(lds + L::K, i, kn); };
-    auto qfrag = [&](int i, int kn) { return by_rows(lds + L::Q, i, kn); };
-    auto ktfrag = [&](int hh, int kk, int kn) {  // tile hh of columns 32 kn .., rows 32 kk ..
-      Terms<IO> v;
-#pragma unroll
-      for (int e = 0; e < IO; ++e) {
-        const unsigned char* s = lds + L::K + tat + e * L::tile + 32 * kk * (NP * 2) + 16 * ((4 * kn + tb) ^ tf) + 8 * hh;
-        const uint2 lo = lds_tr8(s), hi = lds_tr8(s + 4 * (NP * 2));
-        v.v[e] = as_bf16x8(make_uint4(lo.x, lo.y, hi.x, hi.y));
-      }
-      return v;
-    };
-    auto tri = [&](auto terms, int from, int i) {
-      Terms<decltype(terms)::value> v;
-#pragma unroll
-      for (int e = 0; e < decltype(terms)::value; ++e)
-        v.v[e] = as_bf16x8(ld16(lds + L::rec + 16 * lane + from + (e * kTriFrags + i) * kFragBytes));
-      return v;
-    };
     auto of_y = [&](const Terms<ST>& s) {
       Terms<YT> v;
 #pragma unroll
@@ -223,7 +344,6 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
     // Operands are read a group ahead of the products that use them, and the
     // order is held: the compiler by itself reads each right before its use and
     // waits for it.
-    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
     const float end = eg[63];
     f32x4_t R[4], O[4], e[4];
     float xw[4][4];
@@ -242,7 +362,7 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
         for (int i = 0; i < 4; ++i) f[(kn + 1) % 2][i] = kfrag(i, kn + 1);
       } else {
 #pragma unroll
-        for (int i = 0; i < 4 && PASS == 0; ++i) f[(kn + 1) % 2][i] = qfrag(i, 0);
+        for (int i = 0; i < 4 && Y; ++i) f[(kn + 1) % 2][i] = qfrag(i, 0);
         // X by columns, and the decays
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -273,7 +393,7 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
     Terms<ST> tm[kTriFrags];
 #pragma unroll
     for (int kn = 0; kn < KN; ++kn) {
-      if (PASS == 0 && kn + 1 < KN) {
+      if (Y && kn + 1 < KN) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[(KN + kn + 1) % 2][i] = qfrag(i, kn + 1);
       }
@@ -282,7 +402,7 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
         if (i * KN / kTriFrags == kn) tm[i] = tri(st_terms, Rec::T, i);
       hold();
 #pragma unroll
-      for (int pair = 0; pair < term_pairs(YT, IO) && PASS == 0; ++pair)
+      for (int pair = 0; pair < term_pairs(YT, IO) && Y; ++pair)
 #pragma unroll
         for (int i = 0; i < 4; ++i) mul_pair(O[i], of_y(Sv[kn]), f[(KN + kn) % 2][i], pair);
 #pragma unroll
@@ -307,7 +427,7 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
     float er[4];
     Terms<YT> mf[kTriFrags], Uy[2];
 #pragma unroll
-    for (int i = 0; i < 4 && PASS == 0; ++i) er[i] = eg[32 * (i / 2) + 4 * (i % 2) + rt];
+    for (int i = 0; i < 4 && Y; ++i) er[i] = eg[32 * (i / 2) + 4 * (i % 2) + rt];
 #pragma unroll
     for (int i = 0; i < 4; ++i) d[i] = *reinterpret_cast<const f32x4_t*>(ed + 32 * (i / 2) + 8 * g + 4 * (i % 2));
     hold();
@@ -320,18 +440,23 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
 #pragma unroll
         for (int i = 2 * ks; i < 4; ++i) mul_pair(U[i], tm[tri_frag(i / 2, i % 2, ks)], Rv[ks], pair);
 #pragma unroll
-    for (int i = 0; i < 4 && PASS == 0; ++i)
+    for (int i = 0; i < 4 && Y; ++i)
 #pragma unroll
       for (int k = 0; k < 4; ++k) O[i][k] *= a.scale * er[i];
     spread<6 * term_pairs(ST, ST), 2>();
     hold();
 #pragma unroll
-    for (int i = 0; i < kTriFrags && PASS == 0; ++i) mf[i] = tri(y_terms, Rec::M, i);
+    for (int i = 0; i < kTriFrags && Y; ++i) mf[i] = tri(y_terms, Rec::M, i);
+    if constexpr (TWO) {
+#pragma unroll
+      for (int i = 0; i < 4 && PASS == 0; ++i) *reinterpret_cast<f32x4_t*>(u_place + i * 1024) = U[i];
+      __syncthreads();  // U is there
+    }
     hold();
     // operands of y, and U' = e^(g_end - g) U
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
-      if constexpr (PASS == 0) Uy[kk] = split_tiles(y_terms, U[2 * kk], U[2 * kk + 1]);
+      if constexpr (Y) Uy[kk] = split_tiles(y_terms, U[2 * kk], U[2 * kk + 1]);
 #pragma unroll
       for (int i = 2 * kk; i < 2 * kk + 2; ++i)
 #pragma unroll
@@ -345,31 +470,10 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-      for (int pair = 0; pair < term_pairs(YT, YT) && PASS == 0; ++pair)
+      for (int pair = 0; pair < term_pairs(YT, YT) && Y; ++pair)
 #pragma unroll
         for (int i = 2 * ks; i < 4; ++i) mul_pair(O[i], Uy[ks], mf[tri_frag(i / 2, i % 2, ks)], pair);
     hold();
-    // y: rows pw + 4 g .. of a lane at token 32 (i / 2) + 4 (i % 2) + rt
-    auto put_y = [&] {
-      const __amdgpu_buffer_rsrc_t Yr = buffer_range(Yp + t0 * HP, (uint32_t)((n - 1) * HP + a.P) * SZ);
-      const int pr = pw + 4 * g;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t off = (uint32_t)((32 * (i / 2) + 4 * (i % 2) + rt) * HP + pr) * SZ;
-        if constexpr (WHOLE) {
-          const uint32_t where = pr < a.P ? off : kNowhere;
-          if constexpr (SZ == 4) buffer_st16(__builtin_bit_cast(uint4, O[i]), Yr, where);
-          else buffer_st8(make_uint2(pack_bf16x2(O[i][0], O[i][1]), pack_bf16x2(O[i][2], O[i][3])), Yr, where);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t where = pr + k < a.P ? off + k * SZ : kNowhere;
-            if constexpr (SZ == 4) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(O[i][k]), Yr, (int)where, 0, 0);
-            else __builtin_amdgcn_raw_buffer_store_b16(bf16_bits(O[i][k]), Yr, (int)where, 0, 0);
-          }
-        }
-      }
-    };
     // S^T += K^T U'; beside it the terms of the group before, and y
 #pragma unroll
     for (int kn = 0; kn < KN; ++kn) {
@@ -387,9 +491,10 @@ __global__ __launch_bounds__(kThreads) void delta_blocks_kernel(const DeltaArgs 
       if (kn > 0) Sv[kn - 1] = split_tiles(st_terms, S[kn - 1][0], S[kn - 1][1]);
       spread<4 * term_pairs(IO, ST), 2>();
       hold();
-      if (PASS == 0 && kn == 0) put_y();
+      if (Y && kn == 0) put_y(O, t0);
     }
     Sv[KN - 1] = split_tiles(st_terms, S[KN - 1][0], S[KN - 1][1]);
+    hand_over_s();
   }
 
   float* out = PASS == 1 ? a.ends : sl.t1 >= sl.last ? a.final_state : nullptr;
@@ -409,13 +514,16 @@ hipError_t launch_pass(const DeltaArgs& a, hipStream_t s) {
   const int rows_p = PASS == 1 ? a.P + a.N : a.P;
   const uint32_t blocks_p = (rows_p + kCols - 1) / kCols;
   const int64_t pieces = a.seg != 0 ? delta_slots(a, a.seg) : a.seqs();
+  // Waves of two kinds where one workgroup of one kind has a compute unit's LDS to itself.
+  constexpr bool TWO = sizeof(TIO) == 4 ? NP <= 64 : NP == 256;
+  constexpr int threads = TWO ? 2 * kThreads : kThreads;
   auto go = [&](auto kern) {
-    if (!grid_fits(pieces * a.H * blocks_p, kThreads)) return hipErrorInvalidConfiguration;
-    kern<<<dim3((unsigned)(pieces * a.H * blocks_p)), kThreads, 0, s>>>(a, blocks_p);
+    if (!grid_fits(pieces * a.H * blocks_p, threads)) return hipErrorInvalidConfiguration;
+    kern<<<dim3((unsigned)(pieces * a.H * blocks_p)), threads, 0, s>>>(a, blocks_p);
     return hipGetLastError();
   };
   const bool whole = a.N % 8 == 0 && a.P % (16 / sizeof(TIO)) == 0;
-  return whole ? go(delta_blocks_kernel<TIO, NP, true, PASS>) : go(delta_blocks_kernel<TIO, NP, false, PASS>);
+  return whole ? go(delta_blocks_kernel<TIO, NP, true, PASS, TWO>) : go(delta_blocks_kernel<TIO, NP, false, PASS, TWO>);
 }
 
 template <typename TIO, int PASS>
