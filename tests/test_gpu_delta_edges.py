@@ -327,6 +327,44 @@ def test_workspace_of_the_c_abi(own, L, lens):
     assert (ws[n:] == 255).all()
 
 
+# ---- alignment --------------------------------------------------------------------------
+
+
+def shifted(t, by=1):
+    """t's values, dense, ``by`` elements behind an aligned address."""
+    flat = torch.empty(t.numel() + by, dtype=t.dtype, device=DEV)
+    flat[by:] = t.flatten()
+    return flat[by:].view(t.shape)
+
+
+@pytest.mark.parametrize("io,L,H,P,N,lens", [("bf16", 150, 2, 64, 64, None), ("bf16", 150, 2, 128, 128, [70, 0, 80]),
+                                             ("bf16", 1100, 1, 64, 64, None), ("fp32", 150, 2, 64, 64, None),
+                                             ("bf16", 150, 2, 33, 200, None), ("bf16", 9, 2, 20, 24, None), ("fp32", 9, 2, 20, 24, [4, 5])])
+def test_arrays_at_odd_addresses(io, L, H, P, N, lens):
+    """Outputs, states and parameters need the alignment of their elements alone."""
+    s = Delta(1, L, H, P, N, 1, io, io, lens=lens, seed=52)
+    kw, h0, cu = s.to(DEV)
+    rule = (lambda h, **a: ssd.delta_rule(init_state=h, **a)) if lens is None else \
+        (lambda h, final_state=None, **a: ssd.delta_rule_varlen(cu_seqlens=cu, init_states=h, final_states=final_state, **a))
+    want = rule(h0, **kw)
+    note(f"[gpu] delta rule, step, head norm: odd addresses {io} L={L} P={P} N={N}")
+    out = shifted(torch.zeros_like(want[0])), shifted(torch.zeros_like(want[1]))
+    odd = dict(kw, A=shifted(kw["A"]), dt_pre=dict(kw["dt_pre"], bias=shifted(kw["dt_pre"]["bias"])))
+    got = rule(shifted(h0), y=out[0], final_state=out[1], **odd)
+    assert got[0].data_ptr() == out[0].data_ptr() and same(want, got)
+    one = {k: (v[:, 0] if k in TOKENS else v) for k, v in kw.items()}
+    st, so = h0[:1].clone(), shifted(h0[:1])
+    y, yo = ssd.delta_step(state=st, **one), shifted(torch.zeros_like(want[0][:, 0]))
+    ssd.delta_step(state=so, y=yo, **one)
+    assert torch.equal(y, yo) and torch.equal(st, so)
+    q, w, pos, freq = kw["x"], torch.rand(P, device=DEV), positions(1, L), torch.rand(P // 2, device=DEV)
+    for pairs in (False, True):
+        n = ssd.head_norm(q, q, w, w, positions=pos, inv_freq=freq, pairs=pairs)
+        m = shifted(torch.zeros_like(q)), shifted(torch.zeros_like(q))
+        ssd.head_norm(shifted(q), q, shifted(w), w, positions=shifted(pos), inv_freq=shifted(freq), pairs=pairs, q_out=m[0], k_out=m[1])
+        assert same(n, m)
+
+
 # ---- far offsets, many heads -----------------------------------------------------------
 
 
