@@ -588,7 +588,7 @@ bool delta_blocks_apply(const DeltaArgs& a, int io) {
   const double records = packed ? (double)(a.L / kDeltaBlock + a.nseq) : (double)a.batch * ((a.L + kDeltaBlock - 1) / kDeltaBlock);
   const bool chain = io == kBF16 && a.N <= 128;
   const double latency = (chain ? 8 + a.N / 16. : 27) + 4 * longest / kDeltaBlock;
-  const double work = 10 + records * a.H * (chain ? state * 2.6e-6 : state * 6e-6 + 0.03);
+  const double work = 10 + records * a.H * (chain ? state * 2.6e-6 : state * 5.5e-6 + 0.03);
   return (latency > work ? latency : work) < walk;
 }
 
