@@ -71,3 +71,33 @@ def delta_in_terms(x, a, beta, k, q, scale, S0, terms_of, block=64):
         y[part] = mul(M, U, n[6], n[7], acc=scale * eg * mul(Q, S.T, n[4], n[5]))
         S = mul((ed * U).T, K, n[8], n[9], acc=eg[-1, 0] * S)
     return y, S
+
+
+def rms_bounds(x, a, beta, k, q, scale, S0, fp32, block=64):
+    """(y, state): the 2-norms of what the roundings of one head come to, stored
+    roundings of y aside. For transitions that do not grow: the error of a state is
+    passed on with the decay at the most."""
+    one, two = (2.0 ** -20, 2.0 ** -20) if fp32 else (2.0 ** -8, 2.0 ** -16)
+    S = np.zeros((x.shape[1], k.shape[1])) if S0 is None else S0.astype(np.float64)
+    sq, es, ey = lambda m: m * m, 0.0, 0.0  # noqa: E731
+    for t0 in range(0, len(x), block):
+        part = slice(t0, min(len(x), t0 + block))
+        X, b, K, Q = x[part], beta[part], k[part], q[part]
+        g = np.cumsum(np.log(a[part]))
+        i, j = np.indices((len(X), len(X)))
+        dec = np.where(i >= j, np.exp(np.where(i >= j, g[:, None] - g[None], 0.0)), 0.0)
+        T = np.linalg.inv(np.eye(len(X)) + np.where(i > j, b[:, None] * dec * (K @ K.T), 0)) * b[None]
+        M = scale * dec * (Q @ K.T)
+        eg, ed = np.exp(g)[:, None], np.exp(g[-1] - g)[:, None]
+        R = X - eg * (K @ S.T)
+        U = T @ R
+        # off in R: its own rounding, and of S and K in what is taken off
+        eR = two ** 2 * (sq(R) + 2 * sq(eg) * (sq(K) @ sq(S).T))
+        # off in U: T's rounding, and R's through T
+        eU = two ** 2 * (sq(T) @ sq(R)) + sq(T) @ eR
+        own = eU + 2 * two ** 2 * sq(U)
+        ey += np.sum(scale ** 2 * sq(eg) * (2 * one ** 2 * (sq(Q) @ sq(S).T) + np.sum(sq(Q), 1, keepdims=True) * es / x.shape[1]))
+        ey += np.sum(2 * one ** 2 * (sq(M) @ sq(U)) + sq(M) @ eU)
+        es = eg[-1, 0] ** 2 * (es + two ** 2 * np.sum(sq(S))) + np.sum(sq(ed * np.linalg.norm(K, axis=1, keepdims=True)) * own)
+        S = eg[-1, 0] * S + (ed * U).T @ K
+    return np.sqrt(ey), np.sqrt(es)
