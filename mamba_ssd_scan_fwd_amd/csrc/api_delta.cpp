@@ -51,21 +51,19 @@ ssd_status_t plan_delta(const ssd_delta_desc_t* d, int64_t nseq, DeltaPlan* p) {
   return SSD_OK;
 }
 
-// (A launch of too many threads is one of too many rows.)
-ssd_status_t from_launch(hipError_t e) { return e == hipErrorInvalidConfiguration ? SSD_ERR_BAD_SHAPE : from_hip(e); }
-
-// The prompt form: the way it is walked, and the workspace that needs.
+// The prompt form: the way it is walked (token after token too where the form in
+// blocks has more workgroups than can be launched), and the workspace that needs.
 ssd_status_t plan_rule(const ssd_delta_desc_t* d, int64_t nseq, DeltaPlan* p) {
   const ssd_status_t st = plan_delta(d, nseq, p);
   if (st != SSD_OK) return st;
-  p->blocks = delta_blocks_apply(p->a, p->io);
+  p->blocks = false;
   p->total = 0;
-  if (!p->blocks) return SSD_OK;
-  if (delta_slots(p->a) > (kMaxRows - 1) / p->a.H) return SSD_ERR_BAD_SHAPE;  // waves of the first kernel
-  const int64_t bytes = delta_blocks_workspace(p->a, p->io);
-  if (bytes > kMaxElems) return SSD_ERR_BAD_SHAPE;
-  p->total = size_t(bytes);
-  return SSD_OK;
+  if (delta_blocks_apply(p->a, p->io)) {
+    const int64_t bytes = delta_blocks_workspace(p->a, p->io);
+    p->blocks = bytes <= kMaxElems && delta_blocks_fit(p->a, p->io);
+    if (p->blocks) p->total = size_t(bytes);
+  }
+  return p->blocks || delta_walk_fits(p->a) ? SSD_OK : SSD_ERR_BAD_SHAPE;
 }
 
 ssd_status_t run_rule(DeltaPlan& p, const int32_t* cu, const void* x, const void* dt, const float* A, const void* B,
@@ -93,7 +91,7 @@ ssd_status_t run_rule(DeltaPlan& p, const int32_t* cu, const void* x, const void
   if (overlap(rf, ri) && rf.lo != ri.lo) return SSD_ERR_ALIAS;  // the same array or none of it
   a.x = x, a.dt = dt, a.A = A, a.B = B, a.C = C, a.beta = beta, a.init = init, a.y = y, a.final_state = final_state;
   a.cu = cu;
-  if (!p.blocks) return from_launch(launch_delta_walk(a, p.io, p.dt, s));
+  if (!p.blocks) return from_hip(launch_delta_walk(a, p.io, p.dt, s));
   void* w = workspace;
   if (w == nullptr && hipMallocAsync(&w, p.total, s) != hipSuccess) return SSD_ERR_HIP;
   a.ws = static_cast<char*>(w);
@@ -102,7 +100,7 @@ ssd_status_t run_rule(DeltaPlan& p, const int32_t* cu, const void* x, const void
     const hipError_t fe = hipFreeAsync(w, s);
     if (e == hipSuccess) e = fe;
   }
-  return from_launch(e);
+  return from_hip(e);
 }
 
 }  // namespace
@@ -179,7 +177,9 @@ ssd_status_t ssd_delta_step(const ssd_delta_desc_t* desc, const void* x, const v
   r.dto = a.dto;
   r.sigmoid = a.sigmoid;
   r.scale = a.scale;
-  return from_launch(launch_delta_step(r, p.io, p.dt, static_cast<hipStream_t>(stream)));
+  const hipError_t e = launch_delta_step(r, p.io, p.dt, static_cast<hipStream_t>(stream));
+  // a launch of too many threads is one of too many rows
+  return e == hipErrorInvalidConfiguration ? SSD_ERR_BAD_SHAPE : from_hip(e);
 }
 
 ssd_status_t ssd_head_norm(const ssd_head_norm_desc_t* desc, const void* q, const void* k, const float* q_weight,

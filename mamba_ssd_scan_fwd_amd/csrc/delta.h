@@ -28,7 +28,9 @@ struct DeltaArgs {
   float *ends, *enter;             // workspace: segments' ends and entering states
   int64_t seqs() const { return nseq > 0 ? nseq : batch; }
 };
-// The recurrence token after token.
+// The recurrence token after token. Whether its launch can be counted (grid_fits):
+// a call's plan asks, here and below, before anything is launched.
+bool delta_walk_fits(const DeltaArgs& a);
 hipError_t launch_delta_walk(const DeltaArgs& a, int io, int dt, hipStream_t s);
 
 // In blocks of kDeltaBlock tokens. A sequence's blocks begin with it; the blocks
@@ -42,11 +44,22 @@ inline int64_t delta_slots(const DeltaArgs& a, int64_t unit = kDeltaBlock) {
 }
 bool delta_blocks_apply(const DeltaArgs& a, int io);
 int64_t delta_blocks_workspace(DeltaArgs& a, int io);  // in bytes; sets a.seg
+// Whether every launch of the form in blocks can be counted, by whichever walk the
+// rows' addresses and strides will choose. (a.seg is set.)
+bool delta_blocks_fit(const DeltaArgs& a, int io);
 hipError_t launch_delta_blocks(const DeltaArgs& a, int io, int dt, hipStream_t s);
+// The kernels of the form in blocks: their workgroups, and launches.
+int64_t delta_solve_groups(const DeltaArgs& a);
 hipError_t launch_delta_solve(const DeltaArgs& a, int io, int dt, hipStream_t s);
 bool delta_chain_applies(const DeltaArgs& a, int io);
+int64_t delta_chain_groups(const DeltaArgs& a, int pass);
 hipError_t launch_delta_chain(const DeltaArgs& a, int pass, hipStream_t s);
+int64_t delta_join_groups(const DeltaArgs& a);
 hipError_t launch_delta_join(const DeltaArgs& a, hipStream_t s);
+// What the walks over blocks divide among their workgroups: rows of the state (with
+// the unit states' in pass 1), and sequences or segments.
+inline int delta_rows(const DeltaArgs& a, int pass) { return pass == 1 ? a.P + a.N : a.P; }
+inline int64_t delta_pieces(const DeltaArgs& a) { return a.seg != 0 ? delta_slots(a, a.seg) : a.seqs(); }
 
 struct DeltaStepArgs {
   const void *x, *dt, *beta, *B, *C;  // one token per row
@@ -85,8 +98,7 @@ struct HeadNormArgs {
 };
 hipError_t launch_head_norm(const HeadNormArgs& a, int io, hipStream_t s);
 
-// Whether a launch's threads can be counted (in 32 bits). What launches more answers
-// hipErrorInvalidConfiguration, here before any launch.
+// Whether a launch's threads can be counted (in 32 bits).
 inline bool grid_fits(int64_t groups, int threads) { return groups < (int64_t(1) << 32) / threads; }
 
 #ifdef __HIPCC__

@@ -509,17 +509,17 @@ __global__ __launch_bounds__(TWO ? 2 * kThreads : kThreads) void delta_blocks_ke
     }
 }
 
+uint32_t blocks_of(const DeltaArgs& a, int pass) { return (delta_rows(a, pass) + kCols - 1) / kCols; }
+int64_t groups_of(const DeltaArgs& a, int pass) { return delta_pieces(a) * a.H * blocks_of(a, pass); }
+
 template <typename TIO, int NP, int PASS>
 hipError_t launch_pass(const DeltaArgs& a, hipStream_t s) {
-  const int rows_p = PASS == 1 ? a.P + a.N : a.P;
-  const uint32_t blocks_p = (rows_p + kCols - 1) / kCols;
-  const int64_t pieces = a.seg != 0 ? delta_slots(a, a.seg) : a.seqs();
+  const uint32_t blocks_p = blocks_of(a, PASS);
   // Waves of two kinds where one workgroup of one kind has a compute unit's LDS to itself.
   constexpr bool TWO = sizeof(TIO) == 4 ? NP <= 64 : NP == 256;
   constexpr int threads = TWO ? 2 * kThreads : kThreads;
   auto go = [&](auto kern) {
-    if (!grid_fits(pieces * a.H * blocks_p, threads)) return hipErrorInvalidConfiguration;
-    kern<<<dim3((unsigned)(pieces * a.H * blocks_p)), threads, 0, s>>>(a, blocks_p);
+    kern<<<dim3((unsigned)groups_of(a, PASS)), threads, 0, s>>>(a, blocks_p);
     return hipGetLastError();
   };
   const bool whole = a.N % 8 == 0 && a.P % (16 / sizeof(TIO)) == 0;
@@ -598,6 +598,14 @@ int64_t delta_blocks_workspace(DeltaArgs& a, int io) {
   if (a.seg == 0) return records;
   const int64_t states = delta_slots(a, a.seg) * a.H;
   return records + states * (2 * a.P + a.N) * a.N * (int64_t)sizeof(float);
+}
+
+bool delta_blocks_fit(const DeltaArgs& a, int io) {
+  // (twice kThreads: as with partners)
+  auto walks = [&](int pass) {
+    return grid_fits(groups_of(a, pass), 2 * kThreads) && (io != kBF16 || grid_fits(delta_chain_groups(a, pass), 2 * kThreads));
+  };
+  return grid_fits(delta_solve_groups(a), kThreads) && walks(0) && (a.seg == 0 || (walks(1) && grid_fits(delta_join_groups(a), kThreads)));
 }
 
 hipError_t launch_delta_blocks(const DeltaArgs& args, int io, int dt, hipStream_t s) {

@@ -437,16 +437,15 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(const DeltaArgs a
       }
 }
 
+// Workgroups to a head's rows: of 128 of them, of 64 where there are no more.
+uint32_t blocks_of(const DeltaArgs& a, int pass) { return (delta_rows(a, pass) + 127) / 128; }
+
 template <int NP, int PASS> hipError_t launch_np(const DeltaArgs& a, hipStream_t s) {
-  const int rows_p = PASS == 1 ? a.P + a.N : a.P;
-  const int64_t pieces = a.seg != 0 ? delta_slots(a, a.seg) : a.seqs();
-  auto go = [&](auto kern, int cols) {
-    const uint32_t blocks_p = (rows_p + cols - 1) / cols;
-    if (!grid_fits(pieces * a.H * blocks_p, kThreads)) return hipErrorInvalidConfiguration;
-    kern<<<dim3((unsigned)(pieces * a.H * blocks_p)), kThreads, 0, s>>>(a, blocks_p);
-    return hipGetLastError();
-  };
-  return rows_p > 64 ? go(delta_chain_kernel<NP, 2, PASS>, 128) : go(delta_chain_kernel<NP, 1, PASS>, 64);
+  const dim3 grid((unsigned)delta_chain_groups(a, PASS));
+  const uint32_t blocks_p = blocks_of(a, PASS);
+  if (delta_rows(a, PASS) > 64) delta_chain_kernel<NP, 2, PASS><<<grid, kThreads, 0, s>>>(a, blocks_p);
+  else delta_chain_kernel<NP, 1, PASS><<<grid, kThreads, 0, s>>>(a, blocks_p);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -457,6 +456,8 @@ bool delta_chain_applies(const DeltaArgs& a, int io) {
   };
   return io == kBF16 && a.N <= 128 && a.N % 8 == 0 && a.P % 8 == 0 && lies(a.x, a.xs) && lies(a.B, a.bs) && lies(a.C, a.cs);
 }
+
+int64_t delta_chain_groups(const DeltaArgs& a, int pass) { return delta_pieces(a) * a.H * blocks_of(a, pass); }
 
 hipError_t launch_delta_chain(const DeltaArgs& a, int pass, hipStream_t s) {
   if (a.N <= 32) return pass == 1 ? launch_np<32, 1>(a, s) : launch_np<32, 0>(a, s);

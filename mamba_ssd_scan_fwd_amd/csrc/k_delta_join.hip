@@ -98,10 +98,11 @@ __global__ __launch_bounds__(kThreads) void delta_join_kernel(const DeltaArgs a,
 
 }  // namespace
 
+int64_t delta_join_groups(const DeltaArgs& a) { return a.seqs() * a.H * ((a.P + kRows - 1) / kRows); }
+
 hipError_t launch_delta_join(const DeltaArgs& a, hipStream_t s) {
   const uint32_t blocks_p = (a.P + kRows - 1) / kRows;
-  if (!grid_fits(a.seqs() * a.H * blocks_p, kThreads)) return hipErrorInvalidConfiguration;
-  const dim3 grid((unsigned)(a.seqs() * a.H * blocks_p));
+  const dim3 grid((unsigned)delta_join_groups(a));
   if (a.N <= 32) delta_join_kernel<32><<<grid, kThreads, 0, s>>>(a, blocks_p);
   else if (a.N <= 64) delta_join_kernel<64><<<grid, kThreads, 0, s>>>(a, blocks_p);
   else if (a.N <= 128) delta_join_kernel<128><<<grid, kThreads, 0, s>>>(a, blocks_p);

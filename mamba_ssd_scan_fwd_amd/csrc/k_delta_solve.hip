@@ -288,9 +288,8 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TIO) == 2 && NP <= 128 ? 2 : 1)
 
 template <typename TIO, typename TDT>
 hipError_t launch_io(const DeltaArgs& a, hipStream_t s) {
-  const uint32_t tasks = (uint32_t)(delta_slots(a) * a.H);  // below 2^31 (api)
-  if (!grid_fits((tasks + kWaves - 1) / kWaves, 64 * kWaves)) return hipErrorInvalidConfiguration;
-  const dim3 grid((unsigned)((tasks + kWaves - 1) / kWaves));
+  const uint32_t tasks = (uint32_t)(delta_slots(a) * a.H);
+  const dim3 grid((unsigned)delta_solve_groups(a));
   auto go = [&](auto whole, auto other) {
     if (a.N % 8 == 0) whole<<<grid, 64 * kWaves, 0, s>>>(a, tasks);
     else other<<<grid, 64 * kWaves, 0, s>>>(a, tasks);
@@ -304,6 +303,8 @@ hipError_t launch_io(const DeltaArgs& a, hipStream_t s) {
 }
 
 }  // namespace
+
+int64_t delta_solve_groups(const DeltaArgs& a) { return (delta_slots(a) * a.H + kWaves - 1) / kWaves; }
 
 hipError_t launch_delta_solve(const DeltaArgs& a, int io, int dt, hipStream_t s) {
   if (io == kF32) return launch_io<float, float>(a, s);

@@ -132,14 +132,20 @@ __global__ __launch_bounds__(kThreads) void delta_walk_kernel(const DeltaArgs a,
   }
 }
 
+constexpr int kRows = 2;  // rows of the state to a team
+
+// Workgroups to a head's P rows.
+uint32_t blocks_of(const DeltaArgs& a) {
+  const int rows = kRows * kThreads / (selective_padded_states(a.N) / 4);
+  return (a.P + rows - 1) / rows;
+}
+
 template <typename TIO, typename TDT, int NP>
 hipError_t launch_np(const DeltaArgs& a, hipStream_t s) {
-  constexpr int R = 2, TEAMS = kThreads / (NP / 4);
-  const uint32_t blocks_p = (a.P + TEAMS * R - 1) / (TEAMS * R);
-  if (!grid_fits(a.seqs() * a.H * blocks_p, kThreads)) return hipErrorInvalidConfiguration;
+  const uint32_t blocks_p = blocks_of(a);
   const dim3 grid((unsigned)(a.seqs() * a.H * blocks_p));
-  if (a.N % 4 == 0) delta_walk_kernel<TIO, TDT, NP, true, R><<<grid, kThreads, 0, s>>>(a, blocks_p);
-  else delta_walk_kernel<TIO, TDT, NP, false, R><<<grid, kThreads, 0, s>>>(a, blocks_p);
+  if (a.N % 4 == 0) delta_walk_kernel<TIO, TDT, NP, true, kRows><<<grid, kThreads, 0, s>>>(a, blocks_p);
+  else delta_walk_kernel<TIO, TDT, NP, false, kRows><<<grid, kThreads, 0, s>>>(a, blocks_p);
   return hipGetLastError();
 }
 
@@ -155,6 +161,8 @@ hipError_t launch_io(const DeltaArgs& a, hipStream_t s) {
 }
 
 }  // namespace
+
+bool delta_walk_fits(const DeltaArgs& a) { return grid_fits(a.seqs() * a.H * blocks_of(a), kThreads); }
 
 hipError_t launch_delta_walk(const DeltaArgs& a, int io, int dt, hipStream_t s) {
   if (io == kF32) return launch_io<float, float>(a, s);
