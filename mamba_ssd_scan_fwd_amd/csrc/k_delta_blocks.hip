@@ -567,29 +567,51 @@ int64_t delta_segment(const DeltaArgs& a, int io) {
 
 size_t record_bytes(int io) { return io == kBF16 ? DeltaRecord<__hip_bfloat16>::bytes : DeltaRecord<float>::bytes; }
 
+// What either form takes, in microseconds, by a fit to 446 measured calls: 2 to 32 heads of 8 x 8 to
+// 128 x 256, 3 to 16 384 sequences of 1 to 2048 tokens, even ones and one long among ones of a
+// token (root mean square of the error: the walk's 18%, the blocks' 10 to 14%). The walk: the tokens of the
+// longest sequence in turn, or, where the card is full, all tokens' updates and the states, in and
+// out. The blocks: two launches and the blocks of the longest sequence in turn, or a record
+// and a block's products for every block and head.
+struct Times {
+  double start, token, full;       // token after token
+  double latency, block, records;  // in blocks
+  double walk(double longest) const { return start + (full > token * longest ? full : token * longest); }
+  double blocks(double longest) const {
+    const double turn = latency + block * longest / kDeltaBlock;
+    return turn > records ? turn : records;
+  }
+};
+Times times_of(const DeltaArgs& a, int io) {
+  const bool packed = a.nseq > 0, odd = a.N % 4 != 0;
+  const bool chain = io == kBF16 && a.N <= 128 && a.N % 8 == 0 && a.P % 8 == 0;
+  const double state = (double)a.P * a.N, tokens = (double)a.batch * a.L;
+  const double blocks = packed ? (double)(a.L / kDeltaBlock + a.nseq) : (double)a.batch * ((a.L + kDeltaBlock - 1) / kDeltaBlock);
+  const double update = state > 2000 ? state * 3e-7 : 6e-4;
+  Times t;
+  const double search = packed ? 2 : 0;  // for a slot's sequence
+  t.start = 5, t.token = odd ? 0.75 : 0.27 + 8.5e-4 * a.N;
+  t.full = a.H * (tokens * (odd ? 2.7 : 1.) * update + a.seqs() * state * 2e-6);
+  if (chain) {
+    t.latency = search + 6.5 + 0.078 * a.N, t.block = 0.63 + 0.016 * a.N, t.records = 11 + blocks * a.H * (0.013 + 1.6e-6 * state);
+  } else if (io != kBF16) {
+    t.latency = search + 7.4 + 0.255 * a.N, t.block = 0.85 + 0.041 * a.N, t.records = 15 + blocks * a.H * (0.025 + 5.2e-6 * state);
+  } else {
+    t.latency = search + 11.3 + 0.062 * a.N, t.block = 2.5 + 0.013 * a.N, t.records = 14 + blocks * a.H * (0.0033 + 5e-6 * state);
+  }
+  return t;
+}
+
 }  // namespace
 
-// Blocks or token after token, by the times that either was measured to take, in
-// microseconds. The walk: 6, and 0.37 a token of the longest sequence, or, where the card is full,
-// 0.36 a token and million of the state's elements (packed sequences are uneven: half as much
-// again). Blocks: two launches and a block's latency, 16 for aligned rows of
-// N = 128 and 27 for others, and 4 a block; or, where the card is full, what a
-// record and a block's products cost for each head.
-// Measured (blocks / walk): one sequence of 32 heads, P = N = 128, bf16: 16 tokens 19 / 11, 48 tokens 19 / 24;
-// 64 of them: 4 tokens 99 / 95, 8 tokens 101 / 139. 8 sequences of 32 heads, P = N = 64, fp32: 48 tokens 32 / 25,
-// 96 tokens 39 / 46. Packed, bf16: 64 sequences of one token 92 / 66, of 16 tokens 104 / 246.
+// The form that takes less: of the 446 calls the batched ones take 1.00 of the faster form's time in the
+// geometric mean. Of packed sequences the host knows the mean length alone, and takes the
+// longest for twice that.
 bool delta_blocks_apply(const DeltaArgs& a, int io) {
   if ((io != kBF16 && a.N > 128) || a.N < 8 || a.P < 8) return false;
-  const bool packed = a.nseq > 0;
-  const double state = (double)a.P * a.N;
-  const double tokens = (double)a.batch * a.L, longest = packed ? 2. * a.L / a.nseq : (double)a.L;
-  const double full = tokens * a.H * state * (packed ? 5.4e-7 : 3.6e-7), alone = 0.37 * longest;
-  const double walk = 6 + (full > alone ? full : alone);
-  const double records = packed ? (double)(a.L / kDeltaBlock + a.nseq) : (double)a.batch * ((a.L + kDeltaBlock - 1) / kDeltaBlock);
-  const bool chain = io == kBF16 && a.N <= 128;
-  const double latency = (chain ? 8 + a.N / 16. : 27) + 4 * longest / kDeltaBlock;
-  const double work = 10 + records * a.H * (chain ? state * 2.6e-6 : state * 5.5e-6 + 0.03);
-  return (latency > work ? latency : work) < walk;
+  const Times t = times_of(a, io);
+  const double mean2 = a.nseq > 0 ? 2. * a.L / a.nseq : (double)a.L, longest = mean2 < a.L ? mean2 : (double)a.L;
+  return t.blocks(longest) < t.walk(longest);
 }
 
 int64_t delta_blocks_workspace(DeltaArgs& a, int io) {

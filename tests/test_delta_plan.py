@@ -25,3 +25,13 @@ def test_calls_that_no_form_can_launch_are_refused_by_the_query_too(L, S):
     kw = dict(SMALL, batch=1 if S else 1 << 19, seqlen=(L << 19) if S else L)
     assert bytes_of(S=S or 0, **kw)[0] == SHAPE
     assert call(rule(**kw), S=S, **FAR) == SHAPE
+
+
+@pytest.mark.parametrize("P,N", [(8, 8), (16, 16), (32, 32), (64, 16)])
+@pytest.mark.parametrize("batch,L", [(16, 16), (4096, 8), (16384, 8)])
+def test_records_are_paid_for(P, N, batch, L):
+    """A block's record of 18.5 KB for a few tokens of a small state: token after token
+    takes half the time, and none of the workspace."""
+    kw = dict(batch=batch, seqlen=L, nheads=32, ngroups=1, headdim=P, dstate=N)
+    assert bytes_of(**kw) == (OK, 0)
+    assert bytes_of(**dict(kw, seqlen=128, batch=16))[1] > 0
