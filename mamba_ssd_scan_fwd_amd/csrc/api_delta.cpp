@@ -47,7 +47,8 @@ ssd_status_t plan_delta(const ssd_delta_desc_t* d, int64_t nseq, DeltaPlan* p) {
   a.dto = DtOpts{d->dt_bias, d->dt_softplus != 0, d->dt_clamp != 0, d->dt_min, d->dt_max};
   a.sigmoid = d->beta_sigmoid != 0;
   a.scale = d->scale;
-  a.seg = 0;
+  a.seg = a.upto = 0;
+  a.longs = nullptr;
   return SSD_OK;
 }
 
@@ -62,6 +63,7 @@ ssd_status_t plan_rule(const ssd_delta_desc_t* d, int64_t nseq, DeltaPlan* p) {
     const int64_t bytes = delta_blocks_workspace(p->a, p->io);
     p->blocks = bytes <= kMaxElems && delta_blocks_fit(p->a, p->io);
     if (p->blocks) p->total = size_t(bytes);
+    else p->a.upto = 0;
   }
   return p->blocks || delta_walk_fits(p->a) ? SSD_OK : SSD_ERR_BAD_SHAPE;
 }

@@ -24,6 +24,8 @@ struct DeltaArgs {
   float scale;
   // in blocks (set at launch)
   char* ws;                        // workspace: the blocks' records
+  int64_t upto;                    // packed, not 0: sequences of more tokens go in blocks, the others token after token
+  int32_t* longs;                  // workspace, then: which those are, in order, -1 behind the last; else nullptr
   int64_t seg;                     // tokens of a segment; 0: sequences in one piece
   float *ends, *enter;             // workspace: segments' ends and entering states
   int64_t seqs() const { return nseq > 0 ? nseq : batch; }
@@ -38,11 +40,14 @@ hipError_t launch_delta_walk(const DeltaArgs& a, int io, int dt, hipStream_t s);
 // stream from slot offset / kDeltaBlock + s on (so that nobody has to sum the
 // sequences' block counts; a few slots stay empty).
 constexpr int kDeltaBlock = 64;
+// Sequences that go in blocks: all, or as many as can have more than a.upto tokens.
+inline int64_t delta_seqs_in_blocks(const DeltaArgs& a) { return a.upto > 0 ? a.L / (a.upto + 1) : a.seqs(); }
 // (Segments, of several blocks, have slots of the same kind.)
 inline int64_t delta_slots(const DeltaArgs& a, int64_t unit = kDeltaBlock) {
-  return a.nseq > 0 ? a.L / unit + a.nseq : a.batch * ((a.L + unit - 1) / unit);
+  return a.nseq > 0 ? a.L / unit + delta_seqs_in_blocks(a) : a.batch * ((a.L + unit - 1) / unit);
 }
-bool delta_blocks_apply(const DeltaArgs& a, int io);
+// Whether any of the call goes in blocks; sets a.upto.
+bool delta_blocks_apply(DeltaArgs& a, int io);
 int64_t delta_blocks_workspace(DeltaArgs& a, int io);  // in bytes; sets a.seg
 // Whether every launch of the form in blocks can be counted, by whichever walk the
 // rows' addresses and strides will choose. (a.seg is set.)
@@ -59,7 +64,7 @@ hipError_t launch_delta_join(const DeltaArgs& a, hipStream_t s);
 // What the walks over blocks divide among their workgroups: rows of the state (with
 // the unit states' in pass 1), and sequences or segments.
 inline int delta_rows(const DeltaArgs& a, int pass) { return pass == 1 ? a.P + a.N : a.P; }
-inline int64_t delta_pieces(const DeltaArgs& a) { return a.seg != 0 ? delta_slots(a, a.seg) : a.seqs(); }
+inline int64_t delta_pieces(const DeltaArgs& a) { return a.seg != 0 ? delta_slots(a, a.seg) : delta_seqs_in_blocks(a); }
 
 struct DeltaStepArgs {
   const void *x, *dt, *beta, *B, *C;  // one token per row

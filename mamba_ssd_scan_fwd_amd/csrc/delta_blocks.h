@@ -77,27 +77,30 @@ template <int TA, int TB> __device__ __forceinline__ void mul_pair(f32x4_t& acc,
       }
 }
 
-// A slot of `unit` tokens: its sequence, which of the sequence's it is, the
-// sequence's tokens [first, last), of batch row `row`, and the slot's own:
-// from t0 up to t1 (t1 <= t0: the slot is empty).
+// A slot of `unit` tokens: its sequence, the how manieth that is of those in blocks,
+// which of the sequence's slots it is, the sequence's tokens [first, last), of
+// batch row `row`, and the slot's own: from t0 up to t1 (t1 <= t0: the slot is empty).
 struct DeltaSlot {
-  int64_t seq, part, row, first, last, t0, t1;
+  int64_t seq, index, part, row, first, last, t0, t1;
 };
+// Of a packed stream: the sequence that is the i-th in blocks, -1 behind the last; where it begins.
+__device__ __forceinline__ int64_t delta_seq(const DeltaArgs& a, int64_t i) { return a.longs != nullptr ? a.longs[i] : i; }
+__device__ __forceinline__ int64_t delta_begin(const DeltaArgs& a, int64_t seq) { return seq < 0 ? a.L : seq_offset(a.cu, seq, a.L); }
 // (Tokens, slots and units are below 2^31: their quotients are taken in 32 bits.)
-__device__ __forceinline__ int64_t delta_first_slot(const DeltaArgs& a, int64_t s, uint32_t unit) {
-  return a.cu != nullptr ? (uint32_t)seq_offset(a.cu, s, a.L) / unit + s : s * (((uint32_t)a.L + unit - 1) / unit);
+__device__ __forceinline__ int64_t delta_first_slot(const DeltaArgs& a, int64_t i, uint32_t unit) {
+  return a.cu != nullptr ? (uint32_t)delta_begin(a, delta_seq(a, i)) / unit + i : i * (((uint32_t)a.L + unit - 1) / unit);
 }
 // (by a whole wave)
 __device__ __forceinline__ DeltaSlot delta_slot(const DeltaArgs& a, uint32_t slot, uint32_t unit) {
   DeltaSlot r;
   if (a.cu == nullptr) {
     const uint32_t nc = ((uint32_t)a.L + unit - 1) / unit;
-    r.seq = r.row = slot / nc;
+    r.seq = r.index = r.row = slot / nc;
     r.first = 0, r.last = a.L;
   } else {
     // the last sequence whose slots begin at or before this one
     const int lane = threadIdx.x & 63;
-    int64_t lo = 0, n = a.nseq;
+    int64_t lo = 0, n = a.upto > 0 ? (uint32_t)a.L / (uint32_t)(a.upto + 1) : a.nseq;
     while (n > 1) {
       const int64_t step = (n + 63) / 64;
       const int64_t i = lo + lane * step;
@@ -108,10 +111,10 @@ __device__ __forceinline__ DeltaSlot delta_slot(const DeltaArgs& a, uint32_t slo
       lo += k * step;
       n = left < step ? left : step;
     }
-    r.seq = lo, r.row = 0;
-    r.first = seq_offset(a.cu, lo, a.L), r.last = seq_offset(a.cu, lo + 1, a.L);
+    r.seq = delta_seq(a, lo), r.index = lo, r.row = 0;
+    r.first = delta_begin(a, r.seq), r.last = delta_begin(a, r.seq < 0 ? r.seq : r.seq + 1);
   }
-  r.part = (int64_t)slot - delta_first_slot(a, r.seq, unit);
+  r.part = (int64_t)slot - delta_first_slot(a, r.index, unit);
   r.t0 = r.first + r.part * unit;
   r.t1 = r.t0 + unit < r.last ? r.t0 + unit : r.last;
   if (r.part < 0) r.t1 = r.t0;  // (before the first sequence)
@@ -128,9 +131,13 @@ template <int PASS> __device__ __forceinline__ bool delta_piece(const DeltaArgs&
     if (sl.part < 0 || (sl.part > 0 && sl.t1 <= sl.t0)) return false;
     return PASS == 0 || sl.t1 < sl.last;  // nothing begins behind the last one
   }
-  sl.seq = piece, sl.part = 0, sl.row = a.cu != nullptr ? 0 : piece;
-  sl.t0 = sl.first = a.cu != nullptr ? seq_offset(a.cu, piece, a.L) : 0;
-  sl.t1 = sl.last = a.cu != nullptr ? seq_offset(a.cu, piece + 1, a.L) : a.L;
+  sl.seq = sl.index = piece, sl.part = 0, sl.row = a.cu != nullptr ? 0 : piece;
+  if (a.longs != nullptr) {
+    sl.seq = a.longs[piece];
+    if (sl.seq < 0) return false;
+  }
+  sl.t0 = sl.first = a.cu != nullptr ? seq_offset(a.cu, sl.seq, a.L) : 0;
+  sl.t1 = sl.last = a.cu != nullptr ? seq_offset(a.cu, sl.seq + 1, a.L) : a.L;
   return true;
 }
 

@@ -73,7 +73,7 @@ __global__ __launch_bounds__(TWO ? 2 * kThreads : kThreads) void delta_blocks_ke
   DeltaSlot sl;
   if (!delta_piece<PASS>(a, piece, sl)) return;
   const int64_t row = sl.row, first = sl.t0, last = sl.t1;
-  int64_t slot = delta_first_slot(a, sl.seq, kDeltaBlock) + (first - sl.first) / kDeltaBlock;
+  int64_t slot = delta_first_slot(a, sl.index, kDeltaBlock) + (first - sl.first) / kDeltaBlock;
   const int rows_p = PASS == 1 ? a.P + a.N : a.P;  // rows in all
   const int64_t grp = (uint32_t)h / ((uint32_t)a.H / (uint32_t)a.G);
   const TIO* Xp = static_cast<const TIO*>(a.x) + row * a.xs.batch + (int64_t)h * a.P;
@@ -567,6 +567,44 @@ int64_t delta_segment(const DeltaArgs& a, int io) {
 
 size_t record_bytes(int io) { return io == kBF16 ? DeltaRecord<__hip_bfloat16>::bytes : DeltaRecord<float>::bytes; }
 
+// Which of a packed stream's sequences have more than a.upto tokens: one workgroup
+// goes over the offsets.
+constexpr int kPick = 1024, kEach = 4;  // threads, and sequences of each at a time
+__global__ __launch_bounds__(kPick) void delta_pick_kernel(const DeltaArgs a, int64_t room) {
+  __shared__ int counts[kPick / 64];
+  const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+  int64_t found = 0;
+  for (int64_t s0 = 0; s0 < a.nseq; s0 += kPick * kEach) {
+    // (a wave's sequences lie behind one another, a lane's 64 apart)
+    const int64_t mine = s0 + wave * (64 * kEach) + lane;
+    uint64_t is_long[kEach];
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int64_t s = mine + 64 * k;
+      is_long[k] = __ballot(s < a.nseq && seq_offset(a.cu, s + 1, a.L) - seq_offset(a.cu, s, a.L) > a.upto);
+      n += __popcll(is_long[k]);
+    }
+    if (lane == 0) counts[wave] = n;
+    __syncthreads();
+    int64_t at = found;
+#pragma unroll
+    for (int w = 0; w < kPick / 64; ++w) {
+      if (w < wave) at += counts[w];
+      found += counts[w];
+    }
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int64_t i = at + __popcll(is_long[k] & ((uint64_t(1) << lane) - 1));
+      // (offsets that do not rise may have more than there is room for)
+      if ((is_long[k] >> lane & 1) != 0 && i < room) a.longs[i] = (int32_t)(mine + 64 * k);
+      at += __popcll(is_long[k]);
+    }
+    __syncthreads();
+  }
+  for (int64_t i = found + threadIdx.x; i < room; i += kPick) a.longs[i] = -1;
+}
+
 // What either form takes, in microseconds, by a fit to 446 measured calls: 2 to 32 heads of 8 x 8 to
 // 128 x 256, 3 to 16 384 sequences of 1 to 2048 tokens, even ones and one long among ones of a
 // token (root mean square of the error: the walk's 18%, the blocks' 10 to 14%). The walk: the tokens of the
@@ -606,16 +644,30 @@ Times times_of(const DeltaArgs& a, int io) {
 
 // The form that takes less: of the 446 calls the batched ones take 1.00 of the faster form's time in the
 // geometric mean. Of packed sequences the host knows the mean length alone, and takes the
-// longest for twice that.
-bool delta_blocks_apply(const DeltaArgs& a, int io) {
+// longest for twice that. Where token after token is then the faster one, and there are tokens
+// enough for a sequence that it would be slow for, the choice is made sequence by
+// sequence where the lengths are known: those that take longer token after token than in
+// blocks, were they alone, go in blocks, at the price of three launches (9 us) that find
+// nothing to do where there are none. Measured, all token after token / all in blocks / each
+// in its own form: 2048 tokens and 255 sequences of one, fp32, 8 heads of 64 x 64 659 / 162 / 170, bf16, 16 heads of
+// 128 x 256 1643 / 956 / 509; 256 sequences of 4 tokens, fp32, 8 heads of 64 x 64 28 / 110 / 36, 2 heads of
+// 32 x 32 7.3 / 31 / 16.5.
+bool delta_blocks_apply(DeltaArgs& a, int io) {
+  a.upto = 0;
   if ((io != kBF16 && a.N > 128) || a.N < 8 || a.P < 8) return false;
   const Times t = times_of(a, io);
   const double mean2 = a.nseq > 0 ? 2. * a.L / a.nseq : (double)a.L, longest = mean2 < a.L ? mean2 : (double)a.L;
-  return t.blocks(longest) < t.walk(longest);
+  const double walk = t.walk(longest), blocks = t.blocks(longest), launches = 8;
+  if (blocks < walk) return true;
+  const int64_t upto = (int64_t)((t.latency + launches - t.start) / (t.token - t.block / kDeltaBlock));
+  if (a.nseq == 0 || a.L <= 4 * upto) return false;
+  if (blocks > walk + launches) a.upto = upto;
+  return true;
 }
 
 int64_t delta_blocks_workspace(DeltaArgs& a, int io) {
   const int64_t records = delta_slots(a) * a.H * (int64_t)record_bytes(io);
+  if (a.upto > 0) return records + delta_seqs_in_blocks(a) * (int64_t)sizeof(int32_t);
   a.seg = delta_segment(a, io);
   if (a.seg == 0) return records;
   const int64_t states = delta_slots(a, a.seg) * a.H;
@@ -627,6 +679,7 @@ bool delta_blocks_fit(const DeltaArgs& a, int io) {
   auto walks = [&](int pass) {
     return grid_fits(groups_of(a, pass), 2 * kThreads) && (io != kBF16 || grid_fits(delta_chain_groups(a, pass), 2 * kThreads));
   };
+  if (a.upto > 0 && !delta_walk_fits(a)) return false;
   return grid_fits(delta_solve_groups(a), kThreads) && walks(0) && (a.seg == 0 || (walks(1) && grid_fits(delta_join_groups(a), kThreads)));
 }
 
@@ -637,12 +690,19 @@ hipError_t launch_delta_blocks(const DeltaArgs& args, int io, int dt, hipStream_
     a.ends = reinterpret_cast<float*>(a.ws + delta_slots(a) * a.H * (int64_t)record_bytes(io));
     a.enter = a.ends + states * (a.P + a.N) * a.N;
   }
+  if (a.upto > 0) {
+    a.longs = reinterpret_cast<int32_t*>(a.ws + delta_slots(a) * a.H * (int64_t)record_bytes(io));
+    delta_pick_kernel<<<1, kPick, 0, s>>>(a, delta_seqs_in_blocks(a));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   hipError_t e = launch_delta_solve(a, io, dt, s);
   if (e == hipSuccess && a.seg != 0) {
     e = launch_walk<1>(a, io, s);
     if (e == hipSuccess) e = launch_delta_join(a, s);
   }
-  return e == hipSuccess ? launch_walk<0>(a, io, s) : e;
+  if (e == hipSuccess) e = launch_walk<0>(a, io, s);
+  return e == hipSuccess && a.upto > 0 ? launch_delta_walk(a, io, dt, s) : e;
 }
 
 }  // namespace ssd

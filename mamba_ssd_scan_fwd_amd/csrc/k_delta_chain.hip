@@ -67,7 +67,7 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(const DeltaArgs a
   DeltaSlot sl;
   if (!delta_piece<PASS>(a, piece, sl)) return;
   const int64_t first = sl.t0, last = sl.t1;
-  int64_t slot = delta_first_slot(a, sl.seq, kDeltaBlock) + (first - sl.first) / kDeltaBlock;
+  int64_t slot = delta_first_slot(a, sl.index, kDeltaBlock) + (first - sl.first) / kDeltaBlock;
   const int rows_p = PASS == 1 ? a.P + a.N : a.P;  // rows in all
   const int p0 = pb * L::cols, pw = p0 + 16 * PT * wave;
   const bool live = pw < rows_p;

@@ -9,8 +9,8 @@
 //
 // Bound by a wave's instructions and their latency, some 800 cycles a token of one
 // sequence of 32 heads, P = N = 128 (0.38 us), 1.6 us a token of eight of them (two waves a SIMD).
-// For prompts of a few tokens, which the blocks' two kernels do not repay, and
-// for sizes that have no blocks.
+// For prompts of a few tokens, which the blocks' two kernels do not repay, for the
+// short ones of a pack, and for sizes that have no blocks.
 #include "delta.h"
 
 namespace ssd {
@@ -43,6 +43,7 @@ __global__ __launch_bounds__(kThreads) void delta_walk_kernel(const DeltaArgs a,
   const int64_t row = a.cu != nullptr ? 0 : seq;  // batch row
   int64_t first = 0, last = a.L;
   if (a.cu != nullptr) first = seq_offset(a.cu, seq, a.L), last = seq_offset(a.cu, seq + 1, a.L);
+  if (a.upto > 0 && last - first > a.upto) return;  // (in blocks)
   const TIO* xp = static_cast<const TIO*>(a.x) + row * a.xs.batch;
   const TIO* Bp = static_cast<const TIO*>(a.B) + row * a.bs.batch + (int64_t)g * a.N + nc;
   const TIO* Cp = static_cast<const TIO*>(a.C) + row * a.cs.batch + (int64_t)g * a.N + nc;

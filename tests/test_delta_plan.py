@@ -35,3 +35,15 @@ def test_records_are_paid_for(P, N, batch, L):
     kw = dict(batch=batch, seqlen=L, nheads=32, ngroups=1, headdim=P, dstate=N)
     assert bytes_of(**kw) == (OK, 0)
     assert bytes_of(**dict(kw, seqlen=128, batch=16))[1] > 0
+
+
+@pytest.mark.parametrize("io,H,P,N,S,T", [(0, 8, 64, 64, 256, 4096 + 255), (0, 2, 32, 32, 1001, 8192 + 1000), (0, 4, 64, 64, 256, 2048 + 255),
+                                          (1, 4, 64, 64, 256, 512 + 255), (1, 16, 60, 61, 256, 512 + 255)])
+def test_a_pack_that_may_hold_a_long_sequence_has_blocks_for_it(io, H, P, N, S, T):
+    """The host knows the mean length alone. By it alone these go token after token,
+    where a sequence of nearly all tokens takes 4 to 18 times what it does in blocks."""
+    kw = dict(nheads=H, headdim=P, dstate=N, ngroups=H, io_dtype=io, dt_dtype=io)
+    st, need = bytes_of(S=S, batch=1, seqlen=T, **kw)
+    assert st == OK and need >= (T // 64) * H * (18944 if io else 37376)
+    # with fewer tokens than a long sequence has, token after token and no workspace
+    assert bytes_of(S=30, batch=1, seqlen=30, **kw) == (OK, 0)
