@@ -681,7 +681,8 @@ SSD_API ssd_status_t ssd_delta_step(const ssd_delta_desc_t* desc, const void* x,
  *     (v_a, v_b) <- (v_a cos - v_b sin, v_b cos + v_a sin)
  * where (a, b) is (i, i + rot / 2), or (2 i, 2 i + 1) with pairs. Channels from
  * rot on are only normalised. Norms and products are fp32, angles are taken in
- * 64 bits (exact to 2^-24 of a turn for any position); outputs are rounded once.
+ * 64 bits: off by at most 2^-26 of a turn and 3 * 2^-53 of the turns they come to, together
+ * 2^-24 of a turn up to angles of 2^29. Outputs are rounded once.
  *   q, k            [batch, rows, q_heads or k_heads, D]  io dtype, strided
  *                   ([heads, D] contiguous); k_heads 0: no keys, k and k_out NULL
  *   q_weight, k_weight  [D]                 fp32, nullable (1)
