@@ -618,7 +618,9 @@ SSD_API ssd_status_t ssd_group_norm(const ssd_group_norm_desc_t* desc, const voi
  * States, decays and sums are fp32; y is rounded once. Prompts may be taken in
  * blocks of 64 tokens whose products run on the matrix cores: with bf16 io the
  * operands of y's products (states, scores, solutions) are rounded to bf16, those
- * that reach a state are kept to 16 bits (fp32 io: all of them to 24). An infinity
+ * that reach a state are kept to 16 bits (fp32 io: all of them to 24): y is off by
+ * 2.8e-3 of its norm for keys drawn at random, by up to 2e-2 where one key fills a block
+ * (fp32 io: 3e-7 and 6e-6). An infinity
  * or a NaN of a row of x stays in that row p of its head, one of B, C, dt or
  * beta in its group or head, all of them in their sequence; within 64 tokens
  * before it, though, y may be NaN too. */
@@ -642,7 +644,11 @@ typedef struct {
 } ssd_delta_desc_t;
 
 /* Bytes of workspace for ssd_delta_rule (num_seqs = 0) or
- * ssd_delta_rule_varlen. Pure host computation. */
+ * ssd_delta_rule_varlen. Pure host computation. Token after token takes none; in
+ * blocks there is a record of 18 944 bytes (fp32 io: 37 376) for every 64 tokens that a
+ * sequence begins and every head: 155 MB for 8 x 2048 tokens of 32 heads, bf16, 9.5 GB for a
+ * million; and where a long sequence of few heads is walked in segments, 4 (2 P + N) N bytes
+ * for each segment and head. */
 SSD_API ssd_status_t ssd_delta_rule_workspace_bytes(const ssd_delta_desc_t* desc, int64_t num_seqs, size_t* bytes);
 
 /* The rule over a batch of prompts: initial and final states [batch, H, P, N],

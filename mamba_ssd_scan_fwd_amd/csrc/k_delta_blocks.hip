@@ -6,12 +6,15 @@
 // The next block's rows are loaded into registers while a block is worked on; on the way
 // from there to the LDS odd rows are put in order and fp32 is split into terms.
 //
-// Where a workgroup has a compute unit to itself by its LDS (fp32 of N <= 64, bf16 of
-// N > 128) each wave has a partner, which brings the rows and makes y, as in
-// k_delta_chain.hip: handed S0's terms and U in fp32. Elsewhere (two workgroups to a compute unit,
-// or, fp32 of N > 64, no LDS left for S0 and U) the wave does it all. Measured without / with
-// partners, both kernels: 3 sequences of 1001 tokens, 32 heads, P = N = 64, fp32 118 / 102 us (the walk 85 /
-// 69), of N = 32 87 / 74; 16384 tokens of 16 heads, P = 128, N = 256, bf16 716 / 617.
+// Where a workgroup has a compute unit to itself by its LDS (fp32 of N 33 to 64, bf16 of
+// N > 128), and for fp32 of N <= 32, where two would fit, each wave has a partner, which brings
+// the rows and makes y, as in k_delta_chain.hip: handed S0's terms and U in fp32. Elsewhere (bf16 of
+// N <= 128, two workgroups and more to a compute unit, and fp32 of N > 64, no LDS left for S0 and
+// U) the wave does it all. Measured without / with partners, both kernels: 3 sequences of 1001
+// tokens, 32 heads, P = N = 64, fp32 118 / 102 us (the walk 85 / 69), of N = 32 87 / 74; 16384 tokens of
+// 16 heads, P = 128, N = 256, bf16 716 / 617.
+// Of their 256 registers the instances with partners spill, fp32 of N 33 to 64, 5 (18 at odd sizes), and
+// those without, fp32 of N > 64 at odd sizes, 8.
 //
 // S, R and U' = e^(g_end - g) U are held in fp32. As operands they are terms
 // (delta_blocks.h).
@@ -515,7 +518,7 @@ int64_t groups_of(const DeltaArgs& a, int pass) { return delta_pieces(a) * a.H *
 template <typename TIO, int NP, int PASS>
 hipError_t launch_pass(const DeltaArgs& a, hipStream_t s) {
   const uint32_t blocks_p = blocks_of(a, PASS);
-  // Waves of two kinds where one workgroup of one kind has a compute unit's LDS to itself.
+  // Waves of two kinds (the file's head has the sizes and both sides' times).
   constexpr bool TWO = sizeof(TIO) == 4 ? NP <= 64 : NP == 256;
   constexpr int threads = TWO ? 2 * kThreads : kThreads;
   auto go = [&](auto kern) {
@@ -547,7 +550,11 @@ template <int PASS> hipError_t launch_walk(const DeltaArgs& a, int io, hipStream
 // a row), the states are joined in turn, and the segments are walked side by side.
 // In quarters of a block's time on a compute unit; a join takes about a block's.
 // Of packed sequences only the number is known here: the stream is taken for so many
-// of four times their mean length.
+// of four times their mean length. A pack of one long sequence and many short ones is then
+// not cut: 16384 tokens and 36 sequences of one, 32 heads, P = N = 128, 816 us, where the prompt alone
+// takes 395. Cut as if one sequence could be all of the stream (with states of sequences of one
+// segment read where they lie) it took 1178, 16 sequences of 512 113 -> 131 and 200 of 40 338 -> 536:
+// the other sequences' workgroups that find nothing to do cost more than the cut gives.
 int64_t delta_segment(const DeltaArgs& a, int io) {
   int64_t tokens = a.L, seqs = a.batch;
   if (a.nseq > 0) tokens = 4 * ((a.L + a.nseq - 1) / a.nseq) < a.L ? 4 * ((a.L + a.nseq - 1) / a.nseq) : a.L, seqs = (a.L + tokens - 1) / tokens;
