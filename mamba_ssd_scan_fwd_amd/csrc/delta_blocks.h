@@ -83,7 +83,7 @@ template <int TA, int TB> __device__ __forceinline__ void mul_pair(f32x4_t& acc,
       }
 }
 
-// A slot of `unit` tokens: its sequence, the how manieth that is of those in blocks,
+// A slot of `unit` tokens: its sequence, the index of that among those in blocks,
 // which of the sequence's slots it is, the sequence's tokens [first, last), of
 // batch row `row`, and the slot's own: from t0 up to t1 (t1 <= t0: the slot is empty).
 struct DeltaSlot {

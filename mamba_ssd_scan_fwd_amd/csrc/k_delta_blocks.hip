@@ -614,7 +614,7 @@ __global__ __launch_bounds__(kPick) void delta_pick_kernel(const DeltaArgs a, in
 
 // What either form takes, in microseconds, by a fit to 446 measured calls: 2 to 32 heads of 8 x 8 to
 // 128 x 256, 3 to 16 384 sequences of 1 to 2048 tokens, even ones and one long among ones of a
-// token (root mean square of the error: the walk's 18%, the blocks' 10 to 14%). The walk: the tokens of the
+// token (root mean square of the error: the walk's 17%, the blocks' 10 to 14%). The walk: the tokens of the
 // longest sequence in turn, or, where the card is full, all tokens' updates and the states, in and
 // out. The blocks: two launches and the blocks of the longest sequence in turn, or a record
 // and a block's products for every block and head.
